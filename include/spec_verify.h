@@ -547,6 +547,70 @@ int spec_kv_append(const spec_attn_desc* desc, const void* k_new,
                    const int32_t* seq_lens, int32_t* positions,
                    int64_t* cache_loc, void* workspace, void* stream);
 
+/*
+ * Shape of a rotary append.
+ *   batch, q_len     requests B (>= 0; 0 is a no-op) and block rows per
+ *                    request, padded; any q_len >= 1 (one token, a verify
+ *                    block, a prompt); batch * q_len < 2^31
+ *   num_q_heads      Hq >= 0 (0: keys and values only); num_kv_heads Hkv >= 1
+ *   head_dim         must be 256
+ *   page_size, num_pages, max_pages_per_seq, kv_dtype, flags, q_lens
+ *                    as in spec_attn_desc (page_size >= 1 for either type)
+ *   rotary_dim       R: the first R channels of a head are rotated, the rest
+ *                    copied; a multiple of 8, 8..256
+ *   interleaved      0: pair j is channels (j, j + R/2); 1: (2j, 2j + 1)
+ *   attn_factor      finite factor on the rotated channels of q and K (1
+ *                    unless the scaling for long contexts asks for one)
+ *   q_strides, k_strides, v_strides   elements from one request to the next
+ *                    and from one token to the next (multiples of 8, >= 0);
+ *                    heads lie 256 elements apart, so the three may be parts
+ *                    of one projection's output
+ */
+typedef struct {
+  int32_t batch, q_len, num_q_heads, num_kv_heads, head_dim;
+  int32_t page_size, num_pages, max_pages_per_seq;
+  int32_t kv_dtype;
+  uint32_t flags;
+  const int32_t* q_lens;
+  int32_t rotary_dim, interleaved;
+  float attn_factor;
+  int64_t q_strides[2], k_strides[2], v_strides[2];
+} spec_rope_desc;
+
+/*
+ * Rotary positions on a block's queries and keys, and the append of the
+ * rotated keys and the values to the paged cache, in one launch.
+ *
+ * Block row i < q_b of request b is token t = seq_lens[b] - q_b + i, as for
+ * spec_kv_append; it is rotated to its position t: with a = t * freq[j] the
+ * pair j = (x, y) of every query and key head becomes
+ *     (m (x cos a - y sin a), m (y cos a + x sin a)),  m = attn_factor.
+ * The angle is reduced to a turn exactly, so far positions are as accurate
+ * as near ones.  Arithmetic is fp32 and each result is rounded once, where
+ * it is stored (bf16, or the FP8 rule of spec_kv_append on the fp32 values).
+ *
+ *   q         bf16, Hq heads of 256 per token, 16-byte aligned; NULL with
+ *             Hq == 0 (keys and values of a layer whose queries are made
+ *             elsewhere, such as a drafter's from the target's hidden state)
+ *   k_new, v_new  bf16, Hkv heads of 256 per token, 16-byte aligned
+ *   freq      fp64 [R/2]: radians per position, any scaling applied
+ *             (the Python binding makes the usual ones), finite
+ *   q_out     bf16 [B, q_len, Hq, 256] contiguous, 16-byte aligned; may be q
+ *             itself where q is contiguous, and may not overlap it
+ *             otherwise.  Rows that hold no token (i >= q_b, t < 0) are
+ *             zeros; their inputs are not read.
+ *   k_pages, v_pages, k_scales, v_scales, page_table, seq_lens, positions,
+ *   cache_loc, workspace  as in spec_kv_append.  A token without a slot (t
+ *             past the table, a page id outside the pool) is rotated in
+ *             q_out and not appended.
+ */
+int spec_rope_append(const spec_rope_desc* desc, const void* q,
+                     const void* k_new, const void* v_new, const double* freq,
+                     void* q_out, void* k_pages, void* v_pages, void* k_scales,
+                     void* v_scales, const int32_t* page_table,
+                     const int32_t* seq_lens, int32_t* positions,
+                     int64_t* cache_loc, void* workspace, void* stream);
+
 /* Message for the last nonzero return on this thread ("" if none). */
 const char* spec_last_error(void);
 

@@ -37,7 +37,7 @@ EXPORTED = (
     "spec_kv_append", "spec_greedy_accept_commit", "spec_prepare_next_block",
     "spec_stochastic_workspace_size", "spec_stochastic_accept",
     "spec_select_workspace_size", "spec_dflash2_select",
-    "spec_verify_set_wait_limit",
+    "spec_verify_set_wait_limit", "spec_rope_append",
 )
 SELECT_MODES = {"greedy": 0, "map": 1}
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
@@ -57,6 +57,22 @@ class AttnDesc(ctypes.Structure):
                 ("max_pages_per_seq", ctypes.c_int32),
                 ("kv_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32),
                 ("q_lens", ctypes.c_void_p)]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("q_len", ctypes.c_int32),
+                ("num_q_heads", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("max_pages_per_seq", ctypes.c_int32),
+                ("kv_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32),
+                ("q_lens", ctypes.c_void_p),
+                ("rotary_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32),
+                ("attn_factor", ctypes.c_float),
+                ("q_strides", ctypes.c_int64 * 2),
+                ("k_strides", ctypes.c_int64 * 2),
+                ("v_strides", ctypes.c_int64 * 2)]
 
 
 class SelectDesc(ctypes.Structure):
@@ -99,6 +115,8 @@ def load(path: str = LIB_PATH):
     lib.spec_kv_append.argtypes = [ctypes.POINTER(AttnDesc), P, P, P, P, P,
                                    P, P, P, P, P, P, P]
     lib.spec_kv_append.restype = ctypes.c_int
+    lib.spec_rope_append.argtypes = [ctypes.POINTER(RopeDesc)] + [P] * 15
+    lib.spec_rope_append.restype = ctypes.c_int
     lib.spec_verify_set_wait_limit.argtypes = [ctypes.c_int64]
     lib.spec_verify_set_wait_limit.restype = ctypes.c_int
     lib.spec_verify_status.argtypes = [P, ctypes.POINTER(u32), i32, P]
@@ -145,6 +163,58 @@ def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _expect(t: torch.Tensor, dtype, what: str, shape=None,
+            contiguous: bool = False) -> None:
+    """Refuse a tensor of another type, shape or layout before its address
+    is taken."""
+    if t.dtype != dtype:
+        raise SpecError(SPEC_ERR_ARG, f"{what} must be {dtype}, is {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise SpecError(SPEC_ERR_ARG, f"{what} must be {tuple(shape)}, is "
+                                      f"{tuple(t.shape)}")
+    if contiguous and not t.is_contiguous():
+        raise SpecError(SPEC_ERR_ARG, f"{what} must be contiguous")
+
+
+def _on_current_device(*tensors) -> None:
+    """Every tensor lies on the current CUDA device: the library takes plain
+    addresses and launches there."""
+    for t in tensors:
+        if t is not None and not t.is_cuda:
+            raise SpecError(SPEC_ERR_ARG, "tensors must be on a CUDA device")
+    now = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != now:
+            raise SpecError(SPEC_ERR_ARG,
+                            f"a tensor on cuda:{t.device.index} in a call on "
+                            f"cuda:{now}, the current device")
+
+
+def _expect_pools(k_pages, v_pages, k_scales, v_scales, hkv: int,
+                  d: int) -> bool:
+    """Check a K/V page pool; returns whether it is FP8."""
+    fp8 = k_pages.dtype == torch.uint8
+    shape = (k_pages.shape[0], hkv, k_pages.shape[2], d)
+    dtype = torch.uint8 if fp8 else torch.bfloat16
+    _expect(k_pages, dtype, "k_pages", shape, True)
+    _expect(v_pages, dtype, "v_pages", shape, True)
+    if fp8 and k_scales is not None and v_scales is not None:
+        shape = shape[:3] + (d // 64,)
+        _expect(k_scales, torch.float16, "k_scales", shape, True)
+        _expect(v_scales, torch.float16, "v_scales", shape, True)
+    return fp8
+
+
+def _expect_optional(B: int, q_len: int, q_lens, positions=None,
+                     cache_loc=None) -> None:
+    if q_lens is not None:
+        _expect(q_lens, torch.int32, "q_lens", (B,), True)
+    if positions is not None:
+        _expect(positions, torch.int32, "positions", (B, q_len), True)
+    if cache_loc is not None:
+        _expect(cache_loc, torch.int64, "cache_loc", (B, q_len), True)
 
 
 def make_desc(*, batch, q_len, num_q_heads, num_kv_heads, head_dim,
@@ -251,6 +321,68 @@ def kv_append(k_new, v_new, k_pages, v_pages, page_table, seq_lens, *,
         _ptr(v_pages), _ptr(k_scales), _ptr(v_scales), _ptr(page_table),
         _ptr(seq_lens), _ptr(positions), _ptr(cache_loc), _ptr(workspace),
         _stream(stream)))
+
+
+def _strides(t: torch.Tensor, what: str):
+    """(request, token) strides of [B, q_len, H, 256] whose heads and channels
+    are contiguous."""
+    if t.stride(3) != 1 or (t.shape[2] > 1 and t.stride(2) != t.shape[3]):
+        raise SpecError(SPEC_ERR_ARG,
+                        f"{what}: heads and channels must be contiguous")
+    return (t.stride(0) if t.shape[0] > 1 else 0,
+            t.stride(1) if t.shape[1] > 1 else 0)
+
+
+def rope_append(q, k_new, v_new, freq, k_pages, v_pages, page_table, seq_lens,
+                *, interleaved: bool = False, attn_factor: float = 1.0,
+                q_out: Optional[torch.Tensor] = None, k_scales=None,
+                v_scales=None, positions=None, cache_loc=None,
+                checked: bool = False, workspace=None, q_lens=None,
+                stream=None):
+    """Rotate the block's queries and keys to their positions and append K/V
+    to the paged pool in place (quantised on write for an FP8 pool).
+
+    q bf16 [B, q_len, Hq, 256] (None: keys and values only), k_new / v_new
+    bf16 [B, q_len, Hkv, 256], each possibly a view of one projection's
+    output; freq float64 [rotary_dim / 2] radians per position
+    (rope_frequencies).  Returns the rotated queries, bf16
+    [B, q_len, Hq, 256] (q_out, which may be a contiguous q itself), or None.
+    """
+    B, q_len, hkv, d = k_new.shape
+    hq = 0 if q is None else q.shape[2]
+    _expect(k_new, torch.bfloat16, "k_new")
+    _expect(v_new, torch.bfloat16, "v_new", k_new.shape)
+    _expect(freq, torch.float64, "freq", contiguous=True)
+    _expect(page_table, torch.int32, "page_table", contiguous=True)
+    _expect(seq_lens, torch.int32, "seq_lens", (B,), contiguous=True)
+    if q is not None:
+        _expect(q, torch.bfloat16, "q", (B, q_len, hq, d))
+        if q_out is None:
+            q_out = torch.empty((B, q_len, hq, d), dtype=q.dtype,
+                                device=q.device)
+        _expect(q_out, torch.bfloat16, "q_out", (B, q_len, hq, d),
+                contiguous=True)
+    fp8 = _expect_pools(k_pages, v_pages, k_scales, v_scales, hkv, d)
+    _expect_optional(B, q_len, q_lens, positions, cache_loc)
+    _on_current_device(q, k_new, v_new, freq, q_out, k_pages, v_pages,
+                       k_scales, v_scales, page_table, seq_lens, q_lens,
+                       positions, cache_loc, workspace)
+    i64x2 = ctypes.c_int64 * 2
+    desc = RopeDesc(B, q_len, hq, hkv, d, k_pages.shape[2], k_pages.shape[0],
+                    page_table.shape[1],
+                    SPEC_KV_FP8_E4M3 if fp8 else SPEC_KV_BF16,
+                    SPEC_FLAG_CHECKED if checked else 0,
+                    None if q_lens is None else q_lens.data_ptr(),
+                    2 * freq.shape[0], 1 if interleaved else 0, attn_factor,
+                    i64x2(*(_strides(q, "q") if q is not None else (0, 0))),
+                    i64x2(*_strides(k_new, "k_new")),
+                    i64x2(*_strides(v_new, "v_new")))
+    _check(load().spec_rope_append(
+        ctypes.byref(desc), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(freq),
+        _ptr(q_out) if q is not None else None, _ptr(k_pages), _ptr(v_pages),
+        _ptr(k_scales), _ptr(v_scales), _ptr(page_table), _ptr(seq_lens),
+        _ptr(positions), _ptr(cache_loc), _ptr(workspace), _stream(stream)))
+    return q_out
 
 
 def set_wait_limit(cycles: int) -> None:

@@ -2,16 +2,10 @@
 // cache locations.
 //
 // One warp per (request b, block row i, KV head g); lane l owns channels
-// 8l .. 8l+7 (16 bytes of the bf16 input row).  For an FP8 pool the eight
-// lanes of a 64-channel block reduce |x| by shuffles; the scale and the
-// codes are computed in fp32 with correctly rounded division, so the stored
-// bytes follow the rule stated in spec_verify.h exactly:
-//   scale = fp16_rn(amax / 448) (1 if it rounds to zero),
-//   byte  = E4M3_rn_satfinite(x / scale)
-// ("Qwen3.8-27B-FP8" page, "Implemented execution path": E4M3 cache with
-// per-token / per-KV-head FP16 scales over 64-channel blocks).
-#include <cuda_fp8.h>
-
+// 8l .. 8l+7 (16 bytes of the bf16 input row).  For an FP8 pool the row is
+// quantised on write (quantise_row in append.cuh; "Qwen3.8-27B-FP8" page,
+// "Implemented execution path": E4M3 cache with per-token / per-KV-head FP16
+// scales over 64-channel blocks).
 #include "append.cuh"
 #include "common.cuh"
 #include "spec_verify.h"
@@ -69,31 +63,10 @@ __global__ void __launch_bounds__(kWarps * 32)
       x[2 * e] = __low2float(h2[e]);
       x[2 * e + 1] = __high2float(h2[e]);
     }
-    float amax = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1)  // the 8 lanes of this 64-channel block
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    __half scale = __float2half_rn(__fdiv_rn(amax, 448.f));
-    if (__half2float(scale) == 0.f) scale = __float2half_rn(1.f);
-    const float sf = __half2float(scale);
-    uint32_t packed[2] = {0u, 0u};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 qv = make_float2(__fdiv_rn(x[2 * e], sf),
-                                    __fdiv_rn(x[2 * e + 1], sf));
-      const uint32_t pair =
-          __nv_cvt_float2_to_fp8x2(qv, __NV_SATFINITE, __NV_E4M3) & 0xFFFFu;
-      packed[e >> 1] |= pair << (16 * (e & 1));
-    }
-    uint8_t* dst = static_cast<uint8_t*>(kv ? p.v_pages : p.k_pages);
-    *reinterpret_cast<uint2*>(dst + row * kHeadDim + lane * 8) =
-        make_uint2(packed[0], packed[1]);
-    if ((lane & 7) == 0) {
-      __half* sdst = kv ? p.v_scales : p.k_scales;
-      sdst[row * (kHeadDim / 64) + (lane >> 3)] = scale;
-    }
+    quantise_row(x, lane,
+                 static_cast<uint8_t*>(kv ? p.v_pages : p.k_pages) +
+                     row * kHeadDim,
+                 (kv ? p.v_scales : p.k_scales) + row * (kHeadDim / 64));
   }
 }
 

@@ -127,14 +127,11 @@ int current_device(int* dev) {
   return SPEC_OK;
 }
 
-// Split-kernel grid for `rows` query rows per KV head on the current device:
-// every SM filled with as many CTAs as fit.
-int split_grid(int rows, bool tc, bool fp8, int* grid) {
+// SM count of the current device.
+int sm_count(int* sms) {
   int dev;
   int rc = current_device(&dev);
   if (rc) return rc;
-  const bool fp8t = tc && fp8 && rows <= specv::kFp8tMaxRows;
-  const int w = fp8t ? 11 : (tc ? (fp8 ? 10 : 9) : (rows + 15) / 16);
   std::lock_guard<std::mutex> lock(g_mu);
   if (!g_sms[dev]) {
     int n = 0;
@@ -144,6 +141,22 @@ int split_grid(int rows, bool tc, bool fp8, int* grid) {
       return fail(SPEC_ERR_CUDA, "SM count: %s", cudaGetErrorString(e));
     g_sms[dev] = n;
   }
+  *sms = g_sms[dev];
+  return SPEC_OK;
+}
+
+// Split-kernel grid for `rows` query rows per KV head on the current device:
+// every SM filled with as many CTAs as fit.
+int split_grid(int rows, bool tc, bool fp8, int* grid) {
+  int dev;
+  int rc = current_device(&dev);
+  if (rc) return rc;
+  const bool fp8t = tc && fp8 && rows <= specv::kFp8tMaxRows;
+  const int w = fp8t ? 11 : (tc ? (fp8 ? 10 : 9) : (rows + 15) / 16);
+  int sms;
+  rc = sm_count(&sms);
+  if (rc) return rc;
+  std::lock_guard<std::mutex> lock(g_mu);
   if (!g_occ[dev][w]) {
     int occ = fp8t ? specv::verify_split_fp8t_ctas_per_sm()
               : tc  ? specv::verify_split_tc_ctas_per_sm(fp8)
@@ -152,7 +165,7 @@ int split_grid(int rows, bool tc, bool fp8, int* grid) {
       return fail(SPEC_ERR_CUDA, "split kernel does not fit on an SM");
     g_occ[dev][w] = occ;
   }
-  *grid = g_sms[dev] * g_occ[dev][w];
+  *grid = sms * g_occ[dev][w];
   return SPEC_OK;
 }
 
@@ -447,6 +460,125 @@ int spec_kv_append(const spec_attn_desc* desc, const void* k_new,
   e = specv::launch_kv_append(p, s);
   if (e != cudaSuccess)
     return fail(SPEC_ERR_CUDA, "append kernel launch: %s", cudaGetErrorString(e));
+  return SPEC_OK;
+}
+
+int spec_rope_append(const spec_rope_desc* desc, const void* q,
+                     const void* k_new, const void* v_new, const double* freq,
+                     void* q_out, void* k_pages, void* v_pages, void* k_scales,
+                     void* v_scales, const int32_t* page_table,
+                     const int32_t* seq_lens, int32_t* positions,
+                     int64_t* cache_loc, void* workspace, void* stream) {
+  g_err[0] = 0;
+  const spec_rope_desc* d = desc;
+  if (!d) return fail(SPEC_ERR_ARG, "desc is NULL");
+  if (d->batch < 0 || d->q_len < 1 ||
+      (long long)d->batch * d->q_len >= (1LL << 31))
+    return fail(SPEC_ERR_ARG, "batch %d / q_len %d", d->batch, d->q_len);
+  if (d->num_q_heads < 0 || d->num_kv_heads < 1 || d->num_q_heads > 65535 ||
+      d->num_kv_heads > 65535)
+    return fail(SPEC_ERR_ARG, "num_q_heads %d / num_kv_heads %d",
+                d->num_q_heads, d->num_kv_heads);
+  if (d->head_dim != specv::kHeadDim)
+    return fail(SPEC_ERR_UNSUPPORTED, "head_dim %d (only 256)", d->head_dim);
+  if (d->page_size < 1 || d->page_size > 4096 ||
+      (d->page_size & (d->page_size - 1)))
+    return fail(SPEC_ERR_ARG, "page_size %d is not a power of two in [1, 4096]",
+                d->page_size);
+  if (d->num_pages < 1 || d->max_pages_per_seq < 1)
+    return fail(SPEC_ERR_ARG, "num_pages %d / max_pages_per_seq %d must be >= 1",
+                d->num_pages, d->max_pages_per_seq);
+  if ((long long)d->max_pages_per_seq * d->page_size > (1LL << 30))
+    return fail(SPEC_ERR_ARG, "max_pages_per_seq * page_size exceeds 2^30");
+  if (d->kv_dtype != SPEC_KV_BF16 && d->kv_dtype != SPEC_KV_FP8_E4M3)
+    return fail(SPEC_ERR_ARG, "kv_dtype %d", d->kv_dtype);
+  if (d->flags & ~SPEC_FLAG_CHECKED)
+    return fail(SPEC_ERR_ARG, "unknown flags 0x%x", d->flags);
+  if (d->rotary_dim < 8 || d->rotary_dim > specv::kHeadDim || d->rotary_dim % 8)
+    return fail(SPEC_ERR_ARG, "rotary_dim %d: a multiple of 8 in [8, 256]",
+                d->rotary_dim);
+  if (d->interleaved != 0 && d->interleaved != 1)
+    return fail(SPEC_ERR_ARG, "interleaved %d", d->interleaved);
+  if (!(d->attn_factor > -3.0e38f && d->attn_factor < 3.0e38f))
+    return fail(SPEC_ERR_ARG, "attn_factor must be finite");
+  for (int k = 0; k < 2; ++k)
+    if (d->q_strides[k] < 0 || d->k_strides[k] < 0 || d->v_strides[k] < 0 ||
+        d->q_strides[k] % 8 || d->k_strides[k] % 8 || d->v_strides[k] % 8)
+      return fail(SPEC_ERR_ARG, "strides must be multiples of 8 and >= 0");
+  if (d->batch == 0) return SPEC_OK;
+  if (!k_new || !v_new || !freq || !k_pages || !v_pages || !page_table ||
+      !seq_lens)
+    return fail(SPEC_ERR_ARG, "NULL tensor pointer");
+  if (!q != !q_out || !q != (d->num_q_heads == 0))
+    return fail(SPEC_ERR_ARG, "q and q_out go with num_q_heads > 0");
+  if (!aligned(q, 16) || !aligned(q_out, 16) || !aligned(k_new, 16) ||
+      !aligned(v_new, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16))
+    return fail(SPEC_ERR_ALIGN,
+                "q, q_out, k_new, v_new and the pools must be 16-byte aligned");
+  if (!aligned(freq, 8) || !aligned(page_table, 4) || !aligned(seq_lens, 4) ||
+      (d->q_lens && !aligned(d->q_lens, 4)) ||
+      (positions && !aligned(positions, 4)) ||
+      (cache_loc && !aligned(cache_loc, 8)))
+    return fail(SPEC_ERR_ALIGN, "freq or index arrays are misaligned");
+  const bool fp8 = d->kv_dtype == SPEC_KV_FP8_E4M3;
+  if (fp8 && (!k_scales || !v_scales))
+    return fail(SPEC_ERR_ARG, "FP8 KV needs k_scales and v_scales");
+  if (fp8 && (!aligned(k_scales, 16) || !aligned(v_scales, 16)))
+    return fail(SPEC_ERR_ALIGN, "scales must be 16-byte aligned");
+  const bool checked = d->flags & SPEC_FLAG_CHECKED;
+  if (checked && !workspace)
+    return fail(SPEC_ERR_WORKSPACE, "SPEC_FLAG_CHECKED needs a workspace");
+  if (checked && !aligned(workspace, 4))
+    return fail(SPEC_ERR_ALIGN, "workspace must be 4-byte aligned");
+  int sms;
+  int rc = sm_count(&sms);
+  if (rc) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  specv::RopeParams p;
+  std::memset(&p, 0, sizeof p);
+  p.a.k_new = static_cast<const __nv_bfloat16*>(k_new);
+  p.a.v_new = static_cast<const __nv_bfloat16*>(v_new);
+  p.a.k_pages = k_pages;
+  p.a.v_pages = v_pages;
+  p.a.k_scales = fp8 ? static_cast<__half*>(k_scales) : nullptr;
+  p.a.v_scales = fp8 ? static_cast<__half*>(v_scales) : nullptr;
+  p.a.page_table = page_table;
+  p.a.seq_lens = seq_lens;
+  p.a.q_lens = d->q_lens;
+  p.a.positions = positions;
+  p.a.cache_loc = cache_loc;
+  p.a.batch = d->batch;
+  p.a.q_len = d->q_len;
+  p.a.hkv = d->num_kv_heads;
+  p.a.page_size = d->page_size;
+  while ((1 << p.a.log2_ps) < d->page_size) ++p.a.log2_ps;
+  p.a.num_pages = d->num_pages;
+  p.a.max_pages = d->max_pages_per_seq;
+  p.a.max_tokens = (long long)d->max_pages_per_seq * d->page_size;
+  p.a.fp8 = fp8;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_out = static_cast<__nv_bfloat16*>(q_out);
+  p.freq = freq;
+  p.hq = d->num_q_heads;
+  p.rotary = d->rotary_dim;
+  p.factor = d->attn_factor;
+  p.q_req = d->q_strides[0];
+  p.q_tok = d->q_strides[1];
+  p.k_req = d->k_strides[0];
+  p.k_tok = d->k_strides[1];
+  p.v_req = d->v_strides[0];
+  p.v_tok = d->v_strides[1];
+  cudaError_t e;
+  if (checked) {
+    p.a.status = static_cast<uint32_t*>(workspace);
+    e = cudaMemsetAsync(workspace, 0, sizeof(uint32_t), s);
+    if (e != cudaSuccess)
+      return fail(SPEC_ERR_CUDA, "status reset: %s", cudaGetErrorString(e));
+  }
+  e = specv::launch_rope_append(p, d->interleaved == 1, sms, s);
+  if (e != cudaSuccess)
+    return fail(SPEC_ERR_CUDA, "rotary append launch: %s",
+                cudaGetErrorString(e));
   return SPEC_OK;
 }
 

@@ -53,6 +53,9 @@ extern "C" {
                                      not a data condition); output invalid */
 #define SPEC_STATUS_NO_SLOT 4u    /* spec_prepare_next_block: a next-block
                                      row has no reserved cache slot */
+#define SPEC_STATUS_BAD_GROUPS 8u /* spec_verify_attention_shared: group
+                                     borders that run backwards or out of the
+                                     batch; nothing was shared */
 
 typedef enum {
   SPEC_KV_BF16 = 0,     /* K/V elements are bf16 */
@@ -161,6 +164,46 @@ int spec_verify_attention(const spec_attn_desc* desc, const void* q,
                           const int32_t* page_table, const int32_t* seq_lens,
                           float scale, void* out, void* workspace,
                           size_t workspace_bytes, void* stream);
+
+/*
+ * Verify attention of requests that share cached prefixes: each shared part
+ * is read and attended once for all rows of its group.
+ *
+ * Groups are runs of consecutive requests: group n is the requests
+ * [group_starts[n], group_starts[n+1]), and the first shared_lens[n] tokens
+ * of all of them are the same cache entries: their page tables agree over
+ * those tokens (a prefix cache, many samples of one prompt).  The result is
+ * that of spec_verify_attention on the same arguments, up to rounding (the
+ * weights of shared tokens are rounded once to the type of the values).
+ *
+ * shared_lens is a statement, not a mask.  The library attends in one pass
+ * the largest multiple of 128 tokens that does not exceed shared_lens[n] and
+ * that every row of every live request (q_b > 0) sees whole, through the page
+ * table of the group's first live request; all other tokens, and groups with
+ * fewer than two live requests, are read per request.  Requests outside
+ * [group_starts[0], group_starts[groups]) belong to no group.
+ *
+ *   groups       1 .. 1024
+ *   group_starts int32 [groups + 1], non-decreasing, within [0, B]; otherwise
+ *                nothing is shared, and SPEC_FLAG_CHECKED reports
+ *                SPEC_STATUS_BAD_GROUPS
+ *   shared_lens  int32 [groups] tokens (values < 128 share nothing)
+ *   workspace    >= spec_verify_shared_workspace_size(desc, groups) bytes,
+ *                256-byte aligned; contents need no initialisation
+ * Both arrays are DEVICE pointers read by the call's kernels, so they may
+ * change between graph replays.  page_size must be >= 8.  Everything else as
+ * in spec_verify_attention.
+ */
+int spec_verify_attention_shared(
+    const spec_attn_desc* desc, const void* q, const void* k_pages,
+    const void* v_pages, const void* k_scales, const void* v_scales,
+    const int32_t* page_table, const int32_t* seq_lens, int32_t groups,
+    const int32_t* group_starts, const int32_t* shared_lens, float scale,
+    void* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes for spec_verify_attention_shared (0 on a bad desc). */
+size_t spec_verify_shared_workspace_size(const spec_attn_desc* desc,
+                                         int32_t groups);
 
 /*
  * Test hook for the failure path: the main-loop bound, in SM clock cycles,

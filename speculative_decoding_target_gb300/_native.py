@@ -28,6 +28,7 @@ SPEC_FLAG_CHECKED = 1
 SPEC_STATUS_BAD_PAGE = 1
 SPEC_STATUS_TIMEOUT = 2
 SPEC_STATUS_NO_SLOT = 4
+SPEC_STATUS_BAD_GROUPS = 8
 WIDTH_POLICIES = {"fixed": 0, "ewma": 1, "doubling": 2}
 
 EXPORTED = (
@@ -38,6 +39,7 @@ EXPORTED = (
     "spec_stochastic_workspace_size", "spec_stochastic_accept",
     "spec_select_workspace_size", "spec_dflash2_select",
     "spec_verify_set_wait_limit", "spec_rope_append",
+    "spec_verify_attention_shared", "spec_verify_shared_workspace_size",
 )
 SELECT_MODES = {"greedy": 0, "map": 1}
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
@@ -115,6 +117,13 @@ def load(path: str = LIB_PATH):
     lib.spec_kv_append.argtypes = [ctypes.POINTER(AttnDesc), P, P, P, P, P,
                                    P, P, P, P, P, P, P]
     lib.spec_kv_append.restype = ctypes.c_int
+    lib.spec_verify_shared_workspace_size.argtypes = [
+        ctypes.POINTER(AttnDesc), i32]
+    lib.spec_verify_shared_workspace_size.restype = sz
+    lib.spec_verify_attention_shared.argtypes = [
+        ctypes.POINTER(AttnDesc), P, P, P, P, P, P, P, i32, P, P,
+        ctypes.c_float, P, P, sz, P]
+    lib.spec_verify_attention_shared.restype = ctypes.c_int
     lib.spec_rope_append.argtypes = [ctypes.POINTER(RopeDesc)] + [P] * 15
     lib.spec_rope_append.restype = ctypes.c_int
     lib.spec_verify_set_wait_limit.argtypes = [ctypes.c_int64]
@@ -283,6 +292,59 @@ def verify_attention(q, k_pages, v_pages, page_table, seq_lens, *,
         workspace = alloc_workspace(verify_workspace_size(desc), q.device)
     verify_attention_into(desc, q, k_pages, v_pages, k_scales, v_scales,
                           page_table, seq_lens, scale, out, workspace, stream)
+    return out
+
+
+def shared_workspace_size(desc: AttnDesc, groups: int) -> int:
+    n = load().spec_verify_shared_workspace_size(ctypes.byref(desc), groups)
+    if n == 0:
+        raise SpecError(SPEC_ERR_ARG, load().spec_last_error().decode())
+    return int(n)
+
+
+def verify_attention_shared(q, k_pages, v_pages, page_table, seq_lens,
+                            group_starts, shared_lens, *, scale: float,
+                            k_scales=None, v_scales=None,
+                            out: Optional[torch.Tensor] = None,
+                            workspace: Optional[torch.Tensor] = None,
+                            checked: bool = False, q_lens=None,
+                            stream=None) -> torch.Tensor:
+    """Verify attention of requests that share cached prefixes: group n is
+    requests group_starts[n] .. group_starts[n+1] - 1 (int32 [groups + 1]),
+    whose first shared_lens[n] (int32 [groups]) tokens are the same cache
+    entries; each shared part is computed once for its group.  Returns out
+    bf16 [B, q_len, Hq, D]."""
+    B, q_len, hq, d = q.shape
+    _expect(q, torch.bfloat16, "q", contiguous=True)
+    fp8 = _expect_pools(k_pages, v_pages, k_scales, v_scales,
+                        k_pages.shape[1], d)
+    groups = shared_lens.numel()
+    _expect(page_table, torch.int32, "page_table", contiguous=True)
+    if page_table.shape[0] != B:
+        raise SpecError(SPEC_ERR_ARG, f"page_table must have {B} rows")
+    _expect(seq_lens, torch.int32, "seq_lens", (B,), True)
+    _expect(shared_lens, torch.int32, "shared_lens", (groups,), True)
+    _expect(group_starts, torch.int32, "group_starts", (groups + 1,), True)
+    _expect_optional(B, q_len, q_lens)
+    if out is None:
+        out = torch.empty_like(q)
+    _expect(out, torch.bfloat16, "out", q.shape, True)
+    _on_current_device(q, k_pages, v_pages, k_scales, v_scales, page_table,
+                       seq_lens, group_starts, shared_lens, q_lens, out,
+                       workspace)
+    desc = AttnDesc(B, q_len, hq, k_pages.shape[1], d, k_pages.shape[2],
+                    k_pages.shape[0], page_table.shape[1],
+                    SPEC_KV_FP8_E4M3 if fp8 else SPEC_KV_BF16,
+                    SPEC_FLAG_CHECKED if checked else 0,
+                    None if q_lens is None else q_lens.data_ptr())
+    if workspace is None:
+        workspace = alloc_workspace(shared_workspace_size(desc, groups),
+                                    q.device)
+    _check(load().spec_verify_attention_shared(
+        ctypes.byref(desc), _ptr(q), _ptr(k_pages), _ptr(v_pages),
+        _ptr(k_scales), _ptr(v_scales), _ptr(page_table), _ptr(seq_lens),
+        groups, _ptr(group_starts), _ptr(shared_lens), float(scale),
+        _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream)))
     return out
 
 

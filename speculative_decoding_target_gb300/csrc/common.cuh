@@ -38,6 +38,9 @@ struct AttnParams {
   const int32_t* page_table;
   const int32_t* seq_lens;
   const int32_t* q_lens;  // optional [B]: rows of each block (<= q_len)
+  // optional [B]: first token this call attends (a multiple of 128); the
+  // tokens before it are another kernel's, so every piece writes a partial
+  const int32_t* kv_begin;
   __nv_bfloat16* out;
   float* part_o;      // [nslots, rows, 256]
   float* part_lse;    // [nslots, rows] (base 2)
@@ -75,6 +78,15 @@ __device__ __forceinline__ int causal_limit(int len, int qb, int i) {
 
 __device__ __forceinline__ int units_of(int len) {
   return (len + kUnit - 1) / kUnit;
+}
+
+// First token of request b that this call attends, and its plan units.
+__device__ __forceinline__ int first_token(const AttnParams& p, int b) {
+  return p.kv_begin ? p.kv_begin[b] : 0;
+}
+__device__ __forceinline__ int request_units(const AttnParams& p, int b) {
+  const int n = clamp_len(p.seq_lens[b], p.max_tokens) - first_token(p, b);
+  return n > 0 ? units_of(n) : 0;
 }
 
 // The plan runs on virtual units: every (request, KV head) segment is
@@ -115,6 +127,16 @@ __device__ __forceinline__ int seg_splits(const Plan& pl, long long s0, int nt) 
   return chunk_of(pl, s0 + nt - 1) - chunk_of(pl, s0) + 1;
 }
 
+// Splits of a segment as its kernel writes it: 1 goes straight to the output,
+// more (and any piece of a call that attends only part of the tokens) to
+// partials.
+__device__ __forceinline__ int written_splits(const AttnParams& p,
+                                              const Plan& pl, long long s0,
+                                              int nt) {
+  const int S = seg_splits(pl, s0, nt);
+  return p.kv_begin ? max(S, 2) : S;
+}
+
 // Exclusive prefix of virtual units per request (real units + piece_cost)
 // into s_pre[0..batch] (s_pre[0] = 0).  Called by the whole block; ends
 // with __syncthreads().
@@ -126,7 +148,7 @@ __device__ __forceinline__ void plan_prefix(const AttnParams& p, int* s_pre) {
     for (int base = 0; base < p.batch; base += 32) {
       int b = base + lane;
       int v = b < p.batch
-                  ? units_of(clamp_len(p.seq_lens[b], p.max_tokens)) + p.piece_cost
+                  ? request_units(p, b) + p.piece_cost
                   : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {

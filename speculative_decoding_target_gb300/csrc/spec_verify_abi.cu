@@ -12,6 +12,7 @@
 #include "append.cuh"
 #include "next_block.cuh"
 #include "selector.cuh"
+#include "shared_prefix.cuh"
 #include "stochastic.cuh"
 #include "accept.cuh"
 #include "common.cuh"
@@ -41,6 +42,7 @@ int g_sms[kMaxDevices];
 int g_occ[kMaxDevices][12];  // split-kernel CTAs per SM: [w] mma.sync with w
                              // compute warps, [9] tcgen05 bf16, [10] tcgen05
                              // FP8, [11] tcgen05 FP8 with TMEM KV operands
+int g_pairs[kMaxDevices][2];  // resident CTA pairs of the prefix kernel
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 // main-loop wait bound of the split kernels for SPEC_FLAG_CHECKED calls
 // (spec_verify_set_wait_limit); 0 = the default bound
@@ -240,41 +242,12 @@ int layout(const spec_attn_desc* d, Layout* L) {
   return SPEC_OK;
 }
 
-}  // namespace
-
-namespace specv {
-int set_error(int code, const char* fmt, ...) {
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(g_err, sizeof g_err, fmt, ap);
-  va_end(ap);
-  return code;
-}
-}  // namespace specv
-
-extern "C" {
-
-const char* spec_last_error(void) { return g_err; }
-
-const char* spec_version(void) { return "spec_verify 0.2 (sm_103a)"; }
-
-size_t spec_verify_workspace_size(const spec_attn_desc* desc) {
-  if (check_desc(desc)) return 0;
-  Layout L;
-  if (layout(desc, &L)) return 0;
-  return L.bytes;
-}
-
-int spec_verify_attention(const spec_attn_desc* desc, const void* q,
-                          const void* k_pages, const void* v_pages,
-                          const void* k_scales, const void* v_scales,
-                          const int32_t* page_table, const int32_t* seq_lens,
-                          float scale, void* out, void* workspace,
-                          size_t workspace_bytes, void* stream) {
-  g_err[0] = 0;
-  int rc = check_desc(desc);
-  if (rc) return rc;
-  if (desc->batch == 0) return SPEC_OK;
+// Tensor pointers of an attention call (the batch is not empty).
+int check_attention(const spec_attn_desc* desc, const void* q,
+                    const void* k_pages, const void* v_pages,
+                    const void* k_scales, const void* v_scales,
+                    const int32_t* page_table, const int32_t* seq_lens,
+                    float scale, const void* out) {
   if (!q || !k_pages || !v_pages || !page_table || !seq_lens || !out)
     return fail(SPEC_ERR_ARG, "NULL tensor pointer");
   if (!(scale > 0.f) || scale > 3.0e38f)
@@ -284,26 +257,36 @@ int spec_verify_attention(const spec_attn_desc* desc, const void* q,
     return fail(SPEC_ERR_ALIGN, "q, k_pages, v_pages and out must be 16-byte aligned");
   if (!aligned(page_table, 4) || !aligned(seq_lens, 4))
     return fail(SPEC_ERR_ALIGN, "page_table and seq_lens must be 4-byte aligned");
-  const bool fp8 = desc->kv_dtype == SPEC_KV_FP8_E4M3;
-  if (fp8) {
+  if (desc->kv_dtype == SPEC_KV_FP8_E4M3) {
     if (!k_scales || !v_scales)
       return fail(SPEC_ERR_ARG, "FP8 KV needs k_scales and v_scales");
     if (!aligned(k_scales, 16) || !aligned(v_scales, 16))
       return fail(SPEC_ERR_ALIGN, "scales must be 16-byte aligned");
   }
-  Layout L;
-  rc = layout(desc, &L);
-  if (rc) return rc;
+  return SPEC_OK;
+}
+
+int check_workspace(const void* workspace, size_t bytes, size_t need) {
   if (!workspace) return fail(SPEC_ERR_WORKSPACE, "workspace is NULL");
   if (!aligned(workspace, 256))
     return fail(SPEC_ERR_ALIGN, "workspace must be 256-byte aligned");
-  if (workspace_bytes < L.bytes)
-    return fail(SPEC_ERR_WORKSPACE, "workspace %zu bytes < %zu needed",
-                workspace_bytes, L.bytes);
+  if (bytes < need)
+    return fail(SPEC_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", bytes,
+                need);
+  return SPEC_OK;
+}
 
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
+// Launch parameters and tensor maps of the split kernels.
+int attention_params(const spec_attn_desc* desc, const Layout& L, const void* q,
+                     const void* k_pages, const void* v_pages,
+                     const void* k_scales, const void* v_scales,
+                     const int32_t* page_table, const int32_t* seq_lens,
+                     float scale, void* out, void* workspace,
+                     specv::AttnParams* pp, CUtensorMap* tm_k,
+                     CUtensorMap* tm_v) {
+  const bool fp8 = desc->kv_dtype == SPEC_KV_FP8_E4M3;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  specv::AttnParams p;
+  specv::AttnParams& p = *pp;
   std::memset(&p, 0, sizeof p);
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.k_pages = k_pages;
@@ -342,34 +325,229 @@ int spec_verify_attention(const spec_attn_desc* desc, const void* q,
   }
   const bool tc = use_tc(desc);
   const bool fp8t = use_fp8t(desc);
-  CUtensorMap tm_k, tm_v;
-  std::memset(&tm_k, 0, sizeof tm_k);  // unused by the bulk-copy FP8 kernel
-  std::memset(&tm_v, 0, sizeof tm_v);
+  std::memset(tm_k, 0, sizeof *tm_k);  // unused by the bulk-copy FP8 kernel
+  std::memset(tm_v, 0, sizeof *tm_v);
+  int rc = SPEC_OK;
   const long long pool_rows =
       (long long)desc->num_pages * desc->num_kv_heads * desc->page_size;
   if (tc && !fp8) {
-    rc = make_pool_map(&tm_k, k_pages, pool_rows, p.box_rows);
-    if (!rc) rc = make_pool_map(&tm_v, v_pages, pool_rows, p.box_rows);
-    if (rc) return rc;
+    rc = make_pool_map(tm_k, k_pages, pool_rows, p.box_rows);
+    if (!rc) rc = make_pool_map(tm_v, v_pages, pool_rows, p.box_rows);
   } else if (fp8t) {
-    rc = make_pool_map_u8(&tm_k, k_pages, pool_rows, p.box_rows);
-    if (!rc) rc = make_pool_map_u8(&tm_v, v_pages, pool_rows, p.box_rows);
-    if (rc) return rc;
+    rc = make_pool_map_u8(tm_k, k_pages, pool_rows, p.box_rows);
+    if (!rc) rc = make_pool_map_u8(tm_v, v_pages, pool_rows, p.box_rows);
   }
+  return rc;
+}
 
-  cudaError_t e;
-  if (desc->flags & SPEC_FLAG_CHECKED) {
-    p.status = reinterpret_cast<uint32_t*>(ws);
-    e = cudaMemsetAsync(ws, 0, sizeof(uint32_t), s);
-    if (e != cudaSuccess)
-      return fail(SPEC_ERR_CUDA, "status reset: %s", cudaGetErrorString(e));
-  }
-  e = fp8t ? specv::launch_verify_split_fp8t(p, tm_k, tm_v, s)
-       : tc  ? specv::launch_verify_split_tc(p, tm_k, tm_v, s)
-             : specv::launch_verify_split_bf16(p, s);
+// With SPEC_FLAG_CHECKED: zero the status word and let the kernels set it.
+int reset_status(const spec_attn_desc* desc, void* workspace,
+                 specv::AttnParams* p, cudaStream_t s) {
+  if (!(desc->flags & SPEC_FLAG_CHECKED)) return SPEC_OK;
+  p->status = static_cast<uint32_t*>(workspace);
+  cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(uint32_t), s);
+  if (e != cudaSuccess)
+    return fail(SPEC_ERR_CUDA, "status reset: %s", cudaGetErrorString(e));
+  return SPEC_OK;
+}
+
+int launch_split(const spec_attn_desc* desc, const specv::AttnParams& p,
+                 const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                 cudaStream_t s) {
+  cudaError_t e = use_fp8t(desc) ? specv::launch_verify_split_fp8t(p, tm_k, tm_v, s)
+                  : use_tc(desc) ? specv::launch_verify_split_tc(p, tm_k, tm_v, s)
+                                 : specv::launch_verify_split_bf16(p, s);
   if (e != cudaSuccess)
     return fail(SPEC_ERR_CUDA, "split kernel launch: %s", cudaGetErrorString(e));
-  e = specv::launch_verify_merge(p, s);
+  return SPEC_OK;
+}
+
+int check_shared(const spec_attn_desc* d, int32_t groups) {
+  int rc = check_desc(d);
+  if (rc) return rc;
+  if (groups < 1 || groups > specv::kMaxGroups)
+    return fail(SPEC_ERR_ARG, "groups %d outside [1, %d]", groups,
+                specv::kMaxGroups);
+  if (!use_tc(d))
+    return fail(SPEC_ERR_UNSUPPORTED, "shared prefixes need page_size >= %d",
+                specv::kTcMinPageSize);
+  return SPEC_OK;
+}
+
+// The tails' workspace, then the plan and the shared parts' partials.
+struct SharedLayout {
+  Layout tail;
+  int pairs;
+  size_t plan, kv_begin, group_of, pre_o, pre_lse, bytes;
+};
+
+int shared_layout(const spec_attn_desc* d, int32_t groups, SharedLayout* S) {
+  int rc = layout(d, &S->tail);
+  if (rc) return rc;
+  int dev;
+  rc = current_device(&dev);
+  if (rc) return rc;
+  const bool fp8 = d->kv_dtype == SPEC_KV_FP8_E4M3;
+  {
+    std::lock_guard<std::mutex> lock(g_mu);
+    if (!g_pairs[dev][fp8]) {
+      const int n = specv::prefix_attention_pairs(fp8);
+      if (n <= 0)
+        return fail(SPEC_ERR_CUDA, "prefix kernel does not fit on an SM pair");
+      g_pairs[dev][fp8] = n;
+    }
+    S->pairs = g_pairs[dev][fp8];
+  }
+  // partial slots: pair + segment.  Only groups of two or more share, and
+  // each rounds its rows up to one more tile at most.
+  const long long share = groups < d->batch / 2 ? groups : d->batch / 2;
+  const long long tiles =
+      (long long)d->batch * S->tail.rows / specv::kPrefixRows + share;
+  const size_t slots = (size_t)(S->pairs + tiles * d->num_kv_heads);
+  size_t o = S->tail.bytes;
+  auto take = [&](size_t n) {
+    const size_t at = o;
+    o += round_up(n, 256);
+    return at;
+  };
+  S->plan = take((groups + 1) * sizeof(specv::GroupPlan));
+  S->kv_begin = take((size_t)d->batch * sizeof(int32_t));
+  S->group_of = take((size_t)d->batch * sizeof(int32_t));
+  S->pre_o = take(slots * specv::kPrefixRows * specv::kHeadDim * sizeof(float));
+  S->pre_lse = take(slots * specv::kPrefixRows * sizeof(float));
+  S->bytes = o;
+  return SPEC_OK;
+}
+
+}  // namespace
+
+namespace specv {
+int set_error(int code, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_err, sizeof g_err, fmt, ap);
+  va_end(ap);
+  return code;
+}
+}  // namespace specv
+
+extern "C" {
+
+const char* spec_last_error(void) { return g_err; }
+
+const char* spec_version(void) { return "spec_verify 0.2 (sm_103a)"; }
+
+size_t spec_verify_workspace_size(const spec_attn_desc* desc) {
+  if (check_desc(desc)) return 0;
+  Layout L;
+  if (layout(desc, &L)) return 0;
+  return L.bytes;
+}
+
+int spec_verify_attention(const spec_attn_desc* desc, const void* q,
+                          const void* k_pages, const void* v_pages,
+                          const void* k_scales, const void* v_scales,
+                          const int32_t* page_table, const int32_t* seq_lens,
+                          float scale, void* out, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  g_err[0] = 0;
+  int rc = check_desc(desc);
+  if (rc) return rc;
+  if (desc->batch == 0) return SPEC_OK;
+  rc = check_attention(desc, q, k_pages, v_pages, k_scales, v_scales,
+                       page_table, seq_lens, scale, out);
+  if (rc) return rc;
+  Layout L;
+  rc = layout(desc, &L);
+  if (rc) return rc;
+  rc = check_workspace(workspace, workspace_bytes, L.bytes);
+  if (rc) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  specv::AttnParams p;
+  CUtensorMap tm_k, tm_v;
+  rc = attention_params(desc, L, q, k_pages, v_pages, k_scales, v_scales,
+                        page_table, seq_lens, scale, out, workspace, &p, &tm_k,
+                        &tm_v);
+  if (rc) return rc;
+  rc = reset_status(desc, workspace, &p, s);
+  if (rc) return rc;
+  rc = launch_split(desc, p, tm_k, tm_v, s);
+  if (rc) return rc;
+  cudaError_t e = specv::launch_verify_merge(p, s);
+  if (e != cudaSuccess)
+    return fail(SPEC_ERR_CUDA, "merge kernel launch: %s", cudaGetErrorString(e));
+  return SPEC_OK;
+}
+
+size_t spec_verify_shared_workspace_size(const spec_attn_desc* desc,
+                                         int32_t groups) {
+  SharedLayout S;
+  if (check_shared(desc, groups) || shared_layout(desc, groups, &S)) return 0;
+  return S.bytes;
+}
+
+int spec_verify_attention_shared(
+    const spec_attn_desc* desc, const void* q, const void* k_pages,
+    const void* v_pages, const void* k_scales, const void* v_scales,
+    const int32_t* page_table, const int32_t* seq_lens, int32_t groups,
+    const int32_t* group_starts, const int32_t* shared_lens, float scale,
+    void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  g_err[0] = 0;
+  int rc = check_shared(desc, groups);
+  if (rc) return rc;
+  if (desc->batch == 0) return SPEC_OK;
+  rc = check_attention(desc, q, k_pages, v_pages, k_scales, v_scales,
+                       page_table, seq_lens, scale, out);
+  if (rc) return rc;
+  if (!group_starts || !shared_lens)
+    return fail(SPEC_ERR_ARG, "NULL group_starts or shared_lens");
+  if (!aligned(group_starts, 4) || !aligned(shared_lens, 4))
+    return fail(SPEC_ERR_ALIGN,
+                "group_starts and shared_lens must be 4-byte aligned");
+  SharedLayout S;
+  rc = shared_layout(desc, groups, &S);
+  if (rc) return rc;
+  rc = check_workspace(workspace, workspace_bytes, S.bytes);
+  if (rc) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  specv::SharedParams p;
+  std::memset(&p, 0, sizeof p);
+  CUtensorMap tm_k, tm_v;
+  rc = attention_params(desc, S.tail, q, k_pages, v_pages, k_scales, v_scales,
+                        page_table, seq_lens, scale, out, workspace, &p.a,
+                        &tm_k, &tm_v);
+  if (rc) return rc;
+  p.starts = group_starts;
+  p.shared_lens = shared_lens;
+  p.groups = groups;
+  p.plan = reinterpret_cast<specv::GroupPlan*>(ws + S.plan);
+  p.kv_begin = reinterpret_cast<int32_t*>(ws + S.kv_begin);
+  p.group_of = reinterpret_cast<int32_t*>(ws + S.group_of);
+  p.pre_o = reinterpret_cast<float*>(ws + S.pre_o);
+  p.pre_lse = reinterpret_cast<float*>(ws + S.pre_lse);
+  p.pairs = S.pairs;
+  p.a.kv_begin = p.kv_begin;
+  // the FP8 kernel of large blocks copies page runs without a tensor map
+  CUtensorMap pm_k = tm_k, pm_v = tm_v;
+  const bool fp8 = desc->kv_dtype == SPEC_KV_FP8_E4M3;
+  if (fp8 && !use_fp8t(desc)) {
+    const long long rows =
+        (long long)desc->num_pages * desc->num_kv_heads * desc->page_size;
+    rc = make_pool_map_u8(&pm_k, k_pages, rows, p.a.box_rows);
+    if (!rc) rc = make_pool_map_u8(&pm_v, v_pages, rows, p.a.box_rows);
+    if (rc) return rc;
+  }
+  rc = reset_status(desc, workspace, &p.a, s);
+  if (rc) return rc;
+  cudaError_t e = specv::launch_shared_plan(p, s);
+  if (e == cudaSuccess) e = specv::launch_prefix_attention(p, pm_k, pm_v, s);
+  if (e != cudaSuccess)
+    return fail(SPEC_ERR_CUDA, "shared prefix launch: %s",
+                cudaGetErrorString(e));
+  rc = launch_split(desc, p.a, tm_k, tm_v, s);
+  if (rc) return rc;
+  e = specv::launch_shared_merge(p, s);
   if (e != cudaSuccess)
     return fail(SPEC_ERR_CUDA, "merge kernel launch: %s", cudaGetErrorString(e));
   return SPEC_OK;

@@ -977,8 +977,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     pc.nt = ntv - p.piece_cost;
     pc.s0 = vs + p.piece_cost;  // the segment's first real unit
     pc.len = clamp_len(p.seq_lens[pc.b], p.max_tokens);
-    pc.tok_begin = j0 * kUnit;
-    pc.tok_end = min(j1 * kUnit, pc.len);
+    const int first = first_token(p, pc.b);
+    pc.tok_begin = first + j0 * kUnit;
+    pc.tok_end = min(first + j1 * kUnit, pc.len);
     pc.n_tiles = (pc.tok_end - pc.tok_begin + kTile - 1) / kTile;
 
     // The producer and the dequant warps run ahead across pieces, gated by
@@ -995,7 +996,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int S = 0, slot = 0;
       if (warp < 4) {
         // where this piece's result goes
-        S = seg_splits(pl, pc.s0, pc.nt);
+        S = written_splits(p, pl, pc.s0, pc.nt);
         slot = S > 1 ? partial_slot(c, pc.b * p.hkv + pc.g) : 0;
         load_q<NR>(p, pc, smem, red, slot, S);
       }

@@ -504,7 +504,7 @@ __device__ void softmax_piece(const Ctx& cx, const Piece& pc, int gj0,
   const uint32_t lane_base = tmem + ((uint32_t)(32 * w4) << 16);
   const float sl2 = p.scale_log2;
   // where this piece's result goes
-  const int S = seg_splits(pl, pc.s0, pc.nt);
+  const int S = written_splits(p, pl, pc.s0, pc.nt);
   const int slot = S > 1 ? partial_slot(c, pc.b * p.hkv + pc.g) : 0;
 
   float m = -INFINITY, l = 0.f;
@@ -729,8 +729,9 @@ __global__ void __launch_bounds__(Cfg<kFp8>::kThreads, 1)
     pc.nt = ntv - p.piece_cost;
     pc.s0 = vs + p.piece_cost;  // the segment's first real unit
     pc.len = clamp_len(p.seq_lens[pc.b], p.max_tokens);
-    pc.tok_begin = j0 * kUnit;
-    pc.tok_end = min(j1 * kUnit, pc.len);
+    const int first = first_token(p, pc.b);
+    pc.tok_begin = first + j0 * kUnit;
+    pc.tok_end = min(first + j1 * kUnit, pc.len);
     pc.n_tiles = (pc.tok_end - pc.tok_begin + kT - 1) / kT;
 
     // The producer (warp 0) and the FP8 dequant warps run ahead across

@@ -362,6 +362,65 @@ int spec_stochastic_accept(const float* logits, const int32_t* draft_ids,
                            void* workspace, size_t workspace_bytes,
                            void* stream);
 
+/* Types of the logits of spec_sample. */
+#define SPEC_LOGITS_FP32 0
+#define SPEC_LOGITS_BF16 1
+
+/*
+ * Shape of a sampling call.
+ *   rows        0 .. 2^24 (0 is a no-op)
+ *   vocab       1 .. 524,288
+ *   dtype       SPEC_LOGITS_*
+ *   row_stride  elements from one row of logits to the next, >= vocab
+ */
+typedef struct {
+  int32_t rows, vocab, dtype;
+  int64_t row_stride;
+} spec_sample_desc;
+
+/*
+ * The next token of every row from its logits, with temperature, top-k,
+ * top-p and min-p and a given uniform, and the distribution it was drawn from
+ * ("Qwen3.8-27B-FP8" page: temperature, top-p and top-k as sampling options).
+ * Drafts drawn here come with the `draft_probs` rows of
+ * spec_stochastic_accept; target rows filtered here go to it as logits.
+ *
+ * With w(v) = exp((x_v - max x) / T) and the tokens ordered by logit, larger
+ * first, lower id first among equals, the kept tokens are
+ *   top-k  the first k;
+ *   top-p  of those, each before which less than p of their mass lies (the
+ *          first always);
+ *   min-p  of those, the ones with w >= m (the first always).
+ * The token is the smallest id whose running sum of kept weights, in id
+ * order, exceeds u times their sum; its probability is w over that sum.
+ * Weights are multiples of 2^-43 (a token below half of that has none), and
+ * their sums exact: the result does not depend on the order of arithmetic,
+ * and differs from an exact evaluation only where u, or a border of the kept
+ * set, lies within vocab 2^-44 of a token's border.
+ *
+ *   logits       [rows, vocab]; NaN counts as -inf, +inf as the largest
+ *                finite value, subnormals as zero.  -inf is never drawn.
+ *   temperature  optional fp32 [rows] (NULL: 1).  0 takes the largest logit
+ *                (lowest id); below zero or NaN marks an idle row
+ *   top_k        optional int32 [rows]; <= 0 or >= vocab: no cut
+ *   top_p        optional fp32 [rows]; >= 1 or NaN: no cut; <= 0 keeps one
+ *   min_p        optional fp32 [rows]; <= 0 or NaN: no cut; > 1 keeps one
+ *   u            fp32 [rows] in [0, 1) (clamped)
+ *   token        int32 [rows]; -1 for an idle row and one without a finite
+ *                logit
+ *   probs        optional fp32 [rows, vocab], contiguous: the distribution
+ *                (zeros outside the kept set, and for token -1)
+ *   filtered     optional fp32 [rows, vocab], contiguous: the logits of kept
+ *                tokens, -inf elsewhere
+ * probs and filtered may not overlap the logits (fp32 rows of a contiguous
+ * call may be filtered in place: filtered == logits).  4-byte aligned (bf16
+ * logits 2).  One launch, no workspace.
+ */
+int spec_sample(const spec_sample_desc* desc, const void* logits,
+                const float* temperature, const int32_t* top_k,
+                const float* top_p, const float* min_p, const float* u,
+                int32_t* token, float* probs, float* filtered, void* stream);
+
 /* Walks of the DFlash2 candidate selector (spec_select_desc.mode). */
 #define SPEC_SELECT_GREEDY 0  /* best successor of the token already chosen */
 #define SPEC_SELECT_MAP 1     /* the chain with the best total score */

@@ -9,7 +9,7 @@ from ._native import (SpecError, accept_workspace_size, alloc_workspace,
                       desc_for, dflash2_select, dflash2_select_into, greedy_accept, greedy_accept_commit,
                       greedy_accept_commit_into, greedy_accept_into,
                       kv_append, load, make_desc, prepare_next_block,
-                      prepare_next_block_into, rope_append, set_wait_limit,
+                      prepare_next_block_into, rope_append, sample, set_wait_limit,
                       shared_workspace_size,
                       stochastic_accept,
                       stochastic_accept_into, stochastic_workspace_size,
@@ -25,7 +25,7 @@ __all__ = [
     "greedy_accept", "greedy_accept_commit", "greedy_accept_commit_into",
     "greedy_accept_into", "kv_append", "load", "make_desc",
     "prepare_next_block", "prepare_next_block_into", "rope_append",
-    "rope_frequencies", "set_wait_limit", "shared_workspace_size",
+    "rope_frequencies", "sample", "set_wait_limit", "shared_workspace_size",
     "stochastic_accept",
     "stochastic_accept_into", "stochastic_workspace_size", "verify_attention",
     "verify_attention_into", "verify_attention_shared", "verify_status", "verify_workspace_size",

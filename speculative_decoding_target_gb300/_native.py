@@ -40,6 +40,7 @@ EXPORTED = (
     "spec_select_workspace_size", "spec_dflash2_select",
     "spec_verify_set_wait_limit", "spec_rope_append",
     "spec_verify_attention_shared", "spec_verify_shared_workspace_size",
+    "spec_sample",
 )
 SELECT_MODES = {"greedy": 0, "map": 1}
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
@@ -75,6 +76,11 @@ class RopeDesc(ctypes.Structure):
                 ("q_strides", ctypes.c_int64 * 2),
                 ("k_strides", ctypes.c_int64 * 2),
                 ("v_strides", ctypes.c_int64 * 2)]
+
+
+class SampleDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("vocab", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("row_stride", ctypes.c_int64)]
 
 
 class SelectDesc(ctypes.Structure):
@@ -124,6 +130,8 @@ def load(path: str = LIB_PATH):
         ctypes.POINTER(AttnDesc), P, P, P, P, P, P, P, i32, P, P,
         ctypes.c_float, P, P, sz, P]
     lib.spec_verify_attention_shared.restype = ctypes.c_int
+    lib.spec_sample.argtypes = [ctypes.POINTER(SampleDesc)] + [P] * 10
+    lib.spec_sample.restype = ctypes.c_int
     lib.spec_rope_append.argtypes = [ctypes.POINTER(RopeDesc)] + [P] * 15
     lib.spec_rope_append.restype = ctypes.c_int
     lib.spec_verify_set_wait_limit.argtypes = [ctypes.c_int64]
@@ -581,6 +589,55 @@ def stochastic_accept(logits, draft_ids, temperature, u_accept, u_sample, *,
                            temperature, u_accept, u_sample, seq_lens, new,
                            acc, nxt, toks, workspace, stream)
     return acc, nxt, toks, new
+
+
+def sample(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None,
+           probs: Optional[torch.Tensor] = None,
+           filtered: Optional[torch.Tensor] = None,
+           token: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The next token of every row of logits (fp32 or bf16 [.., vocab], rows
+    contiguous, evenly spaced) from the uniforms u (fp32 [..]), with optional
+    per-row temperature, top_p, min_p (fp32) and top_k (int32).  Fills the
+    optional probs (the distribution drawn from) and filtered (the logits,
+    -inf outside the kept set), fp32 of the logits' shape.  Returns token
+    int32 [..]."""
+    lead, vocab = logits.shape[:-1], logits.shape[-1]
+    rows = u.numel()
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise SpecError(SPEC_ERR_ARG, f"logits are {logits.dtype}")
+    if token is None:
+        token = torch.empty(lead, dtype=torch.int32, device=logits.device)
+    for t, dtype, what in ((u, torch.float32, "u"),
+                           (temperature, torch.float32, "temperature"),
+                           (top_k, torch.int32, "top_k"),
+                           (top_p, torch.float32, "top_p"),
+                           (min_p, torch.float32, "min_p"),
+                           (token, torch.int32, "token")):
+        if t is not None:
+            _expect(t, dtype, what, lead, True)
+    for t, what in ((probs, "probs"), (filtered, "filtered")):
+        if t is not None:
+            _expect(t, torch.float32, what, logits.shape, True)
+    _on_current_device(logits, u, temperature, top_k, top_p, min_p, probs,
+                       filtered, token)
+    if logits.dim() == 2 and rows > 1 and logits.stride(1) == 1:
+        stride = logits.stride(0)
+    elif logits.is_contiguous():
+        stride = vocab
+    elif rows == 1 and (vocab == 1 or logits.stride(-1) == 1):
+        stride = vocab
+    else:
+        raise SpecError(SPEC_ERR_ARG, "logits rows must be contiguous and "
+                                      "evenly spaced")
+    if rows > 1 and stride < vocab:
+        raise SpecError(SPEC_ERR_ARG, "logits rows overlap")
+    desc = SampleDesc(rows, vocab, int(logits.dtype == torch.bfloat16),
+                      stride)
+    _check(load().spec_sample(
+        ctypes.byref(desc), _ptr(logits), _ptr(temperature), _ptr(top_k),
+        _ptr(top_p), _ptr(min_p), _ptr(u), _ptr(token), _ptr(probs),
+        _ptr(filtered), _stream(stream)))
+    return token
 
 
 def select_desc(cand_logits, code_a, hidden, *, top: int = 16,

@@ -11,6 +11,7 @@
 
 #include "append.cuh"
 #include "next_block.cuh"
+#include "sample.cuh"
 #include "selector.cuh"
 #include "shared_prefix.cuh"
 #include "stochastic.cuh"
@@ -909,6 +910,59 @@ int spec_stochastic_accept(const float* logits, const int32_t* draft_ids,
   if (e != cudaSuccess)
     return fail(SPEC_ERR_CUDA, "stochastic accept launch: %s",
                 cudaGetErrorString(e));
+  return SPEC_OK;
+}
+
+int spec_sample(const spec_sample_desc* desc, const void* logits,
+                const float* temperature, const int32_t* top_k,
+                const float* top_p, const float* min_p, const float* u,
+                int32_t* token, float* probs, float* filtered, void* stream) {
+  g_err[0] = 0;
+  const spec_sample_desc* d = desc;
+  if (!d) return fail(SPEC_ERR_ARG, "desc is NULL");
+  if (d->rows < 0 || d->rows > (1 << 24))
+    return fail(SPEC_ERR_ARG, "rows %d outside [0, 2^24]", d->rows);
+  if (d->vocab < 1) return fail(SPEC_ERR_ARG, "vocab %d < 1", d->vocab);
+  if (d->vocab > specv::kSampleMaxVocab)
+    return fail(SPEC_ERR_UNSUPPORTED, "vocab %d > %d", d->vocab,
+                specv::kSampleMaxVocab);
+  if (d->dtype != SPEC_LOGITS_FP32 && d->dtype != SPEC_LOGITS_BF16)
+    return fail(SPEC_ERR_ARG, "dtype %d", d->dtype);
+  if (d->row_stride < d->vocab)
+    return fail(SPEC_ERR_ARG, "row_stride %lld < vocab",
+                (long long)d->row_stride);
+  if (d->rows == 0) return SPEC_OK;
+  if (!logits || !u || !token)
+    return fail(SPEC_ERR_ARG, "NULL tensor pointer");
+  const void* a4[] = {temperature, top_k, top_p, min_p, u, token, probs,
+                      filtered};
+  for (const void* q : a4)
+    if (q && !aligned(q, 4))
+      return fail(SPEC_ERR_ALIGN, "tensors must be 4-byte aligned");
+  const bool bf16 = d->dtype == SPEC_LOGITS_BF16;
+  if (!aligned(logits, bf16 ? 2 : 4))
+    return fail(SPEC_ERR_ALIGN, "logits are misaligned");
+  int sms;
+  int rc = sm_count(&sms);
+  if (rc) return rc;
+  specv::SampleParams p;
+  std::memset(&p, 0, sizeof p);
+  p.logits = logits;
+  p.row_stride = d->row_stride;
+  p.temperature = temperature;
+  p.top_k = top_k;
+  p.top_p = top_p;
+  p.min_p = min_p;
+  p.u = u;
+  p.token = token;
+  p.probs = probs;
+  p.filtered = filtered;
+  p.rows = d->rows;
+  p.vocab = d->vocab;
+  cudaError_t e =
+      specv::launch_sample(p, bf16, sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess)
+    return fail(SPEC_ERR_CUDA, "sample kernel launch: %s", cudaGetErrorString(e));
   return SPEC_OK;
 }
 

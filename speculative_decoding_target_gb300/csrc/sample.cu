@@ -14,17 +14,21 @@
 // and a row's total stays below 2^63.
 //
 // One cluster of CTAs holds a row in shared memory (a row is read from HBM
-// once; several clusters per GPC overlap one row's loads with another's
-// passes) and exchanges through distributed shared memory:
-//   1. load, largest and smallest logit            one exchange
-//   2. per active cut (top-k by count, then top-p by mass), rounds of a
-//      512-bin histogram over the candidates, reduced over the cluster and
-//      scanned; the bin that holds the border is the next round's range.
-//      The first round's bins divide the logits evenly, the next ones the
-//      ordered bit patterns (a border is found exactly in at most five
-//      rounds, and two or three on real rows)       two exchanges a round
-//   3. kept mass per CTA in id order, the CTA, thread and token that hold
-//      u W; kept tokens' probabilities              one exchange
+// once; clusters share the SMs, so one row's loads overlap another's passes)
+// and exchanges through distributed shared memory:
+//   1. load, largest and smallest logit                      one exchange
+//   2. a 512-bin histogram over the cluster, by count for top-k and by mass
+//      for top-p, its bins even steps of the logit: the bin with the border
+//      (two exchanges).  Then, by what lies at and above that bin:
+//      - at most kList tokens (any usual top-k, any nucleus of a sure model):
+//        the first CTA gathers and sorts them, and makes every cut and the
+//        draw alone;
+//      - more, but at most kList in the bin: it sorts those and finds the
+//        border among them, the next cut or step 3 follows;
+//      - more than that: the bin is divided by the ordered bit patterns of
+//        (logit, id), 512 parts a round, until one of the two holds.
+//   3. (wide kept sets) kept mass per CTA in id order, then the thread and
+//      the token that hold u W                               one exchange
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -39,9 +43,10 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = kThreads;       // a thread scans one bin
+constexpr int kBatch = 8;             // values of a thread in flight
 constexpr int kMaxCluster = 16;
+constexpr int kPad = kBatch * kThreads;  // a CTA's values come in whole batches
 constexpr float kMaxFinite = 3.402823466e+38f;
-constexpr uint64_t kOne = 1ull << 43;  // the largest token's weight
 
 typedef unsigned long long u64;
 
@@ -78,6 +83,10 @@ __device__ __forceinline__ float as_float(float x) { return x; }
 __device__ __forceinline__ float as_float(__nv_bfloat16 x) {
   return __bfloat162float(x);
 }
+__device__ __forceinline__ void store_float(float* p, float x) { *p = x; }
+__device__ __forceinline__ void store_float(__nv_bfloat16* p, float x) {
+  *p = __float2bfloat16_rn(x);
+}
 // NaN counts as -inf, +inf as the largest finite value, -0 as +0.
 __device__ __forceinline__ float clean(float x) {
   return x == x ? fminf(x, kMaxFinite) + 0.f : -INFINITY;
@@ -96,11 +105,52 @@ struct Table {
   u64 fix;
   float hi, lo;
 };
+__constant__ u64 kPowers[32] = {  // round(2^(50 - j/32))
+    0x4000000000000ull, 0x3ea0ecb6dc8a8ull, 0x3d495f454921bull, 0x3bf92e66f736cull,
+    0x3ab031b9f7491ull, 0x396e41b9df20dull, 0x383337bb0aa54ull, 0x36feede5f6bc9ull,
+    0x35d13f32b5a76ull, 0x34aa07647c4acull, 0x3389230547e12ull, 0x326e6f619b8bdull,
+    0x3159ca845541bull, 0x304b1332999c2ull, 0x2f4228e7d6031ull, 0x2e3eebd1d8beeull,
+    0x2d413cccfe77aull, 0x2c48fd6074ab1ull, 0x2b560fba90a85ull, 0x2a6856ad3a9f0ull,
+    0x297fb5aa6c545ull, 0x289c10c0c3126ull, 0x27bd4c9824684ull, 0x26e34e6e75539ull,
+    0x260dfc14636e3ull, 0x253d3bea3fbdcull, 0x2470f4dceac47ull, 0x23a90e62d1735ull,
+    0x22e57078faa2full, 0x222603a024b6aull, 0x216ab0d9f3122ull, 0x20b361a62b0afull,
+};
+__device__ __forceinline__ Table table_entry(int j) {
+  Table t;
+  t.fix = kPowers[j];
+  t.hi = __fmul_rn(__ull2float_rn(t.fix), 8.8817841970012523e-16f);  // 2^-50
+  t.lo = __fmul_rn(
+      __ll2float_rn((long long)t.fix -
+                    __float2ll_rn(__fmul_rn(t.hi, 1125899906842624.f))),
+      8.8817841970012523e-16f);
+  return t;
+}
 
 struct Row {
   float m;         // largest logit
   float kh, kl;    // log2(e) / T as two floats
 };
+
+// log2(e) / T: the quotient of the leading part, then what it leaves (exact
+// by fma) and the constant's own rest.  Kept finite and above zero, so that
+// 0 k = 0 and inf k = inf.
+__device__ __forceinline__ void set_scale(Row& r, float T) {
+  constexpr float kH = 1.44269502162933349609375f, kL = 1.9259629911e-08f;
+  const float q = __fdiv_rn(kH, T);
+  r.kh = fminf(fmaxf(q, 1e-37f), 1e38f);
+  r.kl = q == r.kh ? __fdiv_rn(__fadd_rn(__fmaf_rn(-q, T, kH), kL), T) : 0.f;
+}
+
+// floor(f W) and ceil(f W) (at least 1) for f in [0, 1), exactly: f is a
+// 64-bit fraction.
+__device__ __forceinline__ u64 floor_part(float f, u64 W) {
+  return __umul64hi(__float2ull_rz(__fmul_rn(f, 18446744073709551616.f)), W);
+}
+__device__ __forceinline__ u64 ceil_part(float f, u64 W) {
+  const u64 F = __float2ull_rz(__fmul_rn(f, 18446744073709551616.f));
+  const u64 c = __umul64hi(F, W) + (F * W != 0 ? 1 : 0);
+  return c ? c : 1;
+}
 
 // round(2^43 2^-y), y = (M - x) log2(e) / T, to about 2^-46 of the largest
 // weight.  The difference and the product are carried as two floats; with
@@ -109,12 +159,33 @@ struct Row {
 // term is below 2^-48), times the table's 2^-(j/32), as an integer multiple
 // of 2^-50 that is shifted by n.  Weights below 2^-28 take exp2 itself: its
 // relative error of 2^-22 is below the integers' step there.
+__device__ __forceinline__ u64 near_weight(const Row& r, float x, float dh,
+                                           float yh, const Table* tab);
+
+__device__ __forceinline__ u64 far_weight(float yh) {
+  return yh > 45.f ? 0ull : (u64)__float2uint_rn(exp2f(__fsub_rn(43.f, yh)));
+}
 __device__ __forceinline__ u64 weight_of(const Row& r, float x,
                                          const Table* tab) {
   const float dh = __fsub_rn(r.m, x);
   const float yh = __fmul_rn(dh, r.kh);
-  if (yh > 28.f)
-    return yh > 45.f ? 0ull : (u64)__float2uint_rn(exp2f(__fsub_rn(43.f, yh)));
+  return yh > 28.f ? far_weight(yh) : near_weight(r, x, dh, yh, tab);
+}
+// The same with one branch for the whole warp, which must be converged.
+__device__ __forceinline__ u64 warp_weight(const Row& r, float x,
+                                           const Table* tab) {
+  const float dh = __fsub_rn(r.m, x);
+  const float yh = __fmul_rn(dh, r.kh);
+  u64 w = far_weight(yh);
+  if (__any_sync(0xffffffffu, yh <= 28.f)) {
+    const u64 v = near_weight(r, x, dh, fminf(yh, 29.f), tab);
+    w = yh > 28.f ? w : v;
+  }
+  return w;
+}
+
+__device__ __forceinline__ u64 near_weight(const Row& r, float x, float dh,
+                                           float yh, const Table* tab) {
   const float b = __fsub_rn(dh, r.m);
   const float dl = __fsub_rn(__fsub_rn(r.m, __fsub_rn(dh, b)), __fadd_rn(x, b));
   float yl = __fmaf_rn(dh, r.kh, -yh);
@@ -157,26 +228,56 @@ __device__ __forceinline__ u64 weight_of(const Row& r, float x,
   return (u64)(e + (64ll << n)) >> (7 + n);
 }
 
-// ---- block and cluster steps ------------------------------------------------
-struct Shared {
-  Table tab[32];
-  u64 hist_m[kBins], red_m[kBins];
-  uint32_t hist_c[kBins], red_c[kBins];
-  u64 warp_m[kWarps];
-  uint32_t warp_c[kWarps];
-  u64 x_m[2];         // exchanged: this CTA's value, one buffer per use
-  uint32_t x_c[2];
-  u64 before_m;       // the border bin and what lies before it
-  uint32_t before_c, bin;
-  uint32_t lo, hi;    // its range of order distances
-  int eq_last;
-};
-
-__device__ __forceinline__ u64 shfl_up64(u64 v, int o) {
-  return __shfl_up_sync(0xffffffffu, v, o);
+// The probability's numerator, 2^-y in fp32 (relative error 2^-22 for the
+// exp2, the rounding of y made good).
+__device__ __forceinline__ float fast_weight(const Row& r, float x) {
+  const float dh = __fsub_rn(r.m, x);
+  const float yh = __fmul_rn(dh, r.kh);
+  const float b = __fsub_rn(dh, r.m);
+  const float dl = __fsub_rn(__fsub_rn(r.m, __fsub_rn(dh, b)), __fadd_rn(x, b));
+  float yl = __fmaf_rn(dh, r.kh, -yh);
+  yl = __fmaf_rn(dh, r.kl, yl);
+  yl = __fmaf_rn(dl, r.kh, yl);
+  const float e = exp2f(-yh);
+  return e > 0.f ? __fmaf_rn(e, -0.6931471806f * yl, e) : 0.f;
 }
 
-// Exclusive prefix over the block (thread order) of a mass and a count.
+// ---- block and cluster steps ------------------------------------------------
+constexpr int kList = 2048;      // candidates that one CTA sorts
+constexpr int kPerThread = kList / kThreads;
+constexpr int kIdBits = 19;      // ids of kSampleMaxVocab tokens
+
+struct Shared {
+  Table tab[32];
+  uint32_t hist_lo[kBins], hist_hi[kBins];  // a bin's mass
+  u64 red_m[kBins];
+  uint32_t hist_c[kBins], red_c[kBins];
+  u64 list[kList];    // (order distance, id) of candidates
+  u64 wts[kList];     // their weights, by rank
+  u64 warp_m[kWarps];
+  uint32_t warp_c[kWarps];
+  u64 x_m[2];         // exchanged: this CTA's value, one per use
+  uint32_t x_c;
+  uint32_t n_list;
+  u64 cut, total;     // broadcast by the first CTA
+  u64 before_m;       // the border bin and what lies before it
+  uint32_t before_c, bin, bin_c;
+  uint32_t lo, hi;    // its range of order distances
+};
+
+// A 64-bit sum by 32-bit additions: the low word returns what it held, so the
+// carry is known, and the high word is touched only by large weights and
+// carries.  Measured against 64-bit atomics on shared memory: 902 instead of
+// 986 us for 224 rows of 248,320.
+__device__ __forceinline__ void add_mass(Shared& s, uint32_t bin, u64 w) {
+  const uint32_t lo = (uint32_t)w;
+  const uint32_t old = atomicAdd(&s.hist_lo[bin], lo);
+  const uint32_t up = (uint32_t)(w >> 32) + (old + lo < old ? 1u : 0u);
+  if (up) atomicAdd(&s.hist_hi[bin], up);
+}
+
+// Exclusive prefix over the block (thread order) of a mass and a count, and
+// their totals.
 __device__ __forceinline__ void block_scan(Shared& s, u64 m, uint32_t c,
                                            u64* em, uint32_t* ec, u64* tm,
                                            uint32_t* tcnt) {
@@ -185,7 +286,7 @@ __device__ __forceinline__ void block_scan(Shared& s, u64 m, uint32_t c,
   uint32_t ic = c;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const u64 a = shfl_up64(im, o);
+    const u64 a = __shfl_up_sync(0xffffffffu, im, o);
     const uint32_t b = __shfl_up_sync(0xffffffffu, ic, o);
     if (lane >= o) {
       im += a;
@@ -220,26 +321,119 @@ __device__ __forceinline__ void block_scan(Shared& s, u64 m, uint32_t c,
 // The cluster's histogram from the CTAs' own, in every CTA: thread (bin,
 // source) of the CTA's slice of bins reads one value, the sources of a bin are
 // summed by shuffles, and each of those lanes stores the sum to one CTA.
-__device__ __forceinline__ void reduce_bins(Shared& s, uint32_t rank, int csize) {
+__device__ __forceinline__ void reduce_bins(Shared& s, uint32_t rank, int csize,
+                                            bool mass) {
   __syncthreads();
   tc::cluster_sync();
   const int tid = threadIdx.x;
   const int bin = (int)rank * (kBins / csize) + tid / csize, src = tid % csize;
-  u64 m = peer_load64(&s.hist_m[bin], src);
+  u64 m = 0;
+  if (mass)
+    m = (u64)peer_load32(&s.hist_hi[bin], src) << 32 |
+        peer_load32(&s.hist_lo[bin], src);
   uint32_t c = peer_load32(&s.hist_c[bin], src);
   for (int o = 1; o < csize; o <<= 1) {
-    m += __shfl_xor_sync(0xffffffffu, m, o);
+    if (mass) m += __shfl_xor_sync(0xffffffffu, m, o);
     c += __shfl_xor_sync(0xffffffffu, c, o);
   }
-  peer_store64(&s.red_m[bin], src, m);
+  if (mass) peer_store64(&s.red_m[bin], src, m);
   peer_store32(&s.red_c[bin], src, c);
   tc::cluster_sync();
 }
 
-struct Cut {
-  uint32_t dk;     // order distance of the border value
-  uint32_t count;  // how many tokens of that value are kept, lowest ids first
-};
+// Bitonic sort of list[0, n), n <= kE * kThreads, ascending; the rest is
+// filled up.  Thread t holds entries t + kThreads e: pairs less than a warp
+// apart are exchanged by shuffles, pairs kThreads and more apart lie in one
+// thread, the others go through shared memory.
+template <int kE>
+__device__ __forceinline__ void sort_entries(u64* list, int n) {
+  const int tid = threadIdx.x;
+  u64 v[kE];
+#pragma unroll
+  for (int e = 0; e < kE; ++e) {
+    const int i = tid + kThreads * e;
+    v[e] = i < n ? list[i] : ~0ull;
+  }
+  int size = 32;
+  while (size < n) size <<= 1;
+  for (int k = 2; k <= size; k <<= 1) {
+#pragma unroll
+    for (int j = kE / 2; j >= 1; j >>= 1) {  // pairs kThreads j apart
+      if (kThreads * j < k) {
+#pragma unroll
+        for (int e = 0; e < kE; ++e) {
+          if (!(e & j)) {
+            const bool up = ((tid + kThreads * e) & k) == 0;
+            const u64 x = v[e], y = v[e | j];
+            if ((x > y) == up) {
+              v[e] = y;
+              v[e | j] = x;
+            }
+          }
+        }
+      }
+    }
+    for (int j = min(k >> 1, kThreads / 2); j >= 32; j >>= 1) {
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < kE; ++e) list[tid + kThreads * e] = v[e];
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < kE; ++e) {
+        const int i = tid + kThreads * e;
+        const u64 y = list[i ^ j];
+        const bool low_half = !(tid & j), up = (i & k) == 0;
+        v[e] = (low_half == up) == (y < v[e]) ? y : v[e];
+      }
+    }
+#pragma unroll
+    for (int j = 16; j > 0; j >>= 1) {
+      if (j < k) {
+#pragma unroll
+        for (int e = 0; e < kE; ++e) {
+          const u64 y = __shfl_xor_sync(0xffffffffu, v[e], j);
+          const bool low_half = !(tid & j),
+                     up = ((tid + kThreads * e) & k) == 0;
+          v[e] = (low_half == up) == (y < v[e]) ? y : v[e];
+        }
+      }
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < kE; ++e) list[tid + kThreads * e] = v[e];
+  __syncthreads();
+}
+__device__ __forceinline__ void sort_list(u64* list, int n) {
+  if (n <= kThreads)
+    sort_entries<1>(list, n);
+  else
+    sort_entries<kPerThread>(list, n);
+}
+
+// The first CTA appends the other CTAs' lists to its own (warp j reads CTA
+// j's); returns their total.  Called between two cluster barriers.
+__device__ __forceinline__ int gather_lists(Shared& s, int csize) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t at = 0, total = 0, mine = 0;
+  for (int j = 0; j < csize; ++j) {
+    const uint32_t c = j ? peer_load32(&s.n_list, j) : s.n_list;
+    if (j < warp) at += c;
+    if (j == warp) mine = c;
+    total += c;
+  }
+  if (warp > 0 && warp < csize)
+    for (uint32_t i = lane; i < mine; i += 32)
+      s.list[at + i] = peer_load64(&s.list[i], warp);
+  __syncthreads();
+  return (int)total;
+}
+
+// The draw's target among W: floor(u W), below W.
+__device__ __forceinline__ u64 target_of(float u, u64 W) {
+  const u64 t = u >= 1.f ? W : (u > 0.f ? floor_part(u, W) : 0);
+  return t < W ? t : W - 1;
+}
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -272,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int tail = head + nv * kE + tid;
     if (tail < n) xs[tail] = src[tail];
   }
-  float T0 = p.temperature ? p.temperature[row] : 1.f;
+  const float T0 = p.temperature ? p.temperature[row] : 1.f;
   const float u = p.u[row];
   int k = p.top_k ? p.top_k[row] : 0;
   const float tp = p.top_p ? p.top_p[row] : 1.f;
@@ -281,29 +475,31 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (k <= 0 || k >= p.vocab) k = 0;
   // cuts that leave the first token alone
   const bool one = T0 == 0.f || k == 1 || tp <= 0.f || mp > 1.f;
-  if (tid < 32) {
-    const double e = exp2(-tid / 32.0);
-    Table t;
-    t.fix = (u64)__double2ll_rn(e * 1125899906842624.0);
-    t.hi = (float)e;
-    t.lo = (float)(e - t.hi);
-    s.tab[tid] = t;
-  }
-  s.hist_m[tid] = 0;
+  if (tid < 32) s.tab[tid] = table_entry(tid);
+  for (int i = n + tid; i < p.padded; i += kThreads)
+    store_float(xs + i, -INFINITY);
+  s.hist_lo[tid] = s.hist_hi[tid] = 0;
   s.hist_c[tid] = 0;
-  if (tid == 0) s.eq_last = -1;
+  if (tid == 0) s.n_list = 0;
   asm volatile("cp.async.commit_group;\ncp.async.wait_group 0;" ::: "memory");
   __syncthreads();
 
   // the largest logit with its lowest id, and the smallest finite one
   u64 best = 0;
   uint32_t low = 0xffffffffu;
-  for (int i = tid; i < n; i += kThreads) {
-    const float x = clean(as_float(xs[i]));
-    const uint32_t key = key_of(x);
-    const u64 v = (u64)key << 32 | (uint32_t)~(uint32_t)(base + i);
-    best = v > best ? v : best;
-    if (x > -INFINITY) low = min(low, key);
+  for (int i0 = tid; i0 < p.padded; i0 += kBatch * kThreads) {
+    float x[kBatch];
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) x[e] = clean(as_float(xs[i0 + e * kThreads]));
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      const int i = i0 + e * kThreads;
+      store_float(xs + i, x[e]);  // later passes read clean values
+      const uint32_t key = key_of(x[e]);
+      const u64 v = (u64)key << 32 | (uint32_t)~(uint32_t)(base + i);
+      best = v > best ? v : best;
+      low = x[e] > -INFINITY ? min(low, key) : low;
+    }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -316,22 +512,29 @@ __global__ void __launch_bounds__(kThreads, 2)
     s.warp_c[warp] = low;
   }
   __syncthreads();
-  if (tid == 0) {
-    for (int w = 1; w < kWarps; ++w) {
-      best = s.warp_m[w] > best ? s.warp_m[w] : best;
-      low = min(low, s.warp_c[w]);
+  if (warp == 0) {
+    best = lane < kWarps ? s.warp_m[lane] : 0;
+    low = lane < kWarps ? s.warp_c[lane] : 0xffffffffu;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
+      const u64 v = __shfl_xor_sync(0xffffffffu, best, o);
+      best = v > best ? v : best;
     }
-    s.x_m[0] = best;
-    s.x_c[0] = low;
+    low = __reduce_min_sync(0xffffffffu, low);
+    if (lane == 0) {
+      s.x_m[0] = best;
+      s.x_c = low;
+    }
   }
   __syncthreads();
   tc::cluster_sync();
-  best = 0;
-  low = 0xffffffffu;
-  for (int j = 0; j < csize; ++j) {
-    const u64 v = peer_load64(&s.x_m[0], j);
+  // one lane per CTA of the cluster, then the same on every lane
+  best = peer_load64(&s.x_m[0], lane % csize);
+  low = __reduce_min_sync(0xffffffffu, peer_load32(&s.x_c, lane % csize));
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
+    const u64 v = __shfl_xor_sync(0xffffffffu, best, o);
     best = v > best ? v : best;
-    low = min(low, peer_load32(&s.x_c[0], j));
   }
   const uint32_t mkey = (uint32_t)(best >> 32);
   const int arg = (int)~(uint32_t)best;
@@ -339,94 +542,251 @@ __global__ void __launch_bounds__(kThreads, 2)
   r.m = value_of(mkey);
   const bool none = idle || !(r.m > -INFINITY);
 
-  Cut cut{0xffffffffu, 0u};  // everything
-  u64 total = 0;
-  int eq_last = -1;          // last kept id (in the chunk) of the border value
+  u64 cut = ~0ull;     // (order distance, id) of the last kept token
+  u64 total = 0;       // kept mass
   u64 minw = 0;
-  if (!none && !one) {
-    // log2(e) / T, kept finite and above zero so that 0 k = 0, inf k = inf
-    double kd = 1.4426950408889634074 / (double)T0;
-    kd = kd > 1e38 ? 1e38 : (kd < 1e-37 ? 1e-37 : kd);
-    r.kh = (float)kd;
-    r.kl = (float)(kd - r.kh);
-    if (mp > 0.f) minw = (u64)ceil((double)mp * (double)kOne);
+  bool done = none || one;
+  if (done) {
+    if (rank == 0 && tid == 0) p.token[row] = none ? -1 : arg;
+  } else {
+    set_scale(r, T0);
+    if (mp > 0.f) minw = __float2ull_ru(__fmul_rn(mp, 8796093022208.f));
+    auto place = [&](float x, int i) {  // a token's place in the order
+      return (u64)(mkey - key_of(x)) << kIdBits | (uint32_t)(base + i);
+    };
+    auto weight_at = [&](u64 c) {
+      return weight_of(r, value_of(mkey - (uint32_t)(c >> kIdBits)), s.tab);
+    };
 
-    // 2. the cuts
-    const bool by_p = tp < 1.f;
-    // the first round's bins: even steps of the logit over what has weight
+    // 2. the cuts.  The first round's bins: even steps of the logit over
+    // what has weight
     const float span = fminf(__fsub_rn(r.m, value_of(low)), 45.f / r.kh);
     const float step = span > 0.f ? fminf((kBins - 1) / span, kMaxFinite) : 0.f;
     auto bin_of = [&](float x) {
       const float f = __fmul_rn(__fsub_rn(r.m, x), step);
       return f < kBins - 1 ? (uint32_t)f : kBins - 1u;  // NaN: the last
     };
-    for (int which = 0; which < 2; ++which) {  // top-k, then top-p
-      if (which == 0 ? k == 0 : !by_p) continue;
+    for (int which = 0; which < 2 && !done; ++which) {  // top-k, then top-p
+      if (which == 0 ? k == 0 : !(tp < 1.f)) continue;
       const bool mass = which == 1;
-      const Cut old = cut;
+      const u64 old = cut;
       u64 want = mass ? 0 : (u64)k;  // the border is where the sum reaches it
-      u64 above = 0;
-      uint32_t lo = 0, hi = 0xffffffffu;
+      u64 above_m = 0, all_m = 0;
+      uint32_t above_c = 0;
+      u64 lo = 0, hi = ~0ull >> 1;
       for (int round = 0;; ++round) {
-        const int shift = max(0, 32 - __clz((int)(hi - lo)) - 9);
-        auto digit = [&](uint32_t dk, float x) {
-          return round == 0 ? bin_of(x) : (dk - lo) >> shift;
-        };
-        for (int i = tid; i < n; i += kThreads) {
-          const float x = clean(as_float(xs[i]));
-          const uint32_t dk = mkey - key_of(x);
-          if (dk < lo || dk > hi || dk >= old.dk) continue;
-          const uint32_t d = digit(dk, x);
-          if (mass) {
-            const u64 w = weight_of(r, x, s.tab);
-            if (w) atomicAdd(&s.hist_m[d], w);
-          } else {
+        const int shift =
+            round ? max(0, 64 - __clzll((long long)(hi - lo)) - 9) : 0;
+        if (round == 0 && !mass) {
+          // every finite value, no order beside its bin
+          for (int i0 = tid; i0 < p.padded; i0 += kBatch * kThreads) {
+            float x[kBatch];
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e)
+              x[e] = as_float(xs[i0 + e * kThreads]);
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e)
+              if (x[e] > -INFINITY) atomicAdd(&s.hist_c[bin_of(x[e])], 1u);
+          }
+        } else if (round == 0) {
+          constexpr int kB = kBatch / 2;
+          for (int i0 = tid; i0 < p.padded; i0 += kB * kThreads) {
+            float x[kB];
+            u64 w[kB];
+#pragma unroll
+            for (int e = 0; e < kB; ++e) x[e] = as_float(xs[i0 + e * kThreads]);
+#pragma unroll
+            for (int e = 0; e < kB; ++e) w[e] = warp_weight(r, x[e], s.tab);
+#pragma unroll
+            for (int e = 0; e < kB; ++e) {
+              if (!(x[e] > -INFINITY) ||
+                  (old != ~0ull && place(x[e], i0 + e * kThreads) > old))
+                continue;
+              const uint32_t d = bin_of(x[e]);
+              atomicAdd(&s.hist_c[d], 1u);
+              if (w[e]) add_mass(s, d, w[e]);
+            }
+          }
+        } else {
+          for (int i = tid; i < n; i += kThreads) {
+            const float x = as_float(xs[i]);
+            const u64 c = place(x, i);
+            if (x == -INFINITY || c > old || c < lo || c > hi) continue;
+            const uint32_t d = (uint32_t)((c - lo) >> shift);
             atomicAdd(&s.hist_c[d], 1u);
+            if (mass) {
+              const u64 w = weight_of(r, x, s.tab);
+              if (w) add_mass(s, d, w);
+            }
           }
         }
-        if (mass && rank == 0 && tid == 0 && old.count && old.dk >= lo &&
-            old.dk <= hi) {
-          // the kept part of the top-k border, as one lump
-          const float x = value_of(mkey - old.dk);
-          atomicAdd(&s.hist_m[digit(old.dk, x)],
-                    old.count * weight_of(r, x, s.tab));
-        }
-        reduce_bins(s, rank, csize);
-        s.hist_m[tid] = 0;
+        reduce_bins(s, rank, csize, mass);
+        s.hist_lo[tid] = s.hist_hi[tid] = 0;
         s.hist_c[tid] = 0;
-        const u64 v = mass ? s.red_m[tid] : (u64)s.red_c[tid];
-        u64 ex, all;
+        if (tid == 0) s.bin = kBins;
+        const uint32_t vc = s.red_c[tid];
+        const u64 vm = mass ? s.red_m[tid] : 0;
+        u64 em, am;
         uint32_t ec, ac;
-        block_scan(s, v, 0u, &ex, &ec, &all, &ac);
+        block_scan(s, vm, vc, &em, &ec, &am, &ac);
         if (round == 0) {
-          if (mass) {  // sums before a kept token are below p W
-            const double t = ceil((double)tp * (double)all);
-            want = t < 1.0 ? 1ull : (u64)t;
-            want = want > all ? all : want;
-          } else if (want > all) {
-            break;  // fewer tokens than k: uniform, every thread has all
+          all_m = am;
+          if (mass) {  // the mass before a kept token is below p W
+            want = ceil_part(tp, am);
+          } else if (want > ac) {
+            break;  // fewer finite logits than k
           }
         }
-        if (tid == 0) s.bin = kBins;
-        __syncthreads();
-        if (above + ex < want && want <= above + ex + v) {
+        const u64 ex = mass ? above_m + em : (u64)above_c + ec;
+        if (ex < want && want <= ex + (mass ? vm : (u64)vc)) {
           s.bin = tid;
-          s.before_m = above + ex;
+          s.bin_c = vc;
+          s.before_m = above_m + em;
+          s.before_c = above_c + ec;
         }
         __syncthreads();
         const uint32_t b = s.bin;
-        if (b == kBins) break;  // no mass left: cannot be reached
-        above = s.before_m;
+        if (b == kBins) break;  // cannot be: the sums reach want
+        above_m = s.before_m;
+        above_c = s.before_c;
+        const uint32_t in_bin = s.bin_c;
+        const bool finish = above_c + in_bin <= kList;
+        if (finish || in_bin <= kList) {
+          // gather: all up to the bin's end, or the bin
+          if (round == 0) {
+            // what lies up to the bin's upper edge is looked at more closely
+            const float edge = b < kBins - 1 ? (float)(b + 1) : INFINITY;
+            for (int i0 = tid; i0 < p.padded; i0 += kBatch * kThreads) {
+              float x[kBatch];
+              bool any = false;
+#pragma unroll
+              for (int e = 0; e < kBatch; ++e) {
+                x[e] = as_float(xs[i0 + e * kThreads]);
+                any |= x[e] > -INFINITY &&
+                       !(__fmul_rn(__fsub_rn(r.m, x[e]), step) >= edge);
+              }
+              if (!any) continue;
+#pragma unroll
+              for (int e = 0; e < kBatch; ++e) {
+                const uint32_t d = bin_of(x[e]);
+                if (!(x[e] > -INFINITY) || !(d == b || (finish && d < b)))
+                  continue;
+                const u64 c = place(x[e], i0 + e * kThreads);
+                if (c <= old) s.list[atomicAdd(&s.n_list, 1u)] = c;
+              }
+            }
+          } else {
+            for (int i = tid; i < n; i += kThreads) {
+              const float x = as_float(xs[i]);
+              const u64 c = place(x, i);
+              if (x == -INFINITY || c > old || c > hi) continue;
+              const bool take = c < lo ? finish
+                                       : (finish ? (c - lo) >> shift <= b
+                                                 : (c - lo) >> shift == b);
+              if (take) s.list[atomicAdd(&s.n_list, 1u)] = c;
+            }
+          }
+          __syncthreads();
+          tc::cluster_sync();
+          if (rank == 0) {
+            const int m = gather_lists(s, csize);
+            sort_list(s.list, m);
+            // ranks kPerThread tid ..: weights and their sums in rank order
+            const int r0 = tid * kPerThread;
+            u64 w[kPerThread], sum = 0;
+#pragma unroll
+            for (int e = 0; e < kPerThread; ++e) {
+              const int q = r0 + e;
+              const bool in = q < m && (!finish || mass || q < k);
+              w[e] = in && (mass || finish) ? weight_at(s.list[q]) : 0;
+              sum += w[e];
+            }
+            u64 before, all;
+            uint32_t x0, x1;
+            block_scan(s, sum, 0u, &before, &x0, &all, &x1);
+            if (!finish) {
+              // the border among the bin's tokens
+              u64 run = above_m + before;
+#pragma unroll
+              for (int e = 0; e < kPerThread; ++e) {
+                const int q = r0 + e;
+                if (mass ? (run < want && want <= run + w[e])
+                         : (u64)above_c + q + 1 == want)
+                  s.cut = s.list[q];
+                run += w[e];
+              }
+              __syncthreads();
+              if (tid < csize) peer_store64(&s.cut, tid, s.cut);
+            } else {
+              // every remaining cut: a prefix of the ranks
+              const int mk = k && !mass ? min(m, k) : m;
+              u64 limit = mass ? want : ~0ull;
+              if (!mass && tp < 1.f) limit = ceil_part(tp, all);
+              uint32_t kept = 0;
+              u64 run = before, kept_m = 0;
+#pragma unroll
+              for (int e = 0; e < kPerThread; ++e) {
+                const int q = r0 + e;
+                const bool keep = q < mk && run < limit && w[e] >= minw;
+                run += w[e];
+                w[e] = keep ? w[e] : 0;
+                kept += keep;
+                kept_m += w[e];
+                if (q < kList) s.wts[q] = w[e];
+              }
+              u64 y0;
+              uint32_t nk;
+              block_scan(s, kept_m, kept, &y0, &x0, &all, &nk);
+              if (tid == 0) {
+                s.cut = s.list[nk - 1];
+                s.total = all;
+              }
+              __syncthreads();
+              if (tid < csize) {
+                peer_store64(&s.cut, tid, s.cut);
+                peer_store64(&s.total, tid, s.total);
+              }
+              __syncthreads();
+              // the draw, in id order
+              for (int q = tid; q < (int)nk; q += kThreads)
+                s.list[q] = (s.list[q] & ((1ull << kIdBits) - 1)) << 32 |
+                            (uint32_t)q;
+              __syncthreads();
+              sort_list(s.list, (int)nk);
+              const u64 t = target_of(u, all);
+              sum = 0;
+#pragma unroll
+              for (int e = 0; e < kPerThread; ++e) {
+                const int q = r0 + e;
+                w[e] = q < (int)nk ? s.wts[(uint32_t)s.list[q]] : 0;
+                sum += w[e];
+              }
+              block_scan(s, sum, 0u, &before, &x0, &all, &x1);
+#pragma unroll
+              for (int e = 0; e < kPerThread; ++e) {
+                if (before <= t && t < before + w[e])
+                  p.token[row] = (int32_t)(s.list[r0 + e] >> 32);
+                before += w[e];
+              }
+            }
+          }
+          done = finish;
+          __syncthreads();
+          tc::cluster_sync();
+          cut = s.cut;
+          if (finish) total = s.total;
+          if (tid == 0) s.n_list = 0;
+          break;
+        }
+        // too many in one bin: its range of places is the next round's
         if (round == 0) {
-          // the range of order distances that falls into bin b: the digit
-          // does not decrease with the distance
+          // order distances in bin b: the digit does not decrease with them
           if (tid < 2) {
             uint32_t a = 0, z = 0xffffffffu;  // first distance with digit >= g
             const uint32_t g = b + tid;
             if (g < kBins) {
               while (a < z) {
                 const uint32_t mid = a + ((z - a) >> 1);
-                // below the smallest value every pattern belongs to the last
                 const bool in = mid <= mkey - low &&
                                 bin_of(value_of(mkey - mid)) < g;
                 if (in) a = mid + 1; else z = mid;
@@ -437,146 +797,93 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
           }
           __syncthreads();
-          lo = s.lo;
-          hi = s.hi;
+          lo = (u64)s.lo << kIdBits;
+          hi = ((u64)s.hi + 1 << kIdBits) - 1;
         } else {
           const u64 end = lo + ((u64)(b + 1) << shift) - 1;
-          hi = end < hi ? (uint32_t)end : hi;
-          lo += b << shift;
-        }
-        if (lo >= hi) {
-          cut.dk = lo;
-          if (mass) {
-            const u64 w = weight_of(r, value_of(mkey - lo), s.tab);
-            cut.count = (uint32_t)((want - above + w - 1) / w);
-          } else {
-            cut.count = (uint32_t)(want - above);
-          }
-          break;
+          hi = end < hi ? end : hi;
+          lo += (u64)b << shift;
         }
         __syncthreads();
       }
       __syncthreads();
     }
 
-    // 3. kept mass, each thread its segment of ids
-    const u64 weq =
-        cut.count ? weight_of(r, value_of(mkey - cut.dk), s.tab) : 0;
-    const uint32_t keep_eq = weq >= minw ? cut.count : 0;
-    u64 m = 0;
-    uint32_t eq = 0;
-    const int i0 = tid * p.seg, i1 = min(n, i0 + p.seg);
-    for (int i = i0; i < i1; ++i) {
-      const float x = clean(as_float(xs[i]));
-      const uint32_t dk = mkey - key_of(x);
-      if (dk < cut.dk) {
-        const u64 w = weight_of(r, x, s.tab);
-        m += w >= minw ? w : 0;
-      } else if (dk == cut.dk) {
-        ++eq;
-      }
-    }
-    u64 em, am;
-    uint32_t ec, ac;
-    block_scan(s, m, eq, &em, &ec, &am, &ac);
-    if (tid == 0) {
-      s.x_m[1] = am;
-      s.x_c[1] = ac;
-    }
-    __syncthreads();
-    tc::cluster_sync();
-    u64 mine = 0, at = 0;     // kept mass before this CTA and in it
-    uint32_t eq_at = 0, eq_before = 0;
-    for (int j = 0; j < csize; ++j) {
-      const u64 cm = peer_load64(&s.x_m[1], j);
-      const uint32_t cc = peer_load32(&s.x_c[1], j);
-      const uint32_t kept = min(cc, keep_eq - min(keep_eq, eq_at));
-      const u64 w = cm + kept * weq;
-      if (j < (int)rank) {
-        at += w;
-        eq_before += cc;
-      }
-      if (j == (int)rank) mine = w;
-      total += w;
-      eq_at += cc;
-    }
-    u64 t = 0;
-    if (u > 0.f) {
-      t = (u64)fmin(floor((double)u * (double)total), 9.2e18);
-      t = t >= total ? total - 1 : t;
-    }
-    // kept tokens of the border value before this thread, and its share
-    const uint32_t eb = eq_before + ec;
-    const uint32_t room = keep_eq - min(keep_eq, eb);
-    const uint32_t kept = min(eq, room);
-    const uint32_t kept_before =
-        min(keep_eq, eb) - min(keep_eq, eq_before);
-    const u64 start = at + em + kept_before * weq;
-    const bool here = start <= t && t < start + m + kept * weq;
-    // every lane of the warp that holds the draw takes a token of that
-    // thread's segment
-    const unsigned who = __ballot_sync(0xffffffffu, here);
-    if (who) {
-      const int l = __ffs(who) - 1;
-      const int b0 = __shfl_sync(0xffffffffu, i0, l);
-      const int b1 = __shfl_sync(0xffffffffu, i1, l);
-      u64 run = __shfl_sync(0xffffffffu, start, l);
-      uint32_t rm = __shfl_sync(0xffffffffu, room, l);
-      for (int e = b0; e < b1; e += 32) {
-        const int i = e + lane;
-        u64 w = 0;
-        bool is_eq = false;
-        if (i < b1) {
-          const float x = clean(as_float(xs[i]));
-          const uint32_t dk = mkey - key_of(x);
-          is_eq = dk == cut.dk;
-          if (dk < cut.dk) {
-            w = weight_of(r, x, s.tab);
-            if (w < minw) w = 0;
-          }
-        }
-        const unsigned eqs = __ballot_sync(0xffffffffu, is_eq);
-        if (is_eq && __popc(eqs & ((1u << lane) - 1)) < (int)rm) w = weq;
-        rm -= min(rm, (uint32_t)__popc(eqs));
-        u64 inc = w;
+    if (!done) {
+      // 3. kept mass, each warp a run of ids
+      const int run_len = p.padded / kWarps;
+      u64 m = 0;
+      for (int i0 = warp * run_len + lane; i0 < (warp + 1) * run_len;
+           i0 += 4 * 32) {
+        float x[4];
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const u64 a = shfl_up64(inc, o);
-          if (lane >= o) inc += a;
+        for (int e = 0; e < 4; ++e) x[e] = as_float(xs[i0 + 32 * e]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bool in = place(x[e], i0 + 32 * e) <= cut;
+          if (!__any_sync(0xffffffffu, in)) continue;
+          const u64 w = warp_weight(r, x[e], s.tab);
+          m += in && w >= minw ? w : 0;
         }
-        const unsigned hit =
-            __ballot_sync(0xffffffffu, w > 0 && run + inc > t);
-        if (hit) {
-          if (lane == 0) p.token[row] = base + e + __ffs(hit) - 1;
-          break;
-        }
-        run += __shfl_sync(0xffffffffu, inc, 31);
       }
-    }
-    // the last kept id of the border value, for the distribution
-    if (p.probs || p.filtered) {
-      if (kept > 0 && (kept < eq || eb + eq >= keep_eq)) {
-        // this thread holds the border itself
-        uint32_t left = kept;
-        for (int i = i0; i < i1 && left; ++i)
-          if (mkey - key_of(clean(as_float(xs[i]))) == cut.dk && --left == 0)
-            s.eq_last = i;
-      } else if (tid == kThreads - 1 && eq_before + ac < keep_eq) {
-        s.eq_last = n;  // every one in this chunk is kept
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+      if (lane == 0) s.warp_m[warp] = m;
+      __syncthreads();
+      if (tid == 0) {
+        u64 all = 0;
+        for (int w = 0; w < kWarps; ++w) all += s.warp_m[w];
+        s.x_m[1] = all;
       }
       __syncthreads();
-      eq_last = s.eq_last;
+      tc::cluster_sync();
+      u64 at = 0, mine = 0;  // kept mass before this CTA and in it
+      for (int j = 0; j < csize; ++j) {
+        const u64 w = peer_load64(&s.x_m[1], j);
+        at += j < (int)rank ? w : 0;
+        mine = j == (int)rank ? w : mine;
+        total += w;
+      }
+      const u64 t = target_of(u, total);
+      if (at <= t && t < at + mine) {  // the same for the whole CTA
+        int w0 = 0;
+        while (at + s.warp_m[w0] <= t) at += s.warp_m[w0++];
+        // the run's tokens again, consecutive ones to a thread
+        const int per = (run_len + kThreads - 1) / kThreads;  // at most 4
+        const int i0 = w0 * run_len + tid * per;
+        const int i1 = (w0 + 1) * run_len;
+        u64 w[4], sum = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          w[e] = 0;
+          if (e < per && i0 + e < i1) {
+            const float x = as_float(xs[i0 + e]);
+            if (place(x, i0 + e) <= cut) w[e] = weight_of(r, x, s.tab);
+            if (w[e] < minw) w[e] = 0;
+          }
+          sum += w[e];
+        }
+        u64 em, am;
+        uint32_t ec, ac;
+        block_scan(s, sum, 0u, &em, &ec, &am, &ac);
+        at += em;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (at <= t && t < at + w[e]) p.token[row] = base + i0 + e;
+          at += w[e];
+        }
+      }
     }
-  } else if (rank == 0 && tid == 0) {
-    p.token[row] = none ? -1 : arg;
   }
 
   // the distribution
   if (p.probs || p.filtered) {
-    const float inv = total ? (float)(8796093022208.0 / (double)total) : 0.f;
+    const float inv =
+        total ? __fdiv_rn(8796093022208.f, __ull2float_rn(total)) : 0.f;
     const long long out = (long long)row * p.vocab + base;
+#pragma unroll 2
     for (int i = tid; i < n; i += kThreads) {
-      const float x = clean(as_float(xs[i]));
+      const float x = as_float(xs[i]);
       bool keep = false;
       float pr = 0.f;
       if (none) {
@@ -584,19 +891,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         keep = base + i == arg;
         pr = keep ? 1.f : 0.f;
       } else {
-        const uint32_t dk = mkey - key_of(x);
-        keep = x > -INFINITY &&
-               (dk < cut.dk || (dk == cut.dk && i <= eq_last));
-        if (keep) {
-          const u64 w = weight_of(r, x, s.tab);
-          keep = w >= minw;
-          if (keep) {
-            // below 2^-19 the integer has too few digits left for fp32
-            pr = (w >> 24) ? __ull2float_rn(w) * 1.13686837721616030e-13f
-                           : exp2f(-__fmul_rn(__fsub_rn(r.m, x), r.kh));
-            pr *= inv;
-          }
-        }
+        const u64 c = (u64)(mkey - key_of(x)) << kIdBits | (uint32_t)(base + i);
+        keep = x > -INFINITY && c <= cut;
+        // beside a cut that already holds it, min-p decides only here
+        if (keep && minw) keep = weight_of(r, x, s.tab) >= minw;
+        if (keep) pr = fast_weight(r, x) * inv;
       }
       if (p.probs) p.probs[out + i] = pr;
       if (p.filtered) p.filtered[out + i] = keep ? x : -INFINITY;
@@ -607,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 template <typename T>
 cudaError_t launch(const SampleParams& p, int csize, cudaStream_t s) {
-  const size_t smem = (size_t)p.chunk * sizeof(T) + 32;
+  const size_t smem = (size_t)p.padded * sizeof(T) + 32;
   // once per device (an attribute call per launch costs microseconds)
   static std::atomic<uint64_t> ready{0};
   int dev;
@@ -653,7 +952,7 @@ cudaError_t launch_sample(SampleParams p, bool bf16, int sms, cudaStream_t s) {
          p.vocab > csize * 4096)
     csize *= 2;
   p.chunk = ((p.vocab + csize - 1) / csize + 7) / 8 * 8;
-  p.seg = ((p.chunk + kThreads - 1) / kThreads) | 1;
+  p.padded = (p.chunk + kPad - 1) / kPad * kPad;
   return bf16 ? launch<__nv_bfloat16>(p, csize, s) : launch<float>(p, csize, s);
 }
 

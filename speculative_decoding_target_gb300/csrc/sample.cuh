@@ -19,7 +19,7 @@ struct SampleParams {
   float* filtered;            // optional [rows, vocab]
   int rows, vocab;
   int chunk;                  // tokens per CTA of a row's cluster
-  int seg;                    // tokens per thread, odd
+  int padded;                 // the same, rounded up
 };
 
 constexpr int kSampleMaxVocab = 524288;

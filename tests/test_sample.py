@@ -5,7 +5,7 @@ Tokens and kept sets have to be equal.  The kernel's weights are multiples of
 2^-43 of the largest, each within 2^-43 of the exact one, so a sum of n weights
 is within n 2^-43; a draw, or a border of the kept set, that lies closer than
 that to another outcome is left out (with n = 250,000 a few draws in 100,000).
-A probability is off by the roundings of its weight and of the sum to fp32 and
+A probability is off by exp2 (2^-22) and the roundings of the sum to fp32 and
 their product, below 2^-21 of its value; a weight 2^-y below 2^-19 of the
 largest is exp2 of an fp32 argument made in three roundings, which adds
 3 y 2^-24 ln 2."""
@@ -194,6 +194,32 @@ def test_ties():
                  uniforms(12, 4)) <= 1
     assert check(xb, None, None, np.linspace(0.05, 0.95, 12), None,
                  uniforms(12, 5)) <= 1
+
+
+@gpu
+def test_one_value_and_wide_borders():
+    # more equal logits at the border than one CTA sorts: the lowest ids
+    V = 200000
+    x = np.zeros((5, V), np.float32)
+    x[1, 5000:5100] = 0.5
+    x[2] = (np.arange(V) % 3).astype(np.float32)
+    x[3] = -np.inf
+    x[3, ::2] = 1.25
+    x[4] = np.where(np.arange(V) < 100000, 2.0, 1.0)
+    u = np.array([0.5, 0.999, 0.25, 0.75, 0.3], np.float32)
+    tok, probs, _ = run(x, None, [70001, 3000, 66700, 50000, 150000], None,
+                        None, u)
+    zero = np.flatnonzero(x[1] == 0)[:2900]
+    want = [np.arange(70001), np.sort(np.r_[np.arange(5000, 5100), zero]),
+            np.sort(np.r_[np.flatnonzero(x[2] == 2),
+                          np.flatnonzero(x[2] == 1)[:66700 - 66666]]),
+            np.arange(0, 100000, 2), np.arange(150000)]
+    for r in range(5):
+        assert np.array_equal(np.flatnonzero(probs[r]), want[r]), r
+    assert tok[0] == 35000 and tok[3] == 75000
+    tok, probs, _ = run(x[:1], None, None, [0.5], None, u[:1])
+    assert np.array_equal(np.flatnonzero(probs[0]), np.arange(V // 2))
+    assert tok[0] == V // 4
 
 
 @gpu

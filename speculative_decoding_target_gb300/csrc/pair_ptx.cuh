@@ -33,6 +33,14 @@ __device__ __forceinline__ void arrive_cluster(uint32_t cluster_bar) {
                    "r"(cluster_bar)
                : "memory");
 }
+// The same without ordering this thread's memory accesses, for what tensor
+// memory holds (tcgen05 fences order that).  The release form waits for every
+// access of the thread at cluster scope, hundreds of cycles.
+__device__ __forceinline__ void arrive_cluster_relaxed(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::
+                   "r"(cluster_bar)
+               : "memory");
+}
 __device__ __forceinline__ void store_cluster(uint32_t cluster_addr,
                                               uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v)

@@ -7,8 +7,8 @@
 // work is bound by the tensor cores (4 D flop per row and token against 4 D
 // bytes per token), unlike the verify block's 48 rows, which HBM bounds.
 //
-// One CTA pair takes a contiguous share of the plan's units (shared_prefix.cuh)
-// and holds kPrefixRows = 256 rows, 128 per CTA.  Tensor memory, 512 columns
+// A piece of the plan (shared_prefix.cuh) is kPrefixRows = 256 rows, 128 per CTA
+// of a pair, over a run of the shared tokens.  Tensor memory, 512 columns
 // in each CTA: O [0, 256), two S buffers of 128 columns (one tile of 128
 // tokens each) [256, 512); P (16-bit) overwrites its S.  Q lies in shared
 // memory.  A measured stream of MMAs takes N / 2 cycles from N = 128 on,
@@ -100,13 +100,19 @@ __device__ __forceinline__ void give_up(const Ctx& cx) {
   if (cx.p->a.status) atomicOr(cx.p->a.status, SPEC_STATUS_TIMEOUT);
 }
 
+// Barriers that carry generic writes of the other CTA (Q, dequantised tiles)
+// are waited for at cluster scope; the others carry tensor-memory or TMA
+// completions.
+template <bool kCluster>
 __device__ __noinline__ bool wait_slow(const Ctx& cx, uint32_t a,
                                        uint32_t parity, bool drain) {
   if (!drain && *cx.abort) return false;
   const long long bound = drain ? kDrainWaitCycles : cx.p->a.wait_cycles;
   const long long t0 = clock64();
   while (true) {
-    if (tc::bar_try_wait_cluster(a, parity)) return true;
+    if (kCluster ? tc::bar_try_wait_cluster(a, parity)
+                 : tc::bar_try_wait(a, parity))
+      return true;
     if (!drain && *cx.abort) return false;
     if (clock64() - t0 > bound) {
       give_up(cx);
@@ -114,11 +120,14 @@ __device__ __noinline__ bool wait_slow(const Ctx& cx, uint32_t a,
     }
   }
 }
+template <bool kCluster = false>
 __device__ __forceinline__ bool wait_bar(const Ctx& cx, uint64_t* bar,
                                          uint32_t parity, bool drain = false) {
   const uint32_t a = tc::smem_u32(bar);
-  if (tc::bar_try_wait_cluster(a, parity)) return true;
-  return wait_slow(cx, a, parity, drain);
+  if (kCluster ? tc::bar_try_wait_cluster(a, parity)
+               : tc::bar_try_wait(a, parity))
+    return true;
+  return wait_slow<kCluster>(cx, a, parity, drain);
 }
 
 // A CTA pair's share of one segment.
@@ -359,7 +368,8 @@ __device__ __forceinline__ bool issue_qk(const Ctx& cx, long long& seq, int gj,
 #pragma unroll
   for (int h = 0; h < 2; ++h, ++seq) {
     const int s = (int)(seq % C::kSlots);
-    if (!wait_bar(cx, &cx.bars->full[s], (uint32_t)(seq / C::kSlots) & 1))
+    if (!wait_bar<kFp8>(cx, &cx.bars->full[s],
+                        (uint32_t)(seq / C::kSlots) & 1))
       return false;
     tc::fence_after();
     const uint32_t kb = tc::smem_u32(smem + C::kOffRing + s * kSlotBytes);
@@ -388,7 +398,8 @@ __device__ __forceinline__ bool issue_pv(const Ctx& cx, long long& seq, int gj,
 #pragma unroll
   for (int h = 0; h < 2; ++h, ++seq) {
     const int s = (int)(seq % C::kSlots);
-    if (!wait_bar(cx, &cx.bars->full[s], (uint32_t)(seq / C::kSlots) & 1))
+    if (!wait_bar<kFp8>(cx, &cx.bars->full[s],
+                        (uint32_t)(seq / C::kSlots) & 1))
       return false;
     tc::fence_after();
     const uint32_t vb = tc::smem_u32(smem + C::kOffRing + s * kSlotBytes);
@@ -407,7 +418,7 @@ __device__ __forceinline__ bool issue_pv(const Ctx& cx, long long& seq, int gj,
 template <bool kFp8>
 __device__ void mma_piece(const Ctx& cx, const Piece& pc, int gj0, int n_piece,
                           long long& seq, uint32_t tmem, uint8_t* smem) {
-  if (!wait_bar(cx, &cx.bars->q_full, (uint32_t)n_piece & 1)) return;
+  if (!wait_bar<true>(cx, &cx.bars->q_full, (uint32_t)n_piece & 1)) return;
   tc::fence_after();
   if (!issue_qk<kFp8>(cx, seq, gj0, tmem, smem)) return;
   for (int j = 0; j < pc.n_tiles; ++j) {
@@ -542,7 +553,8 @@ __device__ void softmax_tiles(const Ctx& cx, const Piece& pc, int gj0,
     tc::fence_before();
     __syncwarp();
     if (lane == 0)
-      tc::arrive_cluster(tc::map_to(tc::smem_u32(&cx.bars->p_full[gj & 1]), 0));
+      tc::arrive_cluster_relaxed(
+          tc::map_to(tc::smem_u32(&cx.bars->p_full[gj & 1]), 0));
   }
 }
 
@@ -573,35 +585,27 @@ __device__ void epilogue(const Ctx& cx, const Piece& pc, int gl, uint32_t tmem,
   tc::fence_before();  // the reads precede this warp's next P
 }
 
-// Decode the pair's next piece from unit u on; false where the range holds
-// only phantom units.  Advances u.
-__device__ __forceinline__ bool next_piece(const SharedParams& p, const Plan& pl,
-                                           int c, uint32_t rank, long long& u,
-                                           long long u_end, Piece* pc) {
-  int lo = 0, hi = p.groups - 1;  // the last group with unit0 <= u and tiles
+__device__ __forceinline__ Piece decode_piece(const SharedParams& p, int i,
+                                              uint32_t rank) {
+  int lo = 0, hi = p.groups - 1;  // the last group that starts at or before i
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (p.plan[mid].unit0 <= u) lo = mid; else hi = mid - 1;
+    if (p.plan[mid].piece0 <= i) lo = mid; else hi = mid - 1;
   }
   const GroupPlan gp = p.plan[lo];
-  const int nu = prefix_units(gp);
-  const long long in = u - gp.unit0;
-  const int seg = (int)(in / nu);
-  const long long s0 = gp.unit0 + (long long)seg * nu;
-  const int j0v = (int)(u - s0);
-  const int j1v = (int)(u_end - s0 < nu ? u_end - s0 : nu);
-  u = s0 + j1v;
-  const int j0 = max(j0v - kPrefixCost, 0), j1 = max(j1v - kPrefixCost, 0);
-  if (j1 <= j0) return false;
-  pc->lead = gp.lead;
-  pc->start = gp.start;
-  pc->rows_total = gp.count * p.a.rows;
-  pc->g = seg / gp.tiles;
-  pc->row0 = (seg - pc->g * gp.tiles) * kPrefixRows + (int)rank * 128;
-  pc->tok = j0 * kT;
-  pc->n_tiles = j1 - j0;
-  pc->slot = c + gp.seg0 + seg;
-  return true;
+  const int in = i - gp.piece0, run = in / gp.tiles;
+  const int c = run % gp.splits;
+  const int j0 = run_start(gp, c), j1 = run_start(gp, c + 1);
+  Piece pc;
+  pc.lead = gp.lead;
+  pc.start = gp.start;
+  pc.rows_total = gp.count * p.a.rows;
+  pc.g = run / gp.splits;
+  pc.row0 = (in - run * gp.tiles) * kPrefixRows + (int)rank * 128;
+  pc.tok = j0 * kT;
+  pc.n_tiles = j1 - j0;
+  pc.slot = i;
+  return pc;
 }
 
 template <bool kFp8>
@@ -622,9 +626,8 @@ __global__ void __cluster_dims__(2, 1, 1)
   // the tails' kernel may be scheduled now; it waits for this grid
   tc_grid_launch_dependents();
   tc_grid_dependency_wait();  // the plan is written by the kernel before
-  const Plan pl = prefix_plan(p);
-  const int c = blockIdx.x >> 1;
-  if (c >= pl.P) return;  // both CTAs of the pair
+  const int pieces = p.plan[p.groups].piece0;
+  if ((int)(blockIdx.x >> 1) >= pieces) return;  // both CTAs of the pair
   const uint32_t rank = tc::cluster_rank();
 
   if (tid == 0) {
@@ -657,16 +660,13 @@ __global__ void __cluster_dims__(2, 1, 1)
   const Ctx cx{&bars, &s_abort,
                tc::map_to(tc::smem_u32(&s_abort), rank ^ 1u), rank, &p};
 
-  long long u = chunk_start(pl, c);
-  const long long u_end = chunk_start(pl, c + 1);
   int gj0 = 0, n_piece = 0;
   Producer pr;
   long long mseq = 0, rseq = 0, sseq = 0;
   float m = 0.f, l = 0.f;
   Piece prev{};
-  while (u < u_end) {
-    Piece pc;
-    if (!next_piece(p, pl, c, rank, u, u_end, &pc)) continue;
+  for (int i = blockIdx.x >> 1; i < pieces; i += gridDim.x >> 1) {
+    const Piece pc = decode_piece(p, i, rank);
     if (warp == 0) {
       if (pr.live) produce<kFp8>(cx, pc, pr, smem, &tm_k, &tm_v);
       __syncwarp();

@@ -23,12 +23,19 @@ __global__ void __launch_bounds__(kPlanThreads)
   __shared__ int s_seen[kMaxGroups];   // tokens that every live row sees
   __shared__ int s_lead[kMaxGroups];
   __shared__ int s_live[kMaxGroups];
-  __shared__ long long s_units[2][kMaxGroups];
-  __shared__ int s_segs[2][kMaxGroups];
+  __shared__ int s_rows[kMaxGroups];   // row tiles over all KV heads
+  __shared__ int s_kv[kMaxGroups];     // 128-token tiles
+  __shared__ int s_pieces[2][kMaxGroups];
+  __shared__ long long s_plan[kPlans]; // (time, pieces) of a candidate
+  __shared__ int s_run[kPlans];
+  __shared__ unsigned long long s_work;
   __shared__ int s_bad;
   const int tid = threadIdx.x, G = p.groups;
   const AttnParams& a = p.a;
-  if (tid == 0) s_bad = 0;
+  if (tid == 0) {
+    s_bad = 0;
+    s_work = 0;
+  }
   for (int n = tid; n <= G; n += kPlanThreads) s_start[n] = p.starts[n];
   if (tid < G) {
     s_seen[tid] = INT_MAX;
@@ -64,49 +71,74 @@ __global__ void __launch_bounds__(kPlanThreads)
   }
   __syncthreads();
   GroupPlan gp{};
-  long long units = 0;
-  int segs = 0;
-  if (tid < G && !bad) {
-    gp.start = s_start[tid];
-    gp.count = s_start[tid + 1] - gp.start;
-    if (s_live[tid] >= 2) {
-      const int eff = min(p.shared_lens[tid], s_seen[tid]);
-      if (eff >= kPrefixTile) {
-        gp.eff = eff / kPrefixTile * kPrefixTile;
-        gp.lead = s_lead[tid];
-        gp.tiles = (gp.count * a.rows + kPrefixRows - 1) / kPrefixRows;
-        segs = a.hkv * gp.tiles;
-        units = (long long)segs * prefix_units(gp);
+  if (tid < G) {
+    if (!bad) {
+      gp.start = s_start[tid];
+      gp.count = s_start[tid + 1] - gp.start;
+      if (s_live[tid] >= 2) {
+        const int eff = min(p.shared_lens[tid], s_seen[tid]);
+        if (eff >= kPrefixTile) {
+          gp.eff = eff / kPrefixTile * kPrefixTile;
+          gp.lead = s_lead[tid];
+          gp.tiles = (gp.count * a.rows + kPrefixRows - 1) / kPrefixRows;
+        }
       }
     }
     s_seen[tid] = gp.eff;  // each thread reads and writes its own entry
+    s_rows[tid] = a.hkv * gp.tiles;
+    s_kv[tid] = gp.eff / kPrefixTile;
+    if (gp.eff)
+      atomicAdd(&s_work, (unsigned long long)s_rows[tid] * s_kv[tid]);
   }
-  // inclusive prefix sums over the groups
-  if (tid < kMaxGroups) {
-    s_units[0][tid] = units;
-    s_segs[0][tid] = segs;
+  __syncthreads();
+  // candidate run lengths, 1.6 down to 0.53 of the even share, one a warp
+  const int warp = tid >> 5, lane = tid & 31;
+  {
+    const float share = (float)s_work / (float)p.pairs;
+    const int run = max(1, (int)ceilf(1.6f * share * __powf(0.965f, warp)));
+    int pieces = 0, longest = 0;
+    for (int n = lane; n < G; n += 32) {
+      if (!s_kv[n]) continue;
+      const int splits = (s_kv[n] + run - 1) / run;
+      pieces += s_rows[n] * splits;
+      longest = max(longest, (s_kv[n] + splits - 1) / splits);
+    }
+    pieces = __reduce_add_sync(0xffffffffu, pieces);
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 0) {
+      const long long waves = (pieces + p.pairs - 1) / p.pairs;
+      s_plan[warp] = waves * (longest + kPrefixCost) << 24 |
+                     min(pieces, (1 << 24) - 1);
+      s_run[warp] = run;
+    }
   }
+  __syncthreads();
+  int pick = 0;
+  for (int j = 1; j < kPlans; ++j)
+    if (s_plan[j] < s_plan[pick]) pick = j;
+  const int run = s_run[pick];
+  // pieces per group, and their prefix sums
+  int mine_pieces = 0;
+  if (tid < G && gp.eff) {
+    gp.splits = (s_kv[tid] + run - 1) / run;
+    mine_pieces = s_rows[tid] * gp.splits;
+  }
+  if (tid < kMaxGroups) s_pieces[0][tid] = mine_pieces;
   __syncthreads();
   int from = 0;
   for (int o = 1; o < G; o <<= 1, from ^= 1) {
-    if (tid < G) {
-      const bool add = tid >= o;
-      s_units[from ^ 1][tid] =
-          s_units[from][tid] + (add ? s_units[from][tid - o] : 0);
-      s_segs[from ^ 1][tid] =
-          s_segs[from][tid] + (add ? s_segs[from][tid - o] : 0);
-    }
+    if (tid < G)
+      s_pieces[from ^ 1][tid] =
+          s_pieces[from][tid] + (tid >= o ? s_pieces[from][tid - o] : 0);
     __syncthreads();
   }
   if (tid < G) {
-    gp.unit0 = s_units[from][tid] - units;
-    gp.seg0 = s_segs[from][tid] - segs;
+    gp.piece0 = s_pieces[from][tid] - mine_pieces;
     p.plan[tid] = gp;
   }
   if (tid == 0) {
     GroupPlan end{};
-    end.unit0 = s_units[from][G - 1];
-    end.seg0 = s_segs[from][G - 1];
+    end.piece0 = s_pieces[from][G - 1];
     p.plan[G] = end;
   }
   if (tid < a.batch) {
@@ -153,7 +185,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   const long long s0 =
       (long long)a.hkv * s_pre[b] + (long long)g * ntv + a.piece_cost;
   const int n_tail = live && nt > 0 ? seg_splits(pl, s0, nt) : 0;
-  long long tail_row = 0, pre_row = 0;
+  long long tail_row = 0, pre_row = 0, pre_step = 0;
   if (n_tail)
     tail_row = (long long)partial_slot(chunk_of(pl, s0), b * a.hkv + g) *
                    a.rows + r;
@@ -163,13 +195,10 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   if (n >= 0) {
     const GroupPlan gp = p.plan[n];
     const int R = (b - gp.start) * a.rows + r;
-    const int seg = g * gp.tiles + R / kPrefixRows;
-    const int nu = prefix_units(gp);
-    const Plan pp = prefix_plan(p);
-    const long long u0 = gp.unit0 + (long long)seg * nu + kPrefixCost;
-    n_pre = seg_splits(pp, u0, nu - kPrefixCost);
-    pre_row = (long long)(chunk_of(pp, u0) + gp.seg0 + seg) * kPrefixRows +
-              R % kPrefixRows;
+    n_pre = gp.splits;
+    pre_step = (long long)gp.tiles * kPrefixRows;
+    pre_row = ((long long)gp.piece0 + (long long)g * gp.splits * gp.tiles +
+               R / kPrefixRows) * kPrefixRows + R % kPrefixRows;
   }
   // the partials are read only once the kernels before are done
   tc_grid_dependency_wait();
@@ -188,7 +217,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
         const bool tail = s < n_tail;
         const long long row =
             tail ? tail_row + (long long)s * a.rows
-                 : pre_row + (long long)(s - n_tail) * kPrefixRows;
+                 : pre_row + (s - n_tail) * pre_step;
         const float* o =
             (tail ? a.part_o : p.pre_o) + row * kHeadDim + lane * 8;
         lv[j] = (tail ? a.part_lse : p.pre_lse)[row];

@@ -9,11 +9,14 @@
 // (normalised rows and base-2 log-sum-exps), which one kernel merges.
 //
 // Plan of the shared part.  The rows of (group n, KV head g), all requests'
-// block rows that read head g, are cut into tiles of kPrefixRows; a
-// (n, g, tile) is a segment of eff / kPrefixTile units, charged kPrefixCost
-// units in front as in common.cuh.  Segments lie end to end, CTA pair c takes
-// the c-th even share of the line, and the partial of segment k from pair c
-// goes to slot c + k.
+// block rows that read head g, are cut into tiles of kPrefixRows, and the
+// group's shared tokens into `splits` even runs of 128-token tiles.  A piece is
+// one row tile over one run; pieces are numbered by (group, head, run, row
+// tile), pair c of P takes pieces c, c + P, ..., and piece i writes its partial
+// to slot i.  Pieces that read the same tokens are neighbours, so they run at
+// the same time and share their tiles in L2.  The run length is the one of
+// kPlans candidates around the even share that ends first, counting each
+// piece's fixed cost as kPrefixCost tiles.
 #pragma once
 
 #include "common.cuh"
@@ -22,19 +25,20 @@ namespace specv {
 
 constexpr int kPrefixTile = 128;   // tokens per tile
 constexpr int kPrefixRows = 256;   // rows per CTA pair
-constexpr int kPrefixCost = 4;     // plan units a segment's start costs
-constexpr int kPrefixMinUnits = 2; // least share of a CTA pair
+constexpr int kPrefixCost = 4;     // tiles' time that a piece's start and end cost
+constexpr int kPlans = 32;         // run lengths tried, a warp each
 constexpr int kMaxGroups = kMaxBatch;
 
-// One entry per group, plus the totals at [groups].
+// One entry per group; [groups].piece0 is the number of pieces.
 struct GroupPlan {
-  long long unit0;   // virtual units before this group
-  int seg0;          // segments before this group
-  int tiles;         // row tiles per KV head (0: nothing is shared)
-  int eff;           // shared tokens attended once
-  int start;         // first request
-  int count;         // requests
-  int lead;          // the live request whose page table is read
+  int piece0;   // first piece
+  int tiles;    // row tiles per KV head (0: nothing is shared)
+  int splits;   // runs of tokens
+  int eff;      // shared tokens attended once
+  int start;    // first request
+  int count;    // requests
+  int lead;     // the live request whose page table is read
+  int pad;
 };
 
 struct SharedParams {
@@ -45,22 +49,20 @@ struct SharedParams {
   GroupPlan* plan;            // [groups + 1]
   int32_t* kv_begin;          // [B]
   int32_t* group_of;          // [B]: group with a shared part, or -1
-  float* pre_o;               // [slots, kPrefixRows, 256]
-  float* pre_lse;             // [slots, kPrefixRows]
+  float* pre_o;               // [pieces, kPrefixRows, 256]
+  float* pre_lse;             // [pieces, kPrefixRows]
   int pairs;                  // CTA pairs of the prefix kernel
 };
 
-__device__ __forceinline__ int prefix_units(const GroupPlan& g) {
-  return g.eff / kPrefixTile + kPrefixCost;
+// First 128-token tile of run c of a group's shared part (c <= splits).
+__device__ __forceinline__ int run_start(const GroupPlan& g, int c) {
+  return (int)((long long)c * (g.eff / kPrefixTile) / g.splits);
 }
 
-// The totals as a plan over the pairs.
-__device__ __forceinline__ Plan prefix_plan(const SharedParams& p) {
-  Plan pl;
-  pl.U = p.plan[p.groups].unit0;
-  const long long want = (pl.U + kPrefixMinUnits - 1) / kPrefixMinUnits;
-  pl.P = want < p.pairs ? (int)want : p.pairs;
-  return pl;
+// Most pieces a plan makes, for `tiles` row tiles in all: the shortest run
+// tried is above half the even share, and each segment rounds up by one.
+inline long long max_pieces(int pairs, long long segments) {
+  return 2LL * pairs + segments;
 }
 
 cudaError_t launch_shared_plan(const SharedParams& p, cudaStream_t s);

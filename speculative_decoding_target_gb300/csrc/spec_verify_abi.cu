@@ -399,12 +399,13 @@ int shared_layout(const spec_attn_desc* d, int32_t groups, SharedLayout* S) {
     }
     S->pairs = g_pairs[dev][fp8];
   }
-  // partial slots: pair + segment.  Only groups of two or more share, and
-  // each rounds its rows up to one more tile at most.
+  // one partial per piece.  Only groups of two or more share, and each rounds
+  // its rows up to one more tile at most.
   const long long share = groups < d->batch / 2 ? groups : d->batch / 2;
   const long long tiles =
       (long long)d->batch * S->tail.rows / specv::kPrefixRows + share;
-  const size_t slots = (size_t)(S->pairs + tiles * d->num_kv_heads);
+  const size_t slots =
+      (size_t)specv::max_pieces(S->pairs, tiles * d->num_kv_heads);
   size_t o = S->tail.bytes;
   auto take = [&](size_t n) {
     const size_t at = o;

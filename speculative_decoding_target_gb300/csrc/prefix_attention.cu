@@ -20,15 +20,17 @@
 // the channels of V.
 //
 // Warp roles (both CTAs, the issuer in the leader only):
-//   warp 0      producer: TMA boxes of the CTA's halves into a ring of 16 KB
-//               slots [64 tokens x 128 channels], 128-byte swizzle, in the
-//               order in which the issuer consumes them: K0 K1 V0 K2 V1 ...
+//   warp 0      producer: TMA boxes of the CTA's halves, [64 tokens x 128
+//               channels] twice a tile for each of K and V, 128-byte swizzle,
+//               into a ring in the order in which the issuer consumes them:
+//               K0 K1 V0 K2 V1 ...
 //   warp 1      issuer: QK_0, then per tile QK_{j+1}, PV_j, so that the
 //               softmax of tile j has a QK and a PV's time to run in
 //   warps 2..5  softmax: one thread per row; running maximum and sum in base
 //               2 and fp32; O is rescaled only when the maximum grows by 2^8;
 //               epilogue (normalised fp32 partial, log-sum-exp)
-//   warps 6..9  FP8 only: E4M3 bytes times scale to fp16 slots
+//   warps 6..13 FP8 only: E4M3 bytes times scale to fp16 slots, two sets of
+//               four warps on alternate staging buffers
 //
 // P is rounded once to the type of V (bf16; fp16 for FP8 KV): the relative
 // error of a weight, at most 2^-8, is independent from token to token and no larger
@@ -48,20 +50,24 @@ namespace specv {
 namespace {
 
 constexpr int kT = kPrefixTile;
-constexpr int kSlotBytes = 64 * 128 * 2;      // 64 tokens x 128 channels
+constexpr int kHalfBytes = 64 * 128 * 2;      // 64 tokens x 128 channels
 constexpr int kBlockBytes = 64 * 128;         // its column block of 64
 constexpr int kQBytes = 128 * kHeadDim * 2;   // 4 column blocks of 128 rows
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 256;
 constexpr float kRescaleLog2 = 8.0f;
-constexpr int kMaxSlots = 9;
+constexpr int kMaxSlots = 6;
 constexpr int kRaw = 3;                       // FP8 staging buffers
 constexpr int kRawBytes = 16384 + 1024;       // bytes and scales
 
 template <bool kFp8>
 struct Cfg {
-  static constexpr int kSlots = kFp8 ? 6 : kMaxSlots;
-  static constexpr int kThreads = kFp8 ? 320 : 192;
+  // a slot holds a CTA's share of K or V of one tile, or for FP8, where
+  // staging takes room and the dequantisation is the pace, half of it
+  static constexpr int kParts = kFp8 ? 2 : 1;
+  static constexpr int kSlots = kFp8 ? 6 : 5;
+  static constexpr int kSlotBytes = 2 * kHalfBytes / kParts;
+  static constexpr int kThreads = kFp8 ? 448 : 192;
   static constexpr int kOffRing = kQBytes;
   static constexpr int kOffRaw = kOffRing + kSlots * kSlotBytes;
   static constexpr int kSmem = kOffRaw + (kFp8 ? kRaw * kRawBytes : 0) + 1024;
@@ -75,7 +81,9 @@ struct Cfg {
 };
 
 struct Bars {
-  uint64_t full[kMaxSlots];    // leader: the slot holds both CTAs' halves
+  // bf16, leader: the slot holds both CTAs' halves (TMA); FP8, both: this
+  // CTA's half is dequantised, and in the leader the other CTA's too
+  uint64_t full[kMaxSlots], peer_full[kMaxSlots];
   uint64_t empty[kMaxSlots];   // both: the slot's MMAs are done
   uint64_t s_full[2];          // both: S_j complete
   uint64_t p_full[2];          // leader: P_j written by both CTAs
@@ -130,7 +138,23 @@ __device__ __forceinline__ bool wait_bar(const Ctx& cx, uint64_t* bar,
   return wait_slow<kCluster>(cx, a, parity, drain);
 }
 
-// A CTA pair's share of one segment.
+// A place in a ring of N buffers and the parity of the wait for its current
+// use (a consumer's; a producer waits for the use before, of the other one).
+template <int N>
+struct Ring {
+  int at = 0;
+  uint32_t parity = 0;
+  bool wrapped = false;
+  __device__ __forceinline__ void next() {
+    if (++at == N) {
+      at = 0;
+      parity ^= 1;
+      wrapped = true;
+    }
+  }
+};
+
+// A piece of the plan as one CTA sees it.
 struct Piece {
   int lead, start, rows_total;  // page-table row, first request, group rows
   int g, row0;                  // KV head, first row of this CTA's 128
@@ -138,10 +162,11 @@ struct Piece {
   int slot;                     // partial slot
 };
 
-__device__ __forceinline__ int checked_page(const AttnParams& p, int lead,
-                                            int t) {
-  int page = __ldg(p.page_table + (long long)lead * p.max_pages +
-                   (t >> p.log2_ps));
+__device__ __forceinline__ int page_id(const AttnParams& p, int lead, int t) {
+  return __ldg(p.page_table + (long long)lead * p.max_pages + (t >> p.log2_ps));
+}
+// Looked at only when the page is used, so that the load of the id runs ahead.
+__device__ __forceinline__ int checked_page(const AttnParams& p, int page) {
   if (page < 0 || page >= p.num_pages) {
     if (p.status) atomicOr(p.status, SPEC_STATUS_BAD_PAGE);
     page = 0;  // in bounds; the affected rows are unspecified
@@ -155,129 +180,169 @@ __device__ __forceinline__ long long pool_row(const AttnParams& p, int page,
 }
 
 // ---- warp 0: loads ----------------------------------------------------------
-// Box b of a 64-token half: tokens b * box_rows ..; a lane owns one box of a
-// column block in each 64 tokens that its CTA loads per tile.
+// A half of 64 tokens is 64 / box_rows boxes of each column block.  With whole
+// boxes (pages of 64 tokens and more, kOne) lane 0 works alone; otherwise lane
+// b looks up the pages of box b, and lane 0 issues the copies, so that a copy's
+// operands are uniform.  (Two lanes issuing a box each, with 64-bit ring
+// arithmetic, took 900 cycles a slot and set the pace of the kernel.)
+template <bool kFp8>
 struct Producer {
-  long long seq = 0;     // slots (bf16) or staging buffers (FP8) used so far
+  Ring<kFp8 ? kRaw : Cfg<kFp8>::kSlots> ring;
   bool live = true;
 };
 
-// bf16: one slot, two column blocks of 64 channels x 64 tokens
-__device__ __forceinline__ bool load_slot(const Ctx& cx, Producer& pr,
-                                          uint8_t* smem, const CUtensorMap* map,
-                                          int x0, long long row, int lane,
-                                          int nb, int box_rows) {
-  using C = Cfg<false>;
-  const int s = (int)(pr.seq % C::kSlots);
-  const long long use = pr.seq / C::kSlots;
-  const bool ok = use == 0 ||
-                  wait_bar(cx, &cx.bars->empty[s], (uint32_t)(use - 1) & 1);
-  if (!__all_sync(0xffffffffu, ok && !*cx.abort)) return false;
-  const uint32_t full = tc::smem_u32(&cx.bars->full[s]);
-  if (cx.rank == 0 && lane == 0)
-    tc::bar_arrive_expect_tx(full, 2 * kSlotBytes);
-  __syncwarp();
-  if (lane < 2 * nb) {
-    const int blk = lane / nb, bi = lane - blk * nb;
-    tc::tma_load_2d_pair(
-        tc::smem_u32(smem + C::kOffRing + s * kSlotBytes + blk * kBlockBytes +
-                     bi * box_rows * 128),
-        map, tc::map_to(full, 0), x0 + blk * 64, (int)row);
-  }
-  ++pr.seq;
-  return true;
+template <bool kOne>
+__device__ __forceinline__ long long box_row(long long row, int b) {
+  return kOne ? row : __shfl_sync(0xffffffffu, row, b);
+}
+template <bool kOne>
+__device__ __forceinline__ bool all_lanes(bool ok) {
+  return kOne ? ok : __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
 }
 
-// FP8: one staging buffer of 16 KB and its scales
-__device__ __forceinline__ bool load_raw(const Ctx& cx, Producer& pr,
-                                         uint8_t* smem, const CUtensorMap* map,
-                                         const __half* scales, bool is_v,
-                                         long long row, int lane, int nb,
-                                         int box_rows) {
-  using C = Cfg<true>;
-  const int s = (int)(pr.seq % kRaw);
-  const long long use = pr.seq / kRaw;
-  const bool ok = use == 0 ||
-                  wait_bar(cx, &cx.bars->raw_empty[s], (uint32_t)(use - 1) & 1);
-  if (!__all_sync(0xffffffffu, ok && !*cx.abort)) return false;
-  const uint32_t full = tc::smem_u32(&cx.bars->raw_full[s]);
-  if (lane == 0)
-    tc::bar_arrive_expect_tx(full, 16384 + (is_v ? 1024 : 512));
-  __syncwarp();
-  const uint32_t base = tc::smem_u32(smem + C::kOffRaw + s * kRawBytes);
-  if (lane < 2 * nb) {
-    // K: two blocks of 128 bytes x 64 tokens; V: the CTA's 128 bytes of 128
-    // tokens, the second 64 in the second block
-    const int blk = lane / nb, bi = lane - blk * nb;
-    tc::tma_load_2d(base + blk * kBlockBytes + bi * box_rows * 128, map, full,
-                    is_v ? (int)cx.rank * 128 : blk * 128, (int)row);
-    if (is_v || blk == 0) {
-      const uint32_t dst = base + 16384 + (blk * 64 + bi * box_rows) * 8;
-      asm volatile(
-          "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes "
-          "[%0], [%1], %2, [%3];" ::"r"(dst),
-          "l"(reinterpret_cast<const uint8_t*>(scales) + row * 8),
-          "r"(box_rows * 8), "r"(full)
-          : "memory");
+// bf16: one slot, two halves of two column blocks of 64 channels x 64 tokens:
+// K, the CTA's 64 tokens of all channels (row1 = row0); V, its 128 channels of
+// all tokens.
+template <bool kOne>
+__device__ __forceinline__ void load_slot(const Ctx& cx, Producer<false>& pr,
+                                          uint32_t smem, uint32_t full0,
+                                          const CUtensorMap* map, bool is_v,
+                                          long long row0, long long row1,
+                                          int nb, int rpb) {
+  using C = Cfg<false>;
+  const int s = pr.ring.at;
+  const bool leads = kOne || (threadIdx.x & 31) == 0;
+  bool ok = true;
+  if (leads && pr.ring.wrapped)
+    ok = wait_bar(cx, &cx.bars->empty[s], pr.ring.parity ^ 1);
+  ok = all_lanes<kOne>(ok);
+  if (!ok) {
+    pr.live = false;
+    return;
+  }
+  if (leads && cx.rank == 0)
+    tc::bar_arrive_expect_tx(tc::smem_u32(&cx.bars->full[s]),
+                             2 * C::kSlotBytes);
+  const uint32_t dst = smem + C::kOffRing + s * C::kSlotBytes;
+  const uint32_t full = full0 + s * 8;
+  const int x0 = is_v ? (int)cx.rank * 128 : 0;
+  const int x1 = is_v ? x0 : 128;
+  for (int b = 0; b < nb; ++b) {
+    const int y0 = (int)box_row<kOne>(row0, b);
+    const int y1 = (int)box_row<kOne>(row1, b);
+    if (leads) {
+      const uint32_t d = dst + b * rpb * 128;
+      tc::tma_load_2d_pair(d, map, full, x0, y0);
+      tc::tma_load_2d_pair(d + kBlockBytes, map, full, x0 + 64, y0);
+      tc::tma_load_2d_pair(d + kHalfBytes, map, full, x1, y1);
+      tc::tma_load_2d_pair(d + kHalfBytes + kBlockBytes, map, full, x1 + 64, y1);
     }
   }
-  ++pr.seq;
-  return true;
+  pr.ring.next();
 }
 
-template <bool kFp8>
-__device__ void produce(const Ctx& cx, const Piece& pc, Producer& pr,
-                        uint8_t* smem, const CUtensorMap* tm_k,
-                        const CUtensorMap* tm_v) {
+__device__ __forceinline__ void copy_scales(uint32_t dst, const __half* scales,
+                                            long long row, int rows,
+                                            uint32_t full) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(reinterpret_cast<const uint8_t*>(scales) + row * 8), "r"(rows * 8),
+      "r"(full)
+      : "memory");
+}
+
+// FP8: one staging buffer of 16 KB and its scales.  K: two blocks of 128 bytes
+// x 64 tokens; V: the CTA's 128 bytes of 128 tokens, the second 64 (row1) in
+// the second block.
+template <bool kOne>
+__device__ __forceinline__ void load_raw(const Ctx& cx, Producer<true>& pr,
+                                         uint32_t smem, const CUtensorMap* map,
+                                         const __half* scales, bool is_v,
+                                         long long row0, long long row1, int nb,
+                                         int rpb) {
+  using C = Cfg<true>;
+  const int s = pr.ring.at;
+  const bool leads = kOne || (threadIdx.x & 31) == 0;
+  bool ok = true;
+  if (leads && pr.ring.wrapped)
+    ok = wait_bar(cx, &cx.bars->raw_empty[s], pr.ring.parity ^ 1);
+  ok = all_lanes<kOne>(ok);
+  if (!ok) {
+    pr.live = false;
+    return;
+  }
+  const uint32_t full = tc::smem_u32(&cx.bars->raw_full[s]);
+  if (leads) tc::bar_arrive_expect_tx(full, 16384 + (is_v ? 1024 : 512));
+  const uint32_t dst = smem + C::kOffRaw + s * kRawBytes;
+  for (int b = 0; b < nb; ++b) {
+    const long long y0 = box_row<kOne>(row0, b), y1 = box_row<kOne>(row1, b);
+    if (leads) {
+      const int x = is_v ? (int)cx.rank * 128 : 0;
+      const uint32_t o = b * rpb;
+      tc::tma_load_2d(dst + o * 128, map, full, x, (int)y0);
+      tc::tma_load_2d(dst + kBlockBytes + o * 128, map, full,
+                      is_v ? x : 128, (int)(is_v ? y1 : y0));
+      copy_scales(dst + 16384 + o * 8, scales, y0, rpb, full);
+      if (is_v) copy_scales(dst + 16384 + (64 + o) * 8, scales, y1, rpb, full);
+    }
+  }
+  pr.ring.next();
+}
+
+template <bool kFp8, bool kOne>
+__device__ __forceinline__ void produce_piece(const Ctx& cx, const Piece& pc,
+                                              Producer<kFp8>& pr, uint32_t smem,
+                                              const CUtensorMap* tm_k,
+                                              const CUtensorMap* tm_v) {
   const AttnParams& p = cx.p->a;
   const int lane = threadIdx.x & 31;
-  const int rpb = p.box_rows, nb = 64 / rpb;
-  const int bi = lane % nb, blk = (lane / nb) & 1;
-  // K: this CTA's 64 tokens; V: all 128, as two halves (bf16: both by every
-  // lane, one after the other; FP8: half blk by this lane)
-  const int tk = pc.tok + (int)cx.rank * 64 + bi * rpb;
-  const int tv = pc.tok + bi * rpb;
-  int pk = 0, pv0 = 0, pv1 = 0;
-  if (lane < 2 * nb) {
-    pk = checked_page(p, pc.lead, tk);
-    pv0 = checked_page(p, pc.lead, tv);
-    pv1 = checked_page(p, pc.lead, tv + 64);
-  }
-  for (int j = -1; j < pc.n_tiles; ++j) {
+  const int rpb = p.box_rows, nb = kOne ? 1 : 64 / rpb;
+  const uint32_t full0 = tc::map_to(tc::smem_u32(&cx.bars->full[0]), 0);
+  const int o = kOne ? 0 : (lane & (nb - 1)) * rpb;
+  // K: this CTA's 64 tokens of a tile; V: all 128, in two halves
+  const int tk = pc.tok + (int)cx.rank * 64 + o, tv = pc.tok + o;
+  int pk = page_id(p, pc.lead, tk);
+  int pv0 = page_id(p, pc.lead, tv), pv1 = page_id(p, pc.lead, tv + 64);
+  for (int j = -1; j < pc.n_tiles && pr.live; ++j) {
     // step j loads K of tile j + 1, then V of tile j
     if (j + 1 < pc.n_tiles) {
       const int t = tk + (j + 1) * kT;
-      const long long row = pool_row(p, pk, pc.g, t);
-      if (lane < 2 * nb && j + 2 < pc.n_tiles)
-        pk = checked_page(p, pc.lead, t + kT);
-      if (kFp8) {
-        if (!load_raw(cx, pr, smem, tm_k, p.k_scales, false, row, lane, nb, rpb))
-          pr.live = false;
+      const long long row = pool_row(p, checked_page(p, pk), pc.g, t);
+      if (j + 2 < pc.n_tiles) pk = page_id(p, pc.lead, t + kT);
+      if constexpr (kFp8) {
+        load_raw<kOne>(cx, pr, smem, tm_k, p.k_scales, false, row, row, nb, rpb);
       } else {
-        for (int h = 0; h < 2 && pr.live; ++h)
-          pr.live = load_slot(cx, pr, smem, tm_k, h * 128, row, lane, nb, rpb);
+        load_slot<kOne>(cx, pr, smem, full0, tm_k, false, row, row, nb, rpb);
       }
-      if (!pr.live) return;
     }
-    if (j >= 0) {
+    if (j >= 0 && pr.live) {
       const int t = tv + j * kT;
-      const long long r0 = pool_row(p, pv0, pc.g, t);
-      const long long r1 = pool_row(p, pv1, pc.g, t + 64);
-      if (lane < 2 * nb && j + 1 < pc.n_tiles) {
-        pv0 = checked_page(p, pc.lead, t + kT);
-        pv1 = checked_page(p, pc.lead, t + kT + 64);
+      const long long r0 = pool_row(p, checked_page(p, pv0), pc.g, t);
+      const long long r1 = pool_row(p, checked_page(p, pv1), pc.g, t + 64);
+      if (j + 1 < pc.n_tiles) {
+        pv0 = page_id(p, pc.lead, t + kT);
+        pv1 = page_id(p, pc.lead, t + kT + 64);
       }
-      if (kFp8) {
-        if (!load_raw(cx, pr, smem, tm_v, p.v_scales, true, blk ? r1 : r0, lane,
-                      nb, rpb))
-          pr.live = false;
+      if constexpr (kFp8) {
+        load_raw<kOne>(cx, pr, smem, tm_v, p.v_scales, true, r0, r1, nb, rpb);
       } else {
-        for (int h = 0; h < 2 && pr.live; ++h)
-          pr.live = load_slot(cx, pr, smem, tm_v, (int)cx.rank * 128,
-                              h ? r1 : r0, lane, nb, rpb);
+        load_slot<kOne>(cx, pr, smem, full0, tm_v, true, r0, r1, nb, rpb);
       }
-      if (!pr.live) return;
     }
+  }
+}
+
+template <bool kFp8>
+__device__ void produce(const Ctx& cx, const Piece& pc, Producer<kFp8>& pr,
+                        uint8_t* smem, const CUtensorMap* tm_k,
+                        const CUtensorMap* tm_v) {
+  const uint32_t base = tc::smem_u32(smem);
+  if (cx.p->a.box_rows == 64) {
+    if ((threadIdx.x & 31) == 0)
+      produce_piece<kFp8, true>(cx, pc, pr, base, tm_k, tm_v);
+  } else {
+    produce_piece<kFp8, false>(cx, pc, pr, base, tm_k, tm_v);
   }
 }
 
@@ -293,19 +358,29 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t pair16, __half2 sc)
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+struct Dequant {
+  Ring<kRaw> raw;
+  Ring<Cfg<true>::kSlots> slot;
+  int turn = 0;  // staging buffers so far
+};
+
 __device__ __forceinline__ void dequant_unit(const Ctx& cx, uint8_t* smem,
-                                             long long& rseq, long long& sseq,
-                                             bool is_v) {
+                                             Dequant& dq, bool is_v) {
   using C = Cfg<true>;
-  const int tid = threadIdx.x - 192, lane = threadIdx.x & 31;
+  if ((dq.turn++ & 1) != (int)(threadIdx.x - 192) >> 7) {  // the other set's
+    dq.raw.next();
+    dq.slot.next();
+    dq.slot.next();
+    return;
+  }
+  const int tid = (threadIdx.x - 192) & 127, lane = threadIdx.x & 31;
   const int c = tid & 7, tok0 = tid >> 3;
-  const int r = (int)(rseq % kRaw);
-  wait_bar(cx, &cx.bars->raw_full[r], (uint32_t)(rseq / kRaw) & 1);
+  const int r = dq.raw.at;
+  wait_bar(cx, &cx.bars->raw_full[r], dq.raw.parity);
   const uint8_t* raw = smem + C::kOffRaw + r * kRawBytes;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int s = (int)(sseq % C::kSlots);
-    const long long use = sseq / C::kSlots;
+    const int s = dq.slot.at;
     uint4 x[4];
     __half sc[4];
 #pragma unroll
@@ -317,8 +392,9 @@ __device__ __forceinline__ void dequant_unit(const Ctx& cx, uint8_t* smem,
                           : tok * 4 + h * 2 + (c >> 2);
       sc[e] = reinterpret_cast<const __half*>(raw + 16384)[at];
     }
-    if (use > 0) wait_bar(cx, &cx.bars->empty[s], (uint32_t)(use - 1) & 1);
-    uint8_t* out = smem + C::kOffRing + s * kSlotBytes + (c >> 2) * kBlockBytes;
+    if (dq.slot.wrapped) wait_bar(cx, &cx.bars->empty[s], dq.slot.parity ^ 1);
+    uint8_t* out =
+        smem + C::kOffRing + s * C::kSlotBytes + (c >> 2) * kBlockBytes;
     const int ch = (c & 3) * 2, flip = c >> 2;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -341,75 +417,94 @@ __device__ __forceinline__ void dequant_unit(const Ctx& cx, uint8_t* smem,
     }
     tc::fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0)
-      tc::arrive_cluster(tc::map_to(tc::smem_u32(&cx.bars->full[s]), 0));
-    ++sseq;
+    if (lane == 0) tc::bar_arrive(tc::smem_u32(&cx.bars->full[s]));
+    dq.slot.next();
   }
   __syncwarp();
   if (lane == 0) tc::bar_arrive(tc::smem_u32(&cx.bars->raw_empty[r]));
-  ++rseq;
+  dq.raw.next();
 }
 
 __device__ void dequant_piece(const Ctx& cx, const Piece& pc, uint8_t* smem,
-                              long long& rseq, long long& sseq) {
+                              Dequant& dq) {
   for (int j = -1; j < pc.n_tiles; ++j) {
-    if (j + 1 < pc.n_tiles) dequant_unit(cx, smem, rseq, sseq, false);
-    if (j >= 0) dequant_unit(cx, smem, rseq, sseq, true);
+    if (j + 1 < pc.n_tiles) dequant_unit(cx, smem, dq, false);
+    if (j >= 0) dequant_unit(cx, smem, dq, true);
   }
 }
 
 // ---- warp 1 of the leader, one thread: MMA issue ----------------------------
+// A descriptor's low bits are the address in 16-byte steps, so the operands of
+// a slot's MMAs are its base descriptor plus constants.  (With the descriptors
+// built anew, issuing took 120 to 160 cycles an MMA, more than the 64 and 128
+// that the MMAs themselves take.)
 template <bool kFp8>
-__device__ __forceinline__ bool issue_qk(const Ctx& cx, long long& seq, int gj,
-                                         uint32_t tmem, uint8_t* smem) {
+using Slots = Ring<Cfg<kFp8>::kSlots>;
+
+template <bool kFp8>
+__device__ __forceinline__ bool wait_slot(const Ctx& cx,
+                                          const Slots<kFp8>& seq) {
+  if (!wait_bar(cx, &cx.bars->full[seq.at], seq.parity)) return false;
+  return !kFp8 ||
+         wait_bar<true>(cx, &cx.bars->peer_full[seq.at], seq.parity);
+}
+
+template <bool kFp8>
+__device__ __forceinline__ bool issue_qk(const Ctx& cx, Slots<kFp8>& seq, int gj,
+                                         uint32_t tmem, uint32_t smem) {
   using C = Cfg<kFp8>;
   const uint32_t d = tmem + kColS + (gj & 1) * kT;
-  const uint32_t q = tc::smem_u32(smem);
 #pragma unroll
-  for (int h = 0; h < 2; ++h, ++seq) {
-    const int s = (int)(seq % C::kSlots);
-    if (!wait_bar<kFp8>(cx, &cx.bars->full[s],
-                        (uint32_t)(seq / C::kSlots) & 1))
-      return false;
-    tc::fence_after();
-    const uint32_t kb = tc::smem_u32(smem + C::kOffRing + s * kSlotBytes);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {  // 16 channels each
-      const uint64_t a = tc::desc_sw128(
-          q + (2 * h + (k >> 2)) * (128 * 128) + (k & 3) * 32, 16, 1024);
-      const uint64_t b =
-          tc::desc_sw128(kb + (k >> 2) * kBlockBytes + (k & 3) * 32, 16, 1024);
-      tc::mma_pair(d, a, b, C::kIdescQK, (h | k) ? 1u : 0u);
+  for (int h = 0; h < 2; ++h) {
+    const uint64_t a = tc::desc_sw128(smem + 2 * h * (128 * 128), 16, 1024);
+    const uint64_t b = tc::desc_sw128(
+        smem + C::kOffRing + seq.at * C::kSlotBytes +
+            (C::kParts == 1 ? h * kHalfBytes : 0),
+        16, 1024);
+    if (C::kParts == 2 || h == 0) {
+      if (!wait_slot<kFp8>(cx, seq)) return false;
+      tc::fence_after();
     }
-    tc::commit_pair(tc::smem_u32(&cx.bars->empty[s]));
+#pragma unroll
+    for (int k = 0; k < 8; ++k)  // 16 channels each
+      tc::mma_pair(d, a + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
+                   b + (((k >> 2) * kBlockBytes + (k & 3) * 32) >> 4),
+                   C::kIdescQK, (h | k) ? 1u : 0u);
+    if (C::kParts == 2 || h == 1) {
+      tc::commit_pair(tc::smem_u32(&cx.bars->empty[seq.at]));
+      seq.next();
+    }
   }
   tc::commit_pair(tc::smem_u32(&cx.bars->s_full[gj & 1]));
   return true;
 }
 
 template <bool kFp8>
-__device__ __forceinline__ bool issue_pv(const Ctx& cx, long long& seq, int gj,
+__device__ __forceinline__ bool issue_pv(const Ctx& cx, Slots<kFp8>& seq, int gj,
                                          bool first, uint32_t tmem,
-                                         uint8_t* smem) {
+                                         uint32_t smem) {
   using C = Cfg<kFp8>;
   if (!wait_bar(cx, &cx.bars->p_full[gj & 1], (uint32_t)(gj >> 1) & 1))
     return false;
   const uint32_t pt = tmem + kColS + (gj & 1) * kT;
 #pragma unroll
-  for (int h = 0; h < 2; ++h, ++seq) {
-    const int s = (int)(seq % C::kSlots);
-    if (!wait_bar<kFp8>(cx, &cx.bars->full[s],
-                        (uint32_t)(seq / C::kSlots) & 1))
-      return false;
-    tc::fence_after();
-    const uint32_t vb = tc::smem_u32(smem + C::kOffRing + s * kSlotBytes);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {  // 16 tokens each
-      const uint64_t b = tc::desc_sw128(vb + k * 2048, kBlockBytes, 1024);
-      tc::mma_pair_ta(tmem, pt + (h * 4 + k) * 8, b, C::kIdescPV,
-                      (first && (h | k) == 0) ? 0u : 1u);
+  for (int h = 0; h < 2; ++h) {
+    const uint64_t b = tc::desc_sw128(
+        smem + C::kOffRing + seq.at * C::kSlotBytes +
+            (C::kParts == 1 ? h * kHalfBytes : 0),
+        kBlockBytes, 1024);
+    if (C::kParts == 2 || h == 0) {
+      if (!wait_slot<kFp8>(cx, seq)) return false;
+      tc::fence_after();
     }
-    tc::commit_pair(tc::smem_u32(&cx.bars->empty[s]));
+#pragma unroll
+    for (int k = 0; k < 4; ++k)  // 16 tokens each
+      tc::mma_pair_ta(tmem, pt + (h * 4 + k) * 8, b + ((k * 2048) >> 4),
+                      C::kIdescPV, (first && (h | k) == 0) ? 0u : 1u);
+    if (C::kParts == 2 || h == 1) {
+      tc::commit_pair(tc::smem_u32(&cx.bars->empty[seq.at]));
+      seq.next();
+    }
   }
   tc::commit_pair(tc::smem_u32(&cx.bars->pv_done[gj & 1]));
   return true;
@@ -417,7 +512,8 @@ __device__ __forceinline__ bool issue_pv(const Ctx& cx, long long& seq, int gj,
 
 template <bool kFp8>
 __device__ void mma_piece(const Ctx& cx, const Piece& pc, int gj0, int n_piece,
-                          long long& seq, uint32_t tmem, uint8_t* smem) {
+                          Slots<kFp8>& seq, uint32_t tmem, uint8_t* smem_ptr) {
+  const uint32_t smem = tc::smem_u32(smem_ptr);
   if (!wait_bar<true>(cx, &cx.bars->q_full, (uint32_t)n_piece & 1)) return;
   tc::fence_after();
   if (!issue_qk<kFp8>(cx, seq, gj0, tmem, smem)) return;
@@ -426,6 +522,17 @@ __device__ void mma_piece(const Ctx& cx, const Piece& pc, int gj0, int n_piece,
         !issue_qk<kFp8>(cx, seq, gj0 + j + 1, tmem, smem))
       return;
     if (!issue_pv<kFp8>(cx, seq, gj0 + j, j == 0, tmem, smem)) return;
+  }
+}
+
+// FP8, the other CTA's warp 1, one thread: tells the issuer which slots its
+// dequant warps have filled.  Their arrivals are local; this thread's release
+// at cluster scope, which waits for hundreds of cycles, is off their path.
+__device__ void relay_piece(const Ctx& cx, const Piece& pc, Slots<true>& seq) {
+  const uint32_t peer0 = tc::map_to(tc::smem_u32(&cx.bars->peer_full[0]), 0);
+  for (int k = 0; k < 4 * pc.n_tiles; ++k, seq.next()) {
+    if (!wait_bar(cx, &cx.bars->full[seq.at], seq.parity)) return;
+    tc::arrive_cluster(peer0 + seq.at * 8);
   }
 }
 
@@ -498,13 +605,21 @@ __device__ void softmax_tiles(const Ctx& cx, const Piece& pc, int gj0,
     const uint32_t sbuf = lane_base + kColS + (gj & 1) * kT;
     wait_bar(cx, &cx.bars->s_full[gj & 1], (uint32_t)(gj >> 1) & 1);
     tc::fence_after();
-    uint32_t raw[kT];
-    tc::tmem_ld_cols<kT>(sbuf, raw);
+    // FP8 (more warps, fewer registers): the scores are read twice, 64
+    // columns at a time
+    constexpr int kC = kFp8 ? 64 : kT;
+    uint32_t raw[kC];
     const float* s = reinterpret_cast<const float*>(raw);
-    float mx4[4] = {s[0], s[1], s[2], s[3]};
+    float mx = -INFINITY;
 #pragma unroll
-    for (int k = 4; k < kT; ++k) mx4[k & 3] = fmaxf(mx4[k & 3], s[k]);
-    const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl2;
+    for (int c = 0; c < kT; c += kC) {
+      tc::tmem_ld_cols<kC>(sbuf + c, raw);
+      float mx4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+      for (int k = 4; k < kC; ++k) mx4[k & 3] = fmaxf(mx4[k & 3], s[k]);
+      mx = fmaxf(mx, fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])));
+    }
+    mx *= sl2;
     bool need = false;
     float alpha = 1.f;
     if (jt == 0) {
@@ -534,21 +649,26 @@ __device__ void softmax_tiles(const Ctx& cx, const Piece& pc, int gj0,
     const float mu = m == -INFINITY ? 0.f : m;
     float sum4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int k = 0; k < kT; k += 2) {
-      const float x0 = exp2f(fmaf(s[k], sl2, -mu));
-      const float x1 = exp2f(fmaf(s[k + 1], sl2, -mu));
-      sum4[k & 3] += x0;
-      sum4[(k & 3) + 1] += x1;
-      if (kFp8) {
-        const __half2 hh = __floats2half2_rn(x0, x1);
-        raw[k >> 1] = *reinterpret_cast<const uint32_t*>(&hh);
-      } else {
-        const __nv_bfloat162 hh = __floats2bfloat162_rn(x0, x1);
-        raw[k >> 1] = *reinterpret_cast<const uint32_t*>(&hh);
+    for (int c = 0; c < kT; c += kC) {
+      if (kFp8) tc::tmem_ld_cols<kC>(sbuf + c, raw);
+#pragma unroll
+      for (int k = 0; k < kC; k += 2) {
+        const float x0 = exp2f(fmaf(s[k], sl2, -mu));
+        const float x1 = exp2f(fmaf(s[k + 1], sl2, -mu));
+        sum4[k & 3] += x0;
+        sum4[(k & 3) + 1] += x1;
+        if (kFp8) {
+          const __half2 hh = __floats2half2_rn(x0, x1);
+          raw[k >> 1] = *reinterpret_cast<const uint32_t*>(&hh);
+        } else {
+          const __nv_bfloat162 hh = __floats2bfloat162_rn(x0, x1);
+          raw[k >> 1] = *reinterpret_cast<const uint32_t*>(&hh);
+        }
       }
+      // P over columns whose scores have been read
+      tc::tmem_st_cols<kC / 2>(sbuf + c / 2, raw);
     }
     l += (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
-    tc::tmem_st_cols<kT / 2>(sbuf, raw);
     tc::tmem_wait_st();
     tc::fence_before();
     __syncwarp();
@@ -633,8 +753,9 @@ __global__ void __cluster_dims__(2, 1, 1)
   if (tid == 0) {
     for (int s = 0; s < C::kSlots; ++s) {
       // bf16: the leader's expect_tx plus both CTAs' bytes; FP8: the four
-      // dequant warps of both CTAs
-      tc::bar_init(tc::smem_u32(&bars.full[s]), kFp8 ? 8 : 1);
+      // dequant warps, and the other CTA's relay
+      tc::bar_init(tc::smem_u32(&bars.full[s]), kFp8 ? 4 : 1);
+      tc::bar_init(tc::smem_u32(&bars.peer_full[s]), 1);
       tc::bar_init(tc::smem_u32(&bars.empty[s]), 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -661,8 +782,9 @@ __global__ void __cluster_dims__(2, 1, 1)
                tc::map_to(tc::smem_u32(&s_abort), rank ^ 1u), rank, &p};
 
   int gj0 = 0, n_piece = 0;
-  Producer pr;
-  long long mseq = 0, rseq = 0, sseq = 0;
+  Producer<kFp8> pr;
+  Slots<kFp8> mseq;
+  Dequant dq;
   float m = 0.f, l = 0.f;
   Piece prev{};
   for (int i = blockIdx.x >> 1; i < pieces; i += gridDim.x >> 1) {
@@ -673,6 +795,9 @@ __global__ void __cluster_dims__(2, 1, 1)
     } else if (warp == 1) {
       if (rank == 0 && lane == 0)
         mma_piece<kFp8>(cx, pc, gj0, n_piece, mseq, tmem, smem);
+      if constexpr (kFp8) {
+        if (rank == 1 && lane == 0) relay_piece(cx, pc, mseq);
+      }
       __syncwarp();
     } else if (warp < 6) {
       if (n_piece) {
@@ -686,7 +811,7 @@ __global__ void __cluster_dims__(2, 1, 1)
       if (n_piece) epilogue(cx, prev, gj0 - 1, tmem, m, l);
       softmax_tiles<kFp8>(cx, pc, gj0, tmem, m, l);
     } else if (kFp8) {
-      dequant_piece(cx, pc, smem, rseq, sseq);
+      dequant_piece(cx, pc, smem, dq);
     }
     prev = pc;
     gj0 += pc.n_tiles;

@@ -31,6 +31,7 @@
 //               epilogue (normalised fp32 partial, log-sum-exp)
 //   warps 6..13 FP8 only: E4M3 bytes times scale to fp16 slots, two sets of
 //               four warps on alternate staging buffers
+//   warps 1, 14 FP8 only, in the other CTA: relays, see relay_piece
 //
 // P is rounded once to the type of V (bf16; fp16 for FP8 KV): the relative
 // error of a weight, at most 2^-8, is independent from token to token and no larger
@@ -56,18 +57,16 @@ constexpr int kQBytes = 128 * kHeadDim * 2;   // 4 column blocks of 128 rows
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 256;
 constexpr float kRescaleLog2 = 8.0f;
-constexpr int kMaxSlots = 6;
+constexpr int kMaxSlots = 5;
 constexpr int kRaw = 3;                       // FP8 staging buffers
 constexpr int kRawBytes = 16384 + 1024;       // bytes and scales
 
 template <bool kFp8>
 struct Cfg {
-  // a slot holds a CTA's share of K or V of one tile, or for FP8, where
-  // staging takes room and the dequantisation is the pace, half of it
-  static constexpr int kParts = kFp8 ? 2 : 1;
-  static constexpr int kSlots = kFp8 ? 6 : 5;
-  static constexpr int kSlotBytes = 2 * kHalfBytes / kParts;
-  static constexpr int kThreads = kFp8 ? 448 : 192;
+  // a slot holds a CTA's share of K or V of one tile
+  static constexpr int kSlots = kFp8 ? 3 : 5;
+  static constexpr int kSlotBytes = 2 * kHalfBytes;
+  static constexpr int kThreads = kFp8 ? 480 : 192;
   static constexpr int kOffRing = kQBytes;
   static constexpr int kOffRaw = kOffRing + kSlots * kSlotBytes;
   static constexpr int kSmem = kOffRaw + (kFp8 ? kRaw * kRawBytes : 0) + 1024;
@@ -347,10 +346,11 @@ __device__ void produce(const Ctx& cx, const Piece& pc, Producer<kFp8>& pr,
 }
 
 // ---- warps 6..9 (FP8): staged bytes to fp16 slots ---------------------------
-// A staging buffer makes two slots of 64 tokens x 128 channels.  Thread t
-// converts 16-byte chunk c = t & 7 (16 channels) of tokens (t >> 3) + 16 e;
-// the two 16-byte stores of lanes c and c + 4 fall into the same banks of two
-// column blocks, so the upper half stores its pair in the other order.
+// A staging buffer makes a slot, two halves of 64 tokens x 128 channels.
+// Thread t converts 16-byte chunk c = t & 7 (16 channels) of tokens
+// (t >> 3) + 16 e; the two 16-byte stores of lanes c and c + 4 fall into the
+// same banks of two column blocks, so the upper half stores its pair in the
+// other order.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t pair16, __half2 sc) {
   const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(
       static_cast<__nv_fp8x2_storage_t>(pair16), __NV_E4M3);
@@ -367,20 +367,24 @@ struct Dequant {
 __device__ __forceinline__ void dequant_unit(const Ctx& cx, uint8_t* smem,
                                              Dequant& dq, bool is_v) {
   using C = Cfg<true>;
+  const int tid = (threadIdx.x - 192) & 127, lane = threadIdx.x & 31;
+  const int c = tid & 7, tok0 = tid >> 3;
+  const int r = dq.raw.at, s = dq.slot.at;
+  // Both sets see every buffer land and release it, the set that converts it
+  // after its last read: with two waiters that each look at every other use
+  // only, one a lap ahead would take the phase before for its own.  One lane
+  // polls: the issuer's thread shares the scheduler.
+  if (lane == 0) wait_bar(cx, &cx.bars->raw_full[r], dq.raw.parity);
+  __syncwarp();
   if ((dq.turn++ & 1) != (int)(threadIdx.x - 192) >> 7) {  // the other set's
+    if (lane == 0) tc::bar_arrive(tc::smem_u32(&cx.bars->raw_empty[r]));
     dq.raw.next();
-    dq.slot.next();
     dq.slot.next();
     return;
   }
-  const int tid = (threadIdx.x - 192) & 127, lane = threadIdx.x & 31;
-  const int c = tid & 7, tok0 = tid >> 3;
-  const int r = dq.raw.at;
-  wait_bar(cx, &cx.bars->raw_full[r], dq.raw.parity);
   const uint8_t* raw = smem + C::kOffRaw + r * kRawBytes;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int s = dq.slot.at;
     uint4 x[4];
     __half sc[4];
 #pragma unroll
@@ -392,9 +396,12 @@ __device__ __forceinline__ void dequant_unit(const Ctx& cx, uint8_t* smem,
                           : tok * 4 + h * 2 + (c >> 2);
       sc[e] = reinterpret_cast<const __half*>(raw + 16384)[at];
     }
-    if (dq.slot.wrapped) wait_bar(cx, &cx.bars->empty[s], dq.slot.parity ^ 1);
-    uint8_t* out =
-        smem + C::kOffRing + s * C::kSlotBytes + (c >> 2) * kBlockBytes;
+    if (h == 0 && dq.slot.wrapped) {
+      if (lane == 0) wait_bar(cx, &cx.bars->empty[s], dq.slot.parity ^ 1);
+      __syncwarp();
+    }
+    uint8_t* out = smem + C::kOffRing + s * C::kSlotBytes + h * kHalfBytes +
+                   (c >> 2) * kBlockBytes;
     const int ch = (c & 3) * 2, flip = c >> 2;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -415,13 +422,14 @@ __device__ __forceinline__ void dequant_unit(const Ctx& cx, uint8_t* smem,
       *reinterpret_cast<uint4*>(row + ((first ^ (tok & 7)) << 4)) = flip ? b : a;
       *reinterpret_cast<uint4*>(row + ((second ^ (tok & 7)) << 4)) = flip ? a : b;
     }
-    tc::fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) tc::bar_arrive(tc::smem_u32(&cx.bars->full[s]));
-    dq.slot.next();
   }
+  tc::fence_proxy_async_smem();
   __syncwarp();
-  if (lane == 0) tc::bar_arrive(tc::smem_u32(&cx.bars->raw_empty[r]));
+  if (lane == 0) {
+    tc::bar_arrive(tc::smem_u32(&cx.bars->full[s]));
+    tc::bar_arrive(tc::smem_u32(&cx.bars->raw_empty[r]));
+  }
+  dq.slot.next();
   dq.raw.next();
 }
 
@@ -454,27 +462,18 @@ __device__ __forceinline__ bool issue_qk(const Ctx& cx, Slots<kFp8>& seq, int gj
                                          uint32_t tmem, uint32_t smem) {
   using C = Cfg<kFp8>;
   const uint32_t d = tmem + kColS + (gj & 1) * kT;
+  const uint64_t a = tc::desc_sw128(smem, 16, 1024);
+  const uint64_t b = tc::desc_sw128(
+      smem + C::kOffRing + seq.at * C::kSlotBytes, 16, 1024);
+  if (!wait_slot<kFp8>(cx, seq)) return false;
+  tc::fence_after();
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint64_t a = tc::desc_sw128(smem + 2 * h * (128 * 128), 16, 1024);
-    const uint64_t b = tc::desc_sw128(
-        smem + C::kOffRing + seq.at * C::kSlotBytes +
-            (C::kParts == 1 ? h * kHalfBytes : 0),
-        16, 1024);
-    if (C::kParts == 2 || h == 0) {
-      if (!wait_slot<kFp8>(cx, seq)) return false;
-      tc::fence_after();
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k)  // 16 channels each
-      tc::mma_pair(d, a + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
-                   b + (((k >> 2) * kBlockBytes + (k & 3) * 32) >> 4),
-                   C::kIdescQK, (h | k) ? 1u : 0u);
-    if (C::kParts == 2 || h == 1) {
-      tc::commit_pair(tc::smem_u32(&cx.bars->empty[seq.at]));
-      seq.next();
-    }
-  }
+  for (int k = 0; k < 16; ++k)  // 16 channels each, 64 a column block
+    tc::mma_pair(d, a + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
+                 b + (((k >> 2) * kBlockBytes + (k & 3) * 32) >> 4),
+                 C::kIdescQK, k ? 1u : 0u);
+  tc::commit_pair(tc::smem_u32(&cx.bars->empty[seq.at]));
+  seq.next();
   tc::commit_pair(tc::smem_u32(&cx.bars->s_full[gj & 1]));
   return true;
 }
@@ -487,25 +486,17 @@ __device__ __forceinline__ bool issue_pv(const Ctx& cx, Slots<kFp8>& seq, int gj
   if (!wait_bar(cx, &cx.bars->p_full[gj & 1], (uint32_t)(gj >> 1) & 1))
     return false;
   const uint32_t pt = tmem + kColS + (gj & 1) * kT;
+  const uint64_t b = tc::desc_sw128(
+      smem + C::kOffRing + seq.at * C::kSlotBytes, kBlockBytes, 1024);
+  if (!wait_slot<kFp8>(cx, seq)) return false;
+  tc::fence_after();
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint64_t b = tc::desc_sw128(
-        smem + C::kOffRing + seq.at * C::kSlotBytes +
-            (C::kParts == 1 ? h * kHalfBytes : 0),
-        kBlockBytes, 1024);
-    if (C::kParts == 2 || h == 0) {
-      if (!wait_slot<kFp8>(cx, seq)) return false;
-      tc::fence_after();
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k)  // 16 tokens each
-      tc::mma_pair_ta(tmem, pt + (h * 4 + k) * 8, b + ((k * 2048) >> 4),
-                      C::kIdescPV, (first && (h | k) == 0) ? 0u : 1u);
-    if (C::kParts == 2 || h == 1) {
-      tc::commit_pair(tc::smem_u32(&cx.bars->empty[seq.at]));
-      seq.next();
-    }
-  }
+  for (int k = 0; k < 8; ++k)  // 16 tokens each, 64 a half
+    tc::mma_pair_ta(tmem, pt + k * 8,
+                    b + (((k >> 2) * kHalfBytes + (k & 3) * 2048) >> 4),
+                    C::kIdescPV, first && k == 0 ? 0u : 1u);
+  tc::commit_pair(tc::smem_u32(&cx.bars->empty[seq.at]));
+  seq.next();
   tc::commit_pair(tc::smem_u32(&cx.bars->pv_done[gj & 1]));
   return true;
 }
@@ -525,14 +516,25 @@ __device__ void mma_piece(const Ctx& cx, const Piece& pc, int gj0, int n_piece,
   }
 }
 
-// FP8, the other CTA's warp 1, one thread: tells the issuer which slots its
-// dequant warps have filled.  Their arrivals are local; this thread's release
-// at cluster scope, which waits for hundreds of cycles, is off their path.
-__device__ void relay_piece(const Ctx& cx, const Piece& pc, Slots<true>& seq) {
+// FP8, one thread each of two warps of the other CTA: tells the issuer which
+// slots its dequant warps have filled.  The dequant warps arrive locally; a
+// release at cluster scope waits for more than 1,000 cycles, too long for
+// their path and, twice a tile, for one thread.  So one thread releases K's
+// slots and the other V's, and each also arrives, without the release, once it
+// has seen the other's: the issuer, and with it the slot's next use, waits for
+// both, so neither thread can miss a phase.
+__device__ void relay_piece(const Ctx& cx, const Piece& pc, Slots<true>& seq,
+                            bool v_side) {
   const uint32_t peer0 = tc::map_to(tc::smem_u32(&cx.bars->peer_full[0]), 0);
-  for (int k = 0; k < 4 * pc.n_tiles; ++k, seq.next()) {
-    if (!wait_bar(cx, &cx.bars->full[seq.at], seq.parity)) return;
-    tc::arrive_cluster(peer0 + seq.at * 8);
+  for (int j = -1; j < pc.n_tiles; ++j) {
+    for (int is_v = j + 1 < pc.n_tiles ? 0 : 1; is_v <= (j >= 0); ++is_v) {
+      if (!wait_bar(cx, &cx.bars->full[seq.at], seq.parity)) return;
+      if ((is_v != 0) == v_side)
+        tc::arrive_cluster(peer0 + seq.at * 8);
+      else
+        tc::arrive_cluster_relaxed(peer0 + seq.at * 8);
+      seq.next();
+    }
   }
 }
 
@@ -753,9 +755,9 @@ __global__ void __cluster_dims__(2, 1, 1)
   if (tid == 0) {
     for (int s = 0; s < C::kSlots; ++s) {
       // bf16: the leader's expect_tx plus both CTAs' bytes; FP8: the four
-      // dequant warps, and the other CTA's relay
+      // dequant warps, and the other CTA's two relays
       tc::bar_init(tc::smem_u32(&bars.full[s]), kFp8 ? 4 : 1);
-      tc::bar_init(tc::smem_u32(&bars.peer_full[s]), 1);
+      tc::bar_init(tc::smem_u32(&bars.peer_full[s]), 2);
       tc::bar_init(tc::smem_u32(&bars.empty[s]), 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -766,7 +768,7 @@ __global__ void __cluster_dims__(2, 1, 1)
     tc::bar_init(tc::smem_u32(&bars.q_full), 8);
     for (int s = 0; s < kRaw; ++s) {
       tc::bar_init(tc::smem_u32(&bars.raw_full[s]), 1);
-      tc::bar_init(tc::smem_u32(&bars.raw_empty[s]), 4);
+      tc::bar_init(tc::smem_u32(&bars.raw_empty[s]), 8);
     }
     tc::bar_init(tc::smem_u32(&bars.drain), 1);
     s_abort = 0;
@@ -796,7 +798,7 @@ __global__ void __cluster_dims__(2, 1, 1)
       if (rank == 0 && lane == 0)
         mma_piece<kFp8>(cx, pc, gj0, n_piece, mseq, tmem, smem);
       if constexpr (kFp8) {
-        if (rank == 1 && lane == 0) relay_piece(cx, pc, mseq);
+        if (rank == 1 && lane == 0) relay_piece(cx, pc, mseq, false);
       }
       __syncwarp();
     } else if (warp < 6) {
@@ -810,8 +812,13 @@ __global__ void __cluster_dims__(2, 1, 1)
       write_q<kFp8>(cx, pc, smem);
       if (n_piece) epilogue(cx, prev, gj0 - 1, tmem, m, l);
       softmax_tiles<kFp8>(cx, pc, gj0, tmem, m, l);
-    } else if (kFp8) {
-      dequant_piece(cx, pc, smem, dq);
+    } else if constexpr (kFp8) {
+      if (warp < 14) {
+        dequant_piece(cx, pc, smem, dq);
+      } else {
+        if (rank == 1 && lane == 0) relay_piece(cx, pc, mseq, true);
+        __syncwarp();
+      }
     }
     prev = pc;
     gj0 += pc.n_tiles;

@@ -281,6 +281,27 @@ def test_captured_graph_streams_and_repeats(kv):
 
 
 @gpu
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_many_calls_in_a_row(kv):
+    # the pipelines of both CTAs of a pair under load: no wait runs out, and
+    # every call gives the same bits
+    c = Case([40], [20000], [100 + b for b in range(40)], q_len=1, page=64,
+             kv=kv, seed=13)
+    ws = sv.alloc_workspace(160 << 20, DEV)
+    first = c.run(checked=True, workspace=ws)
+    outs = [torch.empty_like(first) for _ in range(150)]
+    for o in outs:
+        c.run(out=o, workspace=ws)
+    torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o, first)
+    for _ in range(20):
+        c.run(checked=True, workspace=ws)
+        assert sv.verify_status(ws) == 0
+    c.check(first)
+
+
+@gpu
 def test_large_scores_rescale():
     # keys that grow along the prefix, so the running maximum moves by far
     # more than the threshold, and one that dominates late

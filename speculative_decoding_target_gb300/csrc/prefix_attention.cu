@@ -20,7 +20,7 @@
 // the channels of V.
 //
 // Warp roles (both CTAs, the issuer in the leader only):
-//   warp 0      producer: TMA boxes of the CTA's halves, [64 tokens x 128
+//   warps 0, V  producers of K and of V: TMA boxes of the CTA's halves, [64 tokens x 128
 //               channels] twice a tile for each of K and V, 128-byte swizzle,
 //               into a ring in the order in which the issuer consumes them:
 //               K0 K1 V0 K2 V1 ...
@@ -66,7 +66,8 @@ struct Cfg {
   // a slot holds a CTA's share of K or V of one tile
   static constexpr int kSlots = kFp8 ? 3 : 5;
   static constexpr int kSlotBytes = 2 * kHalfBytes;
-  static constexpr int kThreads = kFp8 ? 480 : 192;
+  static constexpr int kThreads = kFp8 ? 512 : 224;
+  static constexpr int kWarpV = kFp8 ? 15 : 6;  // the producer of V
   static constexpr int kOffRing = kQBytes;
   static constexpr int kOffRaw = kOffRing + kSlots * kSlotBytes;
   static constexpr int kSmem = kOffRaw + (kFp8 ? kRaw * kRawBytes : 0) + 1024;
@@ -214,7 +215,7 @@ __device__ __forceinline__ void load_slot(const Ctx& cx, Producer<false>& pr,
   bool ok = true;
   if (leads && pr.ring.wrapped)
     ok = wait_bar(cx, &cx.bars->empty[s], pr.ring.parity ^ 1);
-  ok = all_lanes<kOne>(ok);
+  ok = all_lanes<kOne>(ok && !*cx.abort);
   if (!ok) {
     pr.live = false;
     return;
@@ -266,7 +267,10 @@ __device__ __forceinline__ void load_raw(const Ctx& cx, Producer<true>& pr,
   bool ok = true;
   if (leads && pr.ring.wrapped)
     ok = wait_bar(cx, &cx.bars->raw_empty[s], pr.ring.parity ^ 1);
-  ok = all_lanes<kOne>(ok);
+  // Once a CTA gives up, its dequant warps release buffers that have not
+  // landed; the flag is set before that, and arming a barrier whose bytes are
+  // still under way is a fault.
+  ok = all_lanes<kOne>(ok && !*cx.abort);
   if (!ok) {
     pr.live = false;
     return;
@@ -289,59 +293,55 @@ __device__ __forceinline__ void load_raw(const Ctx& cx, Producer<true>& pr,
   pr.ring.next();
 }
 
+// One warp loads the K units of the order K0 K1 V0 K2 V1 .., another the V
+// units (with pages of 16 tokens a unit is 16 copies, more than one warp
+// issues in a tile's time); both step through the whole ring.
 template <bool kFp8, bool kOne>
 __device__ __forceinline__ void produce_piece(const Ctx& cx, const Piece& pc,
                                               Producer<kFp8>& pr, uint32_t smem,
-                                              const CUtensorMap* tm_k,
-                                              const CUtensorMap* tm_v) {
+                                              const CUtensorMap* map,
+                                              bool v_side) {
   const AttnParams& p = cx.p->a;
   const int lane = threadIdx.x & 31;
   const int rpb = p.box_rows, nb = kOne ? 1 : 64 / rpb;
   const uint32_t full0 = tc::map_to(tc::smem_u32(&cx.bars->full[0]), 0);
-  const int o = kOne ? 0 : (lane & (nb - 1)) * rpb;
+  const __half* scales = v_side ? p.v_scales : p.k_scales;
   // K: this CTA's 64 tokens of a tile; V: all 128, in two halves
-  const int tk = pc.tok + (int)cx.rank * 64 + o, tv = pc.tok + o;
-  int pk = page_id(p, pc.lead, tk);
-  int pv0 = page_id(p, pc.lead, tv), pv1 = page_id(p, pc.lead, tv + 64);
-  for (int j = -1; j < pc.n_tiles && pr.live; ++j) {
-    // step j loads K of tile j + 1, then V of tile j
+  const int t0 = pc.tok + (kOne ? 0 : (lane & (nb - 1)) * rpb) +
+                 (v_side ? 0 : (int)cx.rank * 64);
+  int page0 = page_id(p, pc.lead, t0);
+  int page1 = v_side ? page_id(p, pc.lead, t0 + 64) : 0;
+  if (v_side) pr.ring.next();  // K0
+  for (int j = 0; j < pc.n_tiles && pr.live; ++j) {
+    // V: K of the next tile lies before V of this one; K: V of the tile
+    // before the last
+    if (v_side && j + 1 < pc.n_tiles) pr.ring.next();
+    const int t = t0 + j * kT;
+    const long long r0 = pool_row(p, checked_page(p, page0), pc.g, t);
+    const long long r1 =
+        v_side ? pool_row(p, checked_page(p, page1), pc.g, t + 64) : r0;
     if (j + 1 < pc.n_tiles) {
-      const int t = tk + (j + 1) * kT;
-      const long long row = pool_row(p, checked_page(p, pk), pc.g, t);
-      if (j + 2 < pc.n_tiles) pk = page_id(p, pc.lead, t + kT);
-      if constexpr (kFp8) {
-        load_raw<kOne>(cx, pr, smem, tm_k, p.k_scales, false, row, row, nb, rpb);
-      } else {
-        load_slot<kOne>(cx, pr, smem, full0, tm_k, false, row, row, nb, rpb);
-      }
+      page0 = page_id(p, pc.lead, t + kT);
+      if (v_side) page1 = page_id(p, pc.lead, t + kT + 64);
     }
-    if (j >= 0 && pr.live) {
-      const int t = tv + j * kT;
-      const long long r0 = pool_row(p, checked_page(p, pv0), pc.g, t);
-      const long long r1 = pool_row(p, checked_page(p, pv1), pc.g, t + 64);
-      if (j + 1 < pc.n_tiles) {
-        pv0 = page_id(p, pc.lead, t + kT);
-        pv1 = page_id(p, pc.lead, t + kT + 64);
-      }
-      if constexpr (kFp8) {
-        load_raw<kOne>(cx, pr, smem, tm_v, p.v_scales, true, r0, r1, nb, rpb);
-      } else {
-        load_slot<kOne>(cx, pr, smem, full0, tm_v, true, r0, r1, nb, rpb);
-      }
-    }
+    if constexpr (kFp8)
+      load_raw<kOne>(cx, pr, smem, map, scales, v_side, r0, r1, nb, rpb);
+    else
+      load_slot<kOne>(cx, pr, smem, full0, map, v_side, r0, r1, nb, rpb);
+    if (!v_side && j > 0) pr.ring.next();  // V of tile j - 1
   }
+  if (!v_side) pr.ring.next();  // V of the last tile
 }
 
 template <bool kFp8>
 __device__ void produce(const Ctx& cx, const Piece& pc, Producer<kFp8>& pr,
-                        uint8_t* smem, const CUtensorMap* tm_k,
-                        const CUtensorMap* tm_v) {
+                        uint8_t* smem, const CUtensorMap* map, bool v_side) {
   const uint32_t base = tc::smem_u32(smem);
   if (cx.p->a.box_rows == 64) {
     if ((threadIdx.x & 31) == 0)
-      produce_piece<kFp8, true>(cx, pc, pr, base, tm_k, tm_v);
+      produce_piece<kFp8, true>(cx, pc, pr, base, map, v_side);
   } else {
-    produce_piece<kFp8, false>(cx, pc, pr, base, tm_k, tm_v);
+    produce_piece<kFp8, false>(cx, pc, pr, base, map, v_side);
   }
 }
 
@@ -745,11 +745,6 @@ __global__ void __cluster_dims__(2, 1, 1)
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // the tails' kernel may be scheduled now; it waits for this grid
-  tc_grid_launch_dependents();
-  tc_grid_dependency_wait();  // the plan is written by the kernel before
-  const int pieces = p.plan[p.groups].piece0;
-  if ((int)(blockIdx.x >> 1) >= pieces) return;  // both CTAs of the pair
   const uint32_t rank = tc::cluster_rank();
 
   if (tid == 0) {
@@ -780,6 +775,12 @@ __global__ void __cluster_dims__(2, 1, 1)
   tc::cluster_sync();  // both CTAs' barriers and tensor memory are ready
   tc::fence_after();
   const uint32_t tmem = s_tmem;
+  // The set-up ran beside the plan kernel, which writes what is read from
+  // here on.  The tails' kernel is released only now: what follows it may then
+  // take the plan as written.
+  tc_grid_dependency_wait();
+  tc_grid_launch_dependents();
+  const int pieces = p.plan[p.groups].piece0;
   const Ctx cx{&bars, &s_abort,
                tc::map_to(tc::smem_u32(&s_abort), rank ^ 1u), rank, &p};
 
@@ -791,8 +792,10 @@ __global__ void __cluster_dims__(2, 1, 1)
   Piece prev{};
   for (int i = blockIdx.x >> 1; i < pieces; i += gridDim.x >> 1) {
     const Piece pc = decode_piece(p, i, rank);
-    if (warp == 0) {
-      if (pr.live) produce<kFp8>(cx, pc, pr, smem, &tm_k, &tm_v);
+    if (warp == 0 || warp == C::kWarpV) {
+      const bool v_side = warp != 0;
+      if (pr.live)
+        produce<kFp8>(cx, pc, pr, smem, v_side ? &tm_v : &tm_k, v_side);
       __syncwarp();
     } else if (warp == 1) {
       if (rank == 0 && lane == 0)

@@ -32,6 +32,8 @@ __global__ void __launch_bounds__(kPlanThreads)
   __shared__ int s_bad;
   const int tid = threadIdx.x, G = p.groups;
   const AttnParams& a = p.a;
+  // the prefix kernel may set itself up now; it waits for this grid
+  tc_grid_launch_dependents();
   if (tid == 0) {
     s_bad = 0;
     s_work = 0;
@@ -167,8 +169,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   const AttnParams& a = p.a;
   // a following attention call's split kernel may be scheduled now
   tc_grid_launch_dependents();
-  // The plan kernel is complete before any kernel after it starts (it does
-  // not release its dependents early), so its results may be read already.
+  // The prefix kernel releases its dependents only after the plan kernel is
+  // complete, so the plan may be read already.
   plan_prefix(a, s_pre);
   const int lane = threadIdx.x & 31;
   const long long w = (long long)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);

@@ -176,6 +176,11 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def _at(t: Optional[torch.Tensor]):
+    """Address of a tensor as ctypes takes it for a void pointer."""
+    return None if t is None else t.data_ptr()
+
+
 def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
         stream = torch.cuda.current_stream()
@@ -186,27 +191,33 @@ def _expect(t: torch.Tensor, dtype, what: str, shape=None,
             contiguous: bool = False) -> None:
     """Refuse a tensor of another type, shape or layout before its address
     is taken."""
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise SpecError(SPEC_ERR_ARG, f"{what} must be {dtype}, is {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise SpecError(SPEC_ERR_ARG, f"{what} must be {tuple(shape)}, is "
                                       f"{tuple(t.shape)}")
     if contiguous and not t.is_contiguous():
         raise SpecError(SPEC_ERR_ARG, f"{what} must be contiguous")
 
 
-def _on_current_device(*tensors) -> None:
-    """Every tensor lies on the current CUDA device: the library takes plain
-    addresses and launches there."""
+def _on_current_device(tensors, stream) -> int:
+    """Check that every tensor (None: absent) and the stream belong to the
+    current CUDA device, where the library launches on plain addresses; the
+    stream's handle (None: the current stream)."""
     for t in tensors:
         if t is not None and not t.is_cuda:
             raise SpecError(SPEC_ERR_ARG, "tensors must be on a CUDA device")
     now = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and t.device.index != now:
+        if t is not None and t.get_device() != now:
             raise SpecError(SPEC_ERR_ARG,
-                            f"a tensor on cuda:{t.device.index} in a call on "
+                            f"a tensor on cuda:{t.get_device()} in a call on "
                             f"cuda:{now}, the current device")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(now)
+    if stream.device_index != now:
+        raise SpecError(SPEC_ERR_ARG, "the stream is another device's")
+    return stream.cuda_stream
 
 
 def _expect_pools(k_pages, v_pages, k_scales, v_scales, hkv: int,
@@ -337,9 +348,9 @@ def verify_attention_shared(q, k_pages, v_pages, page_table, seq_lens,
     if out is None:
         out = torch.empty_like(q)
     _expect(out, torch.bfloat16, "out", q.shape, True)
-    _on_current_device(q, k_pages, v_pages, k_scales, v_scales, page_table,
-                       seq_lens, group_starts, shared_lens, q_lens, out,
-                       workspace)
+    on = _on_current_device((q, k_pages, v_pages, k_scales, v_scales,
+                             page_table, seq_lens, group_starts, shared_lens,
+                             q_lens, out, workspace), stream)
     desc = AttnDesc(B, q_len, hq, k_pages.shape[1], d, k_pages.shape[2],
                     k_pages.shape[0], page_table.shape[1],
                     SPEC_KV_FP8_E4M3 if fp8 else SPEC_KV_BF16,
@@ -348,11 +359,13 @@ def verify_attention_shared(q, k_pages, v_pages, page_table, seq_lens,
     if workspace is None:
         workspace = alloc_workspace(shared_workspace_size(desc, groups),
                                     q.device)
-    _check(load().spec_verify_attention_shared(
-        ctypes.byref(desc), _ptr(q), _ptr(k_pages), _ptr(v_pages),
-        _ptr(k_scales), _ptr(v_scales), _ptr(page_table), _ptr(seq_lens),
-        groups, _ptr(group_starts), _ptr(shared_lens), float(scale),
-        _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream)))
+    rc = load().spec_verify_attention_shared(
+        ctypes.byref(desc), _at(q), _at(k_pages), _at(v_pages), _at(k_scales),
+        _at(v_scales), _at(page_table), _at(seq_lens), groups,
+        _at(group_starts), _at(shared_lens), scale, _at(out), _at(workspace),
+        workspace.numel(), on)
+    if rc:
+        _check(rc)
     return out
 
 
@@ -396,11 +409,12 @@ def kv_append(k_new, v_new, k_pages, v_pages, page_table, seq_lens, *,
 def _strides(t: torch.Tensor, what: str):
     """(request, token) strides of [B, q_len, H, 256] whose heads and channels
     are contiguous."""
-    if t.stride(3) != 1 or (t.shape[2] > 1 and t.stride(2) != t.shape[3]):
+    B, q_len, heads, d = t.shape
+    request, token, head, channel = t.stride()
+    if channel != 1 or (heads > 1 and head != d):
         raise SpecError(SPEC_ERR_ARG,
                         f"{what}: heads and channels must be contiguous")
-    return (t.stride(0) if t.shape[0] > 1 else 0,
-            t.stride(1) if t.shape[1] > 1 else 0)
+    return request if B > 1 else 0, token if q_len > 1 else 0
 
 
 def rope_append(q, k_new, v_new, freq, k_pages, v_pages, page_table, seq_lens,
@@ -434,24 +448,24 @@ def rope_append(q, k_new, v_new, freq, k_pages, v_pages, page_table, seq_lens,
                 contiguous=True)
     fp8 = _expect_pools(k_pages, v_pages, k_scales, v_scales, hkv, d)
     _expect_optional(B, q_len, q_lens, positions, cache_loc)
-    _on_current_device(q, k_new, v_new, freq, q_out, k_pages, v_pages,
-                       k_scales, v_scales, page_table, seq_lens, q_lens,
-                       positions, cache_loc, workspace)
-    i64x2 = ctypes.c_int64 * 2
+    on = _on_current_device((q, k_new, v_new, freq, q_out, k_pages, v_pages,
+                             k_scales, v_scales, page_table, seq_lens, q_lens,
+                             positions, cache_loc, workspace), stream)
     desc = RopeDesc(B, q_len, hq, hkv, d, k_pages.shape[2], k_pages.shape[0],
                     page_table.shape[1],
                     SPEC_KV_FP8_E4M3 if fp8 else SPEC_KV_BF16,
                     SPEC_FLAG_CHECKED if checked else 0,
                     None if q_lens is None else q_lens.data_ptr(),
                     2 * freq.shape[0], 1 if interleaved else 0, attn_factor,
-                    i64x2(*(_strides(q, "q") if q is not None else (0, 0))),
-                    i64x2(*_strides(k_new, "k_new")),
-                    i64x2(*_strides(v_new, "v_new")))
-    _check(load().spec_rope_append(
-        ctypes.byref(desc), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(freq),
-        _ptr(q_out) if q is not None else None, _ptr(k_pages), _ptr(v_pages),
-        _ptr(k_scales), _ptr(v_scales), _ptr(page_table), _ptr(seq_lens),
-        _ptr(positions), _ptr(cache_loc), _ptr(workspace), _stream(stream)))
+                    _strides(q, "q") if q is not None else (0, 0),
+                    _strides(k_new, "k_new"), _strides(v_new, "v_new"))
+    rc = load().spec_rope_append(
+        ctypes.byref(desc), _at(q), _at(k_new), _at(v_new), _at(freq),
+        _at(q_out) if q is not None else None, _at(k_pages), _at(v_pages),
+        _at(k_scales), _at(v_scales), _at(page_table), _at(seq_lens),
+        _at(positions), _at(cache_loc), _at(workspace), on)
+    if rc:
+        _check(rc)
     return q_out
 
 
@@ -618,8 +632,8 @@ def sample(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None,
     for t, what in ((probs, "probs"), (filtered, "filtered")):
         if t is not None:
             _expect(t, torch.float32, what, logits.shape, True)
-    _on_current_device(logits, u, temperature, top_k, top_p, min_p, probs,
-                       filtered, token)
+    on = _on_current_device((logits, u, temperature, top_k, top_p, min_p,
+                             probs, filtered, token), stream)
     if logits.dim() == 2 and rows > 1 and logits.stride(1) == 1:
         stride = logits.stride(0)
     elif logits.is_contiguous():
@@ -633,10 +647,12 @@ def sample(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None,
         raise SpecError(SPEC_ERR_ARG, "logits rows overlap")
     desc = SampleDesc(rows, vocab, int(logits.dtype == torch.bfloat16),
                       stride)
-    _check(load().spec_sample(
-        ctypes.byref(desc), _ptr(logits), _ptr(temperature), _ptr(top_k),
-        _ptr(top_p), _ptr(min_p), _ptr(u), _ptr(token), _ptr(probs),
-        _ptr(filtered), _stream(stream)))
+    rc = load().spec_sample(
+        ctypes.byref(desc), _at(logits), _at(temperature), _at(top_k),
+        _at(top_p), _at(min_p), _at(u), _at(token), _at(probs), _at(filtered),
+        on)
+    if rc:
+        _check(rc)
     return token
 
 

@@ -87,9 +87,13 @@ __device__ __forceinline__ void store_float(float* p, float x) { *p = x; }
 __device__ __forceinline__ void store_float(__nv_bfloat16* p, float x) {
   *p = __float2bfloat16_rn(x);
 }
-// NaN counts as -inf, +inf as the largest finite value, -0 as +0.
-__device__ __forceinline__ float clean(float x) {
-  return x == x ? fminf(x, kMaxFinite) + 0.f : -INFINITY;
+// NaN counts as -inf, +inf as the type's largest finite value, -0 as +0.
+__device__ __forceinline__ float largest(float) { return kMaxFinite; }
+__device__ __forceinline__ float largest(__nv_bfloat16) {
+  return 3.3895313892515355e+38f;
+}
+__device__ __forceinline__ float clean(float x, float most) {
+  return x == x ? fminf(x, most) + 0.f : -INFINITY;
 }
 __device__ __forceinline__ uint32_t key_of(float x) {
   const uint32_t b = __float_as_uint(x);
@@ -152,80 +156,131 @@ __device__ __forceinline__ u64 ceil_part(float f, u64 W) {
   return c ? c : 1;
 }
 
-// round(2^43 2^-y), y = (M - x) log2(e) / T, to about 2^-46 of the largest
-// weight.  The difference and the product are carried as two floats; with
-// y = n + j/32 + r, |r| <= 1/64, the factor 2^-r = e^t, t = -r ln 2, is
-// 1 + t + t^2/2 in two floats and t^3 (1/6 + t/24 + t^2/120) in one (the next
-// term is below 2^-48), times the table's 2^-(j/32), as an integer multiple
-// of 2^-50 that is shifted by n.  Weights below 2^-28 take exp2 itself: its
-// relative error of 2^-22 is below the integers' step there.
-__device__ __forceinline__ u64 near_weight(const Row& r, float x, float dh,
-                                           float yh, const Table* tab);
+// Packed fp32 steps, spelled out so that none is fused with another.
+__device__ __forceinline__ u64 bits2(float2 v) {
+  return (u64)__float_as_uint(v.y) << 32 | __float_as_uint(v.x);
+}
+__device__ __forceinline__ float2 float2_of(u64 v) {
+  return make_float2(__uint_as_float((uint32_t)v),
+                     __uint_as_float((uint32_t)(v >> 32)));
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  u64 d;
+  asm("add.rn.ftz.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)));
+  return float2_of(d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  u64 d;
+  asm("mul.rn.ftz.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)));
+  return float2_of(d);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  u64 d;
+  asm("fma.rn.ftz.f32x2 %0, %1, %2, %3;"
+      : "=l"(d)
+      : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+  return float2_of(d);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 neg(float2 v) {
+  return make_float2(-v.x, -v.y);
+}
 
+// round(2^43 2^-y), y = (M - x) log2(e) / T, to about 2^-46 of the largest
+// weight, of two tokens at once in packed fp32.  The difference and the product
+// are carried as two floats; with y = n + j/32 + r, |r| <= 1/64, the factor
+// 2^-r = e^t, t = -r ln 2, is 1 + t + t^2/2 in two floats and
+// t^3 (1/6 + t/24 + t^2/120) in one, with the t^2/2 that the low part of t adds
+// to it (the next term is below 2^-48), times the table's 2^-(j/32), as an
+// integer multiple of 2^-50 that is shifted by n.
+__device__ __forceinline__ void near_weights(const Row& r, float2 x, float2 dh,
+                                             float2 yh, const Table* tab,
+                                             u64& w0, u64& w1) {
+  const float2 m = both(r.m), kh = both(r.kh);
+  const float2 b = add2(dh, neg(m));
+  const float2 dl = add2(add2(m, neg(add2(dh, neg(b)))),
+                               neg(add2(x, b)));
+  float2 yl = fma2(dh, kh, neg(yh));
+  yl = fma2(dh, both(r.kl), yl);
+  yl = fma2(dl, kh, yl);
+  constexpr float kMagic = 12582912.f;
+  const float2 magic = both(kMagic);
+  // beyond 28: any value that keeps the steps finite
+  const float2 yc = make_float2(fminf(yh.x, 29.f), fminf(yh.y, 29.f));
+  const float2 nt = fma2(yc, both(32.f), magic);
+  const float2 rh =
+      fma2(add2(nt, neg(magic)), both(-0.03125f), yc);
+  constexpr float kLn2H = 0.693147182464599609375f;
+  constexpr float kLn2L = -1.904654299957767e-09f;
+  const float2 l2h = both(-kLn2H), l2l = both(-kLn2L);
+  const float2 th = mul2(rh, l2h);
+  float2 tl = fma2(rh, l2h, neg(th));
+  tl = fma2(rh, l2l, tl);
+  tl = fma2(yl, l2h, tl);
+  const float2 hh = mul2(both(0.5f), th);
+  const float2 sh = mul2(th, hh);
+  float2 sl = fma2(th, hh, neg(sh));
+  sl = fma2(th, tl, sl);
+  float2 c = fma2(th, both(8.333333768e-3f), both(4.166666791e-2f));
+  c = fma2(th, c, both(1.666666716e-1f));
+  const float2 cube = fma2(sh, tl, mul2(mul2(c, th), add2(sh, sh)));
+  const float2 qh = add2(th, sh);
+  const float2 ql = add2(add2(add2(th, neg(qh)), sh),
+                               add2(add2(tl, sl), cube));
+  const int n0 = __float_as_int(nt.x) - 0x4B400000;
+  const int n1 = __float_as_int(nt.y) - 0x4B400000;
+  const Table t0 = tab[n0 & 31], t1 = tab[n1 & 31];
+  const float2 hi = make_float2(t0.hi, t1.hi), lo = make_float2(t0.lo, t1.lo);
+  const float2 g = mul2(hi, qh);
+  float2 gl = fma2(hi, qh, neg(g));
+  gl = fma2(hi, ql, gl);
+  gl = fma2(lo, qh, gl);
+  const float2 i1t = fma2(g, both(67108864.f), magic);
+  const float2 rem = add2(
+      fma2(add2(i1t, neg(magic)),
+                 both(-1.490116119384765625e-08f), g), gl);
+  const float2 i2 = mul2(rem, both(1125899906842624.f));
+  const long long e0 = (long long)t0.fix +
+                       ((long long)(__float_as_int(i1t.x) - 0x4B400000) << 24) +
+                       __float2int_rn(i2.x);
+  const long long e1 = (long long)t1.fix +
+                       ((long long)(__float_as_int(i1t.y) - 0x4B400000) << 24) +
+                       __float2int_rn(i2.y);
+  const int s0 = n0 >> 5, s1 = n1 >> 5;
+  w0 = (u64)(e0 + (64ll << s0)) >> (7 + s0);
+  w1 = (u64)(e1 + (64ll << s1)) >> (7 + s1);
+}
+
+// Weights below 2^-28 take exp2 itself: its relative error of 2^-22 is below
+// the integers' step there.
 __device__ __forceinline__ u64 far_weight(float yh) {
   return yh > 45.f ? 0ull : (u64)__float2uint_rn(exp2f(__fsub_rn(43.f, yh)));
 }
+
+// One token; the same steps, so the same bits.
 __device__ __forceinline__ u64 weight_of(const Row& r, float x,
                                          const Table* tab) {
   const float dh = __fsub_rn(r.m, x);
   const float yh = __fmul_rn(dh, r.kh);
-  return yh > 28.f ? far_weight(yh) : near_weight(r, x, dh, yh, tab);
-}
-// The same with one branch for the whole warp, which must be converged.
-__device__ __forceinline__ u64 warp_weight(const Row& r, float x,
-                                           const Table* tab) {
-  const float dh = __fsub_rn(r.m, x);
-  const float yh = __fmul_rn(dh, r.kh);
-  u64 w = far_weight(yh);
-  if (__any_sync(0xffffffffu, yh <= 28.f)) {
-    const u64 v = near_weight(r, x, dh, fminf(yh, 29.f), tab);
-    w = yh > 28.f ? w : v;
-  }
-  return w;
+  if (yh > 28.f) return far_weight(yh);
+  u64 w0, w1;
+  near_weights(r, both(x), both(dh), both(yh), tab, w0, w1);
+  return w0;
 }
 
-__device__ __forceinline__ u64 near_weight(const Row& r, float x, float dh,
-                                           float yh, const Table* tab) {
-  const float b = __fsub_rn(dh, r.m);
-  const float dl = __fsub_rn(__fsub_rn(r.m, __fsub_rn(dh, b)), __fadd_rn(x, b));
-  float yl = __fmaf_rn(dh, r.kh, -yh);
-  yl = __fmaf_rn(dh, r.kl, yl);
-  yl = __fmaf_rn(dl, r.kh, yl);
-  constexpr float kMagic = 12582912.f;  // 1.5 * 2^23
-  const float nt = __fmaf_rn(yh, 32.f, kMagic);
-  const int ni = __float_as_int(nt) - 0x4B400000;
-  const float rh = __fmaf_rn(__fsub_rn(nt, kMagic), -0.03125f, yh);
-  constexpr float kLn2H = 0.693147182464599609375f;      // ln 2 in fp32
-  constexpr float kLn2L = -1.904654299957767e-09f;       // and the rest
-  const float th = __fmul_rn(rh, -kLn2H);
-  float tl = __fmaf_rn(rh, -kLn2H, -th);
-  tl = __fmaf_rn(rh, -kLn2L, tl);
-  tl = __fmaf_rn(yl, -kLn2H, tl);
-  const float hh = __fmul_rn(0.5f, th);
-  const float sh = __fmul_rn(th, hh);
-  float sl = __fmaf_rn(th, hh, -sh);
-  sl = __fmaf_rn(th, tl, sl);
-  float c = __fmaf_rn(th, 8.333333768e-3f, 4.166666791e-2f);
-  c = __fmaf_rn(th, c, 1.666666716e-1f);
-  const float cube = __fmul_rn(__fmul_rn(c, th), __fadd_rn(sh, sh));
-  const float qh = __fadd_rn(th, sh);
-  const float ql = __fadd_rn(__fadd_rn(__fsub_rn(th, qh), sh),
-                             __fadd_rn(__fadd_rn(tl, sl), cube));
-  const Table t = tab[ni & 31];
-  const float g = __fmul_rn(t.hi, qh);
-  float gl = __fmaf_rn(t.hi, qh, -g);
-  gl = __fmaf_rn(t.hi, ql, gl);
-  gl = __fmaf_rn(t.lo, qh, gl);
-  const float i1t = __fmaf_rn(g, 67108864.f, kMagic);  // 2^26
-  const int i1 = __float_as_int(i1t) - 0x4B400000;
-  const float rem = __fadd_rn(
-      __fmaf_rn(__fsub_rn(i1t, kMagic), -1.490116119384765625e-08f, g), gl);
-  const int i2 = __float2int_rn(__fmul_rn(rem, 1125899906842624.f));  // 2^50
-  const long long e =
-      (long long)t.fix + ((long long)i1 << 24) + (long long)i2;
-  const int n = ni >> 5;
-  // y may round to just below zero steps; the largest token has y = 0
-  return (u64)(e + (64ll << n)) >> (7 + n);
+// Two tokens, with one branch for the whole warp, which must be converged.
+__device__ __forceinline__ void warp_weights(const Row& r, float2 x,
+                                             const Table* tab, u64& w0,
+                                             u64& w1) {
+  const float2 dh = add2(both(r.m), neg(x));
+  const float2 yh = mul2(dh, both(r.kh));
+  w0 = w1 = 0;
+  if (__any_sync(0xffffffffu, fminf(yh.x, yh.y) <= 28.f))
+    near_weights(r, x, dh, yh, tab, w0, w1);
+  if (__any_sync(0xffffffffu, fmaxf(yh.x, yh.y) > 28.f)) {
+    if (yh.x > 28.f) w0 = far_weight(yh.x);
+    if (yh.y > 28.f) w1 = far_weight(yh.y);
+  }
 }
 
 // The probability's numerator, 2^-y in fp32 (relative error 2^-22 for the
@@ -404,7 +459,30 @@ __device__ __forceinline__ void sort_entries(u64* list, int n) {
   for (int e = 0; e < kE; ++e) list[tid + kThreads * e] = v[e];
   __syncthreads();
 }
-__device__ __forceinline__ void sort_list(u64* list, int n) {
+// Short lists: an entry's place is the number of smaller ones (entries are
+// distinct), counted by two threads for half of the list each.
+__device__ __forceinline__ void rank_entries(Shared& s, int n) {
+  const int tid = threadIdx.x, i = tid & 255, half = (n + 1) / 2;
+  const u64 v = i < n ? s.list[i] : 0;
+  const int j0 = tid < 256 ? 0 : half, j1 = tid < 256 ? half : n;
+  int at = 0;
+  if (i < n) {
+#pragma unroll 8
+    for (int j = j0; j < j1; ++j) at += s.list[j] < v;
+    if (tid >= 256) s.hist_c[i] = at;
+  }
+  __syncthreads();
+  if (tid < 256 && i < n) s.list[at + s.hist_c[i]] = v;
+  __syncthreads();
+  s.hist_c[tid] = 0;
+  __syncthreads();
+}
+__device__ __forceinline__ void sort_list(Shared& s, int n) {
+  u64* list = s.list;
+  if (n <= 256) {
+    rank_entries(s, n);
+    return;
+  }
   if (n <= kThreads)
     sort_entries<1>(list, n);
   else
@@ -427,6 +505,20 @@ __device__ __forceinline__ int gather_lists(Shared& s, int csize) {
       s.list[at + i] = peer_load64(&s.list[i], warp);
   __syncthreads();
   return (int)total;
+}
+
+// The last kept token, as a value and an id in this CTA's chunk.
+struct Border {
+  float x;
+  int i;
+  __device__ __forceinline__ bool holds(float v, int id) const {
+    return v > x || (v == x && id <= i);
+  }
+};
+__device__ __forceinline__ Border border_of(u64 cut, uint32_t mkey, int base) {
+  if (cut == ~0ull) return {-INFINITY, -1};  // every finite value
+  return {value_of(mkey - (uint32_t)(cut >> kIdBits)),
+          (int)(cut & ((1u << kIdBits) - 1)) - base};
 }
 
 // The draw's target among W: floor(u W), below W.
@@ -485,22 +577,27 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncthreads();
 
   // the largest logit with its lowest id, and the smallest finite one
-  u64 best = 0;
-  uint32_t low = 0xffffffffu;
+  const float most = largest(T());
+  float top = -INFINITY, least = INFINITY;
+  int top_i = tid;
   for (int i0 = tid; i0 < p.padded; i0 += kBatch * kThreads) {
     float x[kBatch];
 #pragma unroll
-    for (int e = 0; e < kBatch; ++e) x[e] = clean(as_float(xs[i0 + e * kThreads]));
+    for (int e = 0; e < kBatch; ++e)
+      x[e] = clean(as_float(xs[i0 + e * kThreads]), most);
 #pragma unroll
     for (int e = 0; e < kBatch; ++e) {
       const int i = i0 + e * kThreads;
       store_float(xs + i, x[e]);  // later passes read clean values
-      const uint32_t key = key_of(x[e]);
-      const u64 v = (u64)key << 32 | (uint32_t)~(uint32_t)(base + i);
-      best = v > best ? v : best;
-      low = x[e] > -INFINITY ? min(low, key) : low;
+      if (x[e] > top) {           // the first of equals
+        top = x[e];
+        top_i = i;
+      }
+      least = fminf(least, x[e] > -INFINITY ? x[e] : INFINITY);
     }
   }
+  u64 best = (u64)key_of(top) << 32 | (uint32_t)~(uint32_t)(base + top_i);
+  uint32_t low = least < INFINITY ? key_of(least) : 0xffffffffu;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const u64 v = __shfl_xor_sync(0xffffffffu, best, o);
@@ -596,7 +693,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
             for (int e = 0; e < kB; ++e) x[e] = as_float(xs[i0 + e * kThreads]);
 #pragma unroll
-            for (int e = 0; e < kB; ++e) w[e] = warp_weight(r, x[e], s.tab);
+            for (int e = 0; e < kB; e += 2)
+            warp_weights(r, make_float2(x[e], x[e + 1]), s.tab, w[e], w[e + 1]);
 #pragma unroll
             for (int e = 0; e < kB; ++e) {
               if (!(x[e] > -INFINITY) ||
@@ -655,15 +753,18 @@ __global__ void __launch_bounds__(kThreads, 2)
           // gather: all up to the bin's end, or the bin
           if (round == 0) {
             // what lies up to the bin's upper edge is looked at more closely
-            const float edge = b < kBins - 1 ? (float)(b + 1) : INFINITY;
+            // (its edge a little lower: the bins are decided by rounded steps)
+            const float reach = __fdiv_rn((float)(b + 1), step);
+            const float edge = b < kBins - 1 && step > 0.f
+                                   ? __fsub_rn(r.m, __fmul_rn(reach, 1.001f))
+                                   : -kMaxFinite;
             for (int i0 = tid; i0 < p.padded; i0 += kBatch * kThreads) {
               float x[kBatch];
               bool any = false;
 #pragma unroll
               for (int e = 0; e < kBatch; ++e) {
                 x[e] = as_float(xs[i0 + e * kThreads]);
-                any |= x[e] > -INFINITY &&
-                       !(__fmul_rn(__fsub_rn(r.m, x[e]), step) >= edge);
+                any |= x[e] >= edge;
               }
               if (!any) continue;
 #pragma unroll
@@ -690,7 +791,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           tc::cluster_sync();
           if (rank == 0) {
             const int m = gather_lists(s, csize);
-            sort_list(s.list, m);
+            sort_list(s, m);
             // ranks kPerThread tid ..: weights and their sums in rank order
             const int r0 = tid * kPerThread;
             u64 w[kPerThread], sum = 0;
@@ -752,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 s.list[q] = (s.list[q] & ((1ull << kIdBits) - 1)) << 32 |
                             (uint32_t)q;
               __syncthreads();
-              sort_list(s.list, (int)nk);
+              sort_list(s, (int)nk);
               const u64 t = target_of(u, all);
               sum = 0;
 #pragma unroll
@@ -811,6 +912,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 
     if (!done) {
       // 3. kept mass, each warp a run of ids
+      const Border edge = border_of(cut, mkey, base);
+      auto kept = [&](float x, int i) { return edge.holds(x, i); };
       const int run_len = p.padded / kWarps;
       u64 m = 0;
       for (int i0 = warp * run_len + lane; i0 < (warp + 1) * run_len;
@@ -819,11 +922,13 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] = as_float(xs[i0 + 32 * e]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const bool in = place(x[e], i0 + 32 * e) <= cut;
-          if (!__any_sync(0xffffffffu, in)) continue;
-          const u64 w = warp_weight(r, x[e], s.tab);
-          m += in && w >= minw ? w : 0;
+        for (int e = 0; e < 4; e += 2) {
+          const bool in0 = kept(x[e], i0 + 32 * e);
+          const bool in1 = kept(x[e + 1], i0 + 32 * (e + 1));
+          if (!__any_sync(0xffffffffu, in0 || in1)) continue;
+          u64 w0, w1;
+          warp_weights(r, make_float2(x[e], x[e + 1]), s.tab, w0, w1);
+          m += (in0 && w0 >= minw ? w0 : 0) + (in1 && w1 >= minw ? w1 : 0);
         }
       }
 #pragma unroll
@@ -858,7 +963,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           w[e] = 0;
           if (e < per && i0 + e < i1) {
             const float x = as_float(xs[i0 + e]);
-            if (place(x, i0 + e) <= cut) w[e] = weight_of(r, x, s.tab);
+            if (kept(x, i0 + e)) w[e] = weight_of(r, x, s.tab);
             if (w[e] < minw) w[e] = 0;
           }
           sum += w[e];
@@ -881,24 +986,26 @@ __global__ void __launch_bounds__(kThreads, 2)
     const float inv =
         total ? __fdiv_rn(8796093022208.f, __ull2float_rn(total)) : 0.f;
     const long long out = (long long)row * p.vocab + base;
-#pragma unroll 2
-    for (int i = tid; i < n; i += kThreads) {
-      const float x = as_float(xs[i]);
-      bool keep = false;
-      float pr = 0.f;
-      if (none) {
-      } else if (one) {
-        keep = base + i == arg;
-        pr = keep ? 1.f : 0.f;
-      } else {
-        const u64 c = (u64)(mkey - key_of(x)) << kIdBits | (uint32_t)(base + i);
-        keep = x > -INFINITY && c <= cut;
-        // beside a cut that already holds it, min-p decides only here
-        if (keep && minw) keep = weight_of(r, x, s.tab) >= minw;
-        if (keep) pr = fast_weight(r, x) * inv;
+    const Border edge = one ? Border{kMaxFinite, -1} : border_of(cut, mkey, base);
+    for (int i0 = tid; i0 < n; i0 += 4 * kThreads) {
+      float x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = i0 + e * kThreads;
+        x[e] = i < p.padded ? as_float(xs[i]) : -INFINITY;
       }
-      if (p.probs) p.probs[out + i] = pr;
-      if (p.filtered) p.filtered[out + i] = keep ? x : -INFINITY;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = i0 + e * kThreads;
+        if (i >= n) continue;
+        bool keep = !none && (one ? base + i == arg : edge.holds(x[e], i));
+        float pr = one && keep ? 1.f : 0.f;
+        // beside a cut that already holds it, min-p decides only here
+        if (keep && minw) keep = weight_of(r, x[e], s.tab) >= minw;
+        if (keep && !one) pr = fast_weight(r, x[e]) * inv;
+        if (p.probs) __stcs(p.probs + out + i, pr);
+        if (p.filtered) __stcs(p.filtered + out + i, keep ? x[e] : -INFINITY);
+      }
     }
   }
   tc::cluster_sync();  // no CTA leaves while others read its shared memory

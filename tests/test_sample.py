@@ -247,6 +247,15 @@ def test_idle_empty_and_special_rows():
     assert tok[7] in (3, 8) and probs[7][3] == probs[7][8] == 0.5
     assert tok[8] == V - 1
     assert check(x, t, None, None, None, u, (tok, probs, filt)) <= 2
+    # bf16: +inf is the largest finite bf16
+    xb = torch.zeros((2, 3000), dtype=torch.bfloat16, device=DEV)
+    xb[0, [7, 2000]] = float("inf")
+    xb[1, 5], xb[1, 6] = float("nan"), -float("inf")
+    tok, probs, filt = run(xb, None, None, None, None, [0.9, 0.0])
+    assert tok.tolist() == [2000, 0]
+    assert probs[0][7] == probs[0][2000] == 0.5
+    assert filt[0][7] == torch.finfo(torch.bfloat16).max
+    assert probs[1][5] == probs[1][6] == 0 and np.isneginf(filt[1][[5, 6]]).all()
 
 
 @gpu

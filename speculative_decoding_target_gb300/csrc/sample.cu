@@ -105,9 +105,11 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 
 // ---- weights ----------------------------------------------------------------
 // 2^-(j/32) for j < 32: as an integer multiple of 2^-50 and as two floats.
+// One 32-bit word of every entry after the other, so that lanes with different
+// j read different banks (16-byte entries took about 12 wavefronts a load).
 struct Table {
-  u64 fix;
-  float hi, lo;
+  uint32_t fix_lo[32], fix_hi[32];
+  float hi[32], lo[32];
 };
 __constant__ u64 kPowers[32] = {  // round(2^(50 - j/32))
     0x4000000000000ull, 0x3ea0ecb6dc8a8ull, 0x3d495f454921bull, 0x3bf92e66f736cull,
@@ -119,15 +121,16 @@ __constant__ u64 kPowers[32] = {  // round(2^(50 - j/32))
     0x260dfc14636e3ull, 0x253d3bea3fbdcull, 0x2470f4dceac47ull, 0x23a90e62d1735ull,
     0x22e57078faa2full, 0x222603a024b6aull, 0x216ab0d9f3122ull, 0x20b361a62b0afull,
 };
-__device__ __forceinline__ Table table_entry(int j) {
-  Table t;
-  t.fix = kPowers[j];
-  t.hi = __fmul_rn(__ull2float_rn(t.fix), 8.8817841970012523e-16f);  // 2^-50
-  t.lo = __fmul_rn(
-      __ll2float_rn((long long)t.fix -
-                    __float2ll_rn(__fmul_rn(t.hi, 1125899906842624.f))),
+__device__ __forceinline__ void fill_table(Table& t, int j) {
+  const u64 fix = kPowers[j];
+  const float hi = __fmul_rn(__ull2float_rn(fix), 8.8817841970012523e-16f);
+  t.fix_lo[j] = (uint32_t)fix;
+  t.fix_hi[j] = (uint32_t)(fix >> 32);
+  t.hi[j] = hi;  // times 2^-50
+  t.lo[j] = __fmul_rn(
+      __ll2float_rn((long long)fix -
+                    __float2ll_rn(__fmul_rn(hi, 1125899906842624.f))),
       8.8817841970012523e-16f);
-  return t;
 }
 
 struct Row {
@@ -182,9 +185,6 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return float2_of(d);
 }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
-__device__ __forceinline__ float2 neg(float2 v) {
-  return make_float2(-v.x, -v.y);
-}
 
 // round(2^43 2^-y), y = (M - x) log2(e) / T, to about 2^-46 of the largest
 // weight, of two tokens at once in packed fp32.  The difference and the product
@@ -194,58 +194,60 @@ __device__ __forceinline__ float2 neg(float2 v) {
 // to it (the next term is below 2^-48), times the table's 2^-(j/32), as an
 // integer multiple of 2^-50 that is shifted by n.
 __device__ __forceinline__ void near_weights(const Row& r, float2 x, float2 dh,
-                                             float2 yh, const Table* tab,
+                                             float2 yh, const Table& tab,
                                              u64& w0, u64& w1) {
-  const float2 m = both(r.m), kh = both(r.kh);
-  const float2 b = add2(dh, neg(m));
-  const float2 dl = add2(add2(m, neg(add2(dh, neg(b)))),
-                               neg(add2(x, b)));
-  float2 yl = fma2(dh, kh, neg(yh));
-  yl = fma2(dh, both(r.kl), yl);
-  yl = fma2(dl, kh, yl);
-  constexpr float kMagic = 12582912.f;
-  const float2 magic = both(kMagic);
+  // a - b is fma(b, -1, a): packed operands carry no sign of their own
+  const float2 one = both(-1.f), m = both(r.m), kh = both(r.kh);
+  constexpr float kMagic = 12582912.f;  // 1.5 * 2^23
+  const float2 magic = both(kMagic), unmagic = both(-kMagic);
   // beyond 28: any value that keeps the steps finite
   const float2 yc = make_float2(fminf(yh.x, 29.f), fminf(yh.y, 29.f));
   const float2 nt = fma2(yc, both(32.f), magic);
-  const float2 rh =
-      fma2(add2(nt, neg(magic)), both(-0.03125f), yc);
-  constexpr float kLn2H = 0.693147182464599609375f;
-  constexpr float kLn2L = -1.904654299957767e-09f;
-  const float2 l2h = both(-kLn2H), l2l = both(-kLn2L);
+  // what m - x and its product leave
+  const float2 nb = fma2(dh, one, m);
+  const float2 dl = fma2(fma2(nb, one, x), one, fma2(add2(dh, nb), one, m));
+  float2 yl = fma2(dh, kh, mul2(yh, one));
+  yl = fma2(dh, both(r.kl), yl);
+  yl = fma2(dl, kh, yl);
+  const float2 rh = fma2(add2(nt, unmagic), both(-0.03125f), yc);
+  constexpr float kLn2H = 0.693147182464599609375f;      // ln 2 in fp32
+  constexpr float kLn2L = -1.904654299957767e-09f;       // and the rest
+  const float2 l2h = both(-kLn2H);
   const float2 th = mul2(rh, l2h);
-  float2 tl = fma2(rh, l2h, neg(th));
-  tl = fma2(rh, l2l, tl);
+  float2 tl = fma2(rh, l2h, mul2(th, one));
+  tl = fma2(rh, both(-kLn2L), tl);
   tl = fma2(yl, l2h, tl);
   const float2 hh = mul2(both(0.5f), th);
   const float2 sh = mul2(th, hh);
-  float2 sl = fma2(th, hh, neg(sh));
+  float2 sl = fma2(th, hh, mul2(sh, one));
   sl = fma2(th, tl, sl);
   float2 c = fma2(th, both(8.333333768e-3f), both(4.166666791e-2f));
   c = fma2(th, c, both(1.666666716e-1f));
   const float2 cube = fma2(sh, tl, mul2(mul2(c, th), add2(sh, sh)));
   const float2 qh = add2(th, sh);
-  const float2 ql = add2(add2(add2(th, neg(qh)), sh),
-                               add2(add2(tl, sl), cube));
+  const float2 ql = add2(add2(fma2(qh, one, th), sh),
+                         add2(add2(tl, sl), cube));
   const int n0 = __float_as_int(nt.x) - 0x4B400000;
   const int n1 = __float_as_int(nt.y) - 0x4B400000;
-  const Table t0 = tab[n0 & 31], t1 = tab[n1 & 31];
-  const float2 hi = make_float2(t0.hi, t1.hi), lo = make_float2(t0.lo, t1.lo);
+  const int j0 = n0 & 31, j1 = n1 & 31;
+  const float2 hi = make_float2(tab.hi[j0], tab.hi[j1]);
+  const float2 lo = make_float2(tab.lo[j0], tab.lo[j1]);
   const float2 g = mul2(hi, qh);
-  float2 gl = fma2(hi, qh, neg(g));
+  float2 gl = fma2(hi, qh, mul2(g, one));
   gl = fma2(hi, ql, gl);
   gl = fma2(lo, qh, gl);
-  const float2 i1t = fma2(g, both(67108864.f), magic);
+  const float2 i1t = fma2(g, both(67108864.f), magic);  // 2^26
   const float2 rem = add2(
-      fma2(add2(i1t, neg(magic)),
-                 both(-1.490116119384765625e-08f), g), gl);
-  const float2 i2 = mul2(rem, both(1125899906842624.f));
-  const long long e0 = (long long)t0.fix +
-                       ((long long)(__float_as_int(i1t.x) - 0x4B400000) << 24) +
-                       __float2int_rn(i2.x);
-  const long long e1 = (long long)t1.fix +
-                       ((long long)(__float_as_int(i1t.y) - 0x4B400000) << 24) +
-                       __float2int_rn(i2.y);
+      fma2(add2(i1t, unmagic), both(-1.490116119384765625e-08f), g), gl);
+  const float2 i2 = mul2(rem, both(1125899906842624.f));  // 2^50
+  const long long e0 =
+      (long long)((u64)tab.fix_hi[j0] << 32 | tab.fix_lo[j0]) +
+      ((long long)(__float_as_int(i1t.x) - 0x4B400000) << 24) +
+      __float2int_rn(i2.x);
+  const long long e1 =
+      (long long)((u64)tab.fix_hi[j1] << 32 | tab.fix_lo[j1]) +
+      ((long long)(__float_as_int(i1t.y) - 0x4B400000) << 24) +
+      __float2int_rn(i2.y);
   const int s0 = n0 >> 5, s1 = n1 >> 5;
   w0 = (u64)(e0 + (64ll << s0)) >> (7 + s0);
   w1 = (u64)(e1 + (64ll << s1)) >> (7 + s1);
@@ -259,7 +261,7 @@ __device__ __forceinline__ u64 far_weight(float yh) {
 
 // One token; the same steps, so the same bits.
 __device__ __forceinline__ u64 weight_of(const Row& r, float x,
-                                         const Table* tab) {
+                                         const Table& tab) {
   const float dh = __fsub_rn(r.m, x);
   const float yh = __fmul_rn(dh, r.kh);
   if (yh > 28.f) return far_weight(yh);
@@ -270,9 +272,9 @@ __device__ __forceinline__ u64 weight_of(const Row& r, float x,
 
 // Two tokens, with one branch for the whole warp, which must be converged.
 __device__ __forceinline__ void warp_weights(const Row& r, float2 x,
-                                             const Table* tab, u64& w0,
+                                             const Table& tab, u64& w0,
                                              u64& w1) {
-  const float2 dh = add2(both(r.m), neg(x));
+  const float2 dh = fma2(x, both(-1.f), both(r.m));
   const float2 yh = mul2(dh, both(r.kh));
   w0 = w1 = 0;
   if (__any_sync(0xffffffffu, fminf(yh.x, yh.y) <= 28.f))
@@ -303,7 +305,7 @@ constexpr int kPerThread = kList / kThreads;
 constexpr int kIdBits = 19;      // ids of kSampleMaxVocab tokens
 
 struct Shared {
-  Table tab[32];
+  Table tab;
   uint32_t hist_lo[kBins], hist_hi[kBins];  // a bin's mass
   u64 red_m[kBins];
   uint32_t hist_c[kBins], red_c[kBins];
@@ -567,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (k <= 0 || k >= p.vocab) k = 0;
   // cuts that leave the first token alone
   const bool one = T0 == 0.f || k == 1 || tp <= 0.f || mp > 1.f;
-  if (tid < 32) s.tab[tid] = table_entry(tid);
+  if (tid < 32) fill_table(s.tab, tid);
   for (int i = n + tid; i < p.padded; i += kThreads)
     store_float(xs + i, -INFINITY);
   s.hist_lo[tid] = s.hist_hi[tid] = 0;

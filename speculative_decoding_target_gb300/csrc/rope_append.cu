@@ -123,8 +123,15 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
               r < p.hq ? p.q + b * p.q_req + i * p.q_tok + r * kHeadDim
                        : a.k_new + b * p.k_req + i * p.k_tok +
                              (r - p.hq) * kHeadDim;
-          xa[e] = __ldcs(reinterpret_cast<const uint2*>(src + 4 * qa));
-          xb[e] = __ldcs(reinterpret_cast<const uint2*>(src + 4 * qb));
+          if (kInterleaved) {
+            const uint4 v =
+                __ldcs(reinterpret_cast<const uint4*>(src + 8 * lane));
+            xa[e] = make_uint2(v.x, v.y);
+            xb[e] = make_uint2(v.z, v.w);
+          } else {
+            xa[e] = __ldcs(reinterpret_cast<const uint2*>(src + 4 * qa));
+            xb[e] = __ldcs(reinterpret_cast<const uint2*>(src + 4 * qb));
+          }
         } else {
           const uint4 v = __ldcs(reinterpret_cast<const uint4*>(
               a.v_new + b * p.v_req + i * p.v_tok +
@@ -192,8 +199,13 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
                           (slot + (long long)(r - p.hq) * a.page_size) *
                               kHeadDim
                     : p.q_out + ((long long)tok * p.hq + r) * kHeadDim;
-            *reinterpret_cast<uint2*>(dst + 4 * qa) = xa[e];
-            *reinterpret_cast<uint2*>(dst + 4 * qb) = xb[e];
+            if (kInterleaved) {
+              *reinterpret_cast<uint4*>(dst + 8 * lane) =
+                  make_uint4(xa[e].x, xa[e].y, xb[e].x, xb[e].y);
+            } else {
+              *reinterpret_cast<uint2*>(dst + 4 * qa) = xa[e];
+              *reinterpret_cast<uint2*>(dst + 4 * qb) = xb[e];
+            }
           }
         } else if (slot >= 0) {
           const long long row =

@@ -2,6 +2,7 @@
 // shared parts, and the merge of their partials with those of the requests'
 // own tails.  (The shared parts are attended in prefix_attention.cu, the tails
 // by the ordinary split kernels from kv_begin on.)
+#include <algorithm>
 #include <climits>
 
 #include "shared_prefix.cuh"
@@ -10,7 +11,8 @@
 namespace specv {
 namespace {
 
-constexpr int kPlanThreads = 1024;   // >= kMaxBatch and kMaxGroups
+constexpr int kPlanThreads = 1024;   // at most: kMaxBatch, kMaxGroups
+static_assert(kPlanThreads >= kMaxBatch && kPlanThreads >= kMaxGroups, "");
 
 // One CTA: thread b looks at request b, thread n at group n.  A group's shared
 // part is cut to what every row of every live request sees and to whole tiles
@@ -38,7 +40,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     s_bad = 0;
     s_work = 0;
   }
-  for (int n = tid; n <= G; n += kPlanThreads) s_start[n] = p.starts[n];
+  for (int n = tid; n <= G; n += blockDim.x) s_start[n] = p.starts[n];
   if (tid < G) {
     s_seen[tid] = INT_MAX;
     s_lead[tid] = INT_MAX;
@@ -93,11 +95,11 @@ __global__ void __launch_bounds__(kPlanThreads)
       atomicAdd(&s_work, (unsigned long long)s_rows[tid] * s_kv[tid]);
   }
   __syncthreads();
-  // candidate run lengths, 1.6 down to 0.53 of the even share, one a warp
+  // candidate run lengths, 1.6 down to 0.53 of the even share, a warp each
   const int warp = tid >> 5, lane = tid & 31;
-  {
+  for (int cand = warp; cand < kPlans; cand += blockDim.x >> 5) {
     const float share = (float)s_work / (float)p.pairs;
-    const int run = max(1, (int)ceilf(1.6f * share * __powf(0.965f, warp)));
+    const int run = max(1, (int)ceilf(1.6f * share * __powf(0.965f, cand)));
     int pieces = 0, longest = 0;
     for (int n = lane; n < G; n += 32) {
       if (!s_kv[n]) continue;
@@ -109,9 +111,9 @@ __global__ void __launch_bounds__(kPlanThreads)
     longest = __reduce_max_sync(0xffffffffu, longest);
     if (lane == 0) {
       const long long waves = (pieces + p.pairs - 1) / p.pairs;
-      s_plan[warp] = waves * (longest + kPrefixCost) << 24 |
+      s_plan[cand] = waves * (longest + kPrefixCost) << 24 |
                      min(pieces, (1 << 24) - 1);
-      s_run[warp] = run;
+      s_run[cand] = run;
     }
   }
   __syncthreads();
@@ -125,7 +127,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     gp.splits = (s_kv[tid] + run - 1) / run;
     mine_pieces = s_rows[tid] * gp.splits;
   }
-  if (tid < kMaxGroups) s_pieces[0][tid] = mine_pieces;
+  if (tid < G) s_pieces[0][tid] = mine_pieces;
   __syncthreads();
   int from = 0;
   for (int o = 1; o < G; o <<= 1, from ^= 1) {
@@ -159,10 +161,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 
 // out = sum_s 2^(lse_s - lse) o_s over a row's partials, those of its tail
 // and those of its group's shared part.  One warp per output row, lane l
-// channels 8l .. 8l+7, kBatch partials in flight with a running maximum.
+// channels 8l .. 8l+7, kBatch partials in flight with a running maximum: 20 for
+// few rows, which are cut into many runs (one round of loads instead of three
+// or four), 6 for many, where registers cost residency.
 constexpr int kMergeWarps = 8;
-constexpr int kBatch = 6;
 
+template <int kBatch>
 __global__ void __launch_bounds__(kMergeWarps * 32)
     shared_merge_kernel(const SharedParams p) {
   __shared__ int s_pre[kMaxBatch + 1];
@@ -262,7 +266,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
 }  // namespace
 
 cudaError_t launch_shared_plan(const SharedParams& p, cudaStream_t s) {
-  shared_plan_kernel<<<1, kPlanThreads, 0, s>>>(p);
+  // a thread for every request and group; a small block's barriers are cheaper
+  const int need = (std::max(p.a.batch, p.groups) + 31) / 32 * 32;
+  shared_plan_kernel<<<1, std::max(need, 256), 0, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -272,7 +278,9 @@ cudaError_t launch_shared_merge(const SharedParams& p, cudaStream_t s) {
   const cudaLaunchConfig_t cfg =
       pdl_config(dim3((unsigned)((rows + kMergeWarps - 1) / kMergeWarps)),
                  dim3(kMergeWarps * 32), 0, s, attr);
-  return cudaLaunchKernelEx(&cfg, shared_merge_kernel, p);
+  return rows <= (long long)kMergeWarps * 2 * p.pairs
+             ? cudaLaunchKernelEx(&cfg, shared_merge_kernel<20>, p)
+             : cudaLaunchKernelEx(&cfg, shared_merge_kernel<6>, p);
 }
 
 }  // namespace specv

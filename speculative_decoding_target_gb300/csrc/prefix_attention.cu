@@ -19,19 +19,23 @@
 // cycle); the pair halves that, each CTA loading half the tokens of K and half
 // the channels of V.
 //
-// Warp roles (both CTAs, the issuer in the leader only):
-//   warps 0, V  producers of K and of V: TMA boxes of the CTA's halves, [64 tokens x 128
-//               channels] twice a tile for each of K and V, 128-byte swizzle,
-//               into a ring in the order in which the issuer consumes them:
-//               K0 K1 V0 K2 V1 ...
-//   warp 1      issuer: QK_0, then per tile QK_{j+1}, PV_j, so that the
-//               softmax of tile j has a QK and a PV's time to run in
-//   warps 2..5  softmax: one thread per row; running maximum and sum in base
+// Warp roles (both CTAs):
+//   warps 0, 2  producers of K and of V: TMA boxes of the CTA's halves, [64
+//               tokens x 128 channels] twice a tile for each, 128-byte
+//               swizzle, into a ring in the order in which the issuer consumes
+//               them: K0 K1 V0 K2 V1 ...
+//   warp 1      leader: issuer, QK_0, then per tile QK_{j+1}, PV_j, so that
+//               the softmax of tile j has a QK and a PV's time to run in
+//   warps 1, 3  FP8, the other CTA: relays, see relay_piece
+//   warps 4..7  softmax: one thread per row; running maximum and sum in base
 //               2 and fp32; O is rescaled only when the maximum grows by 2^8;
 //               epilogue (normalised fp32 partial, log-sum-exp)
-//   warps 6..13 FP8 only: E4M3 bytes times scale to fp16 slots, two sets of
+//   warps 8..15 FP8 only: E4M3 bytes times scale to fp16 slots, two sets of
 //               four warps on alternate staging buffers
-//   warps 1, 14 FP8 only, in the other CTA: relays, see relay_piece
+// With FP8's sixteen warps in different code the instruction cache is what
+// limits first: loops are rolled and each step has one call site (with
+// everything unrolled and inlined, 3.6 cycles of every issue were spent waiting
+// for instructions and a tile took 4,400 cycles).
 //
 // P is rounded once to the type of V (bf16; fp16 for FP8 KV): the relative
 // error of a weight, at most 2^-8, is independent from token to token and no larger
@@ -66,8 +70,7 @@ struct Cfg {
   // a slot holds a CTA's share of K or V of one tile
   static constexpr int kSlots = kFp8 ? 3 : 5;
   static constexpr int kSlotBytes = 2 * kHalfBytes;
-  static constexpr int kThreads = kFp8 ? 512 : 224;
-  static constexpr int kWarpV = kFp8 ? 15 : 6;  // the producer of V
+  static constexpr int kThreads = kFp8 ? 512 : 256;
   static constexpr int kOffRing = kQBytes;
   static constexpr int kOffRaw = kOffRing + kSlots * kSlotBytes;
   static constexpr int kSmem = kOffRaw + (kFp8 ? kRaw * kRawBytes : 0) + 1024;
@@ -345,7 +348,7 @@ __device__ void produce(const Ctx& cx, const Piece& pc, Producer<kFp8>& pr,
   }
 }
 
-// ---- warps 6..9 (FP8): staged bytes to fp16 slots ---------------------------
+// ---- warps 8..15 (FP8): staged bytes to fp16 slots ---------------------------
 // A staging buffer makes a slot, two halves of 64 tokens x 128 channels.
 // Thread t converts 16-byte chunk c = t & 7 (16 channels) of tokens
 // (t >> 3) + 16 e; the two 16-byte stores of lanes c and c + 4 fall into the
@@ -358,6 +361,11 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t pair16, __half2 sc)
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Whether unit k of a piece's K0 K1 V0 K2 V1 .. V(n-1) is a V.
+__device__ __forceinline__ bool is_v_unit(int k, int units) {
+  return k > 0 && (!(k & 1) || k == units - 1);
+}
+
 struct Dequant {
   Ring<kRaw> raw;
   Ring<Cfg<true>::kSlots> slot;
@@ -367,7 +375,7 @@ struct Dequant {
 __device__ __forceinline__ void dequant_unit(const Ctx& cx, uint8_t* smem,
                                              Dequant& dq, bool is_v) {
   using C = Cfg<true>;
-  const int tid = (threadIdx.x - 192) & 127, lane = threadIdx.x & 31;
+  const int tid = (threadIdx.x - 256) & 127, lane = threadIdx.x & 31;
   const int c = tid & 7, tok0 = tid >> 3;
   const int r = dq.raw.at, s = dq.slot.at;
   // Both sets see every buffer land and release it, the set that converts it
@@ -376,14 +384,14 @@ __device__ __forceinline__ void dequant_unit(const Ctx& cx, uint8_t* smem,
   // polls: the issuer's thread shares the scheduler.
   if (lane == 0) wait_bar(cx, &cx.bars->raw_full[r], dq.raw.parity);
   __syncwarp();
-  if ((dq.turn++ & 1) != (int)(threadIdx.x - 192) >> 7) {  // the other set's
+  if ((dq.turn++ & 1) != (int)(threadIdx.x - 256) >> 7) {  // the other set's
     if (lane == 0) tc::bar_arrive(tc::smem_u32(&cx.bars->raw_empty[r]));
     dq.raw.next();
     dq.slot.next();
     return;
   }
   const uint8_t* raw = smem + C::kOffRaw + r * kRawBytes;
-#pragma unroll
+#pragma unroll 1
   for (int h = 0; h < 2; ++h) {
     uint4 x[4];
     __half sc[4];
@@ -435,10 +443,12 @@ __device__ __forceinline__ void dequant_unit(const Ctx& cx, uint8_t* smem,
 
 __device__ void dequant_piece(const Ctx& cx, const Piece& pc, uint8_t* smem,
                               Dequant& dq) {
-  for (int j = -1; j < pc.n_tiles; ++j) {
-    if (j + 1 < pc.n_tiles) dequant_unit(cx, smem, dq, false);
-    if (j >= 0) dequant_unit(cx, smem, dq, true);
-  }
+  // units K0 K1 V0 K2 V1 .. V(n-2) V(n-1): unit 0 and the odd ones but the
+  // last are K
+  const int units = 2 * pc.n_tiles;
+#pragma unroll 1
+  for (int k = 0; k < units; ++k)
+    dequant_unit(cx, smem, dq, is_v_unit(k, units));
 }
 
 // ---- warp 1 of the leader, one thread: MMA issue ----------------------------
@@ -507,12 +517,12 @@ __device__ void mma_piece(const Ctx& cx, const Piece& pc, int gj0, int n_piece,
   const uint32_t smem = tc::smem_u32(smem_ptr);
   if (!wait_bar<true>(cx, &cx.bars->q_full, (uint32_t)n_piece & 1)) return;
   tc::fence_after();
-  if (!issue_qk<kFp8>(cx, seq, gj0, tmem, smem)) return;
-  for (int j = 0; j < pc.n_tiles; ++j) {
+#pragma unroll 1
+  for (int j = -1; j < pc.n_tiles; ++j) {
     if (j + 1 < pc.n_tiles &&
         !issue_qk<kFp8>(cx, seq, gj0 + j + 1, tmem, smem))
       return;
-    if (!issue_pv<kFp8>(cx, seq, gj0 + j, j == 0, tmem, smem)) return;
+    if (j >= 0 && !issue_pv<kFp8>(cx, seq, gj0 + j, j == 0, tmem, smem)) return;
   }
 }
 
@@ -526,19 +536,18 @@ __device__ void mma_piece(const Ctx& cx, const Piece& pc, int gj0, int n_piece,
 __device__ void relay_piece(const Ctx& cx, const Piece& pc, Slots<true>& seq,
                             bool v_side) {
   const uint32_t peer0 = tc::map_to(tc::smem_u32(&cx.bars->peer_full[0]), 0);
-  for (int j = -1; j < pc.n_tiles; ++j) {
-    for (int is_v = j + 1 < pc.n_tiles ? 0 : 1; is_v <= (j >= 0); ++is_v) {
-      if (!wait_bar(cx, &cx.bars->full[seq.at], seq.parity)) return;
-      if ((is_v != 0) == v_side)
-        tc::arrive_cluster(peer0 + seq.at * 8);
-      else
-        tc::arrive_cluster_relaxed(peer0 + seq.at * 8);
-      seq.next();
-    }
+  const int units = 2 * pc.n_tiles;
+#pragma unroll 1
+  for (int k = 0; k < units; ++k, seq.next()) {
+    if (!wait_bar(cx, &cx.bars->full[seq.at], seq.parity)) return;
+    if (is_v_unit(k, units) == v_side)
+      tc::arrive_cluster(peer0 + seq.at * 8);
+    else
+      tc::arrive_cluster_relaxed(peer0 + seq.at * 8);
   }
 }
 
-// ---- warps 2..5: Q, softmax, epilogue ---------------------------------------
+// ---- warps 4..7: Q, softmax, epilogue ---------------------------------------
 // A warp writes its 32 rows of Q, one row at a time: lane l moves chunk l (8
 // channels) of the row, eight rows in flight.
 template <bool kFp8>
@@ -607,21 +616,20 @@ __device__ void softmax_tiles(const Ctx& cx, const Piece& pc, int gj0,
     const uint32_t sbuf = lane_base + kColS + (gj & 1) * kT;
     wait_bar(cx, &cx.bars->s_full[gj & 1], (uint32_t)(gj >> 1) & 1);
     tc::fence_after();
-    // FP8 (more warps, fewer registers): the scores are read twice, 64
-    // columns at a time
-    constexpr int kC = kFp8 ? 64 : kT;
+    // bf16: the tile's scores in registers; FP8: 32 columns at a time, read
+    // twice, in rolled loops
+    constexpr int kC = kFp8 ? 32 : kT;
     uint32_t raw[kC];
     const float* s = reinterpret_cast<const float*>(raw);
-    float mx = -INFINITY;
-#pragma unroll
+    float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
     for (int c = 0; c < kT; c += kC) {
       tc::tmem_ld_cols<kC>(sbuf + c, raw);
-      float mx4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-      for (int k = 4; k < kC; ++k) mx4[k & 3] = fmaxf(mx4[k & 3], s[k]);
-      mx = fmaxf(mx, fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])));
+      for (int k = 0; k < kC; ++k) mx4[k & 3] = fmaxf(mx4[k & 3], s[k]);
     }
-    mx *= sl2;
+    const float mx =
+        fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl2;
     bool need = false;
     float alpha = 1.f;
     if (jt == 0) {
@@ -650,7 +658,7 @@ __device__ void softmax_tiles(const Ctx& cx, const Piece& pc, int gj0,
     }
     const float mu = m == -INFINITY ? 0.f : m;
     float sum4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
+#pragma unroll 1
     for (int c = 0; c < kT; c += kC) {
       if (kFp8) tc::tmem_ld_cols<kC>(sbuf + c, raw);
 #pragma unroll
@@ -680,8 +688,8 @@ __device__ void softmax_tiles(const Ctx& cx, const Piece& pc, int gj0,
   }
 }
 
-__device__ void epilogue(const Ctx& cx, const Piece& pc, int gl, uint32_t tmem,
-                         float m, float l) {
+__device__ void epilogue(const Ctx& cx, const Piece& pc, uint32_t tmem, float m,
+                         float l) {
   const int lane = threadIdx.x & 31, w4 = (threadIdx.x >> 5) & 3;
   const uint32_t lane_base = tmem + ((uint32_t)(32 * w4) << 16);
   const int r = w4 * 32 + lane;
@@ -784,54 +792,54 @@ __global__ void __cluster_dims__(2, 1, 1)
   const Ctx cx{&bars, &s_abort,
                tc::map_to(tc::smem_u32(&s_abort), rank ^ 1u), rank, &p};
 
-  int gj0 = 0, n_piece = 0;
-  Producer<kFp8> pr;
-  Slots<kFp8> mseq;
-  Dequant dq;
-  float m = 0.f, l = 0.f;
-  Piece prev{};
-  for (int i = blockIdx.x >> 1; i < pieces; i += gridDim.x >> 1) {
-    const Piece pc = decode_piece(p, i, rank);
-    if (warp == 0 || warp == C::kWarpV) {
-      const bool v_side = warp != 0;
-      if (pr.live)
-        produce<kFp8>(cx, pc, pr, smem, v_side ? &tm_v : &tm_k, v_side);
-      __syncwarp();
-    } else if (warp == 1) {
-      if (rank == 0 && lane == 0)
-        mma_piece<kFp8>(cx, pc, gj0, n_piece, mseq, tmem, smem);
-      if constexpr (kFp8) {
-        if (rank == 1 && lane == 0) relay_piece(cx, pc, mseq, false);
+  // Every role walks the pair's pieces by itself.
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  if (warp < 4) {
+    Producer<kFp8> pr;
+    Slots<kFp8> seq;
+    int gj0 = 0, n_piece = 0;
+    for (int i = first; i < pieces; i += step, ++n_piece) {
+      const Piece pc = decode_piece(p, i, rank);
+      if (warp == 0 || warp == 2) {
+        const bool v_side = warp != 0;
+        if (pr.live)
+          produce<kFp8>(cx, pc, pr, smem, v_side ? &tm_v : &tm_k, v_side);
+      } else if (lane == 0) {
+        if (rank == 0 && warp == 1)
+          mma_piece<kFp8>(cx, pc, gj0, n_piece, seq, tmem, smem);
+        if constexpr (kFp8) {
+          if (rank == 1) relay_piece(cx, pc, seq, warp == 3);
+        }
       }
       __syncwarp();
-    } else if (warp < 6) {
-      if (n_piece) {
+      gj0 += pc.n_tiles;
+    }
+  } else if (warp < 8) {
+    float m = 0.f, l = 0.f;
+    Piece prev{};
+    int gj0 = 0;
+    for (int i = first;; i += step) {
+      const bool more = i < pieces;
+      Piece pc{};
+      if (more) pc = decode_piece(p, i, rank);
+      if (gj0) {
         // the last piece's MMAs are done: Q may be replaced and O read, the
         // new Q first, so that its QK runs under the epilogue
         wait_bar(cx, &bars.pv_done[(gj0 - 1) & 1],
                  (uint32_t)((gj0 - 1) >> 1) & 1);
         tc::fence_after();
       }
-      write_q<kFp8>(cx, pc, smem);
-      if (n_piece) epilogue(cx, prev, gj0 - 1, tmem, m, l);
+      if (more) write_q<kFp8>(cx, pc, smem);
+      if (gj0) epilogue(cx, prev, tmem, m, l);
+      if (!more) break;
       softmax_tiles<kFp8>(cx, pc, gj0, tmem, m, l);
-    } else if constexpr (kFp8) {
-      if (warp < 14) {
-        dequant_piece(cx, pc, smem, dq);
-      } else {
-        if (rank == 1 && lane == 0) relay_piece(cx, pc, mseq, true);
-        __syncwarp();
-      }
+      prev = pc;
+      gj0 += pc.n_tiles;
     }
-    prev = pc;
-    gj0 += pc.n_tiles;
-    ++n_piece;
-  }
-  if (warp >= 2 && warp < 6 && n_piece) {
-    wait_bar(cx, &bars.pv_done[(gj0 - 1) & 1],
-             (uint32_t)((gj0 - 1) >> 1) & 1);
-    tc::fence_after();
-    epilogue(cx, prev, gj0 - 1, tmem, m, l);
+  } else if constexpr (kFp8) {
+    Dequant dq;
+    for (int i = first; i < pieces; i += step)
+      dequant_piece(cx, decode_piece(p, i, rank), smem, dq);
   }
 
   // teardown: no copy or MMA may still be in flight in either CTA.  Every

@@ -517,7 +517,7 @@ __device__ void mma_piece(const Ctx& cx, const Piece& pc, int gj0, int n_piece,
   const uint32_t smem = tc::smem_u32(smem_ptr);
   if (!wait_bar<true>(cx, &cx.bars->q_full, (uint32_t)n_piece & 1)) return;
   tc::fence_after();
-#pragma unroll 1
+#pragma unroll (kFp8 ? 1 : 2)
   for (int j = -1; j < pc.n_tiles; ++j) {
     if (j + 1 < pc.n_tiles &&
         !issue_qk<kFp8>(cx, seq, gj0 + j + 1, tmem, smem))

@@ -487,6 +487,8 @@ __device__ __forceinline__ void sort_list(Shared& s, int n) {
   }
   if (n <= kThreads)
     sort_entries<1>(list, n);
+  else if (n <= 2 * kThreads)
+    sort_entries<2>(list, n);
   else
     sort_entries<kPerThread>(list, n);
 }

@@ -79,8 +79,14 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
   const int n_rows = p.hq + 2 * a.hkv;
   const int tokens = a.batch * a.q_len;
   int buf = 0;
+  int b = blockIdx.x / a.q_len, i = blockIdx.x - b * a.q_len;
+  const int step_b = gridDim.x / a.q_len, step_i = gridDim.x - step_b * a.q_len;
   for (int tok = blockIdx.x; tok < tokens; tok += gridDim.x, buf ^= 1) {
-    const int b = tok / a.q_len, i = tok - b * a.q_len;
+    // the token's rows, at this lane's channels (8 lane on for values)
+    const __nv_bfloat16* q_src = p.q + b * p.q_req + i * p.q_tok;
+    const __nv_bfloat16* k_src = a.k_new + b * p.k_req + i * p.k_tok;
+    const __nv_bfloat16* v_src = a.v_new + b * p.v_req + i * p.v_tok + 8 * lane;
+    __nv_bfloat16* q_dst = p.q_out + (long long)tok * p.hq * kHeadDim;
     const int width =
         a.q_lens ? min(max(a.q_lens[b], 0), a.q_len) : a.q_len;
     const long long t = (long long)a.seq_lens[b] - width + i;
@@ -119,10 +125,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
         xa[e] = xb[e] = make_uint2(0u, 0u);
         if (r >= n_rows || !live) continue;
         if (r < p.hq + a.hkv) {
-          const __nv_bfloat16* src =
-              r < p.hq ? p.q + b * p.q_req + i * p.q_tok + r * kHeadDim
-                       : a.k_new + b * p.k_req + i * p.k_tok +
-                             (r - p.hq) * kHeadDim;
+          const __nv_bfloat16* src = r < p.hq
+                                         ? q_src + r * kHeadDim
+                                         : k_src + (r - p.hq) * kHeadDim;
           if (kInterleaved) {
             const uint4 v =
                 __ldcs(reinterpret_cast<const uint4*>(src + 8 * lane));
@@ -134,8 +139,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
           }
         } else {
           const uint4 v = __ldcs(reinterpret_cast<const uint4*>(
-              a.v_new + b * p.v_req + i * p.v_tok +
-              (r - p.hq - a.hkv) * kHeadDim + 8 * lane));
+              v_src + (r - p.hq - a.hkv) * kHeadDim));
           xa[e] = make_uint2(v.x, v.y);
           xb[e] = make_uint2(v.z, v.w);
         }
@@ -198,7 +202,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
                 key ? static_cast<__nv_bfloat16*>(a.k_pages) +
                           (slot + (long long)(r - p.hq) * a.page_size) *
                               kHeadDim
-                    : p.q_out + ((long long)tok * p.hq + r) * kHeadDim;
+                    : q_dst + r * kHeadDim;
             if (kInterleaved) {
               *reinterpret_cast<uint4*>(dst + 8 * lane) =
                   make_uint4(xa[e].x, xa[e].y, xb[e].x, xb[e].y);
@@ -226,6 +230,12 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
       }
     }
     if (!ready) __syncthreads();  // a warp without rows
+    b += step_b;
+    i += step_i;
+    if (i >= a.q_len) {
+      i -= a.q_len;
+      ++b;
+    }
   }
 }
 

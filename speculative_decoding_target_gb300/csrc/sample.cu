@@ -45,6 +45,9 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBins = kThreads;       // a thread scans one bin
 constexpr int kBatch = 8;             // values of a thread in flight
 constexpr int kMaxCluster = 16;
+constexpr int kWideRows = 7;            // rows that may take 16 CTAs each
+constexpr int kMaxChunkBytes = 131072;  // of a row, in a CTA
+static_assert(kSampleMaxVocab * 4 <= kMaxCluster * kMaxChunkBytes, "");
 constexpr int kPad = kBatch * kThreads;  // a CTA's values come in whole batches
 constexpr float kMaxFinite = 3.402823466e+38f;
 
@@ -1027,7 +1030,7 @@ cudaError_t launch(const SampleParams& p, int csize, cudaStream_t s) {
   if (!(ready.load(std::memory_order_relaxed) & bit)) {
     e = cudaFuncSetAttribute(
         sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-        kSampleMaxVocab / kMaxCluster * (int)sizeof(T) + 32);
+        kMaxChunkBytes + 32);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(
           sample_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -1052,15 +1055,21 @@ cudaError_t launch(const SampleParams& p, int csize, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_sample(SampleParams p, bool bf16, int sms, cudaStream_t s) {
-  // The smallest cluster whose CTAs hold at most 64 KB of the row, so that
-  // more than one fits on an SM; with few rows, more CTAs per row while SMs
-  // would stay empty and a CTA keeps a few tokens per thread.
-  const size_t esz = bf16 ? 2 : 4;
+  // The smallest cluster whose CTAs hold at most 64 KB of the row, two to an
+  // SM, but no more than 8 while 128 KB, one to an SM, will do: few clusters of
+  // 16 are resident at a time (64 fp32 rows of 248,320: 112 us with 8 CTAs a
+  // row, 126 with 16; 224 bf16 rows: 772 us with 8, 909 with 4, 1,237 with 16).
+  // With few rows, more CTAs per row while SMs would stay empty and a CTA keeps
+  // a few tokens per thread; 16 for at most kWideRows rows (of 248,320; top-k
+  // and top-p, then top-p alone over a flat row: 7 rows 21.4 and 53 us with 16,
+  // 23.0 and 76 with 8; 8 rows, a second wave, 25.8 and 59 against 23.0 and 76;
+  // 9 rows 27.9 and 78.5 against 23.8 and 78.5).
+  const size_t bytes = (size_t)p.vocab * (bf16 ? 2 : 4);
   int csize = 1;
-  while (csize < kMaxCluster && (size_t)p.vocab * esz > (size_t)csize * 65536)
-    csize *= 2;
-  while (csize < kMaxCluster && (long long)p.rows * csize * 2 <= sms &&
-         p.vocab > csize * 4096)
+  while (csize < 8 && bytes > (size_t)csize * 65536) csize *= 2;
+  if (bytes > (size_t)csize * kMaxChunkBytes) csize = kMaxCluster;
+  while (csize < (p.rows <= kWideRows ? kMaxCluster : 8) &&
+         (long long)p.rows * csize * 2 <= sms && p.vocab > csize * 4096)
     csize *= 2;
   p.chunk = ((p.vocab + csize - 1) / csize + 7) / 8 * 8;
   p.padded = (p.chunk + kPad - 1) / kPad * kPad;

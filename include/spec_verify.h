@@ -396,7 +396,7 @@ typedef struct {
  * Weights are multiples of 2^-43 (a token below half of that has none), and
  * their sums exact: the result does not depend on the order of arithmetic,
  * and differs from an exact evaluation only where u, or a border of the kept
- * set, lies within vocab 2^-44 of a token's border.
+ * set, lies within vocab 2^-43 of a token's border.
  *
  *   logits       [rows, vocab]; NaN counts as -inf, +inf as the largest
  *                finite value, subnormals as zero.  -inf is never drawn.

@@ -17,7 +17,7 @@
 // once; clusters share the SMs, so one row's loads overlap another's passes)
 // and exchanges through distributed shared memory:
 //   1. load, largest and smallest logit                      one exchange
-//   2. a 512-bin histogram over the cluster, by count for top-k and by mass
+//   2. a histogram over the cluster, 512 bins by count for top-k, 1,024 by mass
 //      for top-p, its bins even steps of the logit: the bin with the border
 //      (two exchanges).  Then, by what lies at and above that bin:
 //      - at most kList tokens (any usual top-k, any nucleus of a sure model):
@@ -26,7 +26,7 @@
 //      - more, but at most kList in the bin: it sorts those and finds the
 //        border among them, the next cut or step 3 follows;
 //      - more than that: the bin is divided by the ordered bit patterns of
-//        (logit, id), 512 parts a round, until one of the two holds.
+//        (logit, id), as many parts a round, until one of the two holds.
 //   3. (wide kept sets) kept mass per CTA in id order, then the thread and
 //      the token that hold u W                               one exchange
 #include <cuda_bf16.h>
@@ -42,7 +42,14 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = kThreads;       // a thread scans one bin
+// Bins of a round over the mass, where fewer tokens in the border's bin save
+// gathers and rounds, and of one over counts, which usually ends after the
+// first (224 rows of 248,320: bf16, flat, top-p 552 us with 1,024 and 591 with
+// 512; fp32, top-k then top-p 331 us with 1,024 for the counts and 325 with
+// 512).
+constexpr int kMassBits = 10, kCountBits = 9;
+constexpr int kBins = 1 << kMassBits;  // a thread scans two bins
+static_assert(kBins == 2 * kThreads, "");
 constexpr int kBatch = 8;             // values of a thread in flight
 constexpr int kMaxCluster = 16;
 constexpr int kWideRows = 7;            // rows that may take 16 CTAs each
@@ -309,11 +316,16 @@ constexpr int kIdBits = 19;      // ids of kSampleMaxVocab tokens
 
 struct Shared {
   Table tab;
-  uint32_t hist_lo[kBins], hist_hi[kBins];  // a bin's mass
-  u64 red_m[kBins];
-  uint32_t hist_c[kBins], red_c[kBins];
+  union {
+    struct {
+      uint32_t hist_lo[kBins], hist_hi[kBins];  // a bin's mass
+      uint32_t hist_c[kBins], red_c[kBins];     // and tokens
+      u64 red_m[kBins];
+    };
+    u64 wts[kList];   // the candidates' weights by rank, once no bins are left
+  };
   u64 list[kList];    // (order distance, id) of candidates
-  u64 wts[kList];     // their weights, by rank
+  int part[256];      // rank_entries
   u64 warp_m[kWarps];
   uint32_t warp_c[kWarps];
   u64 x_m[2];         // exchanged: this CTA's value, one per use
@@ -382,22 +394,24 @@ __device__ __forceinline__ void block_scan(Shared& s, u64 m, uint32_t c,
 // source) of the CTA's slice of bins reads one value, the sources of a bin are
 // summed by shuffles, and each of those lanes stores the sum to one CTA.
 __device__ __forceinline__ void reduce_bins(Shared& s, uint32_t rank, int csize,
-                                            bool mass) {
+                                            bool mass, int bins) {
   __syncthreads();
   tc::cluster_sync();
-  const int tid = threadIdx.x;
-  const int bin = (int)rank * (kBins / csize) + tid / csize, src = tid % csize;
-  u64 m = 0;
-  if (mass)
-    m = (u64)peer_load32(&s.hist_hi[bin], src) << 32 |
-        peer_load32(&s.hist_lo[bin], src);
-  uint32_t c = peer_load32(&s.hist_c[bin], src);
-  for (int o = 1; o < csize; o <<= 1) {
-    if (mass) m += __shfl_xor_sync(0xffffffffu, m, o);
-    c += __shfl_xor_sync(0xffffffffu, c, o);
+  const int src = threadIdx.x % csize;
+  for (int k = threadIdx.x; k < bins; k += kThreads) {
+    const int bin = (int)rank * (bins / csize) + k / csize;
+    u64 m = 0;
+    if (mass)
+      m = (u64)peer_load32(&s.hist_hi[bin], src) << 32 |
+          peer_load32(&s.hist_lo[bin], src);
+    uint32_t c = peer_load32(&s.hist_c[bin], src);
+    for (int o = 1; o < csize; o <<= 1) {
+      if (mass) m += __shfl_xor_sync(0xffffffffu, m, o);
+      c += __shfl_xor_sync(0xffffffffu, c, o);
+    }
+    if (mass) peer_store64(&s.red_m[bin], src, m);
+    peer_store32(&s.red_c[bin], src, c);
   }
-  if (mass) peer_store64(&s.red_m[bin], src, m);
-  peer_store32(&s.red_c[bin], src, c);
   tc::cluster_sync();
 }
 
@@ -474,12 +488,10 @@ __device__ __forceinline__ void rank_entries(Shared& s, int n) {
   if (i < n) {
 #pragma unroll 8
     for (int j = j0; j < j1; ++j) at += s.list[j] < v;
-    if (tid >= 256) s.hist_c[i] = at;
+    if (tid >= 256) s.part[i] = at;
   }
   __syncthreads();
-  if (tid < 256 && i < n) s.list[at + s.hist_c[i]] = v;
-  __syncthreads();
-  s.hist_c[tid] = 0;
+  if (tid < 256 && i < n) s.list[at + s.part[i]] = v;
   __syncthreads();
 }
 __device__ __forceinline__ void sort_list(Shared& s, int n) {
@@ -577,8 +589,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (tid < 32) fill_table(s.tab, tid);
   for (int i = n + tid; i < p.padded; i += kThreads)
     store_float(xs + i, -INFINITY);
-  s.hist_lo[tid] = s.hist_hi[tid] = 0;
-  s.hist_c[tid] = 0;
+  for (int j = tid; j < kBins; j += kThreads)
+    s.hist_lo[j] = s.hist_hi[j] = s.hist_c[j] = 0;
   if (tid == 0) s.n_list = 0;
   asm volatile("cp.async.commit_group;\ncp.async.wait_group 0;" ::: "memory");
   __syncthreads();
@@ -665,14 +677,15 @@ __global__ void __launch_bounds__(kThreads, 2)
     // 2. the cuts.  The first round's bins: even steps of the logit over
     // what has weight
     const float span = fminf(__fsub_rn(r.m, value_of(low)), 45.f / r.kh);
-    const float step = span > 0.f ? fminf((kBins - 1) / span, kMaxFinite) : 0.f;
-    auto bin_of = [&](float x) {
-      const float f = __fmul_rn(__fsub_rn(r.m, x), step);
-      return f < kBins - 1 ? (uint32_t)f : kBins - 1u;  // NaN: the last
-    };
     for (int which = 0; which < 2 && !done; ++which) {  // top-k, then top-p
       if (which == 0 ? k == 0 : !(tp < 1.f)) continue;
       const bool mass = which == 1;
+      const int bits = mass ? kMassBits : kCountBits, bins = 1 << bits;
+      const float step = span > 0.f ? fminf((bins - 1) / span, kMaxFinite) : 0.f;
+      auto bin_of = [&](float x) {
+        const float f = __fmul_rn(__fsub_rn(r.m, x), step);
+        return f < bins - 1 ? (uint32_t)f : (uint32_t)bins - 1;  // NaN: the last
+      };
       const u64 old = cut;
       u64 want = mass ? 0 : (u64)k;  // the border is where the sum reaches it
       u64 above_m = 0, all_m = 0;
@@ -680,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       u64 lo = 0, hi = ~0ull >> 1;
       for (int round = 0;; ++round) {
         const int shift =
-            round ? max(0, 64 - __clzll((long long)(hi - lo)) - 9) : 0;
+            round ? max(0, 64 - __clzll((long long)(hi - lo)) - bits) : 0;
         if (round == 0 && !mass) {
           // every finite value, no order beside its bin
           for (int i0 = tid; i0 < p.padded; i0 += kBatch * kThreads) {
@@ -725,15 +738,18 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
           }
         }
-        reduce_bins(s, rank, csize, mass);
-        s.hist_lo[tid] = s.hist_hi[tid] = 0;
-        s.hist_c[tid] = 0;
+        reduce_bins(s, rank, csize, mass, bins);
+        for (int j = tid; j < bins; j += kThreads)
+          s.hist_lo[j] = s.hist_hi[j] = s.hist_c[j] = 0;
         if (tid == 0) s.bin = kBins;
-        const uint32_t vc = s.red_c[tid];
-        const u64 vm = mass ? s.red_m[tid] : 0;
+        const bool two = 2 * tid < bins;
+        const uint32_t vc0 = two ? s.red_c[2 * tid] : 0;
+        const uint32_t vc1 = two ? s.red_c[2 * tid + 1] : 0;
+        const u64 vm0 = mass ? s.red_m[2 * tid] : 0;
+        const u64 vm1 = mass ? s.red_m[2 * tid + 1] : 0;
         u64 em, am;
         uint32_t ec, ac;
-        block_scan(s, vm, vc, &em, &ec, &am, &ac);
+        block_scan(s, vm0 + vm1, vc0 + vc1, &em, &ec, &am, &ac);
         if (round == 0) {
           all_m = am;
           if (mass) {  // the mass before a kept token is below p W
@@ -743,11 +759,14 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
         }
         const u64 ex = mass ? above_m + em : (u64)above_c + ec;
-        if (ex < want && want <= ex + (mass ? vm : (u64)vc)) {
-          s.bin = tid;
-          s.bin_c = vc;
-          s.before_m = above_m + em;
-          s.before_c = above_c + ec;
+        const u64 mid = ex + (mass ? vm0 : (u64)vc0);
+        const u64 end = mid + (mass ? vm1 : (u64)vc1);
+        if (ex < want && want <= end) {
+          const bool second = want > mid;
+          s.bin = 2 * tid + second;
+          s.bin_c = second ? vc1 : vc0;
+          s.before_m = above_m + em + (second ? vm0 : 0);
+          s.before_c = above_c + ec + (second ? vc0 : 0);
         }
         __syncthreads();
         const uint32_t b = s.bin;
@@ -762,7 +781,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             // what lies up to the bin's upper edge is looked at more closely
             // (its edge a little lower: the bins are decided by rounded steps)
             const float reach = __fdiv_rn((float)(b + 1), step);
-            const float edge = b < kBins - 1 && step > 0.f
+            const float edge = b < bins - 1 && step > 0.f
                                    ? __fsub_rn(r.m, __fmul_rn(reach, 1.001f))
                                    : -kMaxFinite;
             for (int i0 = tid; i0 < p.padded; i0 += kBatch * kThreads) {
@@ -892,7 +911,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (tid < 2) {
             uint32_t a = 0, z = 0xffffffffu;  // first distance with digit >= g
             const uint32_t g = b + tid;
-            if (g < kBins) {
+            if (g < bins) {
               while (a < z) {
                 const uint32_t mid = a + ((z - a) >> 1);
                 const bool in = mid <= mkey - low &&

@@ -53,9 +53,13 @@ static_assert(kBins == 2 * kThreads, "");
 constexpr int kBatch = 8;             // values of a thread in flight
 constexpr int kMaxCluster = 16;
 constexpr int kWideRows = 7;            // rows that may take 16 CTAs each
-constexpr int kMaxChunkBytes = 131072;  // of a row, in a CTA
-static_assert(kSampleMaxVocab * 4 <= kMaxCluster * kMaxChunkBytes, "");
+constexpr int kMaxChunk = 32768;        // tokens of a row, in a CTA
+static_assert(kSampleMaxVocab <= kMaxCluster * kMaxChunk, "");
 constexpr int kPad = kBatch * kThreads;  // a CTA's values come in whole batches
+// a thread's share of a warp's run in the draw (step 3)
+constexpr int kPerDraw = kMaxChunk / kWarps / kThreads;
+static_assert(kMaxChunk % kPad == 0 && kPerDraw * kWarps * kThreads == kMaxChunk,
+              "");
 constexpr float kMaxFinite = 3.402823466e+38f;
 
 typedef unsigned long long u64;
@@ -980,12 +984,12 @@ __global__ void __launch_bounds__(kThreads, 2)
         int w0 = 0;
         while (at + s.warp_m[w0] <= t) at += s.warp_m[w0++];
         // the run's tokens again, consecutive ones to a thread
-        const int per = (run_len + kThreads - 1) / kThreads;  // at most 4
+        const int per = (run_len + kThreads - 1) / kThreads;
         const int i0 = w0 * run_len + tid * per;
         const int i1 = (w0 + 1) * run_len;
-        u64 w[4], sum = 0;
+        u64 w[kPerDraw], sum = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < kPerDraw; ++e) {
           w[e] = 0;
           if (e < per && i0 + e < i1) {
             const float x = as_float(xs[i0 + e]);
@@ -999,7 +1003,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         block_scan(s, sum, 0u, &em, &ec, &am, &ac);
         at += em;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < kPerDraw; ++e) {
           if (at <= t && t < at + w[e]) p.token[row] = base + i0 + e;
           at += w[e];
         }
@@ -1049,7 +1053,7 @@ cudaError_t launch(const SampleParams& p, int csize, cudaStream_t s) {
   if (!(ready.load(std::memory_order_relaxed) & bit)) {
     e = cudaFuncSetAttribute(
         sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-        kMaxChunkBytes + 32);
+        kMaxChunk * (int)sizeof(T) + 32);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(
           sample_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -1075,7 +1079,7 @@ cudaError_t launch(const SampleParams& p, int csize, cudaStream_t s) {
 
 cudaError_t launch_sample(SampleParams p, bool bf16, int sms, cudaStream_t s) {
   // The smallest cluster whose CTAs hold at most 64 KB of the row, two to an
-  // SM, but no more than 8 while 128 KB, one to an SM, will do: few clusters of
+  // SM, but no more than 8 while kMaxChunk tokens each will do: few clusters of
   // 16 are resident at a time (64 fp32 rows of 248,320: 112 us with 8 CTAs a
   // row, 126 with 16; 224 bf16 rows: 772 us with 8, 909 with 4, 1,237 with 16).
   // With few rows, more CTAs per row while SMs would stay empty and a CTA keeps
@@ -1086,7 +1090,7 @@ cudaError_t launch_sample(SampleParams p, bool bf16, int sms, cudaStream_t s) {
   const size_t bytes = (size_t)p.vocab * (bf16 ? 2 : 4);
   int csize = 1;
   while (csize < 8 && bytes > (size_t)csize * 65536) csize *= 2;
-  if (bytes > (size_t)csize * kMaxChunkBytes) csize = kMaxCluster;
+  if (p.vocab > csize * kMaxChunk) csize = kMaxCluster;
   while (csize < (p.rows <= kWideRows ? kMaxCluster : 8) &&
          (long long)p.rows * csize * 2 <= sms && p.vocab > csize * 4096)
     csize *= 2;

@@ -143,6 +143,20 @@ def test_every_cut(vocab, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("vocab", [262144, 262145, 300007, 524288])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows", [3, 10])
+def test_largest_vocabularies(vocab, dtype, rows):
+    # wide kept sets, drawn over the whole row: each CTA's share at its largest
+    g = torch.Generator(device=DEV).manual_seed(vocab + rows)
+    x = torch.randn((rows, vocab), generator=g, device=DEV).to(dtype)
+    u = (np.arange(rows) + uniforms(rows, vocab)).astype(np.float32) / rows
+    u = np.minimum(u, np.float32(1 - 2.0 ** -24))
+    assert check(x, [1.3] * rows, None, None, None, u) <= 1
+    assert check(x, [0.9] * rows, None, [0.97] * rows, None, u) <= 1
+
+
+@gpu
 def test_peaked_rows_and_wide_ranges():
     rng = np.random.default_rng(1)
     n, V = 16, 50000

@@ -157,6 +157,31 @@ def test_largest_vocabularies(vocab, dtype, rows):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_small_top_k_where_few_threads_hold_the_values(dtype):
+    # the threads' maxima tell little: finite values in few columns of 512,
+    # one value in most of the row, fewer finite values than k
+    V, n = 60000, 8
+    g = torch.Generator(device=DEV).manual_seed(3)
+    x = torch.randn((n, V), generator=g, device=DEV) * 2
+    few = torch.full_like(x, -float("inf"))
+    few[:, 5::512] = x[:, 5::512]
+    few[1, 5::512] = 1.25
+    flat = torch.where(x > 6, x, torch.full_like(x, -1.0))
+    flat[2] = torch.where(x[2] > 4, torch.full_like(x[2], 3.0), x[2] * 0)
+    some = torch.full_like(x, -float("inf"))
+    some[:, 1000:1030] = x[:, 1000:1030]
+    dense = x.clone()                       # the largest values side by side
+    dense[:, 7000:12000] = 9 + x[:, 7000:12000].abs() / 8
+    k = [1, 2, 20, 50, 117, 118, 500, 1024]
+    for i, y in enumerate((few, flat, some, dense)):
+        y = y.to(dtype)
+        u = uniforms(n, i)
+        assert check(y, None, k, None, None, u) <= 1
+        assert check(y, [0.8] * n, k, [0.9] * n, [0.01] * n, u) <= 1
+
+
+@gpu
 def test_peaked_rows_and_wide_ranges():
     rng = np.random.default_rng(1)
     n, V = 16, 50000

@@ -1030,7 +1030,22 @@ __global__ void __launch_bounds__(kThreads, 2)
         total ? __fdiv_rn(8796093022208.f, __ull2float_rn(total)) : 0.f;
     const long long out = (long long)row * p.vocab + base;
     const Border edge = one ? Border{kMaxFinite, -1} : border_of(cut, mkey, base);
-    for (int i0 = tid; i0 < n; i0 += 4 * kThreads) {
+    int i0 = tid;
+    if (!p.filtered && !none && !one && !minw) {
+      // the usual call: whole batches with nothing else to look at
+      float* o = p.probs + out + tid;
+      for (; i0 + 3 * kThreads < n; i0 += 4 * kThreads, o += 4 * kThreads) {
+        float x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = as_float(xs[i0 + e * kThreads]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float w = fast_weight(r, x[e]) * inv;
+          __stcs(o + e * kThreads, edge.holds(x[e], i0 + e * kThreads) ? w : 0.f);
+        }
+      }
+    }
+    for (; i0 < n; i0 += 4 * kThreads) {
       float x[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {

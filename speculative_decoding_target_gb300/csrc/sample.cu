@@ -960,7 +960,18 @@ __global__ void __launch_bounds__(kThreads, 2)
       const Border edge = border_of(cut, mkey, base);
       auto kept = [&](float x, int i) { return edge.holds(x, i); };
       const int run_len = p.padded / kWarps;
+      // The weights, most of the time here, are made for full pairs of warps:
+      // kept tokens of mixed ones are queued until there are 64 (at most 127,
+      // where the lists were), in any order, as the sum is an integer.
+      float* queue = reinterpret_cast<float*>(s.list) + warp * 128;
+      const uint32_t below = (1u << lane) - 1;
+      int queued = 0;
       u64 m = 0;
+      auto add_kept = [&](float2 v) {
+        u64 w0, w1;
+        warp_weights(r, v, s.tab, w0, w1);
+        m += (w0 >= minw ? w0 : 0) + (w1 >= minw ? w1 : 0);
+      };
       for (int i0 = warp * run_len + lane; i0 < (warp + 1) * run_len;
            i0 += 4 * 32) {
         float x[4];
@@ -970,12 +981,28 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int e = 0; e < 4; e += 2) {
           const bool in0 = kept(x[e], i0 + 32 * e);
           const bool in1 = kept(x[e + 1], i0 + 32 * (e + 1));
-          if (!__any_sync(0xffffffffu, in0 || in1)) continue;
-          u64 w0, w1;
-          warp_weights(r, make_float2(x[e], x[e + 1]), s.tab, w0, w1);
-          m += (in0 && w0 >= minw ? w0 : 0) + (in1 && w1 >= minw ? w1 : 0);
+          const uint32_t m0 = __ballot_sync(0xffffffffu, in0);
+          const uint32_t m1 = __ballot_sync(0xffffffffu, in1);
+          if (!(m0 | m1)) continue;
+          float2 v = make_float2(x[e], x[e + 1]);
+          if ((m0 & m1) != 0xffffffffu) {
+            if (in0) queue[queued + __popc(m0 & below)] = v.x;
+            queued += __popc(m0);
+            if (in1) queue[queued + __popc(m1 & below)] = v.y;
+            queued += __popc(m1);
+            if (queued < 64) continue;
+            queued -= 64;
+            __syncwarp();
+            v = make_float2(queue[queued + lane], queue[queued + 32 + lane]);
+            __syncwarp();
+          }
+          add_kept(v);
         }
       }
+      __syncwarp();
+      add_kept(make_float2(
+          lane < queued ? queue[lane] : -INFINITY,
+          lane + 32 < queued ? queue[lane + 32] : -INFINITY));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
       if (lane == 0) s.warp_m[warp] = m;

@@ -81,11 +81,14 @@ __device__ __forceinline__ int units_of(int len) {
 }
 
 // First token of request b that this call attends, and its plan units.
+// (kTail false: a kernel for calls without kv_begin.)
+template <bool kTail = true>
 __device__ __forceinline__ int first_token(const AttnParams& p, int b) {
-  return p.kv_begin ? p.kv_begin[b] : 0;
+  return kTail && p.kv_begin ? p.kv_begin[b] : 0;
 }
+template <bool kTail = true>
 __device__ __forceinline__ int request_units(const AttnParams& p, int b) {
-  const int n = clamp_len(p.seq_lens[b], p.max_tokens) - first_token(p, b);
+  const int n = clamp_len(p.seq_lens[b], p.max_tokens) - first_token<kTail>(p, b);
   return n > 0 ? units_of(n) : 0;
 }
 
@@ -130,16 +133,18 @@ __device__ __forceinline__ int seg_splits(const Plan& pl, long long s0, int nt) 
 // Splits of a segment as its kernel writes it: 1 goes straight to the output,
 // more (and any piece of a call that attends only part of the tokens) to
 // partials.
+template <bool kTail = true>
 __device__ __forceinline__ int written_splits(const AttnParams& p,
                                               const Plan& pl, long long s0,
                                               int nt) {
   const int S = seg_splits(pl, s0, nt);
-  return p.kv_begin ? max(S, 2) : S;
+  return kTail && p.kv_begin ? max(S, 2) : S;
 }
 
 // Exclusive prefix of virtual units per request (real units + piece_cost)
 // into s_pre[0..batch] (s_pre[0] = 0).  Called by the whole block; ends
 // with __syncthreads().
+template <bool kTail = true>
 __device__ __forceinline__ void plan_prefix(const AttnParams& p, int* s_pre) {
   const int tid = threadIdx.x;
   if (tid < 32) {
@@ -148,7 +153,7 @@ __device__ __forceinline__ void plan_prefix(const AttnParams& p, int* s_pre) {
     for (int base = 0; base < p.batch; base += 32) {
       int b = base + lane;
       int v = b < p.batch
-                  ? request_units(p, b) + p.piece_cost
+                  ? request_units<kTail>(p, b) + p.piece_cost
                   : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {

@@ -897,7 +897,7 @@ __device__ void softmax_piece(const Ctx& cx, const Piece& pc, int gj0,
   tc::bar_sync_named(2, 128);
 }
 
-template <int NR>
+template <int NR, bool kTail>
 __global__ void __launch_bounds__(kThreads, 1)
     verify_split_fp8t_kernel(const AttnParams p,
                              const __grid_constant__ CUtensorMap tm_k,
@@ -916,7 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // stream (it was scheduled while that one ran): every input and output
   // is touched only once that grid is complete
   tc_grid_dependency_wait();
-  plan_prefix(p, s_pre);
+  plan_prefix<kTail>(p, s_pre);
   const Plan pl = make_plan(p, (long long)p.hkv * s_pre[p.batch]);
   const int c = blockIdx.x;
   if (c >= pl.P) return;  // uniform over the CTA, before any TMEM or barrier use
@@ -977,7 +977,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     pc.nt = ntv - p.piece_cost;
     pc.s0 = vs + p.piece_cost;  // the segment's first real unit
     pc.len = clamp_len(p.seq_lens[pc.b], p.max_tokens);
-    const int first = first_token(p, pc.b);
+    const int first = first_token<kTail>(p, pc.b);
     pc.tok_begin = first + j0 * kUnit;
     pc.tok_end = min(first + j1 * kUnit, pc.len);
     pc.n_tiles = (pc.tok_end - pc.tok_begin + kTile - 1) / kTile;
@@ -996,7 +996,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int S = 0, slot = 0;
       if (warp < 4) {
         // where this piece's result goes
-        S = written_splits(p, pl, pc.s0, pc.nt);
+        S = written_splits<kTail>(p, pl, pc.s0, pc.nt);
         slot = S > 1 ? partial_slot(c, pc.b * p.hkv + pc.g) : 0;
         load_q<NR>(p, pc, smem, red, slot, S);
       }
@@ -1045,12 +1045,18 @@ cudaError_t launch(const AttnParams& p, const CUtensorMap& tm_k,
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg =
       pdl_config(dim3(p.grid), dim3(kThreads), kSmem, s, attr);
-  return cudaLaunchKernelEx(&cfg, verify_split_fp8t_kernel<NR>, p, tm_k, tm_v);
+  return p.kv_begin ? cudaLaunchKernelEx(&cfg, verify_split_fp8t_kernel<NR, true>,
+                                         p, tm_k, tm_v)
+                    : cudaLaunchKernelEx(&cfg, verify_split_fp8t_kernel<NR, false>,
+                                         p, tm_k, tm_v);
 }
 
 template <int NR>
 bool set_smem() {
-  return cudaFuncSetAttribute(verify_split_fp8t_kernel<NR>,
+  return cudaFuncSetAttribute(verify_split_fp8t_kernel<NR, false>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              kSmem) == cudaSuccess &&
+         cudaFuncSetAttribute(verify_split_fp8t_kernel<NR, true>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize,
                               kSmem) == cudaSuccess;
 }
@@ -1075,7 +1081,7 @@ int verify_split_fp8t_ctas_per_sm() {
     return 0;
   int n = 0;
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-          &n, verify_split_fp8t_kernel<48>, kThreads, kSmem) != cudaSuccess)
+          &n, verify_split_fp8t_kernel<48, false>, kThreads, kSmem) != cudaSuccess)
     return 0;
   return n < 1 ? 0 : 1;  // TMEM: one 512-column allocation per SM
 }

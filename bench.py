@@ -63,12 +63,12 @@ COLD_AND_WARM = ("b1_q8_p4k_ps16", "b1_q16_p256k")
 # (the traffic follows them: every KV byte is read once, and the partials
 # are a small fixed share).
 NCU_TRAFFIC = {
-    "tc": {"source_hash": "4940d50b31ed6ff9", "captured_on": "b1_q16_p256k",
-           "read": 1074314496, "write": 3420672,
+    "tc": {"source_hash": "2a957a203adea30e", "captured_on": "b1_q16_p256k",
+           "read": 1074375424, "write": 3379968,
            "algorithmic": 262160 * 4 * 1024},
-    "fp8t": {"source_hash": "a3b122c912ef3bfd",
+    "fp8t": {"source_hash": "35a304ebdcf3101b",
              "captured_on": "b8_q8_p16k_fp8",
-             "read": 279394816, "write": 4690176,
+             "read": 279381504, "write": 4225024,
              "algorithmic": 8 * 16392 * 4 * 528},
 }
 

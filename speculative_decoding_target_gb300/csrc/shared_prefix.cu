@@ -99,7 +99,9 @@ __global__ void __launch_bounds__(kPlanThreads)
   const int warp = tid >> 5, lane = tid & 31;
   for (int cand = warp; cand < kPlans; cand += blockDim.x >> 5) {
     const float share = (float)s_work / (float)p.pairs;
-    const int run = max(1, (int)ceilf(1.6f * share * __powf(0.965f, cand)));
+    // (no run is longer than the 2^23 tiles of the longest cache)
+    const float tiles = ceilf(1.6f * share * __powf(0.965f, cand));
+    const int run = (int)fminf(fmaxf(tiles, 1.f), 8388608.f);
     int pieces = 0, longest = 0;
     for (int n = lane; n < G; n += 32) {
       if (!s_kv[n]) continue;

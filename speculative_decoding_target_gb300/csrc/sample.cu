@@ -30,6 +30,15 @@
 //        (logit, id), as many parts a round, until one of the two holds.
 //   3. (wide kept sets) kept mass per CTA in id order, then the thread and
 //      the token that hold u W                               one exchange
+//
+// Measured (248,320 tokens): one row with top-k and top-p 18.9 us, 64 fp32 rows
+// with mixed settings 107 us, 224 bf16 rows (top-p over a flat row) with
+// their distributions 598 us.  Rows cost instructions and latency, not bytes
+// (the last reads and writes 274 MB, 41 us of the copy rate): issue slots are 63%
+// busy, a flat row's weights (about 45 packed fp32 steps a pair of tokens,
+// made once for the bins and once more for what is kept) being the largest
+// share, and a row with top-k waits on barriers, about 35,000 cycles from its
+// load to its token.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -41,6 +50,8 @@
 namespace specv {
 namespace {
 
+// (1,024 where a CTA has its SM alone: 64 fp32 rows with top-k 96 us instead of
+// 85, flat with top-p 231 instead of 245, one row 22 instead of 19)
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 // Bins of a round over the mass, where fewer tokens in the border's bin save

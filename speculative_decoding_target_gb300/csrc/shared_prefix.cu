@@ -165,7 +165,10 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // and those of its group's shared part.  One warp per output row, lane l
 // channels 8l .. 8l+7, kBatch partials in flight with a running maximum: 20 for
 // few rows, which are cut into many runs (one round of loads instead of three
-// or four), 6 for many, where registers cost residency.
+// or four), 6 for many, where registers cost residency (4 single-token requests
+// over 4K tokens: 30.5 us a call with 20, 31.6 with 6; 32 blocks of 8 over 32K:
+// 189 us with 20, 179.4 with 6).  A merge of 6,144 rows of 5 to 7 partials
+// takes 14 us, mostly from L2.
 constexpr int kMergeWarps = 8;
 
 template <int kBatch>

@@ -16,7 +16,8 @@
 // to slot i.  Pieces that read the same tokens are neighbours, so they run at
 // the same time and share their tiles in L2.  The run length is the one of
 // kPlans candidates around the even share that ends first, counting each
-// piece's fixed cost as kPrefixCost tiles.
+// piece's fixed cost as kPrefixCost tiles (charges of 1, 4 and 12 measure alike
+// within 0.5 us on calls of 30 to 180 us).
 #pragma once
 
 #include "common.cuh"

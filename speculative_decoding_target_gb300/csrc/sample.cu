@@ -22,23 +22,21 @@
 //      top-p, its bins even steps of the logit: the bin with the border (two
 //      exchanges).  Then, by what lies at and above that bin:
 //      - at most kList tokens (any usual top-k, any nucleus of a sure model):
-//        the first CTA gathers and sorts them, and makes every cut and the
-//        draw alone;
-//      - more, but at most kList in the bin: it sorts those and finds the
-//        border among them, the next cut or step 3 follows;
+//        the first CTA gathers them, and makes every cut and the draw alone;
+//      - more, but at most kList in the bin: it finds the border among those,
+//        the next cut or step 3 follows;
 //      - more than that: the bin is divided by the ordered bit patterns of
 //        (logit, id), as many parts a round, until one of the two holds.
 //   3. (wide kept sets) kept mass per CTA in id order, then the thread and
 //      the token that hold u W                               one exchange
 //
-// Measured (248,320 tokens): one row with top-k and top-p 18.9 us, 64 fp32 rows
-// with mixed settings 107 us, 224 bf16 rows (top-p over a flat row) with
-// their distributions 598 us.  Rows cost instructions and latency, not bytes
-// (the last reads and writes 274 MB, 41 us of the copy rate): issue slots are 63%
-// busy, a flat row's weights (about 45 packed fp32 steps a pair of tokens,
-// made once for the bins and once more for what is kept) being the largest
-// share, and a row with top-k waits on barriers, about 35,000 cycles from its
-// load to its token.
+// Measured (248,320 tokens): one row with top-k and top-p 19 us, 64 fp32 rows
+// with mixed settings 96 us, 224 bf16 rows (top-p over a flat row) with
+// their distributions 586 us.  Rows cost instructions and latency, not bytes
+// (the last reads and writes 334 MB, 49 us of the copy rate): a flat row's
+// weights (about 45 packed fp32 steps a pair of tokens, made once for the bins
+// and once more for what is kept) are the largest share, and a row with top-k
+// waits on barriers, about 30,000 cycles from its load to its token.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -328,6 +326,7 @@ __device__ __forceinline__ float fast_weight(const Row& r, float x) {
 // ---- block and cluster steps ------------------------------------------------
 constexpr int kList = 2048;      // candidates that one CTA sorts
 constexpr int kPerThread = kList / kThreads;
+constexpr int kRanked = 256;     // candidates that are sorted, by counting
 constexpr int kIdBits = 19;      // ids of kSampleMaxVocab tokens
 
 struct Shared {
@@ -338,7 +337,7 @@ struct Shared {
       uint32_t hist_c[kBins], red_c[kBins];     // and tokens
       u64 red_m[kBins];
     };
-    u64 wts[kList];   // the candidates' weights by rank, once no bins are left
+    u64 wts[kRanked];  // the candidates' weights by rank, once no bins are left
   };
   u64 list[kList];    // (order distance, id) of candidates
   int part[256];      // rank_entries
@@ -417,69 +416,6 @@ __device__ __forceinline__ void reduce_bins(Shared& s, uint32_t rank, int csize,
   tc::cluster_sync();
 }
 
-// Bitonic sort of list[0, n), n <= kE * kThreads, ascending; the rest is
-// filled up.  Thread t holds entries t + kThreads e: pairs less than a warp
-// apart are exchanged by shuffles, pairs kThreads and more apart lie in one
-// thread, the others go through shared memory.
-template <int kE>
-__device__ __forceinline__ void sort_entries(u64* list, int n) {
-  const int tid = threadIdx.x;
-  u64 v[kE];
-#pragma unroll
-  for (int e = 0; e < kE; ++e) {
-    const int i = tid + kThreads * e;
-    v[e] = i < n ? list[i] : ~0ull;
-  }
-  int size = 32;
-  while (size < n) size <<= 1;
-  for (int k = 2; k <= size; k <<= 1) {
-#pragma unroll
-    for (int j = kE / 2; j >= 1; j >>= 1) {  // pairs kThreads j apart
-      if (kThreads * j < k) {
-#pragma unroll
-        for (int e = 0; e < kE; ++e) {
-          if (!(e & j)) {
-            const bool up = ((tid + kThreads * e) & k) == 0;
-            const u64 x = v[e], y = v[e | j];
-            if ((x > y) == up) {
-              v[e] = y;
-              v[e | j] = x;
-            }
-          }
-        }
-      }
-    }
-    for (int j = min(k >> 1, kThreads / 2); j >= 32; j >>= 1) {
-      __syncthreads();
-#pragma unroll
-      for (int e = 0; e < kE; ++e) list[tid + kThreads * e] = v[e];
-      __syncthreads();
-#pragma unroll
-      for (int e = 0; e < kE; ++e) {
-        const int i = tid + kThreads * e;
-        const u64 y = list[i ^ j];
-        const bool low_half = !(tid & j), up = (i & k) == 0;
-        v[e] = (low_half == up) == (y < v[e]) ? y : v[e];
-      }
-    }
-#pragma unroll
-    for (int j = 16; j > 0; j >>= 1) {
-      if (j < k) {
-#pragma unroll
-        for (int e = 0; e < kE; ++e) {
-          const u64 y = __shfl_xor_sync(0xffffffffu, v[e], j);
-          const bool low_half = !(tid & j),
-                     up = ((tid + kThreads * e) & k) == 0;
-          v[e] = (low_half == up) == (y < v[e]) ? y : v[e];
-        }
-      }
-    }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int e = 0; e < kE; ++e) list[tid + kThreads * e] = v[e];
-  __syncthreads();
-}
 // Short lists: an entry's place is the number of smaller ones (entries are
 // distinct), counted by two threads for half of the list each.
 __device__ __forceinline__ void rank_entries(Shared& s, int n) {
@@ -496,36 +432,101 @@ __device__ __forceinline__ void rank_entries(Shared& s, int n) {
   if (tid < 256 && i < n) s.list[at + s.part[i]] = v;
   __syncthreads();
 }
-__device__ __forceinline__ void sort_list(Shared& s, int n) {
-  u64* list = s.list;
-  if (n <= 256) {
-    rank_entries(s, n);
-    return;
+
+// The largest of the block's values, in every thread.
+__device__ __forceinline__ u64 block_max(u64* warps, u64 v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const u64 a = __shfl_xor_sync(0xffffffffu, v, o);
+    v = a > v ? a : v;
   }
-  if (n <= kThreads)
-    sort_entries<1>(list, n);
-  else if (n <= 2 * kThreads)
-    sort_entries<2>(list, n);
-  else
-    sort_entries<kPerThread>(list, n);
+  __syncthreads();
+  if (lane == 0) warps[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = warps[lane % kWarps];
+#pragma unroll
+  for (int o = kWarps / 2; o > 0; o >>= 1) {
+    const u64 a = __shfl_xor_sync(0xffffffffu, v, o);
+    v = a > v ? a : v;
+  }
+  return v;
 }
 
-// The first CTA appends the other CTAs' lists to its own (warp j reads CTA
-// j's) if all fit; returns their total.  Called between two cluster barriers.
-__device__ __forceinline__ int gather_lists(Shared& s, int csize) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint32_t at = 0, total = 0, mine = 0;
-  for (int j = 0; j < csize; ++j) {
-    const uint32_t c = j ? peer_load32(&s.n_list, j) : s.n_list;
-    if (j < warp) at += c;
-    if (j == warp) mine = c;
-    total += c;
+// Longer lists are not sorted: the key (all are distinct) at which the running
+// sum of the weights, in the keys' order, reaches want, which is above zero and
+// at most their sum.  Rounds of a histogram over what is left of the keys'
+// range, until one key is; the bins are zero before and after.  (A flat row
+// with top-p 43 us; 50 to 63 with a sort of the list, up to 50,000 cycles for
+// 1,273 entries.)
+__device__ __forceinline__ u64 key_at(Shared& s, const u64 (&key)[kPerThread],
+                                   const u64 (&w)[kPerThread], u64 want) {
+  const int tid = threadIdx.x;
+  u64 lo = 0, hi = 0;
+#pragma unroll
+  for (int e = 0; e < kPerThread; ++e)
+    if (w[e]) {
+      hi = key[e] > hi ? key[e] : hi;
+      lo = ~key[e] > lo ? ~key[e] : lo;
+    }
+  hi = block_max(s.warp_m, hi);
+  lo = ~block_max(s.warp_m, lo);
+  for (;;) {
+    const int shift = max(0, 64 - __clzll((long long)(hi - lo)) - kMassBits);
+#pragma unroll
+    for (int e = 0; e < kPerThread; ++e)
+      if (w[e] && key[e] >= lo && key[e] <= hi) {
+        const uint32_t d = (uint32_t)((key[e] - lo) >> shift);
+        atomicAdd(&s.hist_c[d], 1u);
+        add_mass(s, d, w[e]);
+      }
+    __syncthreads();
+    u64 m[2];
+    uint32_t c[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int d = 2 * tid + e;
+      m[e] = (u64)s.hist_hi[d] << 32 | s.hist_lo[d];
+      c[e] = s.hist_c[d];
+      s.hist_hi[d] = s.hist_lo[d] = s.hist_c[d] = 0;
+    }
+    u64 all;
+    const u64 before = block_scan(s.warp_m, m[0] + m[1], &all);
+    if (before < want && want <= before + m[0] + m[1]) {
+      const bool second = want > before + m[0];
+      s.bin = 2 * tid + second;
+      s.bin_c = second ? c[1] : c[0];
+      s.before_m = before + (second ? m[0] : 0);
+    }
+    __syncthreads();
+    want -= s.before_m;
+    lo += (u64)s.bin << shift;
+    const u64 end = lo + ((1ull << shift) - 1);
+    hi = end < hi ? end : hi;
+    if (!shift) return lo;
+    if (s.bin_c == 1) {
+#pragma unroll
+      for (int e = 0; e < kPerThread; ++e)
+        if (w[e] && key[e] >= lo && key[e] <= hi) s.cut = key[e];
+      __syncthreads();
+      return s.cut;
+    }
   }
-  if (warp > 0 && warp < csize && total <= kList)
-    for (uint32_t i = lane; i < mine; i += 32)
-      s.list[at + i] = peer_load64(&s.list[i], warp);
-  __syncthreads();
-  return (int)total;
+}
+
+// The CTAs' lists one after the other in the first CTA, if all fit; returns
+// their total in every thread.  Between two cluster barriers.
+__device__ __forceinline__ int join_lists(Shared& s, uint32_t rank, int csize) {
+  const int lane = threadIdx.x & 31;
+  const int mine = (int)s.n_list;
+  const int end = warp_prefix<kMaxCluster>(
+      lane < csize ? (int)peer_load32(&s.n_list, lane) : 0);
+  const int total = __shfl_sync(0xffffffffu, end, kMaxCluster - 1);
+  const int at = __shfl_sync(0xffffffffu, end, rank) - mine;
+  if (rank && total <= kList)
+    for (int i = threadIdx.x; i < mine; i += kThreads)
+      peer_store64(&s.list[at + i], 0, s.list[i]);
+  return total;
 }
 
 // The last kept token, as a value and an id in this CTA's chunk.
@@ -669,6 +670,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   u64 total = 0;       // kept mass
   u64 minw = 0;
   bool done = none || one;
+  bool leave = false;  // the first CTA finishes alone
   if (done) {
     if (rank == 0 && tid == 0) p.token[row] = none ? -1 : arg;
   } else {
@@ -837,102 +839,122 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
           __syncthreads();
           tc::cluster_sync();
-          int m = 0;
-          if (rank == 0) {
-            m = gather_lists(s, csize);
-            if (quick && tid < csize) peer_store32(&s.bin_c, tid, (uint32_t)m);
-          }
-          if (rank == 0 && m <= kList) {
-            sort_list(s, m);
-            // ranks kPerThread tid ..: weights and their sums in rank order
-            const int r0 = tid * kPerThread;
-            u64 w[kPerThread], sum = 0;
-#pragma unroll
-            for (int e = 0; e < kPerThread; ++e) {
-              const int q = r0 + e;
-              const bool in = q < m && (!finish || mass || q < k);
-              w[e] = in && (mass || finish) ? weight_at(s.list[q]) : 0;
-              sum += w[e];
-            }
-            u64 all;
-            const u64 before = block_scan(s.warp_m, sum, &all);
-            if (!finish) {
-              // the border among the bin's tokens
-              u64 run = s.before_m + before;
-#pragma unroll
-              for (int e = 0; e < kPerThread; ++e) {
-                const int q = r0 + e;
-                if (mass ? (run < want && want <= run + w[e])
-                         : (u64)s.before_c + q + 1 == want)
-                  s.cut = s.list[q];
-                run += w[e];
-              }
-              __syncthreads();
-              if (tid < csize) peer_store64(&s.cut, tid, s.cut);
-            } else {
-              // every remaining cut: a prefix of the ranks
-              const int mk = k && !mass ? min(m, k) : m;
-              u64 limit = mass ? want : ~0ull;
-              if (!mass && s.top_p < 1.f) limit = ceil_part(s.top_p, all);
-              uint32_t kept = 0;
-              u64 run = before, kept_m = 0;
-#pragma unroll
-              for (int e = 0; e < kPerThread; ++e) {
-                const int q = r0 + e;
-                const bool keep = q < mk && run < limit && w[e] >= minw;
-                run += w[e];
-                w[e] = keep ? w[e] : 0;
-                kept += keep;
-                kept_m += w[e];
-                if (q < kList) s.wts[q] = w[e];
-              }
-              uint32_t nk;
-              block_scan(s.warp_m, kept_m, &all);
-              block_scan(s.warp_c, kept, &nk);
-              if (tid == 0) {
-                s.cut = s.list[nk - 1];
-                s.total = all;
-              }
-              __syncthreads();
-              if (tid < csize) {
-                peer_store64(&s.cut, tid, s.cut);
-                peer_store64(&s.total, tid, s.total);
-              }
-              __syncthreads();
-              // the draw, in id order
-              for (int q = tid; q < (int)nk; q += kThreads)
-                s.list[q] = (s.list[q] & ((1ull << kIdBits) - 1)) << 32 |
-                            (uint32_t)q;
-              __syncthreads();
-              sort_list(s, (int)nk);
-              const u64 t = target_of(s.u, all);
-              sum = 0;
-#pragma unroll
-              for (int e = 0; e < kPerThread; ++e) {
-                const int q = r0 + e;
-                w[e] = q < (int)nk ? s.wts[(uint32_t)s.list[q]] : 0;
-                sum += w[e];
-              }
-              run = block_scan(s.warp_m, sum, &all);
-#pragma unroll
-              for (int e = 0; e < kPerThread; ++e) {
-                if (run <= t && t < run + w[e])
-                  p.token[row] = (int32_t)(s.list[r0 + e] >> 32);
-                run += w[e];
-              }
-            }
-          }
-          __syncthreads();
+          const int m = join_lists(s, rank, csize);
           tc::cluster_sync();
           if (tid == 0) s.n_list = 0;
-          if (quick && s.bin_c > kList) {  // more than the maxima showed
+          if (m > kList) {  // round -1: more than the maxima showed
             if (tid == 0) s.before_c = 0;
             __syncthreads();
             continue;
           }
+          // Without a distribution to write, the first CTA goes on alone; the
+          // SMs of the others are free for the next row (64 fp32 rows with
+          // top-k 85 -> 67 us; one row 18.6 -> 19.4 for the second barrier).
+          leave = finish && !p.probs && !p.filtered;
+          constexpr u64 kIdMask = (1ull << kIdBits) - 1;
+          if (rank == 0 && m > kRanked) {
+            u64 key[kPerThread], w[kPerThread], sum = 0, all;
+#pragma unroll
+            for (int e = 0; e < kPerThread; ++e) {
+              const int q = tid + e * kThreads;
+              key[e] = q < m ? s.list[q] : ~0ull;
+              w[e] = q < m;
+            }
+            u64 last = ~0ull - 1;  // the last kept one so far
+#pragma unroll 1
+            for (int step = 0; step < 3; ++step) {  // top-k, top-p, the draw
+              bool need = true;
+              u64 to;
+              if (step == 0) {
+                need = !mass && (!finish || k < m);
+                to = finish ? k : want - s.before_c;
+              } else if (step == 1) {
+                sum = 0;
+#pragma unroll
+                for (int e = 0; e < kPerThread; ++e) {
+                  w[e] = key[e] <= last && (mass || finish) ? weight_at(key[e]) : 0;
+                  sum += w[e];
+                }
+                block_scan(s.warp_m, sum, &all);
+                need = mass || (finish && s.top_p < 1.f);
+                to = !mass ? ceil_part(s.top_p, all)
+                           : finish ? want : want - s.before_m;
+              } else {
+                if (!finish) break;
+                u64 far = 0;
+                sum = 0;
+#pragma unroll
+                for (int e = 0; e < kPerThread; ++e) {
+                  const bool keep = key[e] <= last && w[e] >= minw;
+                  far = keep && key[e] > far ? key[e] : far;
+                  w[e] = keep ? w[e] : 0;
+                  sum += w[e];
+                  key[e] &= kIdMask;
+                }
+                last = block_max(s.warp_m, far);
+                block_scan(s.warp_m, sum, &all);
+                to = target_of(s.u, all) + 1;
+              }
+              if (!need) continue;
+              const u64 at = key_at(s, key, w, to);
+              if (step < 2)
+                last = at;
+              else if (tid == 0)
+                p.token[row] = (int32_t)at;
+            }
+            if (!leave && tid < csize) {  // (the others are gone, else)
+              peer_store64(&s.cut, tid, last);
+              if (finish) peer_store64(&s.total, tid, all);
+            }
+          } else if (rank == 0) {
+            // an entry a thread, in order
+            rank_entries(s, m);
+            const int q = tid;
+            const bool in = q < m && (!finish || mass || q < k);
+            u64 w = in && (mass || finish) ? weight_at(s.list[q]) : 0, all;
+            const u64 run = block_scan(s.warp_m, w, &all);
+            if (!finish) {
+              // the border among the bin's tokens
+              const u64 at = s.before_m + run;
+              if (q < m && (mass ? at < want && want <= at + w
+                                 : (u64)s.before_c + q + 1 == want))
+                s.cut = s.list[q];
+              __syncthreads();
+              // (not finished: every CTA is still here)
+              if (tid < csize) peer_store64(&s.cut, tid, s.cut);
+            } else {
+              // every remaining cut: a prefix of the ranks
+              u64 limit = mass ? want : ~0ull;
+              if (!mass && s.top_p < 1.f) limit = ceil_part(s.top_p, all);
+              const bool keep = in && run < limit && w >= minw;
+              w = keep ? w : 0;
+              if (q < kRanked) s.wts[q] = w;
+              uint32_t nk;
+              block_scan(s.warp_m, w, &all);
+              block_scan(s.warp_c, keep ? 1u : 0u, &nk);
+              if (!leave && tid < csize) {
+                peer_store64(&s.cut, tid, s.list[nk - 1]);
+                peer_store64(&s.total, tid, all);
+              }
+              __syncthreads();
+              // the draw, in id order
+              if (q < (int)nk) s.list[q] = (s.list[q] & kIdMask) << 32 | (uint32_t)q;
+              __syncthreads();
+              rank_entries(s, (int)nk);
+              const u64 t = target_of(s.u, all);
+              w = q < (int)nk ? s.wts[(uint32_t)s.list[q]] : 0;
+              const u64 at = block_scan(s.warp_m, w, &all);
+              if (at <= t && t < at + w)
+                p.token[row] = (int32_t)(s.list[q] >> 32);
+            }
+          }
+          if (!leave) {
+            __syncthreads();
+            tc::cluster_sync();
+            cut = s.cut;
+            if (finish) total = s.total;
+          }
           done = finish;
-          cut = s.cut;
-          if (finish) total = s.total;
           break;
         }
         // too many in one bin: its range of places is the next round's
@@ -1104,7 +1126,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
   }
-  tc::cluster_sync();  // no CTA leaves while others read its shared memory
+  // no CTA leaves while others read its shared memory
+  if (!leave) tc::cluster_sync();
 }
 
 template <typename T>

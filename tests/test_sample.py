@@ -182,6 +182,38 @@ def test_small_top_k_where_few_threads_hold_the_values(dtype):
 
 
 @gpu
+@pytest.mark.parametrize("vocab", [20011, 140009])
+def test_many_rows_of_mixed_settings(vocab):
+    # more clusters than are resident, rows that end at different steps, with
+    # and without distributions, twice on two streams at once
+    n = 230
+    g = torch.Generator(device=DEV).manual_seed(vocab)
+    x = torch.randn((n, vocab), generator=g, device=DEV) * 2.5
+    rng = np.random.default_rng(vocab)
+    t = rng.choice([0.0, 0.6, 1.0, 1.3, -1.0], n)
+    k = rng.choice([0, 0, 1, 40, 300, 900, 5000], n)
+    p = rng.choice([1.0, 0.5, 0.9, 0.99], n)
+    m = rng.choice([0.0, 0.0, 0.02], n)
+    u = uniforms(n, vocab)
+    assert check(x, t, k, p, m, u) <= 1
+    f = lambda a, d=torch.float32: torch.as_tensor(a, dtype=d, device=DEV)
+    args = dict(temperature=f(t), top_k=f(k, torch.int32), top_p=f(p),
+                min_p=f(m))
+    want = sv.sample(x, f(u), **args)
+    torch.cuda.synchronize()
+    uu = f(u)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(4):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(sv.sample(x, uu, **args))
+    torch.cuda.synchronize()
+    for y in got:
+        assert torch.equal(y, want)
+
+
+@gpu
 def test_peaked_rows_and_wide_ranges():
     rng = np.random.default_rng(1)
     n, V = 16, 50000

@@ -7,6 +7,7 @@ or fails to load, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -220,6 +221,14 @@ def _on_current_device(tensors, stream) -> int:
     return stream.cuda_stream
 
 
+def _made_on(stream):
+    """Allocate a call's own buffers for the stream that the call runs on:
+    memory of another stream could be handed out again, when the buffer is
+    dropped, before the call has run."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(
+        stream)
+
+
 def _expect_pools(k_pages, v_pages, k_scales, v_scales, hkv: int,
                   d: int) -> bool:
     """Check a K/V page pool; returns whether it is FP8."""
@@ -339,14 +348,15 @@ def verify_attention_shared(q, k_pages, v_pages, page_table, seq_lens,
                         k_pages.shape[1], d)
     groups = shared_lens.numel()
     _expect(page_table, torch.int32, "page_table", contiguous=True)
-    if page_table.shape[0] != B:
+    if page_table.dim() != 2 or page_table.shape[0] != B:
         raise SpecError(SPEC_ERR_ARG, f"page_table must have {B} rows")
     _expect(seq_lens, torch.int32, "seq_lens", (B,), True)
     _expect(shared_lens, torch.int32, "shared_lens", (groups,), True)
     _expect(group_starts, torch.int32, "group_starts", (groups + 1,), True)
     _expect_optional(B, q_len, q_lens)
     if out is None:
-        out = torch.empty_like(q)
+        with _made_on(stream):
+            out = torch.empty_like(q)
     _expect(out, torch.bfloat16, "out", q.shape, True)
     on = _on_current_device((q, k_pages, v_pages, k_scales, v_scales,
                              page_table, seq_lens, group_starts, shared_lens,
@@ -357,8 +367,9 @@ def verify_attention_shared(q, k_pages, v_pages, page_table, seq_lens,
                     SPEC_FLAG_CHECKED if checked else 0,
                     None if q_lens is None else q_lens.data_ptr())
     if workspace is None:
-        workspace = alloc_workspace(shared_workspace_size(desc, groups),
-                                    q.device)
+        with _made_on(stream):
+            workspace = alloc_workspace(shared_workspace_size(desc, groups),
+                                        q.device)
     rc = load().spec_verify_attention_shared(
         ctypes.byref(desc), _at(q), _at(k_pages), _at(v_pages), _at(k_scales),
         _at(v_scales), _at(page_table), _at(seq_lens), groups,
@@ -436,18 +447,24 @@ def rope_append(q, k_new, v_new, freq, k_pages, v_pages, page_table, seq_lens,
     hq = 0 if q is None else q.shape[2]
     _expect(k_new, torch.bfloat16, "k_new")
     _expect(v_new, torch.bfloat16, "v_new", k_new.shape)
-    _expect(freq, torch.float64, "freq", contiguous=True)
+    _expect(freq, torch.float64, "freq", (freq.numel(),), contiguous=True)
     _expect(page_table, torch.int32, "page_table", contiguous=True)
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise SpecError(SPEC_ERR_ARG, f"page_table must have {B} rows")
     _expect(seq_lens, torch.int32, "seq_lens", (B,), contiguous=True)
     if q is not None:
         _expect(q, torch.bfloat16, "q", (B, q_len, hq, d))
         if q_out is None:
-            q_out = torch.empty((B, q_len, hq, d), dtype=q.dtype,
-                                device=q.device)
+            with _made_on(stream):
+                q_out = torch.empty((B, q_len, hq, d), dtype=q.dtype,
+                                    device=q.device)
         _expect(q_out, torch.bfloat16, "q_out", (B, q_len, hq, d),
                 contiguous=True)
     fp8 = _expect_pools(k_pages, v_pages, k_scales, v_scales, hkv, d)
     _expect_optional(B, q_len, q_lens, positions, cache_loc)
+    if (checked and workspace is not None
+            and workspace.numel() * workspace.element_size() < 4):
+        raise SpecError(SPEC_ERR_WORKSPACE, "workspace of fewer than 4 bytes")
     on = _on_current_device((q, k_new, v_new, freq, q_out, k_pages, v_pages,
                              k_scales, v_scales, page_table, seq_lens, q_lens,
                              positions, cache_loc, workspace), stream)
@@ -620,7 +637,8 @@ def sample(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None,
     if logits.dtype not in (torch.float32, torch.bfloat16):
         raise SpecError(SPEC_ERR_ARG, f"logits are {logits.dtype}")
     if token is None:
-        token = torch.empty(lead, dtype=torch.int32, device=logits.device)
+        with _made_on(stream):
+            token = torch.empty(lead, dtype=torch.int32, device=logits.device)
     for t, dtype, what in ((u, torch.float32, "u"),
                            (temperature, torch.float32, "temperature"),
                            (top_k, torch.int32, "top_k"),

@@ -399,6 +399,14 @@ def test_binding_refuses_wrong_tensors():
     refused(kp=pool[:, :2])
     refused(vp=pool.half())
     refused()                                   # host tensors
+    for kw, what in ((dict(t=table[:1]), "rows"), (dict(t=table[0]), "rows"),
+                     (dict(f=f.view(4, 8)), "freq")):
+        a = {**good, **kw}
+        with pytest.raises(sv.SpecError, match=what):
+            sv.rope_append(x, x, x, a["f"], pool, pool, a["t"], seq)
+    with pytest.raises(sv.SpecError, match="4 bytes"):
+        sv.rope_append(x, x, x, f, pool, pool, table, seq, checked=True,
+                       workspace=torch.zeros(3, dtype=torch.uint8))
 
 
 def test_frequencies():

@@ -302,6 +302,36 @@ def test_many_calls_in_a_row(kv):
 
 
 @gpu
+def test_own_buffers_belong_to_the_call_s_stream(monkeypatch):
+    # a workspace dropped while its stream is still busy must not come back
+    # from the allocator of the current stream
+    build.build()
+    B, ps = 4, 64
+    q = torch.randn((B, 1, 24, 256), device=DEV).to(torch.bfloat16)
+    pool = torch.randn((24, 4, ps, 256), device=DEV).to(torch.bfloat16)
+    i = lambda *a: torch.tensor(a, dtype=torch.int32, device=DEV)
+    table = torch.arange(8, dtype=torch.int32, device=DEV).repeat(B, 1)
+    args = (q, pool, pool, table, i(500, 480, 512, 490), i(0, B), i(448))
+    want = sv.verify_attention_shared(*args, scale=0.06)
+    sizes, plain = [], _native.alloc_workspace
+
+    def recorded(n, device):
+        w = plain(n, device)
+        sizes.append((n, w.data_ptr()))
+        return w
+    monkeypatch.setattr(_native, "alloc_workspace", recorded)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    s = torch.cuda.Stream()
+    out = sv.verify_attention_shared(*args, scale=0.06, stream=s)
+    (n, at), = sizes
+    again = [plain(n, DEV) for _ in range(3)]
+    assert all(w.data_ptr() != at for w in again)
+    s.synchronize()
+    assert torch.equal(out, want)
+
+
+@gpu
 def test_large_scores_rescale():
     # keys that grow along the prefix, so the running maximum moves by far
     # more than the threshold, and one that dominates late

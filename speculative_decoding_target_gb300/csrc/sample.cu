@@ -128,7 +128,12 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 }
 
 // ---- weights ----------------------------------------------------------------
-// 2^-(j/32) for j < 32: as an integer multiple of 2^-50 and as two floats.
+// 1.5 * 2^23: an addition of it rounds to an integer, which the sum's low bits
+// hold above the constant's.
+constexpr float kMagic = 12582912.f;
+constexpr uint32_t kMagicBits = 0x4B400000u;
+// 2^-(j/32) for j < 32: as an integer multiple of 2^-50, less what kMagicBits
+// will add to it (near_weights), and as two floats.
 // One 32-bit word of every entry after the other, so that lanes with different
 // j read different banks (16-byte entries took about 12 wavefronts a load).
 struct Table {
@@ -148,8 +153,9 @@ __constant__ u64 kPowers[32] = {  // round(2^(50 - j/32))
 __device__ __forceinline__ void fill_table(Table& t, int j) {
   const u64 fix = kPowers[j];
   const float hi = __fmul_rn(__ull2float_rn(fix), 8.8817841970012523e-16f);
-  t.fix_lo[j] = (uint32_t)fix;
-  t.fix_hi[j] = (uint32_t)(fix >> 32);
+  const u64 base = fix - ((u64)kMagicBits << 24);
+  t.fix_lo[j] = (uint32_t)base;
+  t.fix_hi[j] = (uint32_t)(base >> 32);
   t.hi[j] = hi;  // times 2^-50
   t.lo[j] = __fmul_rn(
       __ll2float_rn((long long)fix -
@@ -210,6 +216,17 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
+// The integer of 2^-50 steps from the table's entry, a multiple of 2^24 and a
+// rest, rounded to 2^-43 and shifted by n / 32 at once.
+__device__ __forceinline__ u64 assemble(const Table& tab, uint32_t n, float i1,
+                                        float i2) {
+  const int j = n & 31;
+  u64 e = (u64)tab.fix_hi[j] << 32 | tab.fix_lo[j];
+  asm("mad.wide.s32 %0, %1, 16777216, %0;" : "+l"(e) : "r"(__float_as_int(i1)));
+  asm("mad.wide.s32 %0, %1, 1, %0;" : "+l"(e) : "r"(__float2int_rn(i2)));
+  return (e >> ((n >> 5) - (kMagicBits >> 5) + 6)) + 1 >> 1;
+}
+
 // round(2^43 2^-y), y = (M - x) log2(e) / T, to about 2^-46 of the largest
 // weight, of two tokens at once in packed fp32.  The difference and the product
 // are carried as two floats; with y = n + j/32 + r, |r| <= 1/64, the factor
@@ -222,7 +239,6 @@ __device__ __forceinline__ void near_weights(const Row& r, float2 x, float2 dh,
                                              u64& w0, u64& w1) {
   // a - b is fma(b, -1, a): packed operands carry no sign of their own
   const float2 one = both(-1.f), m = both(r.m), kh = both(r.kh);
-  constexpr float kMagic = 12582912.f;  // 1.5 * 2^23
   const float2 magic = both(kMagic), unmagic = both(-kMagic);
   // beyond 28: any value that keeps the steps finite
   const float2 yc = make_float2(fminf(yh.x, 29.f), fminf(yh.y, 29.f));
@@ -251,8 +267,7 @@ __device__ __forceinline__ void near_weights(const Row& r, float2 x, float2 dh,
   const float2 qh = add2(th, sh);
   const float2 ql = add2(add2(fma2(qh, one, th), sh),
                          add2(add2(tl, sl), cube));
-  const int n0 = __float_as_int(nt.x) - 0x4B400000;
-  const int n1 = __float_as_int(nt.y) - 0x4B400000;
+  const uint32_t n0 = __float_as_uint(nt.x), n1 = __float_as_uint(nt.y);
   const int j0 = n0 & 31, j1 = n1 & 31;
   const float2 hi = make_float2(tab.hi[j0], tab.hi[j1]);
   const float2 lo = make_float2(tab.lo[j0], tab.lo[j1]);
@@ -264,17 +279,8 @@ __device__ __forceinline__ void near_weights(const Row& r, float2 x, float2 dh,
   const float2 rem = add2(
       fma2(add2(i1t, unmagic), both(-1.490116119384765625e-08f), g), gl);
   const float2 i2 = mul2(rem, both(1125899906842624.f));  // 2^50
-  const long long e0 =
-      (long long)((u64)tab.fix_hi[j0] << 32 | tab.fix_lo[j0]) +
-      ((long long)(__float_as_int(i1t.x) - 0x4B400000) << 24) +
-      __float2int_rn(i2.x);
-  const long long e1 =
-      (long long)((u64)tab.fix_hi[j1] << 32 | tab.fix_lo[j1]) +
-      ((long long)(__float_as_int(i1t.y) - 0x4B400000) << 24) +
-      __float2int_rn(i2.y);
-  const int s0 = n0 >> 5, s1 = n1 >> 5;
-  w0 = (u64)(e0 + (64ll << s0)) >> (7 + s0);
-  w1 = (u64)(e1 + (64ll << s1)) >> (7 + s1);
+  w0 = assemble(tab, n0, i1t.x, i2.x);
+  w1 = assemble(tab, n1, i1t.y, i2.y);
 }
 
 // Weights below 2^-28 take exp2 itself: its relative error of 2^-22 is below

@@ -31,8 +31,8 @@
 //      the token that hold u W                               one exchange
 //
 // Measured (248,320 tokens): one row with top-k and top-p 19 us, 64 fp32 rows
-// with mixed settings 96 us, 224 bf16 rows (top-p over a flat row) with
-// their distributions 586 us.  Rows cost instructions and latency, not bytes
+// with mixed settings 95 us, 224 bf16 rows (top-p over a flat row) with
+// their distributions 561 us.  Rows cost instructions and latency, not bytes
 // (the last reads and writes 334 MB, 49 us of the copy rate): a flat row's
 // weights (about 45 packed fp32 steps a pair of tokens, made once for the bins
 // and once more for what is kept) are the largest share, and a row with top-k
@@ -812,24 +812,41 @@ __global__ void __launch_bounds__(kThreads, 2)
                                    ? fmaxf(__fsub_rn(r.m, __fmul_rn(reach, 1.001f)),
                                            -kMaxFinite)
                                    : -kMaxFinite;
-            for (int i0 = tid; i0 < p.padded; i0 += kBatch * kThreads) {
-              float x[kBatch];
-              bool any = false;
+            auto append = [&](float x, int i) {
+              const u64 c = place(x, i);
+              if (c > old) return;
+              const uint32_t at = atomicAdd(&s.n_list, 1u);
+              if (at < kList) s.list[at] = c;  // more: too many anyway
+            };
+            if (finish) {
+              for (int i0 = tid; i0 < p.padded; i0 += kBatch * kThreads) {
+                float x[kBatch];
+                bool any = false;
 #pragma unroll
-              for (int e = 0; e < kBatch; ++e) {
-                x[e] = as_float(xs[i0 + e * kThreads]);
-                any |= x[e] >= edge;
+                for (int e = 0; e < kBatch; ++e) {
+                  x[e] = as_float(xs[i0 + e * kThreads]);
+                  any |= x[e] >= edge;
+                }
+                if (!any) continue;
+#pragma unroll
+                for (int e = 0; e < kBatch; ++e)
+                  if (x[e] >= edge && (quick || bin_of(x[e]) <= b))
+                    append(x[e], i0 + e * kThreads);
               }
-              if (!any) continue;
+            } else {
+              // within the bin alone, few tokens pass (224 flat bf16 rows 455
+              // us; 468 where all above the bin are looked at as well)
+              const float inner = __fdiv_rn(__fmul_rn((float)b, 0.999f), step);
+              const float upper = step > 0.f ? __fsub_rn(r.m, inner) : kMaxFinite;
+              for (int i0 = tid; i0 < p.padded; i0 += kBatch * kThreads) {
+                float x[kBatch];
 #pragma unroll
-              for (int e = 0; e < kBatch; ++e) {
-                if (!(x[e] >= edge)) continue;
-                const uint32_t d = bin_of(x[e]);
-                if (!quick && d != b && !(finish && d < b)) continue;
-                const u64 c = place(x[e], i0 + e * kThreads);
-                if (c > old) continue;
-                const uint32_t at = atomicAdd(&s.n_list, 1u);
-                if (at < kList) s.list[at] = c;  // more: too many anyway
+                for (int e = 0; e < kBatch; ++e)
+                  x[e] = as_float(xs[i0 + e * kThreads]);
+#pragma unroll
+                for (int e = 0; e < kBatch; ++e)
+                  if (x[e] >= edge && x[e] <= upper && bin_of(x[e]) == b)
+                    append(x[e], i0 + e * kThreads);
               }
             }
           } else {

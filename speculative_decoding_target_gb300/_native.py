@@ -205,15 +205,13 @@ def _on_current_device(tensors, stream) -> int:
     """Check that every tensor (None: absent) and the stream belong to the
     current CUDA device, where the library launches on plain addresses; the
     stream's handle (None: the current stream)."""
-    for t in tensors:
-        if t is not None and not t.is_cuda:
-            raise SpecError(SPEC_ERR_ARG, "tensors must be on a CUDA device")
+    on = {t.get_device() for t in tensors if t is not None}  # -1: the host
+    if -1 in on:
+        raise SpecError(SPEC_ERR_ARG, "tensors must be on a CUDA device")
     now = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != now:
-            raise SpecError(SPEC_ERR_ARG,
-                            f"a tensor on cuda:{t.get_device()} in a call on "
-                            f"cuda:{now}, the current device")
+    if on != {now}:
+        raise SpecError(SPEC_ERR_ARG, f"tensors on devices {sorted(on)} in a "
+                                      f"call on cuda:{now}, the current device")
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(now)
     if stream.device_index != now:

@@ -915,11 +915,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   // launched as a programmatic dependent of the kernel before it on the
   // stream (it was scheduled while that one ran): every input and output
   // is touched only once that grid is complete
-  tc_grid_dependency_wait();
+  // (Tails of a call with shared prefixes, kTail: the kernel before is the
+  // prefix kernel, whose results only the merge reads.  It released this one
+  // when everything before it, the plan among it, was complete; the wait at the
+  // end keeps the order for the merge.)
+  if (!kTail) tc_grid_dependency_wait();
   plan_prefix<kTail>(p, s_pre);
   const Plan pl = make_plan(p, (long long)p.hkv * s_pre[p.batch]);
   const int c = blockIdx.x;
-  if (c >= pl.P) return;  // uniform over the CTA, before any TMEM or barrier use
+  if (c >= pl.P) {  // uniform over the CTA, before any TMEM or barrier use
+    if (kTail) tc_grid_dependency_wait();
+    return;
+  }
 
   if (tid == 0) {
     for (int s = 0; s < kKStages; ++s) {
@@ -1035,6 +1042,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::fence_after();
   if (warp == kWarpQK) tc::tmem_dealloc(tmem, kTmemCols);
+  if (kTail) tc_grid_dependency_wait();
 }
 
 template <int NR>

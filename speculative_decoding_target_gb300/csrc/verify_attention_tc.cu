@@ -488,7 +488,7 @@ __device__ __forceinline__ void load_q_tmem(const AttnParams& p, const Piece& pc
   tc::tmem_wait_st();
 }
 
-template <bool kFp8>
+template <bool kFp8, bool kTail>
 __device__ void softmax_piece(const Ctx& cx, const Piece& pc, int gj0,
                               uint32_t tmem, uint8_t* smem,
                               const Plan& pl, int c) {
@@ -504,7 +504,7 @@ __device__ void softmax_piece(const Ctx& cx, const Piece& pc, int gj0,
   const uint32_t lane_base = tmem + ((uint32_t)(32 * w4) << 16);
   const float sl2 = p.scale_log2;
   // where this piece's result goes
-  const int S = written_splits(p, pl, pc.s0, pc.nt);
+  const int S = written_splits<kTail>(p, pl, pc.s0, pc.nt);
   const int slot = S > 1 ? partial_slot(c, pc.b * p.hkv + pc.g) : 0;
 
   float m = -INFINITY, l = 0.f;
@@ -653,7 +653,7 @@ __device__ void softmax_piece(const Ctx& cx, const Piece& pc, int gj0,
 
 constexpr int kPieceThreads = 5 * 32;  // warps 1..5: MMA issuer + softmax
 
-template <bool kFp8>
+template <bool kFp8, bool kTail>
 __global__ void __launch_bounds__(Cfg<kFp8>::kThreads, 1)
     verify_split_tc_kernel(const AttnParams p,
                            const __grid_constant__ CUtensorMap tm_k,
@@ -671,11 +671,18 @@ __global__ void __launch_bounds__(Cfg<kFp8>::kThreads, 1)
   // launched as a programmatic dependent of the kernel before it on the
   // stream (it was scheduled while that one ran): every input and output
   // is touched only once that grid is complete
-  tc_grid_dependency_wait();
-  plan_prefix(p, s_pre);
+  // (Tails of a call with shared prefixes, kTail: the kernel before is the
+  // prefix kernel, whose results only the merge reads.  It released this one
+  // when everything before it, the plan among it, was complete; the wait at the
+  // end keeps the order for the merge.)
+  if (!kTail) tc_grid_dependency_wait();
+  plan_prefix<kTail>(p, s_pre);
   const Plan pl = make_plan(p, (long long)p.hkv * s_pre[p.batch]);
   const int c = blockIdx.x;  // this kernel runs static plans only
-  if (c >= pl.P) return;  // uniform over the CTA, before any TMEM or barrier use
+  if (c >= pl.P) {  // uniform over the CTA, before any TMEM or barrier use
+    if (kTail) tc_grid_dependency_wait();
+    return;
+  }
 
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
@@ -729,7 +736,7 @@ __global__ void __launch_bounds__(Cfg<kFp8>::kThreads, 1)
     pc.nt = ntv - p.piece_cost;
     pc.s0 = vs + p.piece_cost;  // the segment's first real unit
     pc.len = clamp_len(p.seq_lens[pc.b], p.max_tokens);
-    const int first = first_token(p, pc.b);
+    const int first = first_token<kTail>(p, pc.b);
     pc.tok_begin = first + j0 * kUnit;
     pc.tok_end = min(first + j1 * kUnit, pc.len);
     pc.n_tiles = (pc.tok_end - pc.tok_begin + kT - 1) / kT;
@@ -757,7 +764,7 @@ __global__ void __launch_bounds__(Cfg<kFp8>::kThreads, 1)
         if (lane == 0) mma_piece<kFp8>(cx, pc, gj0, tmem, smem);
         __syncwarp();
       } else {
-        softmax_piece<kFp8>(cx, pc, gj0, tmem, smem, pl, c);
+        softmax_piece<kFp8, kTail>(cx, pc, gj0, tmem, smem, pl, c);
       }
       tc::fence_before();
       tc::bar_sync_named(1, kPieceThreads);
@@ -784,6 +791,7 @@ __global__ void __launch_bounds__(Cfg<kFp8>::kThreads, 1)
   __syncthreads();
   tc::fence_after();
   if (warp == 1) tc::tmem_dealloc(tmem, kTmemCols);
+  if (kTail) tc_grid_dependency_wait();
 }
 
 template <bool kFp8>
@@ -796,19 +804,25 @@ cudaError_t launch(const AttnParams& p, const CUtensorMap& tm_k,
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg =
       pdl_config(dim3(p.grid), dim3(C::kThreads), C::kSmem, s, attr);
-  return cudaLaunchKernelEx(&cfg, verify_split_tc_kernel<kFp8>, p, tm_k, tm_v);
+  return p.kv_begin ? cudaLaunchKernelEx(&cfg, verify_split_tc_kernel<kFp8, true>,
+                                         p, tm_k, tm_v)
+                    : cudaLaunchKernelEx(&cfg, verify_split_tc_kernel<kFp8, false>,
+                                         p, tm_k, tm_v);
 }
 
 template <bool kFp8>
 int ctas_per_sm() {
   using C = Cfg<kFp8>;
-  if (cudaFuncSetAttribute(verify_split_tc_kernel<kFp8>,
+  if (cudaFuncSetAttribute(verify_split_tc_kernel<kFp8, false>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           C::kSmem) != cudaSuccess ||
+      cudaFuncSetAttribute(verify_split_tc_kernel<kFp8, true>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize,
                            C::kSmem) != cudaSuccess)
     return 0;
   int n = 0;
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-          &n, verify_split_tc_kernel<kFp8>, C::kThreads, C::kSmem) !=
+          &n, verify_split_tc_kernel<kFp8, false>, C::kThreads, C::kSmem) !=
       cudaSuccess)
     return 0;
   return n < 1 ? 0 : 1;  // TMEM: one 512-column allocation per SM

@@ -63,12 +63,12 @@ COLD_AND_WARM = ("b1_q8_p4k_ps16", "b1_q16_p256k")
 # (the traffic follows them: every KV byte is read once, and the partials
 # are a small fixed share).
 NCU_TRAFFIC = {
-    "tc": {"source_hash": "2a957a203adea30e", "captured_on": "b1_q16_p256k",
-           "read": 1074375424, "write": 3379968,
+    "tc": {"source_hash": "802bc7cd0ad7ba62", "captured_on": "b1_q16_p256k",
+           "read": 1074321408, "write": 3225344,
            "algorithmic": 262160 * 4 * 1024},
-    "fp8t": {"source_hash": "35a304ebdcf3101b",
+    "fp8t": {"source_hash": "b555c9c604a8008e",
              "captured_on": "b8_q8_p16k_fp8",
-             "read": 279381504, "write": 4225024,
+             "read": 279409920, "write": 4262656,
              "algorithmic": 8 * 16392 * 4 * 528},
 }
 

@@ -28,8 +28,8 @@
 //               the softmax of tile j has a QK and a PV's time to run in
 //   warps 1, 3  FP8, the other CTA: relays, see relay_piece
 //   warps 4..7  softmax: one thread per row; running maximum and sum in base
-//               2 and fp32; O is rescaled only when the maximum grows by 2^8;
-//               epilogue (normalised fp32 partial, log-sum-exp)
+//               2 and fp32; O is rescaled only when the maximum grows by 2^8
+//               (FP8: 2^4); epilogue (normalised fp32 partial, log-sum-exp)
 //   warps 8..15 FP8 only: E4M3 bytes times scale to fp16 slots, two sets of
 //               four warps on alternate staging buffers
 // With FP8's sixteen warps in different code the instruction cache is what
@@ -37,11 +37,17 @@
 // everything unrolled and inlined, 3.6 cycles of every issue were spent waiting
 // for instructions and a tile took 4,400 cycles).
 //
-// P is rounded once to the type of V (bf16; fp16 for FP8 KV): the relative
-// error of a weight, at most 2^-8, is independent from token to token and no larger
-// than that of the bf16 output itself.  (The verify kernel splits P into two
-// bf16 terms, free where HBM is the bound; here it would add half again to
-// the MMAs.)
+// P is rounded once to the type of V.  bf16: a weight is off by at most 2^-8 of
+// itself, whatever its size, as the bf16 output is of its value.  (The verify
+// kernel splits P into two bf16 terms, free where HBM is the bound; here it
+// would add half again to the MMAs.)  FP8 KV: fp16, off by at most 2^-11 of
+// itself down to 2^-14 and by 2^-25 below, where its steps are even; a long
+// prefix may hold much of its mass in weights that small beside the largest one.
+// So P, O and the sum carry a factor of 2^11: with O rescaled at a growth of 2^4,
+// P lies at most at 2^15, and a weight that is w of the largest (or of the
+// maximum in use, if that is smaller) is off by 2^-11 w or, below w = 2^-25, by
+// 2^-36; a million tokens that small together by 2^-16 of the row.  The factor
+// leaves with the division by the sum, and the log-sum-exp's 11.
 //
 // Measured (24 query heads, 4 KV heads): bf16, 32 requests x 8 rows over 32,768
 // shared tokens, 206 Gflop: 121-126 us, 1.64 to 1.70 Pflop/s, 0.86 to 0.89 of
@@ -68,7 +74,6 @@ constexpr int kBlockBytes = 64 * 128;         // its column block of 64
 constexpr int kQBytes = 128 * kHeadDim * 2;   // 4 column blocks of 128 rows
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 256;
-constexpr float kRescaleLog2 = 8.0f;
 constexpr int kMaxSlots = 5;
 constexpr int kRaw = 3;                       // FP8 staging buffers
 constexpr int kRawBytes = 16384 + 1024;       // bytes and scales
@@ -83,6 +88,10 @@ struct Cfg {
   static constexpr int kOffRaw = kOffRing + kSlots * kSlotBytes;
   static constexpr int kSmem = kOffRaw + (kFp8 ? kRaw * kRawBytes : 0) + 1024;
   static constexpr uint32_t kAB = kFp8 ? 0u : 1u;  // fp16 or bf16 inputs
+  // growth of the maximum (log2) that rescales O, and the factor that P and
+  // the sum carry (log2); 2^(4 + 11) is fp16's 32,768
+  static constexpr float kRescaleLog2 = kFp8 ? 4.f : 8.f;
+  static constexpr float kShiftLog2 = kFp8 ? 11.f : 0.f;
   static constexpr uint32_t kIdescQK = (1u << 4) | (kAB << 7) | (kAB << 10) |
                                        ((uint32_t)(kT >> 3) << 17) |
                                        ((uint32_t)(256 >> 4) << 24);
@@ -614,6 +623,7 @@ __device__ __forceinline__ void store8(float* dst, const float* v, float k) {
 template <bool kFp8>
 __device__ void softmax_tiles(const Ctx& cx, const Piece& pc, int gj0,
                               uint32_t tmem, float& m, float& l) {
+  using C = Cfg<kFp8>;
   const int lane = threadIdx.x & 31, w4 = (threadIdx.x >> 5) & 3;
   const uint32_t lane_base = tmem + ((uint32_t)(32 * w4) << 16);
   const float sl2 = cx.p->a.scale_log2;
@@ -642,7 +652,7 @@ __device__ void softmax_tiles(const Ctx& cx, const Piece& pc, int gj0,
     float alpha = 1.f;
     if (jt == 0) {
       m = mx;
-    } else if (mx > m + kRescaleLog2) {
+    } else if (mx > m + C::kRescaleLog2) {
       need = true;
       alpha = exp2f(m - mx);
       m = mx;
@@ -664,7 +674,7 @@ __device__ void softmax_tiles(const Ctx& cx, const Piece& pc, int gj0,
       tc::tmem_wait_st();
       l *= alpha;
     }
-    const float mu = m == -INFINITY ? 0.f : m;
+    const float mu = (m == -INFINITY ? 0.f : m) - C::kShiftLog2;
     float sum4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
     for (int c = 0; c < kT; c += kC) {
@@ -696,8 +706,9 @@ __device__ void softmax_tiles(const Ctx& cx, const Piece& pc, int gj0,
   }
 }
 
+// `shift`: the factor (log2) that O and l carry.
 __device__ void epilogue(const Ctx& cx, const Piece& pc, uint32_t tmem, float m,
-                         float l) {
+                         float l, float shift) {
   const int lane = threadIdx.x & 31, w4 = (threadIdx.x >> 5) & 3;
   const uint32_t lane_base = tmem + ((uint32_t)(32 * w4) << 16);
   const int r = w4 * 32 + lane;
@@ -719,7 +730,7 @@ __device__ void epilogue(const Ctx& cx, const Piece& pc, uint32_t tmem, float m,
   }
   if (valid)
     cx.p->pre_lse[row] =
-        l > 0.f ? (m == -INFINITY ? 0.f : m) + log2f(l) : -INFINITY;
+        l > 0.f ? (m == -INFINITY ? 0.f : m) - shift + log2f(l) : -INFINITY;
   tc::fence_before();  // the reads precede this warp's next P
 }
 
@@ -838,7 +849,7 @@ __global__ void __cluster_dims__(2, 1, 1)
         tc::fence_after();
       }
       if (more) write_q<kFp8>(cx, pc, smem);
-      if (gj0) epilogue(cx, prev, tmem, m, l);
+      if (gj0) epilogue(cx, prev, tmem, m, l, C::kShiftLog2);
       if (!more) break;
       softmax_tiles<kFp8>(cx, pc, gj0, tmem, m, l);
       prev = pc;

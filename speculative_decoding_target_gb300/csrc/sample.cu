@@ -946,15 +946,19 @@ __global__ void __launch_bounds__(kThreads, 2)
               // (not finished: every CTA is still here)
               if (tid < csize) peer_store64(&s.cut, tid, s.cut);
             } else {
-              // every remaining cut: a prefix of the ranks
+              // Every remaining cut: a prefix of the ranks, and of those
+              // the ones that min-p keeps.  Those need not be a prefix: of
+              // two close logits the smaller may have the larger integer, a
+              // step of 2^-43 above.  So the ranks go up to the last kept
+              // one, and one between that is not kept has no weight.
               u64 limit = mass ? want : ~0ull;
               if (!mass && s.top_p < 1.f) limit = ceil_part(s.top_p, all);
               const bool keep = in && run < limit && w >= minw;
               w = keep ? w : 0;
               if (q < kRanked) s.wts[q] = w;
-              uint32_t nk;
               block_scan(s.warp_m, w, &all);
-              block_scan(s.warp_c, keep ? 1u : 0u, &nk);
+              const uint32_t nk =
+                  (uint32_t)block_max(s.warp_m, keep ? (u64)q + 1 : 0);
               if (!leave && tid < csize) {
                 peer_store64(&s.cut, tid, s.list[nk - 1]);
                 peer_store64(&s.total, tid, all);

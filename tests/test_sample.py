@@ -421,6 +421,61 @@ def test_drafts_and_filtered_targets_in_stochastic_verify():
         assert bool(kept[torch.arange(B), j, toks[:, j].long()].all())
 
 
+# Two neighbouring logits whose integer weights fall the other way round: the
+# larger logit's is one step of 2^-43 below min_p, the smaller's is min_p.
+# (temperature, largest logit, the larger, the smaller, min_p)
+TURNED = [
+    ("0x1.83611ap+0", "0x1.3edb4cp-2", "-0x1p-26", "-0x1.000002p-26",
+     "0x1.a0c668p-1"),
+    ("0x1.651896p+1", "0x1.1e31f6p+0", "-0x1.fffffep-25", "-0x1p-24",
+     "0x1.56f472p-1"),
+    ("0x1.b660e4p+1", "0x1.f744fcp+0", "-0x1p-24", "-0x1.000002p-24",
+     "0x1.2063b8p-1"),
+    ("0x1.0ebccp-1", "0x1.6b97cp-3", "-0x1p-27", "-0x1.000002p-27",
+     "0x1.6dfb24p-1"),
+]
+
+
+@gpu
+@pytest.mark.parametrize("cut", ["top-k", "top-p", "both", "none"])
+def test_min_p_between_neighbouring_logits(cut):
+    # whichever of the two min-p keeps, the token, the distribution and the
+    # filtered logits are those of one kept set
+    build.build()
+    V, rows = 6000, len(TURNED)
+    vals = [[float.fromhex(a) for a in r] for r in TURNED]
+    x = torch.full((rows, V), -float("inf"))
+    for r, (_, top, more, less, _) in enumerate(vals):
+        x[r, 4000], x[r, 3000], x[r, 17] = top, more, less
+        x[r, 5000] = top - 1000.0           # no weight: never kept
+    x = x.to(DEV)
+    f = lambda a, d=torch.float32: torch.tensor(a, dtype=d, device=DEV)
+    kw = dict(temperature=f([v[0] for v in vals]),
+              min_p=f([v[4] for v in vals]))
+    if cut in ("top-k", "both"):
+        kw["top_k"] = f([3] * rows, torch.int32)
+    if cut in ("top-p", "both"):
+        kw["top_p"] = f([0.9999999] * rows)
+    for u in (0.0, 0.2, 0.35, 0.5, 0.75, 0.99):
+        uu = f([u] * rows)
+        probs = torch.full_like(x, float("nan"))
+        filt = torch.full_like(x, float("nan"))
+        tok = sv.sample(x, uu, probs=probs, filtered=filt, **kw)
+        alone = sv.sample(x, uu, **kw)
+        assert torch.equal(tok, alone)
+        kept = torch.isfinite(filt)
+        assert torch.equal(kept, probs > 0)
+        assert bool(kept[:, 4000].all())
+        # the smaller logit of the two is at the border, not below it
+        assert bool(kept[:, 17].all())
+        assert int(kept.sum(1).max()) <= 3
+        p = probs.double()
+        assert bool(((p.sum(1) - 1).abs() < 2.0 ** -20).all())
+        run = p.cumsum(1)
+        want = (run > u * run[:, -1:]).int().argmax(1)
+        assert torch.equal(tok.long(), want)
+
+
 # ---------------------------------------------------------------- CPU tests
 
 FAKE = ctypes.c_void_p(0x100000)   # never dereferenced: checks come first

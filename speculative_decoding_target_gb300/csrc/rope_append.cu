@@ -83,11 +83,14 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
     qb = rot ? lane + n8 : qa + 1;
   }
   const int n_rows = p.hq + 2 * a.hkv;
-  const int tokens = a.batch * a.q_len;
+  // up to 2^31 - 1 tokens: the step past the last one needs the 32nd bit
+  const uint32_t q_len = a.q_len, tokens = a.batch * q_len;
   int buf = 0;
-  int b = blockIdx.x / a.q_len, i = blockIdx.x - b * a.q_len;
-  const int step_b = gridDim.x / a.q_len, step_i = gridDim.x - step_b * a.q_len;
-  for (int tok = blockIdx.x; tok < tokens; tok += gridDim.x, buf ^= 1) {
+  int b = blockIdx.x / q_len;
+  uint32_t i = blockIdx.x - b * q_len;
+  const int step_b = gridDim.x / q_len;
+  const uint32_t step_i = gridDim.x - step_b * q_len;
+  for (uint32_t tok = blockIdx.x; tok < tokens; tok += gridDim.x, buf ^= 1) {
     // the token's rows, at this lane's channels (8 lane on for values)
     const __nv_bfloat16* q_src = p.q + b * p.q_req + i * p.q_tok;
     const __nv_bfloat16* k_src = a.k_new + b * p.k_req + i * p.k_tok;
@@ -96,7 +99,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
     const int width =
         a.q_lens ? min(max(a.q_lens[b], 0), a.q_len) : a.q_len;
     const long long t = (long long)a.seq_lens[b] - width + i;
-    const bool live = i < width && t >= 0;
+    const bool live = (int)i < width && t >= 0;
     long long slot = -1;  // row of KV head 0 in the pool
     if (live && t < a.max_tokens) {
       const int page =
@@ -238,8 +241,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
     if (!ready) __syncthreads();  // a warp without rows
     b += step_b;
     i += step_i;
-    if (i >= a.q_len) {
-      i -= a.q_len;
+    if (i >= q_len) {
+      i -= q_len;
       ++b;
     }
   }

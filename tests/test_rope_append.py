@@ -310,6 +310,35 @@ def test_in_place_keys_only_stream_and_graph():
     assert torch.equal(out, again) and not torch.equal(out, want)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("batch", [1, 3])
+def test_as_many_rows_as_a_call_allows(batch):
+    # keys and values of a block padded to the largest batch * q_len, through
+    # strides of 0; the rows behind each width hold no token
+    build.build()
+    q_len = (2 ** 31 - 1) // batch
+    g = torch.Generator(device=DEV).manual_seed(4)
+    k, v = (torch.randn((1, 1, 1, 256), generator=g, device=DEV).to(
+        torch.bfloat16) for _ in range(2))
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device=DEV)
+    widths, seqs = [5, 0, 3][:batch], [5, 7, 20][:batch]
+    table = torch.arange(2 * batch, dtype=torch.int32, device=DEV).view(
+        batch, 2)
+    freq = sv.rope_frequencies(64, device=DEV)[0]
+    pools = []
+    for n in (8, q_len):
+        kp, vp = (torch.zeros((2 * batch, 1, 16, 256), dtype=torch.bfloat16,
+                              device=DEV) for _ in range(2))
+        assert sv.rope_append(
+            None, k.expand(batch, n, 1, 256), v.expand(batch, n, 1, 256), freq,
+            kp, vp, table, i32(*seqs), q_lens=i32(*widths)) is None
+        torch.cuda.synchronize()
+        pools.append((kp, vp))
+    assert torch.equal(pools[0][0], pools[1][0])
+    assert torch.equal(pools[0][1], pools[1][1])
+    assert int(pools[0][1].abs().amax(-1).count_nonzero()) == sum(widths)
+
+
 # ---------------------------------------------------------------- CPU tests
 
 FAKE = ctypes.c_void_p(0x100000)   # never dereferenced: checks come first

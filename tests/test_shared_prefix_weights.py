@@ -8,6 +8,8 @@ weight: 2^-36 max(w) sum_t |v_t|."""
 import pytest
 import torch
 
+import speculative_decoding_target_gb300 as sv
+import test_shared_prefix as base
 from test_shared_prefix import D, DEV, Case
 
 gpu = pytest.mark.gpu
@@ -71,3 +73,92 @@ def test_small_weights_beside_dominating_tokens(kv, bits):
         c.v &= 0x7F
     c.v[first, :, 0] = 0
     compare(c, c.run())
+
+
+# ---- every tile of a shared prefix counts ------------------------------------
+
+def mark_tiles(c):
+    """The shared tokens of 128-token tile n keep their value, made positive,
+    in channel n % 256 alone: that channel of the output is the weight of the
+    tile, whatever the length of the prefix, and its tolerance a fraction of
+    it."""
+    starts = c.starts.tolist()
+    for n, shared in enumerate(c.shared.tolist()):
+        ids = c.table[starts[n], :shared // c.page].long()
+        if not len(ids):
+            continue
+        tile = torch.arange(shared, device=c.v.device).view(
+            len(ids), 1, c.page, 1) // 128
+        own = tile % D == torch.arange(D, device=c.v.device)
+        x = c.v[ids]
+        x = x & 0x7F if c.kv == "fp8" else x.abs()
+        c.v[ids] = torch.where(own, x, torch.zeros_like(x))
+    return c
+
+
+def evaluate(c, wrong=None):
+    """The attention of c in 64 bits, rounded to bf16, with a mistake in the
+    shared tokens of tile 7: (what, ...)."""
+    out = torch.zeros_like(c.q)
+    G = c.hq // c.hkv
+    for b in range(c.B):
+        w, n = c.widths[b], c.seqs[b]
+        k, v = (c.dense(p, s, b, n) for p, s in ((c.k, c.ks), (c.v, c.vs)))
+        a, z = slice(7 * 128, 8 * 128), slice(12 * 128, 13 * 128)
+        count = torch.ones(n, dtype=torch.float64)
+        if wrong == "dropped":
+            count[a] = 0
+        elif wrong == "twice":
+            count[a] = 2
+        elif wrong == "other V":
+            v[:, a] = v[:, z].clone()
+        elif wrong == "other K":
+            k[:, a] = k[:, z].clone()
+        elif wrong == "halves of V":
+            v[:, a] = v[:, a].roll(64, 1)
+        for i in range(w):
+            m = n - w + i + 1
+            q = c.q[b, i].double().view(c.hkv, G, D)
+            s = torch.einsum("hgd,htd->hgt", q, k[:, :m]) * c.scale
+            p = torch.softmax(s, -1) * count[:m]
+            p = p / p.sum(-1, keepdim=True)
+            out[b, i] = torch.einsum("hgt,htd->hgd", p, v[:, :m]).reshape(
+                c.hq, D).to(torch.bfloat16)
+    return out
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_a_mistake_in_one_tile_shows(kv, monkeypatch):
+    # on the CPU: the tolerance holds the exact result, and none with one tile
+    # of a long prefix dropped, counted twice or with another tile's K or V
+    monkeypatch.setattr(base, "DEV", "cpu")
+    c = mark_tiles(Case([2], [30000], [100, 31], q_len=2, page=64, kv=kv,
+                        hq=6, hkv=1, seed=11))
+    c.check(evaluate(c))
+    for wrong in ("dropped", "twice", "other V", "other K", "halves of V"):
+        with pytest.raises(AssertionError):
+            c.check(evaluate(c, wrong))
+
+
+@gpu
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("shape", ["long", "one row", "small pages",
+                                   "many groups"])
+def test_every_tile_counts(kv, shape):
+    if shape == "long":            # several runs and pieces a CTA pair
+        c = Case([9, 2], [30000, 9000], [100] * 11, q_len=6, page=64, kv=kv,
+                 seed=11)
+    elif shape == "one row":
+        c = Case([40], [20000], [100 + b for b in range(40)], q_len=1,
+                 page=64, kv=kv, seed=13)
+    elif shape == "small pages":
+        c = Case([3, 4], [12000, 7000], [9 * b for b in range(7)], q_len=8,
+                 page=8, kv=kv, seed=14)
+    else:                          # 240 segments of ten tiles
+        c = Case([3] * 60, [1280] * 60, [20] * 180, q_len=2, page=64, kv=kv,
+                 seed=15)
+    mark_tiles(c)
+    ws = sv.alloc_workspace(256 << 20, DEV)
+    out = c.run(checked=True, workspace=ws)
+    assert sv.verify_status(ws) == 0
+    c.check(out)

@@ -162,3 +162,59 @@ def test_every_tile_counts(kv, shape):
     out = c.run(checked=True, workspace=ws)
     assert sv.verify_status(ws) == 0
     c.check(out)
+
+
+# ---- maxima that grow along the prefix ---------------------------------------
+
+def plant(c, b, row, tok, beta):
+    """Make shared token `tok` of request b's group beta times the queries of
+    block row `row` of request b, one head of each KV head: their scores grow
+    by about 23 beta (base 2), other rows' hardly."""
+    pg, at = c.table[b, tok // c.page].item(), tok % c.page
+    G = c.hq // c.hkv
+    for g in range(c.hkv):
+        x = c.q[b, row, g * G + (b + g) % G].float() * beta
+        if c.kv == "bf16":
+            c.k[pg, g, at] = x.to(torch.bfloat16)
+            continue
+        s = (x.view(4, 64).abs().amax(1) / 448).half()
+        c.ks[pg, g, at] = s
+        c.k[pg, g, at] = (x / s.float().repeat_interleave(64)).clamp(
+            -448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+
+
+@gpu
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_maxima_of_single_rows_grow(kv):
+    # one row of a warp at a time: in the second tile, in the middle twice in
+    # a row, in the last; with 240 pieces on 76 CTA pairs also behind another
+    # piece, in either of a pair's score buffers
+    c = Case([3] * 60, [1280] * 60, [20] * 180, q_len=2, page=64, kv=kv,
+             seed=31)
+    mark_tiles(c)
+    for n in range(60):
+        b = 3 * n
+        plant(c, b, 0, 128 + 5 + n, 0.6)
+        plant(c, b + 1, 1, 4 * 128 + 2 * n, 0.5)
+        plant(c, b + 1, 1, 5 * 128 + 127 - n, 1.0)
+        plant(c, b + 2, 0, 9 * 128 + n, 0.8)
+        plant(c, b, 0, 9 * 128 + 64 + n, 1.2)
+    ws = sv.alloc_workspace(256 << 20, DEV)
+    out = c.run(checked=True, workspace=ws)
+    assert sv.verify_status(ws) == 0
+    compare(c, out)
+
+
+@gpu
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("pre", [2048, 30016])
+def test_maxima_of_all_rows_grow_tile_by_tile(kv, pre):
+    # keys that grow from page to page; 30,016 tokens are cut into runs that
+    # each begin with a maximum of their own
+    c = Case([5], [pre], [20] * 5, seed=10, page=64, kv=kv)
+    n = pre // 64
+    grow = (6.2 / n) * torch.arange(n, device=DEV)
+    ids = c.table[0, :n].long()
+    x = c.k if kv == "bf16" else c.ks
+    x[ids] = (x[ids].float() * grow[:, None, None, None]).to(x.dtype)
+    compare(c, c.run())

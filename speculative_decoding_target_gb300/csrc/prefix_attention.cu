@@ -160,8 +160,18 @@ __device__ __forceinline__ bool wait_bar(const Ctx& cx, uint64_t* bar,
 
 // A place in a ring of N buffers and the parity of the wait for its current
 // use (a consumer's; a producer waits for the use before, of the other one).
+// The producers of K and of V, and the two dequantising sets, wait for the
+// release of a buffer (`empty`, `raw_empty`) only before their own units and
+// step over the others'.  A wait by parity returns at once while the phase
+// before the one it means is still open, as the phase before that has the same
+// parity.  Before unit i, the wait is for the release of unit i - N, and the
+// phase before is that of unit i - 2 N.  Units are released in order, and at
+// most 3 lie from one of a waiter's own to the next (V(n-1) K0 K1 V0 across a
+// piece border; the sets alternate), so the units up to i - 3 - N are known to
+// be released: i - 2 N is among them while N >= 3.
 template <int N>
 struct Ring {
+  static_assert(N >= 3, "a wait could take an earlier phase for its own");
   int at = 0;
   uint32_t parity = 0;
   bool wrapped = false;

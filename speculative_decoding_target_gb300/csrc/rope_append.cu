@@ -20,11 +20,12 @@
 // keys, then values), four rows in flight.  A lane's four pairs are the same
 // for every row, so their sines stay in registers.
 //
-// Measured: 8,192 tokens (268 MB) 47 us in a graph, 0.85 of the copy rate; what
-// is left is instructions (issue 66% busy, the ALU 54%), not trigonometry
-// (without it: the same time).  Four CTAs an SM (51.6 us a call) against three
-// (56.0), five (57.9, spills); reading lengths and page ids ahead cost more
-// instructions than it hid (58.8).
+// Measured: 8,192 tokens (268 MB) 48 us in a graph, 0.83 of the copy rate, 49.5
+// a call; what is left is instructions (issue 66% busy, the ALU 56%), not
+// trigonometry (without it: the same time).  On an earlier form of the loop, a
+// call took 51.6 us with four CTAs an SM, 56.0 with three and 57.9 with five
+// (spills), and 58.8 where lengths and page ids were read ahead, which cost more
+// instructions than it hid.
 #include "append.cuh"
 #include "common.cuh"
 #include "spec_verify.h"

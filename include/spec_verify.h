@@ -713,6 +713,44 @@ int spec_rope_append(const spec_rope_desc* desc, const void* q,
                      const int32_t* seq_lens, int32_t* positions,
                      int64_t* cache_loc, void* workspace, void* stream);
 
+/* Types of the norm weights of spec_norm_rope_append. */
+#define SPEC_WEIGHTS_FP32 0
+#define SPEC_WEIGHTS_BF16 1
+
+/*
+ * Norms of query and key heads.
+ *   weight_dtype   SPEC_WEIGHTS_*
+ *   eps            finite, > 0
+ *   weight_offset  finite; 0 for weights kept as they multiply, 1 for weights
+ *                  kept as their distance from one
+ *   q_weight       [256], one for all query heads, 4-byte aligned device
+ *                  pointer; NULL with num_q_heads == 0
+ *   k_weight       [256], one for all key heads, 4-byte aligned
+ */
+typedef struct {
+  int32_t weight_dtype;
+  float eps, weight_offset;
+  const void* q_weight;
+  const void* k_weight;
+} spec_norm_desc;
+
+/*
+ * spec_rope_append with an RMS norm of every query and key head before its
+ * rotation, in the same launch:
+ *     x_c <- x_c / sqrt(mean_c x_c^2 + eps) (weight_offset + weight_c)
+ * over the head's 256 channels.  Values are appended as they are.  Arithmetic
+ * is fp32 (squares of the inputs must lie in its range) and each result is
+ * rounded once, where it is stored.  Everything else as in spec_rope_append.
+ */
+int spec_norm_rope_append(const spec_rope_desc* desc,
+                          const spec_norm_desc* norm, const void* q,
+                          const void* k_new, const void* v_new,
+                          const double* freq, void* q_out, void* k_pages,
+                          void* v_pages, void* k_scales, void* v_scales,
+                          const int32_t* page_table, const int32_t* seq_lens,
+                          int32_t* positions, int64_t* cache_loc,
+                          void* workspace, void* stream);
+
 /* Message for the last nonzero return on this thread ("" if none). */
 const char* spec_last_error(void);
 

@@ -8,7 +8,8 @@ it is missing.
 from ._native import (SpecError, accept_workspace_size, alloc_workspace,
                       desc_for, dflash2_select, dflash2_select_into, greedy_accept, greedy_accept_commit,
                       greedy_accept_commit_into, greedy_accept_into,
-                      kv_append, load, make_desc, prepare_next_block,
+                      kv_append, load, make_desc, norm_rope_append,
+                      prepare_next_block,
                       prepare_next_block_into, rope_append, sample, set_wait_limit,
                       shared_workspace_size,
                       stochastic_accept,
@@ -24,7 +25,7 @@ __all__ = [
     "dflash2_select", "dflash2_select_into",
     "greedy_accept", "greedy_accept_commit", "greedy_accept_commit_into",
     "greedy_accept_into", "kv_append", "load", "make_desc",
-    "prepare_next_block", "prepare_next_block_into", "rope_append",
+    "norm_rope_append", "prepare_next_block", "prepare_next_block_into", "rope_append",
     "rope_frequencies", "sample", "set_wait_limit", "shared_workspace_size",
     "stochastic_accept",
     "stochastic_accept_into", "stochastic_workspace_size", "verify_attention",

@@ -41,7 +41,7 @@ EXPORTED = (
     "spec_select_workspace_size", "spec_dflash2_select",
     "spec_verify_set_wait_limit", "spec_rope_append",
     "spec_verify_attention_shared", "spec_verify_shared_workspace_size",
-    "spec_sample",
+    "spec_sample", "spec_norm_rope_append",
 )
 SELECT_MODES = {"greedy": 0, "map": 1}
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
@@ -77,6 +77,12 @@ class RopeDesc(ctypes.Structure):
                 ("q_strides", ctypes.c_int64 * 2),
                 ("k_strides", ctypes.c_int64 * 2),
                 ("v_strides", ctypes.c_int64 * 2)]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [("weight_dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("weight_offset", ctypes.c_float),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p)]
 
 
 class SampleDesc(ctypes.Structure):
@@ -135,6 +141,9 @@ def load(path: str = LIB_PATH):
     lib.spec_sample.restype = ctypes.c_int
     lib.spec_rope_append.argtypes = [ctypes.POINTER(RopeDesc)] + [P] * 15
     lib.spec_rope_append.restype = ctypes.c_int
+    lib.spec_norm_rope_append.argtypes = (
+        [ctypes.POINTER(RopeDesc), ctypes.POINTER(NormDesc)] + [P] * 15)
+    lib.spec_norm_rope_append.restype = ctypes.c_int
     lib.spec_verify_set_wait_limit.argtypes = [ctypes.c_int64]
     lib.spec_verify_set_wait_limit.restype = ctypes.c_int
     lib.spec_verify_status.argtypes = [P, ctypes.POINTER(u32), i32, P]
@@ -441,6 +450,34 @@ def rope_append(q, k_new, v_new, freq, k_pages, v_pages, page_table, seq_lens,
     (rope_frequencies).  Returns the rotated queries, bf16
     [B, q_len, Hq, 256] (q_out, which may be a contiguous q itself), or None.
     """
+    return _rope_append(q, k_new, v_new, None, freq, k_pages, v_pages,
+                        page_table, seq_lens, interleaved, attn_factor, q_out,
+                        k_scales, v_scales, positions, cache_loc, checked,
+                        workspace, q_lens, stream)
+
+
+def norm_rope_append(q, k_new, v_new, q_weight, k_weight, freq, k_pages,
+                     v_pages, page_table, seq_lens, *, eps: float = 1e-6,
+                     weight_offset: float = 0.0, interleaved: bool = False,
+                     attn_factor: float = 1.0,
+                     q_out: Optional[torch.Tensor] = None, k_scales=None,
+                     v_scales=None, positions=None, cache_loc=None,
+                     checked: bool = False, workspace=None, q_lens=None,
+                     stream=None):
+    """rope_append with an RMS norm of every query and key head before its
+    rotation: x / sqrt(mean(x^2) + eps) * (weight_offset + weight), weights
+    bf16 or fp32 [256] (q_weight None with q None).  Returns the rotated
+    queries, or None."""
+    return _rope_append(q, k_new, v_new, (q_weight, k_weight, eps,
+                                          weight_offset), freq, k_pages,
+                        v_pages, page_table, seq_lens, interleaved,
+                        attn_factor, q_out, k_scales, v_scales, positions,
+                        cache_loc, checked, workspace, q_lens, stream)
+
+
+def _rope_append(q, k_new, v_new, norm, freq, k_pages, v_pages, page_table,
+                 seq_lens, interleaved, attn_factor, q_out, k_scales, v_scales,
+                 positions, cache_loc, checked, workspace, q_lens, stream):
     B, q_len, hkv, d = k_new.shape
     hq = 0 if q is None else q.shape[2]
     _expect(k_new, torch.bfloat16, "k_new")
@@ -458,6 +495,16 @@ def rope_append(q, k_new, v_new, freq, k_pages, v_pages, page_table, seq_lens,
                                     device=q.device)
         _expect(q_out, torch.bfloat16, "q_out", (B, q_len, hq, d),
                 contiguous=True)
+    q_w = k_w = None
+    if norm is not None:
+        q_w, k_w, eps, offset = norm
+        if (k_w is None or (q_w is None) != (q is None)
+                or k_w.dtype not in (torch.bfloat16, torch.float32)):
+            raise SpecError(SPEC_ERR_ARG, "q_weight goes with q; weights are "
+                                          "bf16 or fp32")
+        _expect(k_w, k_w.dtype, "k_weight", (d,), contiguous=True)
+        if q_w is not None:
+            _expect(q_w, k_w.dtype, "q_weight", (d,), contiguous=True)
     fp8 = _expect_pools(k_pages, v_pages, k_scales, v_scales, hkv, d)
     _expect_optional(B, q_len, q_lens, positions, cache_loc)
     if (checked and workspace is not None
@@ -465,7 +512,8 @@ def rope_append(q, k_new, v_new, freq, k_pages, v_pages, page_table, seq_lens,
         raise SpecError(SPEC_ERR_WORKSPACE, "workspace of fewer than 4 bytes")
     on = _on_current_device((q, k_new, v_new, freq, q_out, k_pages, v_pages,
                              k_scales, v_scales, page_table, seq_lens, q_lens,
-                             positions, cache_loc, workspace), stream)
+                             positions, cache_loc, workspace, q_w, k_w),
+                            stream)
     desc = RopeDesc(B, q_len, hq, hkv, d, k_pages.shape[2], k_pages.shape[0],
                     page_table.shape[1],
                     SPEC_KV_FP8_E4M3 if fp8 else SPEC_KV_BF16,
@@ -474,11 +522,17 @@ def rope_append(q, k_new, v_new, freq, k_pages, v_pages, page_table, seq_lens,
                     2 * freq.shape[0], 1 if interleaved else 0, attn_factor,
                     _strides(q, "q") if q is not None else (0, 0),
                     _strides(k_new, "k_new"), _strides(v_new, "v_new"))
-    rc = load().spec_rope_append(
-        ctypes.byref(desc), _at(q), _at(k_new), _at(v_new), _at(freq),
-        _at(q_out) if q is not None else None, _at(k_pages), _at(v_pages),
-        _at(k_scales), _at(v_scales), _at(page_table), _at(seq_lens),
-        _at(positions), _at(cache_loc), _at(workspace), on)
+    args = (_at(q), _at(k_new), _at(v_new), _at(freq),
+            _at(q_out) if q is not None else None, _at(k_pages), _at(v_pages),
+            _at(k_scales), _at(v_scales), _at(page_table), _at(seq_lens),
+            _at(positions), _at(cache_loc), _at(workspace), on)
+    if norm is None:
+        rc = load().spec_rope_append(ctypes.byref(desc), *args)
+    else:
+        nd = NormDesc(int(k_w.dtype == torch.bfloat16), eps, offset, _at(q_w),
+                      _at(k_w))
+        rc = load().spec_norm_rope_append(ctypes.byref(desc),
+                                          ctypes.byref(nd), *args)
     if rc:
         _check(rc)
     return q_out

@@ -37,6 +37,11 @@ struct RopeParams {
   int hq, rotary;
   float factor;             // on the rotated channels
   long long q_req, q_tok, k_req, k_tok, v_req, v_tok;
+  // head norms before the rotation (q_weight also NULL without queries)
+  const void* q_weight;     // [256], bf16 or fp32; k_weight NULL: no norms
+  const void* k_weight;
+  int w_bf16;
+  float eps, w_offset;
 };
 
 // Quantise-on-write of one cached row by a whole warp: lane l holds channels

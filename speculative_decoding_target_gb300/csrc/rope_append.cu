@@ -59,13 +59,23 @@ __device__ __forceinline__ uint2 pack4(const float* x) {
                     *reinterpret_cast<const uint32_t*>(&hi));
 }
 
-template <bool kInterleaved>
+__device__ __forceinline__ float norm_weight(const RopeParams& p, const void* w,
+                                             int c) {
+  if (!w) return 0.f;  // no queries
+  return p.w_offset + (p.w_bf16
+                           ? __bfloat162float(
+                                 static_cast<const __nv_bfloat16*>(w)[c])
+                           : static_cast<const float*>(w)[c]);
+}
+
+template <bool kInterleaved, bool kNorm>
 __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
     rope_append_kernel(const RopeParams p) {
   // two buffers: a token's table is written while slow warps still read the
   // one before it
   __shared__ __align__(16) float2 s_cs[2][kHeadDim / 2];
   __shared__ __align__(16) float s_row[kWarps][kHeadDim];
+  __shared__ __align__(16) float s_w[kNorm ? 2 : 1][kNorm ? kHeadDim : 1];
   // the attention call that follows may be scheduled now (it waits for this
   // grid before touching memory)
   tc_grid_launch_dependents();
@@ -82,6 +92,11 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
     const int n8 = p.rotary >> 3;
     qa = rot ? lane : 2 * lane;
     qb = rot ? lane + n8 : qa + 1;
+  }
+  if constexpr (kNorm) {
+    s_w[0][tid] = norm_weight(p, p.q_weight, tid);
+    s_w[1][tid] = norm_weight(p, p.k_weight, tid);
+    __syncthreads();
   }
   const int n_rows = p.hq + 2 * a.hkv;
   // up to 2^31 - 1 tokens: the step past the last one needs the 32nd bit
@@ -172,10 +187,27 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
         if (r < p.hq + a.hkv) {
           const bool key = r >= p.hq;
           if (key && slot < 0) continue;
-          if (live && rot) {
+          if (live && (kNorm || rot)) {
             float x[8];
             unpack4(xa[e], x);
             unpack4(xb[e], x + 4);
+            if constexpr (kNorm) {
+              float ss = 0.f;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) ss = fmaf(x[k], x[k], ss);
+#pragma unroll
+              for (int o = 16; o; o >>= 1)
+                ss += __shfl_xor_sync(0xffffffffu, ss, o);
+              const float n = rsqrtf(fmaf(ss, 1.f / kHeadDim, p.eps));
+              const float4 wa =
+                  *reinterpret_cast<const float4*>(&s_w[key][4 * qa]);
+              const float4 wb =
+                  *reinterpret_cast<const float4*>(&s_w[key][4 * qb]);
+              x[0] *= n * wa.x; x[1] *= n * wa.y;
+              x[2] *= n * wa.z; x[3] *= n * wa.w;
+              x[4] *= n * wb.x; x[5] *= n * wb.y;
+              x[6] *= n * wb.z; x[7] *= n * wb.w;
+            }
             float y[8];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -256,10 +288,14 @@ cudaError_t launch_rope_append(const RopeParams& p, bool interleaved, int sms,
   const int tokens = p.a.batch * p.a.q_len;
   if (tokens == 0) return cudaSuccess;
   const int grid = min(tokens, sms * kCtasPerSm);
-  if (interleaved)
-    rope_append_kernel<true><<<grid, kWarps * 32, 0, s>>>(p);
+  if (p.k_weight && interleaved)
+    rope_append_kernel<true, true><<<grid, kWarps * 32, 0, s>>>(p);
+  else if (p.k_weight)
+    rope_append_kernel<false, true><<<grid, kWarps * 32, 0, s>>>(p);
+  else if (interleaved)
+    rope_append_kernel<true, false><<<grid, kWarps * 32, 0, s>>>(p);
   else
-    rope_append_kernel<false><<<grid, kWarps * 32, 0, s>>>(p);
+    rope_append_kernel<false, false><<<grid, kWarps * 32, 0, s>>>(p);
   return cudaGetLastError();
 }
 

@@ -643,14 +643,14 @@ int spec_kv_append(const spec_attn_desc* desc, const void* k_new,
   return SPEC_OK;
 }
 
-int spec_rope_append(const spec_rope_desc* desc, const void* q,
-                     const void* k_new, const void* v_new, const double* freq,
-                     void* q_out, void* k_pages, void* v_pages, void* k_scales,
-                     void* v_scales, const int32_t* page_table,
-                     const int32_t* seq_lens, int32_t* positions,
-                     int64_t* cache_loc, void* workspace, void* stream) {
+namespace {
+int rope_append(const spec_rope_desc* d, const spec_norm_desc* norm,
+                const void* q, const void* k_new, const void* v_new,
+                const double* freq, void* q_out, void* k_pages, void* v_pages,
+                void* k_scales, void* v_scales, const int32_t* page_table,
+                const int32_t* seq_lens, int32_t* positions,
+                int64_t* cache_loc, void* workspace, void* stream) {
   g_err[0] = 0;
-  const spec_rope_desc* d = desc;
   if (!d) return fail(SPEC_ERR_ARG, "desc is NULL");
   if (d->batch < 0 || d->q_len < 1 ||
       (long long)d->batch * d->q_len >= (1LL << 31))
@@ -685,7 +685,22 @@ int spec_rope_append(const spec_rope_desc* desc, const void* q,
     if (d->q_strides[k] < 0 || d->k_strides[k] < 0 || d->v_strides[k] < 0 ||
         d->q_strides[k] % 8 || d->k_strides[k] % 8 || d->v_strides[k] % 8)
       return fail(SPEC_ERR_ARG, "strides must be multiples of 8 and >= 0");
+  if (norm) {
+    if (norm->weight_dtype != SPEC_WEIGHTS_FP32 &&
+        norm->weight_dtype != SPEC_WEIGHTS_BF16)
+      return fail(SPEC_ERR_ARG, "weight_dtype %d", norm->weight_dtype);
+    if (!(norm->eps > 0.f && norm->eps < 3.0e38f))
+      return fail(SPEC_ERR_ARG, "eps must be finite and > 0");
+    if (!(norm->weight_offset > -3.0e38f && norm->weight_offset < 3.0e38f))
+      return fail(SPEC_ERR_ARG, "weight_offset must be finite");
+  }
   if (d->batch == 0) return SPEC_OK;
+  if (norm) {
+    if (!norm->k_weight || !norm->q_weight != (d->num_q_heads == 0))
+      return fail(SPEC_ERR_ARG, "k_weight, and q_weight with num_q_heads > 0");
+    if (!aligned(norm->k_weight, 4) || !aligned(norm->q_weight, 4))
+      return fail(SPEC_ERR_ALIGN, "norm weights must be 4-byte aligned");
+  }
   if (!k_new || !v_new || !freq || !k_pages || !v_pages || !page_table ||
       !seq_lens)
     return fail(SPEC_ERR_ARG, "NULL tensor pointer");
@@ -748,6 +763,13 @@ int spec_rope_append(const spec_rope_desc* desc, const void* q,
   p.k_tok = d->k_strides[1];
   p.v_req = d->v_strides[0];
   p.v_tok = d->v_strides[1];
+  if (norm) {
+    p.q_weight = norm->q_weight;
+    p.k_weight = norm->k_weight;
+    p.w_bf16 = norm->weight_dtype == SPEC_WEIGHTS_BF16;
+    p.eps = norm->eps;
+    p.w_offset = norm->weight_offset;
+  }
   cudaError_t e;
   if (checked) {
     p.a.status = static_cast<uint32_t*>(workspace);
@@ -760,6 +782,32 @@ int spec_rope_append(const spec_rope_desc* desc, const void* q,
     return fail(SPEC_ERR_CUDA, "rotary append launch: %s",
                 cudaGetErrorString(e));
   return SPEC_OK;
+}
+}  // namespace
+
+int spec_rope_append(const spec_rope_desc* desc, const void* q,
+                     const void* k_new, const void* v_new, const double* freq,
+                     void* q_out, void* k_pages, void* v_pages, void* k_scales,
+                     void* v_scales, const int32_t* page_table,
+                     const int32_t* seq_lens, int32_t* positions,
+                     int64_t* cache_loc, void* workspace, void* stream) {
+  return rope_append(desc, nullptr, q, k_new, v_new, freq, q_out, k_pages,
+                     v_pages, k_scales, v_scales, page_table, seq_lens,
+                     positions, cache_loc, workspace, stream);
+}
+
+int spec_norm_rope_append(const spec_rope_desc* desc,
+                          const spec_norm_desc* norm, const void* q,
+                          const void* k_new, const void* v_new,
+                          const double* freq, void* q_out, void* k_pages,
+                          void* v_pages, void* k_scales, void* v_scales,
+                          const int32_t* page_table, const int32_t* seq_lens,
+                          int32_t* positions, int64_t* cache_loc,
+                          void* workspace, void* stream) {
+  if (!norm) return fail(SPEC_ERR_ARG, "norm is NULL");
+  return rope_append(desc, norm, q, k_new, v_new, freq, q_out, k_pages,
+                     v_pages, k_scales, v_scales, page_table, seq_lens,
+                     positions, cache_loc, workspace, stream);
 }
 
 int spec_prepare_next_block(const spec_width_policy* pol, int32_t batch,

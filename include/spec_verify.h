@@ -206,6 +206,36 @@ size_t spec_verify_shared_workspace_size(const spec_attn_desc* desc,
                                          int32_t groups);
 
 /*
+ * Attention of a chunk of new tokens over the paged cache: a prompt, or a piece
+ * of one, whose keys and values are already appended (spec_rope_append).
+ *
+ * spec_verify_attention for any q_len >= 1 (batch * q_len * Hq < 2^31): row i <
+ * q_b of request b is token seq_lens[b] - q_b + i and attends causally to the
+ * first seq_lens[b] - q_b + i + 1 cached tokens; rows i >= q_b, and rows whose
+ * window is empty, output zeros.  q_len * Hq / Hkv is not bounded.  The weights
+ * are rounded once to the type of the values (fp16 for FP8 KV).  What lies in
+ * the pool behind a request's tokens may hold any bits; cached values that some
+ * row of the chunk sees have to be finite.
+ *
+ *   page_size  >= 8 (below: SPEC_ERR_UNSUPPORTED unless the chunk fits
+ *              spec_verify_attention's block)
+ *   workspace  >= spec_chunk_workspace_size(desc) bytes, 256-byte aligned;
+ *              contents need no initialisation
+ * Everything else as in spec_verify_attention; all lengths are read on the
+ * device and may change between graph replays.  The result is the same on
+ * every run.
+ */
+int spec_chunk_attention(const spec_attn_desc* desc, const void* q,
+                         const void* k_pages, const void* v_pages,
+                         const void* k_scales, const void* v_scales,
+                         const int32_t* page_table, const int32_t* seq_lens,
+                         float scale, void* out, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/* Workspace bytes for spec_chunk_attention (0 on a bad desc). */
+size_t spec_chunk_workspace_size(const spec_attn_desc* desc);
+
+/*
  * Test hook for the failure path: the main-loop bound, in SM clock cycles,
  * of every mbarrier wait of the split kernels in calls made with
  * SPEC_FLAG_CHECKED.  0 (the default) restores the normal bound of about

@@ -6,6 +6,7 @@ this package does not load the library; the first call does, and raises if
 it is missing.
 """
 from ._native import (SpecError, accept_workspace_size, alloc_workspace,
+                      chunk_attention, chunk_workspace_size,
                       desc_for, dflash2_select, dflash2_select_into, greedy_accept, greedy_accept_commit,
                       greedy_accept_commit_into, greedy_accept_into,
                       kv_append, load, make_desc, norm_rope_append,
@@ -21,7 +22,8 @@ from ._native import (SpecError, accept_workspace_size, alloc_workspace,
 from .rope import rope_frequencies
 
 __all__ = [
-    "SpecError", "accept_workspace_size", "alloc_workspace", "desc_for",
+    "SpecError", "accept_workspace_size", "alloc_workspace", "chunk_attention",
+    "chunk_workspace_size", "desc_for",
     "dflash2_select", "dflash2_select_into",
     "greedy_accept", "greedy_accept_commit", "greedy_accept_commit_into",
     "greedy_accept_into", "kv_append", "load", "make_desc",

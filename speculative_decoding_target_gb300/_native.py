@@ -41,7 +41,8 @@ EXPORTED = (
     "spec_select_workspace_size", "spec_dflash2_select",
     "spec_verify_set_wait_limit", "spec_rope_append",
     "spec_verify_attention_shared", "spec_verify_shared_workspace_size",
-    "spec_sample", "spec_norm_rope_append",
+    "spec_sample", "spec_norm_rope_append", "spec_chunk_attention",
+    "spec_chunk_workspace_size",
 )
 SELECT_MODES = {"greedy": 0, "map": 1}
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
@@ -137,6 +138,10 @@ def load(path: str = LIB_PATH):
         ctypes.POINTER(AttnDesc), P, P, P, P, P, P, P, i32, P, P,
         ctypes.c_float, P, P, sz, P]
     lib.spec_verify_attention_shared.restype = ctypes.c_int
+    lib.spec_chunk_workspace_size.argtypes = [ctypes.POINTER(AttnDesc)]
+    lib.spec_chunk_workspace_size.restype = sz
+    lib.spec_chunk_attention.argtypes = lib.spec_verify_attention.argtypes
+    lib.spec_chunk_attention.restype = ctypes.c_int
     lib.spec_sample.argtypes = [ctypes.POINTER(SampleDesc)] + [P] * 10
     lib.spec_sample.restype = ctypes.c_int
     lib.spec_rope_append.argtypes = [ctypes.POINTER(RopeDesc)] + [P] * 15
@@ -382,6 +387,56 @@ def verify_attention_shared(q, k_pages, v_pages, page_table, seq_lens,
         _at(v_scales), _at(page_table), _at(seq_lens), groups,
         _at(group_starts), _at(shared_lens), scale, _at(out), _at(workspace),
         workspace.numel(), on)
+    if rc:
+        _check(rc)
+    return out
+
+
+def chunk_workspace_size(desc: AttnDesc) -> int:
+    n = load().spec_chunk_workspace_size(ctypes.byref(desc))
+    if n == 0:
+        raise SpecError(SPEC_ERR_ARG, load().spec_last_error().decode())
+    return int(n)
+
+
+def chunk_attention(q, k_pages, v_pages, page_table, seq_lens, *,
+                    scale: float, k_scales=None, v_scales=None,
+                    out: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None,
+                    checked: bool = False, q_lens=None,
+                    stream=None) -> torch.Tensor:
+    """Attention of a chunk of new tokens (a prompt or a piece of one, already
+    appended) over the paged cache, causal within the chunk: q bf16
+    [B, q_len, Hq, 256] for any q_len, q_lens optional int32 [B] tokens per
+    request of a chunk padded to q_len.  Returns out bf16 [B, q_len, Hq, 256]."""
+    B, q_len, hq, d = q.shape
+    _expect(q, torch.bfloat16, "q", contiguous=True)
+    fp8 = _expect_pools(k_pages, v_pages, k_scales, v_scales,
+                        k_pages.shape[1], d)
+    _expect(page_table, torch.int32, "page_table", contiguous=True)
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise SpecError(SPEC_ERR_ARG, f"page_table must have {B} rows")
+    _expect(seq_lens, torch.int32, "seq_lens", (B,), True)
+    _expect_optional(B, q_len, q_lens)
+    if out is None:
+        with _made_on(stream):
+            out = torch.empty_like(q)
+    _expect(out, torch.bfloat16, "out", q.shape, True)
+    on = _on_current_device((q, k_pages, v_pages, k_scales, v_scales,
+                             page_table, seq_lens, q_lens, out, workspace),
+                            stream)
+    desc = AttnDesc(B, q_len, hq, k_pages.shape[1], d, k_pages.shape[2],
+                    k_pages.shape[0], page_table.shape[1],
+                    SPEC_KV_FP8_E4M3 if fp8 else SPEC_KV_BF16,
+                    SPEC_FLAG_CHECKED if checked else 0,
+                    None if q_lens is None else q_lens.data_ptr())
+    if workspace is None:
+        with _made_on(stream):
+            workspace = alloc_workspace(chunk_workspace_size(desc), q.device)
+    rc = load().spec_chunk_attention(
+        ctypes.byref(desc), _at(q), _at(k_pages), _at(v_pages), _at(k_scales),
+        _at(v_scales), _at(page_table), _at(seq_lens), scale, _at(out),
+        _at(workspace), workspace.numel() * workspace.element_size(), on)
     if rc:
         _check(rc)
     return out

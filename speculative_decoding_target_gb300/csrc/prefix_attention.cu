@@ -60,6 +60,9 @@
 // Every wait is bounded as in verify_attention_tc.cu.
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
+#include "chunk_attention.cuh"
 #include "pair_ptx.cuh"
 #include "shared_prefix.cuh"
 #include "spec_verify.h"
@@ -111,6 +114,9 @@ struct Bars {
   uint64_t q_full;             // leader: Q written by both CTAs
   uint64_t raw_full[kRaw];     // FP8, own: staged bytes landed
   uint64_t raw_empty[kRaw];    // FP8, own: staged bytes converted
+  // chunk, bf16, own: V that needs zeros landed.  One a slot, as with short
+  // pieces several such slots may have landed before the first is looked at.
+  uint64_t tail_full[kMaxSlots];
   uint64_t drain;              // both: every MMA issued is done
 };
 
@@ -119,13 +125,15 @@ struct Ctx {
   volatile int* abort;
   uint32_t peer_abort;         // cluster address of the other CTA's flag
   uint32_t rank;
-  const SharedParams* p;
+  const AttnParams* a;
+  float* pre_o;
+  float* pre_lse;
 };
 
 __device__ __forceinline__ void give_up(const Ctx& cx) {
   *cx.abort = 1;
   tc::store_cluster(cx.peer_abort, 1u);
-  if (cx.p->a.status) atomicOr(cx.p->a.status, SPEC_STATUS_TIMEOUT);
+  if (cx.a->status) atomicOr(cx.a->status, SPEC_STATUS_TIMEOUT);
 }
 
 // Barriers that carry generic writes of the other CTA (Q, dequantised tiles)
@@ -135,7 +143,7 @@ template <bool kCluster>
 __device__ __noinline__ bool wait_slow(const Ctx& cx, uint32_t a,
                                        uint32_t parity, bool drain) {
   if (!drain && *cx.abort) return false;
-  const long long bound = drain ? kDrainWaitCycles : cx.p->a.wait_cycles;
+  const long long bound = drain ? kDrainWaitCycles : cx.a->wait_cycles;
   const long long t0 = clock64();
   while (true) {
     if (kCluster ? tc::bar_try_wait_cluster(a, parity)
@@ -189,11 +197,25 @@ struct Piece {
   int lead, start, rows_total;  // page-table row, first request, group rows
   int g, row0;                  // KV head, first row of this CTA's 128
   int tok, n_tiles;
-  int slot;                     // partial slot
+  int slot;                     // partial slot, or -1: straight to the output
+  // a chunk's piece
+  int last;                     // last cached token of the request
+  int first;                    // block row of row 0
+  int limit;                    // tokens that row 0 sees
+  // Cached tokens of the last tile; behind them its V rows become zeros: their
+  // weights are zero, but what lies there may not be a number.
+  __device__ __forceinline__ int tail_tokens() const {
+    return min(last + 1 - (tok + (n_tiles - 1) * kT), kT);
+  }
 };
 
-__device__ __forceinline__ int page_id(const AttnParams& p, int lead, int t) {
-  return __ldg(p.page_table + (long long)lead * p.max_pages + (t >> p.log2_ps));
+// Behind the cache the page of its last token stands in: the tokens are masked.
+template <bool kCausal>
+__device__ __forceinline__ int page_id(const AttnParams& p, const Piece& pc,
+                                       int t) {
+  if (kCausal) t = min(t, pc.last);
+  return __ldg(p.page_table + (long long)pc.lead * p.max_pages +
+               (t >> p.log2_ps));
 }
 // Looked at only when the page is used, so that the load of the id runs ahead.
 __device__ __forceinline__ int checked_page(const AttnParams& p, int page) {
@@ -237,8 +259,8 @@ template <bool kOne>
 __device__ __forceinline__ void load_slot(const Ctx& cx, Producer<false>& pr,
                                           uint32_t smem, uint32_t full0,
                                           const CUtensorMap* map, bool is_v,
-                                          long long row0, long long row1,
-                                          int nb, int rpb) {
+                                          bool tail, long long row0,
+                                          long long row1, int nb, int rpb) {
   using C = Cfg<false>;
   const int s = pr.ring.at;
   const bool leads = kOne || (threadIdx.x & 31) == 0;
@@ -250,11 +272,22 @@ __device__ __forceinline__ void load_slot(const Ctx& cx, Producer<false>& pr,
     pr.live = false;
     return;
   }
-  if (leads && cx.rank == 0)
-    tc::bar_arrive_expect_tx(tc::smem_u32(&cx.bars->full[s]),
-                             2 * C::kSlotBytes);
+  // A tail's bytes count on each CTA's own barrier, for the warps that write
+  // its zeros; the issuer learns of them with P.
+  if (leads && tail)
+    tc::bar_arrive_expect_tx(tc::smem_u32(&cx.bars->tail_full[s]),
+                             C::kSlotBytes);
+  if (leads && cx.rank == 0) {
+    if (tail)
+      tc::bar_arrive(tc::smem_u32(&cx.bars->full[s]));
+    else
+      tc::bar_arrive_expect_tx(tc::smem_u32(&cx.bars->full[s]),
+                               2 * C::kSlotBytes);
+  }
   const uint32_t dst = smem + C::kOffRing + s * C::kSlotBytes;
-  const uint32_t full = full0 + s * 8;
+  const uint32_t full =
+      tail ? tc::map_to(tc::smem_u32(&cx.bars->tail_full[s]), cx.rank)
+           : full0 + s * 8;
   const int x0 = is_v ? (int)cx.rank * 128 : 0;
   const int x1 = is_v ? x0 : 128;
   for (int b = 0; b < nb; ++b) {
@@ -326,12 +359,12 @@ __device__ __forceinline__ void load_raw(const Ctx& cx, Producer<true>& pr,
 // One warp loads the K units of the order K0 K1 V0 K2 V1 .., another the V
 // units (with pages of 16 tokens a unit is 16 copies, more than one warp
 // issues in a tile's time); both step through the whole ring.
-template <bool kFp8, bool kOne>
+template <bool kFp8, bool kCausal, bool kOne>
 __device__ __forceinline__ void produce_piece(const Ctx& cx, const Piece& pc,
                                               Producer<kFp8>& pr, uint32_t smem,
                                               const CUtensorMap* map,
                                               bool v_side) {
-  const AttnParams& p = cx.p->a;
+  const AttnParams& p = *cx.a;
   const int lane = threadIdx.x & 31;
   const int rpb = p.box_rows, nb = kOne ? 1 : 64 / rpb;
   const uint32_t full0 = tc::map_to(tc::smem_u32(&cx.bars->full[0]), 0);
@@ -339,8 +372,9 @@ __device__ __forceinline__ void produce_piece(const Ctx& cx, const Piece& pc,
   // K: this CTA's 64 tokens of a tile; V: all 128, in two halves
   const int t0 = pc.tok + (kOne ? 0 : (lane & (nb - 1)) * rpb) +
                  (v_side ? 0 : (int)cx.rank * 64);
-  int page0 = page_id(p, pc.lead, t0);
-  int page1 = v_side ? page_id(p, pc.lead, t0 + 64) : 0;
+  int page0 = page_id<kCausal>(p, pc, t0);
+  int page1 = v_side ? page_id<kCausal>(p, pc, t0 + 64) : 0;
+  const bool tails = kCausal && !kFp8 && v_side && pc.tail_tokens() < kT;
   if (v_side) pr.ring.next();  // K0
   for (int j = 0; j < pc.n_tiles && pr.live; ++j) {
     // V: K of the next tile lies before V of this one; K: V of the tile
@@ -351,27 +385,28 @@ __device__ __forceinline__ void produce_piece(const Ctx& cx, const Piece& pc,
     const long long r1 =
         v_side ? pool_row(p, checked_page(p, page1), pc.g, t + 64) : r0;
     if (j + 1 < pc.n_tiles) {
-      page0 = page_id(p, pc.lead, t + kT);
-      if (v_side) page1 = page_id(p, pc.lead, t + kT + 64);
+      page0 = page_id<kCausal>(p, pc, t + kT);
+      if (v_side) page1 = page_id<kCausal>(p, pc, t + kT + 64);
     }
     if constexpr (kFp8)
       load_raw<kOne>(cx, pr, smem, map, scales, v_side, r0, r1, nb, rpb);
     else
-      load_slot<kOne>(cx, pr, smem, full0, map, v_side, r0, r1, nb, rpb);
+      load_slot<kOne>(cx, pr, smem, full0, map, v_side,
+                      tails && j + 1 == pc.n_tiles, r0, r1, nb, rpb);
     if (!v_side && j > 0) pr.ring.next();  // V of tile j - 1
   }
   if (!v_side) pr.ring.next();  // V of the last tile
 }
 
-template <bool kFp8>
+template <bool kFp8, bool kCausal>
 __device__ void produce(const Ctx& cx, const Piece& pc, Producer<kFp8>& pr,
                         uint8_t* smem, const CUtensorMap* map, bool v_side) {
   const uint32_t base = tc::smem_u32(smem);
-  if (cx.p->a.box_rows == 64) {
+  if (cx.a->box_rows == 64) {
     if ((threadIdx.x & 31) == 0)
-      produce_piece<kFp8, true>(cx, pc, pr, base, map, v_side);
+      produce_piece<kFp8, kCausal, true>(cx, pc, pr, base, map, v_side);
   } else {
-    produce_piece<kFp8, false>(cx, pc, pr, base, map, v_side);
+    produce_piece<kFp8, kCausal, false>(cx, pc, pr, base, map, v_side);
   }
 }
 
@@ -399,8 +434,11 @@ struct Dequant {
   int turn = 0;  // staging buffers so far
 };
 
+// `tokens`: those of the unit that are cached (chunk: the others become zeros).
+template <bool kCausal>
 __device__ __forceinline__ void dequant_unit(const Ctx& cx, uint8_t* smem,
-                                             Dequant& dq, bool is_v) {
+                                             Dequant& dq, bool is_v,
+                                             int tokens) {
   using C = Cfg<true>;
   const int tid = (threadIdx.x - 256) & 127, lane = threadIdx.x & 31;
   const int c = tid & 7, tok0 = tid >> 3;
@@ -452,6 +490,7 @@ __device__ __forceinline__ void dequant_unit(const Ctx& cx, uint8_t* smem,
       b.y = e4m3x2_to_f16x2(w[2] >> 16, s2);
       b.z = e4m3x2_to_f16x2(w[3] & 0xFFFF, s2);
       b.w = e4m3x2_to_f16x2(w[3] >> 16, s2);
+      if (kCausal && h * 64 + tok >= tokens) a = b = make_uint4(0, 0, 0, 0);
       uint8_t* row = out + tok * 128;
       const int first = ch + flip, second = ch + 1 - flip;
       *reinterpret_cast<uint4*>(row + ((first ^ (tok & 7)) << 4)) = flip ? b : a;
@@ -468,6 +507,7 @@ __device__ __forceinline__ void dequant_unit(const Ctx& cx, uint8_t* smem,
   dq.raw.next();
 }
 
+template <bool kCausal>
 __device__ void dequant_piece(const Ctx& cx, const Piece& pc, uint8_t* smem,
                               Dequant& dq) {
   // units K0 K1 V0 K2 V1 .. V(n-2) V(n-1): unit 0 and the odd ones but the
@@ -475,7 +515,8 @@ __device__ void dequant_piece(const Ctx& cx, const Piece& pc, uint8_t* smem,
   const int units = 2 * pc.n_tiles;
 #pragma unroll 1
   for (int k = 0; k < units; ++k)
-    dequant_unit(cx, smem, dq, is_v_unit(k, units));
+    dequant_unit<kCausal>(cx, smem, dq, is_v_unit(k, units),
+                          kCausal && k == units - 1 ? pc.tail_tokens() : kT);
 }
 
 // ---- warp 1 of the leader, one thread: MMA issue ----------------------------
@@ -515,12 +556,15 @@ __device__ __forceinline__ bool issue_qk(const Ctx& cx, Slots<kFp8>& seq, int gj
   return true;
 }
 
+// tail: P comes with zeros in V, written by both CTAs.
 template <bool kFp8>
 __device__ __forceinline__ bool issue_pv(const Ctx& cx, Slots<kFp8>& seq, int gj,
-                                         bool first, uint32_t tmem,
+                                         bool first, bool tail, uint32_t tmem,
                                          uint32_t smem) {
   using C = Cfg<kFp8>;
-  if (!wait_bar(cx, &cx.bars->p_full[gj & 1], (uint32_t)(gj >> 1) & 1))
+  uint64_t* p_full = &cx.bars->p_full[gj & 1];
+  const uint32_t phase = (uint32_t)(gj >> 1) & 1;
+  if (tail ? !wait_bar<true>(cx, p_full, phase) : !wait_bar(cx, p_full, phase))
     return false;
   const uint32_t pt = tmem + kColS + (gj & 1) * kT;
   const uint64_t b = tc::desc_sw128(
@@ -538,18 +582,21 @@ __device__ __forceinline__ bool issue_pv(const Ctx& cx, Slots<kFp8>& seq, int gj
   return true;
 }
 
-template <bool kFp8>
+template <bool kFp8, bool kCausal>
 __device__ void mma_piece(const Ctx& cx, const Piece& pc, int gj0, int n_piece,
                           Slots<kFp8>& seq, uint32_t tmem, uint8_t* smem_ptr) {
   const uint32_t smem = tc::smem_u32(smem_ptr);
   if (!wait_bar<true>(cx, &cx.bars->q_full, (uint32_t)n_piece & 1)) return;
   tc::fence_after();
+  const bool tails = kCausal && !kFp8 && pc.tail_tokens() < kT;
 #pragma unroll (kFp8 ? 1 : 2)
   for (int j = -1; j < pc.n_tiles; ++j) {
     if (j + 1 < pc.n_tiles &&
         !issue_qk<kFp8>(cx, seq, gj0 + j + 1, tmem, smem))
       return;
-    if (j >= 0 && !issue_pv<kFp8>(cx, seq, gj0 + j, j == 0, tmem, smem)) return;
+    if (j >= 0 && !issue_pv<kFp8>(cx, seq, gj0 + j, j == 0,
+                                  tails && j + 1 == pc.n_tiles, tmem, smem))
+      return;
   }
 }
 
@@ -577,14 +624,20 @@ __device__ void relay_piece(const Ctx& cx, const Piece& pc, Slots<true>& seq,
 // ---- warps 4..7: Q, softmax, epilogue ---------------------------------------
 // A warp writes its 32 rows of Q, one row at a time: lane l moves chunk l (8
 // channels) of the row, eight rows in flight.
-template <bool kFp8>
+template <bool kFp8, bool kCausal>
 __device__ void write_q(const Ctx& cx, const Piece& pc, uint8_t* smem) {
-  const AttnParams& p = cx.p->a;
+  const AttnParams& p = *cx.a;
   const int lane = threadIdx.x & 31, w4 = (threadIdx.x >> 5) & 3;
   // this lane's row: its place in q, or -1
   const int R = pc.row0 + w4 * 32 + lane;
   long long src = -1;
-  if (R < pc.rows_total) {
+  if (kCausal) {
+    if (R < pc.rows_total) {
+      const int tok = R / p.group;
+      src = (((long long)pc.lead * p.q_len + pc.first + tok) * p.hq +
+             pc.g * p.group + (R - tok * p.group)) * kHeadDim;
+    }
+  } else if (R < pc.rows_total) {
     const int bq = R / p.rows, r = R - bq * p.rows;
     const int b = pc.start + bq, i = r / p.group;
     if (i < block_rows(p, b))
@@ -630,17 +683,55 @@ __device__ __forceinline__ void store8(float* dst, const float* v, float k) {
                : "memory");
 }
 
-template <bool kFp8>
+// This CTA's half of the last tile's V has landed: thread r makes the row of
+// token r zeros if nothing is cached there.
+__device__ __forceinline__ void zero_tail(const Ctx& cx, const Piece& pc,
+                                          uint8_t* smem, int slot,
+                                          uint32_t parity) {
+  wait_bar(cx, &cx.bars->tail_full[slot], parity);
+  const int r = threadIdx.x & 127;
+  if (r >= pc.tail_tokens()) {
+    uint8_t* row = smem + Cfg<false>::kOffRing + slot * Cfg<false>::kSlotBytes +
+                   (r >> 6) * kHalfBytes + (r & 63) * 128;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      *reinterpret_cast<uint4*>(row + c * 16) = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(row + kBlockBytes + c * 16) =
+          make_uint4(0, 0, 0, 0);
+    }
+  }
+  tc::fence_proxy_async_smem();
+}
+
+// Scores from column n on count for nothing.
+template <int N>
+__device__ __forceinline__ void hide(uint32_t* s, int n) {
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+    if (k >= n) s[k] = 0xff800000u;  // -inf
+}
+
+// `tails`: the parities of the slots' tail barriers.
+template <bool kFp8, bool kCausal>
 __device__ void softmax_tiles(const Ctx& cx, const Piece& pc, int gj0,
-                              uint32_t tmem, float& m, float& l) {
+                              uint32_t tmem, uint8_t* smem, uint32_t& tails,
+                              float& m, float& l) {
   using C = Cfg<kFp8>;
   const int lane = threadIdx.x & 31, w4 = (threadIdx.x >> 5) & 3;
   const uint32_t lane_base = tmem + ((uint32_t)(32 * w4) << 16);
-  const float sl2 = cx.p->a.scale_log2;
+  const float sl2 = cx.a->scale_log2;
   m = -INFINITY;
   l = 0.f;
+  // tokens of the piece that this row sees, and that the warp's first row does
+  int seen = 0, seen0 = 0;
+  if (kCausal) {
+    const int R = pc.row0 + w4 * 32;
+    seen = pc.limit + (R + lane) / cx.a->group - pc.tok;
+    seen0 = pc.limit + R / cx.a->group - pc.tok;
+  }
   for (int jt = 0; jt < pc.n_tiles; ++jt) {
     const int gj = gj0 + jt;
+    const bool masked = kCausal && seen0 < (jt + 1) * kT;
     const uint32_t sbuf = lane_base + kColS + (gj & 1) * kT;
     wait_bar(cx, &cx.bars->s_full[gj & 1], (uint32_t)(gj >> 1) & 1);
     tc::fence_after();
@@ -653,6 +744,7 @@ __device__ void softmax_tiles(const Ctx& cx, const Piece& pc, int gj0,
 #pragma unroll 1
     for (int c = 0; c < kT; c += kC) {
       tc::tmem_ld_cols<kC>(sbuf + c, raw);
+      if (masked) hide<kC>(raw, seen - jt * kT - c);
 #pragma unroll
       for (int k = 0; k < kC; ++k) mx4[k & 3] = fmaxf(mx4[k & 3], s[k]);
     }
@@ -688,7 +780,10 @@ __device__ void softmax_tiles(const Ctx& cx, const Piece& pc, int gj0,
     float sum4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
     for (int c = 0; c < kT; c += kC) {
-      if (kFp8) tc::tmem_ld_cols<kC>(sbuf + c, raw);
+      if (kFp8) {
+        tc::tmem_ld_cols<kC>(sbuf + c, raw);
+        if (masked) hide<kC>(raw, seen - jt * kT - c);
+      }
 #pragma unroll
       for (int k = 0; k < kC; k += 2) {
         const float x0 = exp2f(fmaf(s[k], sl2, -mu));
@@ -709,11 +804,60 @@ __device__ void softmax_tiles(const Ctx& cx, const Piece& pc, int gj0,
     l += (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
     tc::tmem_wait_st();
     tc::fence_before();
+    const uint32_t p_full =
+        tc::map_to(tc::smem_u32(&cx.bars->p_full[gj & 1]), 0);
+    if (kCausal && !kFp8 && jt + 1 == pc.n_tiles && pc.tail_tokens() < kT) {
+      // V of the piece's last tile is its last unit, two a tile
+      const int slot = (2 * gj + 1) % C::kSlots;
+      zero_tail(cx, pc, smem, slot, tails >> slot & 1);
+      tails ^= 1u << slot;
+      __syncwarp();
+      if (lane == 0) tc::arrive_cluster(p_full);
+      continue;
+    }
     __syncwarp();
-    if (lane == 0)
-      tc::arrive_cluster_relaxed(
-          tc::map_to(tc::smem_u32(&cx.bars->p_full[gj & 1]), 0));
+    if (lane == 0) tc::arrive_cluster_relaxed(p_full);
   }
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(uint32_t lo, uint32_t hi, float k) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(lo) * k,
+                                                 __uint_as_float(hi) * k);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// A whole row tile of a chunk: rows to the output.
+__device__ void write_out(const Ctx& cx, const Piece& pc, uint32_t tmem, float l) {
+  const AttnParams& p = *cx.a;
+  const int lane = threadIdx.x & 31, w4 = (threadIdx.x >> 5) & 3;
+  const uint32_t lane_base = tmem + ((uint32_t)(32 * w4) << 16);
+  const int R = pc.row0 + w4 * 32 + lane;
+  const int tok = R / p.group;
+  __nv_bfloat16* dst =
+      p.out + (((long long)pc.lead * p.q_len + pc.first + tok) * p.hq +
+               pc.g * p.group + (R - tok * p.group)) * kHeadDim;
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll 1
+  for (int cb = 0; cb < 4; ++cb) {
+    uint32_t o[64];
+    tc::tmem_ld_cols<64>(lane_base + cb * 64, o);
+    if (R < pc.rows_total) {
+#pragma unroll
+      for (int k = 0; k < 64; k += 16) {
+        uint32_t v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          v[e] = bf16_pair(o[k + 2 * e], o[k + 2 * e + 1], inv);
+        asm volatile(
+            "st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(
+                dst + cb * 64 + k),
+            "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]),
+            "r"(v[6]), "r"(v[7])
+            : "memory");
+      }
+    }
+  }
+  tc::fence_before();  // the reads precede this warp's next P
 }
 
 // `shift`: the factor (log2) that O and l carry.
@@ -725,7 +869,7 @@ __device__ void epilogue(const Ctx& cx, const Piece& pc, uint32_t tmem, float m,
   const bool valid = pc.row0 + r < pc.rows_total;
   const long long row =
       (long long)pc.slot * kPrefixRows + cx.rank * 128 + r;
-  float* dst = cx.p->pre_o + row * kHeadDim;
+  float* dst = cx.pre_o + row * kHeadDim;
   const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll 1
   for (int cb = 0; cb < 4; ++cb) {
@@ -739,7 +883,7 @@ __device__ void epilogue(const Ctx& cx, const Piece& pc, uint32_t tmem, float m,
     }
   }
   if (valid)
-    cx.p->pre_lse[row] =
+    cx.pre_lse[row] =
         l > 0.f ? (m == -INFINITY ? 0.f : m) - shift + log2f(l) : -INFINITY;
   tc::fence_before();  // the reads precede this warp's next P
 }
@@ -767,12 +911,76 @@ __device__ __forceinline__ Piece decode_piece(const SharedParams& p, int i,
   return pc;
 }
 
-template <bool kFp8>
+// The pieces of a CTA pair: groups' shared prefixes, numbered i, i + pairs, ..
+struct PrefixWork {
+  const SharedParams& p;
+  uint32_t rank;
+  int i, pieces;
+  __device__ PrefixWork(const SharedParams& p, uint32_t rank)
+      : p(p), rank(rank), i(blockIdx.x >> 1), pieces(p.plan[p.groups].piece0) {}
+  __device__ __forceinline__ bool next(Piece& pc) {
+    if (i >= pieces) return false;
+    pc = decode_piece(p, i, rank);
+    i += gridDim.x >> 1;
+    return true;
+  }
+};
+
+// A chunk's: whole row tiles in rounds, then the pair's run of the rest.
+struct ChunkWork {
+  const ChunkParams& p;
+  uint32_t rank;
+  ChunkHead h;
+  int pair, round, unit, end;
+  __device__ ChunkWork(const ChunkParams& p, uint32_t rank)
+      : p(p), rank(rank), h(*p.head), pair(blockIdx.x >> 1), round(0),
+        unit(p.ranges[pair]), end(p.ranges[pair + 1]) {}
+  __device__ __forceinline__ bool next(Piece& pc) {
+    const int at = round & 1 ? p.pairs - 1 - pair : pair;
+    long long i = (long long)round * p.pairs + at;
+    int from = 0, to = -1, slot = -1;
+    if (round < h.rounds || (!h.split && round == h.rounds && at < h.rest)) {
+      ++round;
+    } else if (h.split && unit < end) {
+      int lo = 0, hi = h.rest - 1;  // the last piece that starts at or before
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.rest_units[mid] <= unit) lo = mid; else hi = mid - 1;
+      }
+      const int u0 = p.rest_units[lo], u1 = p.rest_units[lo + 1];
+      from = unit - u0;
+      to = min(end, u1) - u0;
+      if (from > 0 || end < u1) slot = pair + lo;
+      i = (long long)h.rounds * p.pairs + lo;
+      unit = min(end, u1);
+    } else {
+      return false;
+    }
+    const int4 e = p.pieces[i];
+    const ChunkRows r = chunk_rows(p.a, e.x);
+    pc.lead = pc.start = e.x;
+    pc.rows_total = r.rows;
+    pc.g = e.z;
+    pc.row0 = e.y * kPrefixRows + (int)rank * 128;
+    pc.tok = from * kT;
+    pc.n_tiles = (to < 0 ? e.w : to) - from;
+    pc.slot = slot;
+    pc.last = r.len - 1;
+    pc.first = r.first;
+    pc.limit = r.len - r.live + 1;
+    return true;
+  }
+};
+
+template <bool kFp8, bool kCausal>
 __global__ void __cluster_dims__(2, 1, 1)
     __launch_bounds__(Cfg<kFp8>::kThreads, 1)
-        prefix_attention_kernel(const __grid_constant__ SharedParams p,
-                                const __grid_constant__ CUtensorMap tm_k,
-                                const __grid_constant__ CUtensorMap tm_v) {
+        prefix_attention_kernel(
+            const __grid_constant__
+                std::conditional_t<kCausal, ChunkParams, SharedParams> p,
+            const __grid_constant__ CUtensorMap tm_k,
+            const __grid_constant__ CUtensorMap tm_v) {
+  using Work = std::conditional_t<kCausal, ChunkWork, PrefixWork>;
   using C = Cfg<kFp8>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -791,6 +999,7 @@ __global__ void __cluster_dims__(2, 1, 1)
       tc::bar_init(tc::smem_u32(&bars.full[s]), kFp8 ? 4 : 1);
       tc::bar_init(tc::smem_u32(&bars.peer_full[s]), 2);
       tc::bar_init(tc::smem_u32(&bars.empty[s]), 1);
+      tc::bar_init(tc::smem_u32(&bars.tail_full[s]), 1);
     }
     for (int s = 0; s < 2; ++s) {
       tc::bar_init(tc::smem_u32(&bars.s_full[s]), 1);
@@ -817,25 +1026,26 @@ __global__ void __cluster_dims__(2, 1, 1)
   // take the plan as written.
   tc_grid_dependency_wait();
   tc_grid_launch_dependents();
-  const int pieces = p.plan[p.groups].piece0;
   const Ctx cx{&bars, &s_abort,
-               tc::map_to(tc::smem_u32(&s_abort), rank ^ 1u), rank, &p};
+               tc::map_to(tc::smem_u32(&s_abort), rank ^ 1u), rank, &p.a,
+               p.pre_o, p.pre_lse};
 
   // Every role walks the pair's pieces by itself.
-  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  Work work(p, rank);
   if (warp < 4) {
     Producer<kFp8> pr;
     Slots<kFp8> seq;
     int gj0 = 0, n_piece = 0;
-    for (int i = first; i < pieces; i += step, ++n_piece) {
-      const Piece pc = decode_piece(p, i, rank);
+    Piece pc;
+    for (; work.next(pc); ++n_piece) {
       if (warp == 0 || warp == 2) {
         const bool v_side = warp != 0;
         if (pr.live)
-          produce<kFp8>(cx, pc, pr, smem, v_side ? &tm_v : &tm_k, v_side);
+          produce<kFp8, kCausal>(cx, pc, pr, smem, v_side ? &tm_v : &tm_k,
+                                 v_side);
       } else if (lane == 0) {
         if (rank == 0 && warp == 1)
-          mma_piece<kFp8>(cx, pc, gj0, n_piece, seq, tmem, smem);
+          mma_piece<kFp8, kCausal>(cx, pc, gj0, n_piece, seq, tmem, smem);
         if constexpr (kFp8) {
           if (rank == 1) relay_piece(cx, pc, seq, warp == 3);
         }
@@ -847,10 +1057,10 @@ __global__ void __cluster_dims__(2, 1, 1)
     float m = 0.f, l = 0.f;
     Piece prev{};
     int gj0 = 0;
-    for (int i = first;; i += step) {
-      const bool more = i < pieces;
+    uint32_t tails = 0;
+    while (true) {
       Piece pc{};
-      if (more) pc = decode_piece(p, i, rank);
+      const bool more = work.next(pc);
       if (gj0) {
         // the last piece's MMAs are done: Q may be replaced and O read, the
         // new Q first, so that its QK runs under the epilogue
@@ -858,17 +1068,22 @@ __global__ void __cluster_dims__(2, 1, 1)
                  (uint32_t)((gj0 - 1) >> 1) & 1);
         tc::fence_after();
       }
-      if (more) write_q<kFp8>(cx, pc, smem);
-      if (gj0) epilogue(cx, prev, tmem, m, l, C::kShiftLog2);
+      if (more) write_q<kFp8, kCausal>(cx, pc, smem);
+      if (gj0) {
+        if (kCausal && prev.slot < 0)
+          write_out(cx, prev, tmem, l);
+        else
+          epilogue(cx, prev, tmem, m, l, C::kShiftLog2);
+      }
       if (!more) break;
-      softmax_tiles<kFp8>(cx, pc, gj0, tmem, m, l);
+      softmax_tiles<kFp8, kCausal>(cx, pc, gj0, tmem, smem, tails, m, l);
       prev = pc;
       gj0 += pc.n_tiles;
     }
   } else if constexpr (kFp8) {
     Dequant dq;
-    for (int i = first; i < pieces; i += step)
-      dequant_piece(cx, decode_piece(p, i, rank), smem, dq);
+    Piece pc;
+    while (work.next(pc)) dequant_piece<kCausal>(cx, pc, smem, dq);
   }
 
   // teardown: no copy or MMA may still be in flight in either CTA.  Every
@@ -891,10 +1106,10 @@ __global__ void __cluster_dims__(2, 1, 1)
   tc::cluster_sync();  // neither CTA leaves while the other frees
 }
 
-template <bool kFp8>
+template <bool kFp8, bool kCausal>
 int pairs_resident() {
   using C = Cfg<kFp8>;
-  if (cudaFuncSetAttribute(prefix_attention_kernel<kFp8>,
+  if (cudaFuncSetAttribute(prefix_attention_kernel<kFp8, kCausal>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize,
                            C::kSmem) != cudaSuccess)
     return 0;
@@ -910,20 +1125,20 @@ int pairs_resident() {
   cfg.attrs = at;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, prefix_attention_kernel<kFp8>, &cfg) !=
+  if (cudaOccupancyMaxActiveClusters(&n, prefix_attention_kernel<kFp8, kCausal>, &cfg) !=
       cudaSuccess)
     return 0;
   return n;
 }
 
-template <bool kFp8>
-cudaError_t launch(const SharedParams& p, const CUtensorMap& tm_k,
+template <bool kFp8, bool kCausal, typename P>
+cudaError_t launch(const P& p, const CUtensorMap& tm_k,
                    const CUtensorMap& tm_v, cudaStream_t s) {
   using C = Cfg<kFp8>;
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg =
       pdl_config(dim3(2 * p.pairs), dim3(C::kThreads), C::kSmem, s, attr);
-  return cudaLaunchKernelEx(&cfg, prefix_attention_kernel<kFp8>, p, tm_k, tm_v);
+  return cudaLaunchKernelEx(&cfg, prefix_attention_kernel<kFp8, kCausal>, p, tm_k, tm_v);
 }
 
 }  // namespace
@@ -931,12 +1146,23 @@ cudaError_t launch(const SharedParams& p, const CUtensorMap& tm_k,
 cudaError_t launch_prefix_attention(const SharedParams& p,
                                     const CUtensorMap& tm_k,
                                     const CUtensorMap& tm_v, cudaStream_t s) {
-  return p.a.k_scales ? launch<true>(p, tm_k, tm_v, s)
-                      : launch<false>(p, tm_k, tm_v, s);
+  return p.a.k_scales ? launch<true, false>(p, tm_k, tm_v, s)
+                      : launch<false, false>(p, tm_k, tm_v, s);
+}
+
+cudaError_t launch_chunk_attention(const ChunkParams& p,
+                                   const CUtensorMap& tm_k,
+                                   const CUtensorMap& tm_v, cudaStream_t s) {
+  return p.a.k_scales ? launch<true, true>(p, tm_k, tm_v, s)
+                      : launch<false, true>(p, tm_k, tm_v, s);
 }
 
 int prefix_attention_pairs(bool fp8) {
-  return fp8 ? pairs_resident<true>() : pairs_resident<false>();
+  return fp8 ? pairs_resident<true, false>() : pairs_resident<false, false>();
+}
+
+int chunk_attention_pairs(bool fp8) {
+  return fp8 ? pairs_resident<true, true>() : pairs_resident<false, true>();
 }
 
 }  // namespace specv

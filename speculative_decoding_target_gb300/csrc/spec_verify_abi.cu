@@ -1,6 +1,7 @@
 // C ABI of the verify library: host-side validation, workspace layout and
 // kernel launches.  Every error is detected here, before anything is
 // enqueued, except a failed launch (SPEC_ERR_CUDA).
+#include <climits>
 #include <cstdarg>
 #include <cstdio>
 #include <atomic>
@@ -10,6 +11,7 @@
 #include <cudaTypedefs.h>
 
 #include "append.cuh"
+#include "chunk_attention.cuh"
 #include "next_block.cuh"
 #include "sample.cuh"
 #include "selector.cuh"
@@ -43,7 +45,8 @@ int g_sms[kMaxDevices];
 int g_occ[kMaxDevices][12];  // split-kernel CTAs per SM: [w] mma.sync with w
                              // compute warps, [9] tcgen05 bf16, [10] tcgen05
                              // FP8, [11] tcgen05 FP8 with TMEM KV operands
-int g_pairs[kMaxDevices][2];  // resident CTA pairs of the prefix kernel
+int g_pairs[kMaxDevices][4];  // resident CTA pairs of the prefix kernel: bf16,
+                              // FP8, and of its causal instances
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 // main-loop wait bound of the split kernels for SPEC_FLAG_CHECKED calls
 // (spec_verify_set_wait_limit); 0 = the default bound
@@ -172,13 +175,14 @@ int split_grid(int rows, bool tc, bool fp8, int* grid) {
   return SPEC_OK;
 }
 
-int check_desc(const spec_attn_desc* d) {
+// q_max: the most block rows a request may have (16 for the verify block).
+int check_desc(const spec_attn_desc* d, int q_max = 16) {
   if (!d) return fail(SPEC_ERR_ARG, "desc is NULL");
   if (d->batch < 0 || d->batch > specv::kMaxBatch)
     return fail(SPEC_ERR_ARG, "batch %d outside [0, %d]", d->batch,
                 specv::kMaxBatch);
-  if (d->q_len < 1 || d->q_len > 16)
-    return fail(SPEC_ERR_ARG, "q_len %d outside [1, 16]", d->q_len);
+  if (d->q_len < 1 || d->q_len > q_max)
+    return fail(SPEC_ERR_ARG, "q_len %d outside [1, %d]", d->q_len, q_max);
   if (d->num_q_heads < 1 || d->num_kv_heads < 1 ||
       d->num_q_heads % d->num_kv_heads)
     return fail(SPEC_ERR_ARG, "num_q_heads %d not a multiple of num_kv_heads %d",
@@ -187,7 +191,7 @@ int check_desc(const spec_attn_desc* d) {
     return fail(SPEC_ERR_UNSUPPORTED, "head_dim %d (only 256)", d->head_dim);
   const long long rows =
       (long long)d->q_len * (d->num_q_heads / d->num_kv_heads);
-  if (rows > specv::kMaxRows)
+  if (rows > specv::kMaxRows && q_max == 16)
     return fail(SPEC_ERR_UNSUPPORTED, "q_len * group = %lld > %d", rows,
                 specv::kMaxRows);
   if (d->page_size < 1 || d->page_size > 4096 ||
@@ -363,6 +367,24 @@ int launch_split(const spec_attn_desc* desc, const specv::AttnParams& p,
   return SPEC_OK;
 }
 
+// Resident CTA pairs of the prefix kernel or its causal instance.
+int pair_count(bool causal, bool fp8, int* pairs) {
+  int dev;
+  const int rc = current_device(&dev);
+  if (rc) return rc;
+  std::lock_guard<std::mutex> lock(g_mu);
+  int& n = g_pairs[dev][2 * causal + fp8];
+  if (!n) {
+    const int found = causal ? specv::chunk_attention_pairs(fp8)
+                             : specv::prefix_attention_pairs(fp8);
+    if (found <= 0)
+      return fail(SPEC_ERR_CUDA, "prefix kernel does not fit on an SM pair");
+    n = found;
+  }
+  *pairs = n;
+  return SPEC_OK;
+}
+
 int check_shared(const spec_attn_desc* d, int32_t groups) {
   int rc = check_desc(d);
   if (rc) return rc;
@@ -385,20 +407,8 @@ struct SharedLayout {
 int shared_layout(const spec_attn_desc* d, int32_t groups, SharedLayout* S) {
   int rc = layout(d, &S->tail);
   if (rc) return rc;
-  int dev;
-  rc = current_device(&dev);
+  rc = pair_count(false, d->kv_dtype == SPEC_KV_FP8_E4M3, &S->pairs);
   if (rc) return rc;
-  const bool fp8 = d->kv_dtype == SPEC_KV_FP8_E4M3;
-  {
-    std::lock_guard<std::mutex> lock(g_mu);
-    if (!g_pairs[dev][fp8]) {
-      const int n = specv::prefix_attention_pairs(fp8);
-      if (n <= 0)
-        return fail(SPEC_ERR_CUDA, "prefix kernel does not fit on an SM pair");
-      g_pairs[dev][fp8] = n;
-    }
-    S->pairs = g_pairs[dev][fp8];
-  }
   // one partial per piece.  Only groups of two or more share, and each rounds
   // its rows up to one more tile at most.
   const long long share = groups < d->batch / 2 ? groups : d->batch / 2;
@@ -418,6 +428,55 @@ int shared_layout(const spec_attn_desc* d, int32_t groups, SharedLayout* S) {
   S->pre_o = take(slots * specv::kPrefixRows * specv::kHeadDim * sizeof(float));
   S->pre_lse = take(slots * specv::kPrefixRows * sizeof(float));
   S->bytes = o;
+  return SPEC_OK;
+}
+
+// Chunks that the verify kernels take: they read the cache at the copy rate,
+// and split it further than the pairs do.
+bool chunk_is_block(const spec_attn_desc* d) {
+  return d->q_len <= 16 &&
+         (long long)d->q_len * (d->num_q_heads / d->num_kv_heads) <=
+             specv::kMaxRows;
+}
+
+int check_chunk(const spec_attn_desc* d) {
+  int rc = check_desc(d, INT_MAX);
+  if (rc) return rc;
+  if ((long long)d->batch * d->q_len * d->num_q_heads >= (1LL << 31))
+    return fail(SPEC_ERR_ARG, "batch * q_len * num_q_heads must be < 2^31");
+  if (!chunk_is_block(d) && !use_tc(d))
+    return fail(SPEC_ERR_UNSUPPORTED, "chunks need page_size >= %d",
+                specv::kTcMinPageSize);
+  return SPEC_OK;
+}
+
+struct ChunkLayout {
+  int pairs;
+  size_t head, pieces, units, ranges, o, lse, bytes;
+};
+
+int chunk_layout(const spec_attn_desc* d, ChunkLayout* C) {
+  int rc = pair_count(true, d->kv_dtype == SPEC_KV_FP8_E4M3, &C->pairs);
+  if (rc) return rc;
+  const long long rows =
+      (long long)d->q_len * (d->num_q_heads / d->num_kv_heads);
+  const size_t tiles = (size_t)d->batch * d->num_kv_heads *
+                       ((rows + specv::kPrefixRows - 1) / specv::kPrefixRows);
+  size_t o = specv::kWsHeader;
+  auto take = [&](size_t n) {
+    const size_t at = o;
+    o += round_up(n, 256);
+    return at;
+  };
+  C->head = take(sizeof(specv::ChunkHead));
+  C->pieces = take(tiles * sizeof(int4));
+  C->units = take((C->pairs + 1) * sizeof(int));
+  C->ranges = take((C->pairs + 1) * sizeof(int));
+  // a partial slot is its pair's number plus its piece's in the rest
+  const size_t slots = 2 * (size_t)C->pairs * specv::kPrefixRows;
+  C->o = take(slots * specv::kHeadDim * sizeof(float));
+  C->lse = take(slots * sizeof(float));
+  C->bytes = o;
   return SPEC_OK;
 }
 
@@ -552,6 +611,75 @@ int spec_verify_attention_shared(
   e = specv::launch_shared_merge(p, s);
   if (e != cudaSuccess)
     return fail(SPEC_ERR_CUDA, "merge kernel launch: %s", cudaGetErrorString(e));
+  return SPEC_OK;
+}
+
+size_t spec_chunk_workspace_size(const spec_attn_desc* desc) {
+  if (check_chunk(desc)) return 0;
+  if (chunk_is_block(desc)) return spec_verify_workspace_size(desc);
+  ChunkLayout C;
+  if (chunk_layout(desc, &C)) return 0;
+  return C.bytes;
+}
+
+int spec_chunk_attention(const spec_attn_desc* desc, const void* q,
+                         const void* k_pages, const void* v_pages,
+                         const void* k_scales, const void* v_scales,
+                         const int32_t* page_table, const int32_t* seq_lens,
+                         float scale, void* out, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  g_err[0] = 0;
+  int rc = check_chunk(desc);
+  if (rc) return rc;
+  if (chunk_is_block(desc))
+    return spec_verify_attention(desc, q, k_pages, v_pages, k_scales, v_scales,
+                                 page_table, seq_lens, scale, out, workspace,
+                                 workspace_bytes, stream);
+  if (desc->batch == 0) return SPEC_OK;
+  rc = check_attention(desc, q, k_pages, v_pages, k_scales, v_scales,
+                       page_table, seq_lens, scale, out);
+  if (rc) return rc;
+  ChunkLayout C;
+  rc = chunk_layout(desc, &C);
+  if (rc) return rc;
+  rc = check_workspace(workspace, workspace_bytes, C.bytes);
+  if (rc) return rc;
+  int sms;
+  rc = sm_count(&sms);
+  if (rc) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  specv::ChunkParams p;
+  std::memset(&p, 0, sizeof p);
+  CUtensorMap tm_k, tm_v;
+  Layout none;
+  std::memset(&none, 0, sizeof none);
+  rc = attention_params(desc, none, q, k_pages, v_pages, k_scales, v_scales,
+                        page_table, seq_lens, scale, out, workspace, &p.a,
+                        &tm_k, &tm_v);
+  if (rc) return rc;
+  if (desc->kv_dtype == SPEC_KV_FP8_E4M3) {
+    const long long rows =
+        (long long)desc->num_pages * desc->num_kv_heads * desc->page_size;
+    rc = make_pool_map_u8(&tm_k, k_pages, rows, p.a.box_rows);
+    if (!rc) rc = make_pool_map_u8(&tm_v, v_pages, rows, p.a.box_rows);
+    if (rc) return rc;
+  }
+  p.head = reinterpret_cast<specv::ChunkHead*>(ws + C.head);
+  p.pieces = reinterpret_cast<int4*>(ws + C.pieces);
+  p.rest_units = reinterpret_cast<int*>(ws + C.units);
+  p.ranges = reinterpret_cast<int*>(ws + C.ranges);
+  p.pre_o = reinterpret_cast<float*>(ws + C.o);
+  p.pre_lse = reinterpret_cast<float*>(ws + C.lse);
+  p.pairs = C.pairs;
+  rc = reset_status(desc, workspace, &p.a, s);
+  if (rc) return rc;
+  cudaError_t e = specv::launch_chunk_plan(p, s);
+  if (e == cudaSuccess) e = specv::launch_chunk_attention(p, tm_k, tm_v, s);
+  if (e == cudaSuccess) e = specv::launch_chunk_merge(p, sms, s);
+  if (e != cudaSuccess)
+    return fail(SPEC_ERR_CUDA, "chunk attention launch: %s",
+                cudaGetErrorString(e));
   return SPEC_OK;
 }
 

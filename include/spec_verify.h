@@ -451,6 +451,52 @@ int spec_sample(const spec_sample_desc* desc, const void* logits,
                 const float* top_p, const float* min_p, const float* u,
                 int32_t* token, float* probs, float* filtered, void* stream);
 
+/*
+ * Shape of a log-probability call.
+ *   rows        0 .. 2^24 (0 is a no-op)
+ *   vocab       1 .. 524,288
+ *   dtype       SPEC_LOGITS_*
+ *   top         alternatives per row, 0 .. 32
+ *   row_stride  elements from one row of logits to the next, >= vocab
+ */
+typedef struct {
+  int32_t rows, vocab, dtype, top;
+  int64_t row_stride;
+} spec_logprob_desc;
+
+/*
+ * Log probabilities of given tokens (a prompt's, the ones that a verify step
+ * committed, the ones that were drawn), the entropy of the distributions they
+ * come from, and the most likely alternatives.
+ *
+ * With z_v = x_v / T and log p(v) = z_v - log sum_w exp(z_w):
+ *   logprob       log p(token)
+ *   entropy       -sum_v p(v) log p(v), in nats
+ *   top_ids       the first `top` tokens by logit, larger first, lower id first
+ *                 among equals; top_logprobs their log p
+ *
+ *   logits       [rows, vocab]; NaN counts as -inf, +inf as the type's largest
+ *                finite value.  A token at -inf has log p -inf and is no
+ *                alternative: ids behind the last finite logit are -1 and their
+ *                log p -inf.  A row without a finite logit: logprob -inf,
+ *                entropy 0.
+ *   token        optional int32 [rows]; a row whose token lies outside
+ *                [0, vocab) is idle (the -1 of padded blocks): its logits are
+ *                not read, logprob and entropy are 0, ids -1 and their log p
+ *                -inf.  NULL: no row is idle for it; logprob must be NULL
+ *   temperature  optional fp32 [rows] (NULL: 1).  0 puts all the mass on the
+ *                first of the largest logits (log p 0, all others -inf, entropy
+ *                0); below zero, NaN or infinite marks an idle row
+ *   logprob, entropy   optional fp32 [rows]
+ *   top_ids int32, top_logprobs fp32 [rows, top], contiguous; NULL with top 0
+ * 4-byte aligned (bf16 logits 2).  One launch, no workspace; the result is the
+ * same on every run.
+ */
+int spec_logprobs(const spec_logprob_desc* desc, const void* logits,
+                  const int32_t* token, const float* temperature,
+                  float* logprob, float* entropy, int32_t* top_ids,
+                  float* top_logprobs, void* stream);
+
 /* Walks of the DFlash2 candidate selector (spec_select_desc.mode). */
 #define SPEC_SELECT_GREEDY 0  /* best successor of the token already chosen */
 #define SPEC_SELECT_MAP 1     /* the chain with the best total score */

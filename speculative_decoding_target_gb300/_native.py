@@ -42,7 +42,7 @@ EXPORTED = (
     "spec_verify_set_wait_limit", "spec_rope_append",
     "spec_verify_attention_shared", "spec_verify_shared_workspace_size",
     "spec_sample", "spec_norm_rope_append", "spec_chunk_attention",
-    "spec_chunk_workspace_size",
+    "spec_chunk_workspace_size", "spec_logprobs",
 )
 SELECT_MODES = {"greedy": 0, "map": 1}
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
@@ -89,6 +89,12 @@ class NormDesc(ctypes.Structure):
 class SampleDesc(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int32), ("vocab", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("row_stride", ctypes.c_int64)]
+
+
+class LogprobDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("vocab", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("top", ctypes.c_int32),
+                ("row_stride", ctypes.c_int64)]
 
 
 class SelectDesc(ctypes.Structure):
@@ -144,6 +150,8 @@ def load(path: str = LIB_PATH):
     lib.spec_chunk_attention.restype = ctypes.c_int
     lib.spec_sample.argtypes = [ctypes.POINTER(SampleDesc)] + [P] * 10
     lib.spec_sample.restype = ctypes.c_int
+    lib.spec_logprobs.argtypes = [ctypes.POINTER(LogprobDesc)] + [P] * 8
+    lib.spec_logprobs.restype = ctypes.c_int
     lib.spec_rope_append.argtypes = [ctypes.POINTER(RopeDesc)] + [P] * 15
     lib.spec_rope_append.restype = ctypes.c_int
     lib.spec_norm_rope_append.argtypes = (
@@ -729,6 +737,23 @@ def stochastic_accept(logits, draft_ids, temperature, u_accept, u_sample, *,
     return acc, nxt, toks, new
 
 
+def _row_stride(logits: torch.Tensor, rows: int) -> int:
+    """Elements from one row of logits [.., vocab] to the next."""
+    vocab = logits.shape[-1]
+    if logits.dim() == 2 and rows > 1 and logits.stride(1) == 1:
+        stride = logits.stride(0)
+    elif logits.is_contiguous():
+        stride = vocab
+    elif rows == 1 and (vocab == 1 or logits.stride(-1) == 1):
+        stride = vocab
+    else:
+        raise SpecError(SPEC_ERR_ARG, "logits rows must be contiguous and "
+                                      "evenly spaced")
+    if rows > 1 and stride < vocab:
+        raise SpecError(SPEC_ERR_ARG, "logits rows overlap")
+    return stride
+
+
 def sample(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None,
            probs: Optional[torch.Tensor] = None,
            filtered: Optional[torch.Tensor] = None,
@@ -759,17 +784,7 @@ def sample(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None,
             _expect(t, torch.float32, what, logits.shape, True)
     on = _on_current_device((logits, u, temperature, top_k, top_p, min_p,
                              probs, filtered, token), stream)
-    if logits.dim() == 2 and rows > 1 and logits.stride(1) == 1:
-        stride = logits.stride(0)
-    elif logits.is_contiguous():
-        stride = vocab
-    elif rows == 1 and (vocab == 1 or logits.stride(-1) == 1):
-        stride = vocab
-    else:
-        raise SpecError(SPEC_ERR_ARG, "logits rows must be contiguous and "
-                                      "evenly spaced")
-    if rows > 1 and stride < vocab:
-        raise SpecError(SPEC_ERR_ARG, "logits rows overlap")
+    stride = _row_stride(logits, rows)
     desc = SampleDesc(rows, vocab, int(logits.dtype == torch.bfloat16),
                       stride)
     rc = load().spec_sample(
@@ -779,6 +794,46 @@ def sample(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None,
     if rc:
         _check(rc)
     return token
+
+
+def logprobs(logits, token=None, *, temperature=None, top: int = 0,
+             stream=None) -> dict:
+    """Log probabilities of the given tokens (int32 [..], or None) under the
+    rows of logits (fp32 or bf16 [.., vocab], rows contiguous, evenly spaced),
+    with an optional per-row temperature (fp32 [..]).  Returns a dict of
+    logprob fp32 [..] (with token), entropy fp32 [..], and with top > 0 the
+    most likely tokens top_ids int32 [.., top] and their top_logprobs fp32
+    [.., top].  Rows whose token lies outside the vocabulary are idle: zeros,
+    ids -1."""
+    lead, vocab = logits.shape[:-1], logits.shape[-1]
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise SpecError(SPEC_ERR_ARG, f"logits are {logits.dtype}")
+    if token is not None:
+        _expect(token, torch.int32, "token", lead, True)
+    if temperature is not None:
+        _expect(temperature, torch.float32, "temperature", lead, True)
+    on = _on_current_device((logits, token, temperature), stream)
+    rows = lead.numel()
+    stride = _row_stride(logits, rows)
+    out = {}
+    with _made_on(stream):
+        f32 = dict(dtype=torch.float32, device=logits.device)
+        if token is not None:
+            out["logprob"] = torch.empty(lead, **f32)
+        out["entropy"] = torch.empty(lead, **f32)
+        if top > 0:
+            out["top_ids"] = torch.empty((*lead, top), dtype=torch.int32,
+                                         device=logits.device)
+            out["top_logprobs"] = torch.empty((*lead, top), **f32)
+    desc = LogprobDesc(rows, vocab, int(logits.dtype == torch.bfloat16), top,
+                       stride)
+    rc = load().spec_logprobs(
+        ctypes.byref(desc), _at(logits), _at(token), _at(temperature),
+        _at(out.get("logprob")), _at(out["entropy"]), _at(out.get("top_ids")),
+        _at(out.get("top_logprobs")), on)
+    if rc:
+        _check(rc)
+    return out
 
 
 def select_desc(cand_logits, code_a, hidden, *, top: int = 16,

@@ -12,6 +12,7 @@
 
 #include "append.cuh"
 #include "chunk_attention.cuh"
+#include "logprobs.cuh"
 #include "next_block.cuh"
 #include "sample.cuh"
 #include "selector.cuh"
@@ -1140,6 +1141,66 @@ int spec_sample(const spec_sample_desc* desc, const void* logits,
       specv::launch_sample(p, bf16, sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess)
     return fail(SPEC_ERR_CUDA, "sample kernel launch: %s", cudaGetErrorString(e));
+  return SPEC_OK;
+}
+
+int spec_logprobs(const spec_logprob_desc* desc, const void* logits,
+                  const int32_t* token, const float* temperature,
+                  float* logprob, float* entropy, int32_t* top_ids,
+                  float* top_logprobs, void* stream) {
+  g_err[0] = 0;
+  const spec_logprob_desc* d = desc;
+  if (!d) return fail(SPEC_ERR_ARG, "desc is NULL");
+  if (d->rows < 0 || d->rows > (1 << 24))
+    return fail(SPEC_ERR_ARG, "rows %d outside [0, 2^24]", d->rows);
+  if (d->vocab < 1) return fail(SPEC_ERR_ARG, "vocab %d < 1", d->vocab);
+  if (d->vocab > specv::kLogprobMaxVocab)
+    return fail(SPEC_ERR_UNSUPPORTED, "vocab %d > %d", d->vocab,
+                specv::kLogprobMaxVocab);
+  if (d->dtype != SPEC_LOGITS_FP32 && d->dtype != SPEC_LOGITS_BF16)
+    return fail(SPEC_ERR_ARG, "dtype %d", d->dtype);
+  if (d->row_stride < d->vocab)
+    return fail(SPEC_ERR_ARG, "row_stride %lld < vocab",
+                (long long)d->row_stride);
+  if (d->top < 0 || d->top > specv::kLogprobMaxTop)
+    return fail(SPEC_ERR_ARG, "top %d outside [0, %d]", d->top,
+                specv::kLogprobMaxTop);
+  if (d->rows == 0) return SPEC_OK;
+  if (!logits) return fail(SPEC_ERR_ARG, "NULL tensor pointer");
+  if (logprob && !token) return fail(SPEC_ERR_ARG, "logprob needs token");
+  if (!top_ids != (d->top == 0) || !top_logprobs != (d->top == 0))
+    return fail(SPEC_ERR_ARG, "top_ids and top_logprobs go with top > 0");
+  if (!logprob && !entropy && !top_ids)
+    return fail(SPEC_ERR_ARG, "no output is asked for");
+  const void* a4[] = {token, temperature, logprob, entropy, top_ids,
+                      top_logprobs};
+  for (const void* q : a4)
+    if (q && !aligned(q, 4))
+      return fail(SPEC_ERR_ALIGN, "tensors must be 4-byte aligned");
+  const bool bf16 = d->dtype == SPEC_LOGITS_BF16;
+  if (!aligned(logits, bf16 ? 2 : 4))
+    return fail(SPEC_ERR_ALIGN, "logits are misaligned");
+  int sms;
+  int rc = sm_count(&sms);
+  if (rc) return rc;
+  specv::LogprobParams p;
+  std::memset(&p, 0, sizeof p);
+  p.logits = logits;
+  p.row_stride = d->row_stride;
+  p.token = token;
+  p.temperature = temperature;
+  p.logprob = logprob;
+  p.entropy = entropy;
+  p.top_ids = top_ids;
+  p.top_logprobs = top_logprobs;
+  p.rows = d->rows;
+  p.vocab = d->vocab;
+  p.top = d->top;
+  cudaError_t e =
+      specv::launch_logprobs(p, bf16, sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess)
+    return fail(SPEC_ERR_CUDA, "logprobs kernel launch: %s",
+                cudaGetErrorString(e));
   return SPEC_OK;
 }
 

@@ -1,0 +1,326 @@
+"""Log probabilities, entropy and alternatives: the CUDA path against the
+definition in 64 bits, and the calls that are refused.
+
+Tolerances.  With z = (x - max) / T, E the mean of |z| under p: the factor
+log2(e) / T is off by 2^-24 and its constant by 2^-25, t by two more roundings:
+3.5 2^-24 of z, in a token's own z and in every weight's: 2.1e-7 (|z| + E).  A
+weight is off by ex2's 2^-22.  A sum passes at most 16 + 2 additions in its
+batch, 32 batches, each perhaps with a change of the reference (two roundings
+and an ex2), and 5 more inside the warp: below 40 2^-24 + 32 (2^-23 + 2^-22) <
+1.5e-5 of S.  So log p is off by 1.6e-5 + 2.1e-7 (|z| + E) and its own
+rounding, 2^-24 of it; the entropy, of which both ln S and a mean of z have
+that error, by 1.6e-5 (1 + E) + 2.1e-7 E and 2^-24 of itself."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import speculative_decoding_target_gb300 as sv
+from speculative_decoding_target_gb300 import _native, build
+
+DEV = "cuda"
+MOST = {t: torch.finfo(t).max for t in (torch.float32, torch.bfloat16)}
+
+
+def reference(x, token, t, top, most):
+    """One row in 64 bits: (logprob, entropy, ids, their log p, E, z)."""
+    x = np.where(np.isnan(x), -np.inf, np.minimum(x.astype(np.float64), most))
+    order = np.argsort(-x, kind="stable")
+    order = order[x[order] > -np.inf]
+    lp = np.full(len(x), -np.inf)
+    if len(order) == 0:
+        H, E = 0.0, 0.0
+    elif t == 0:
+        lp[order[0]], H, E = 0.0, 0.0, 0.0
+    else:
+        z = (x - x[order[0]]) / t
+        e = np.exp(z)
+        S = e.sum()
+        lp = z - np.log(S)
+        p = e / S
+        E = -(p[order] * np.maximum(z[order], -1e300)).sum()
+        H = np.log(S) + E
+    ids = np.full(top, -1)
+    n = min(top, len(order))
+    ids[:n] = order[:n]
+    best = np.full(top, -np.inf)
+    best[:n] = lp[order[:n]]
+    return (lp[token] if token is not None else None), H, ids, best, E
+
+
+def check(x, out, token, t, top):
+    rows = x.shape[0]
+    xs = x.float().cpu().numpy()
+    got = {k: v.double().cpu().numpy() for k, v in out.items()}
+    for r in range(rows):
+        tok = None if token is None else int(token[r])
+        tr = 1.0 if t is None else float(t[r])
+        idle = (tok is not None and not 0 <= tok < x.shape[1]) or not (
+            0 <= tr < np.inf)
+        if idle:
+            assert got["entropy"][r] == 0
+            assert token is None or got["logprob"][r] == 0
+            if top:
+                assert (got["top_ids"][r] == -1).all()
+                assert (got["top_logprobs"][r] == -np.inf).all()
+            continue
+        lp, H, ids, best, E = reference(xs[r], tok, tr, top, MOST[x.dtype])
+
+        def near(a, b, tol):
+            fin = np.isfinite(b)
+            assert np.array_equal(np.isfinite(a), fin), (r, a, b)
+            assert np.all(np.abs(a[fin] - b[fin]) <= tol[fin]), (r, a, b)
+        lp_tol = lambda v: (1.6e-5 + 2.1e-7 * (np.abs(v) + H + E)
+                            + 2.0 ** -24 * np.abs(v))
+        if token is not None:
+            v = np.array([lp])
+            near(got["logprob"][r:r + 1], v, lp_tol(v))
+        assert abs(got["entropy"][r] - H) <= (
+            1.6e-5 * (1 + E) + 2.1e-7 * E + 2.0 ** -24 * H), (r, H)
+        if top:
+            assert np.array_equal(got["top_ids"][r], ids), (
+                r, got["top_ids"][r], ids)
+            near(got["top_logprobs"][r], best, lp_tol(best))
+
+
+def run(x, token=None, t=None, top=0, **kw):
+    build.build()
+    i32 = lambda v: None if v is None else torch.as_tensor(
+        v, dtype=torch.int32, device=DEV)
+    f32 = lambda v: None if v is None else torch.as_tensor(
+        v, dtype=torch.float32, device=DEV)
+    return sv.logprobs(x, i32(token), temperature=f32(t), top=top, **kw)
+
+
+def logits(rows, vocab, dtype, seed=0, spread=2.0, peaks=4):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    x = torch.randn((rows, vocab), generator=g, device=DEV) * spread
+    if peaks and vocab > 8:
+        at = torch.randint(0, vocab, (rows, peaks), generator=g, device=DEV)
+        x.scatter_add_(1, at, torch.full(at.shape, 9.0, device=DEV))
+    return x.to(dtype)
+
+
+# ---------------------------------------------------------------- GPU tests
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,vocab,top", [
+    (1, 1, 1), (3, 2, 5), (2, 7, 32), (5, 31, 20), (9, 900, 1), (4, 5003, 32),
+    (17, 50001, 8), (1, 248320, 20), (40, 248320, 5), (3, 524288, 32),
+    (400, 4099, 3), (700, 33000, 0)])
+def test_sizes(dtype, rows, vocab, top):
+    x = logits(rows, vocab, dtype, seed=vocab)
+    r = np.random.default_rng(rows)
+    token = r.integers(0, vocab, rows)
+    t = r.uniform(0.3, 2.0, rows).astype(np.float32)
+    check(x, run(x, token, t, top), token, t, top)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("off,stride", [(0, 5003), (1, 5001), (3, 5007),
+                                        (7, 5000), (5, 9001)])
+def test_strides_and_alignment(dtype, off, stride):
+    buf = logits(1, 8 * stride + 16, dtype, seed=off, peaks=40)[0]
+    x = buf[off:off + 8 * stride].view(8, stride)[:, :5000]
+    token = np.arange(8) * 600
+    check(x, run(x, token, None, 9), token, None, 9)
+    # the largest in front of the first and behind the last whole vector
+    buf[off], buf[off + 4999] = 30.0, 30.0
+    buf[off + stride], buf[off + stride + 1] = 30.0, 31.0
+    check(x, run(x, token, None, 3), token, None, 3)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,vocab", [(6, 60000), (400, 20011)])
+def test_equal_logits(dtype, rows, vocab):
+    # rows of one value; two values, the larger behind; few values; equals
+    # that lie in one thread's vectors
+    x = torch.zeros((rows, vocab), device=DEV)
+    x[1] = -3.5
+    x[2, vocab // 2:] = 1.0
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x[3] = torch.randint(0, 3, (vocab,), generator=g, device=DEV).float()
+    x[4, ::4096] = 2.0
+    x[5, 8 * 512 * torch.arange(vocab // 4096, device=DEV) + 17] = 5.0
+    x = x.to(dtype)
+    token = np.arange(rows) % vocab
+    check(x, run(x, token, None, 32), token, None, 32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("vocab", [700, 40000])
+def test_one_thread_holds_the_best(dtype, vocab):
+    # sorted rows, and rows whose best lie in the same few vectors
+    x = logits(4, vocab, dtype, peaks=0)
+    x[0] = x[0].sort()[0]
+    x[1] = x[1].sort(descending=True)[0]
+    x[2, 64:104] += 50.0
+    for v in range(0, vocab, 4096):
+        x[3, v:v + 8] += 40.0
+    token = [3, 600, 70, 0]
+    check(x, run(x, token, None, 32), token, None, 32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("vocab", [65, 30011])
+def test_values_that_are_not_finite(dtype, vocab):
+    inf, nan = float("inf"), float("nan")
+    x = logits(9, vocab, dtype, seed=3)
+    x[0] = -inf
+    x[1] = nan
+    x[2, 1:] = -inf
+    x[2, 0] = -3e38
+    x[3, ::2] = -inf
+    x[3, 1::4] = nan
+    x[4, 60], x[4, 61] = inf, MOST[dtype]
+    x[5] = torch.finfo(dtype).min
+    x[5, 64] = nan
+    x[6, 5:] = torch.finfo(dtype).min
+    x[7, :60] = -1e30
+    x[8, 7] = 3e38
+    token = [4, 5, 0, 2, 61, 3, 60, 1, 7]
+    check(x, run(x, token, None, 7), token, None, 7)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,vocab", [(12, 30000), (330, 9001)])
+def test_temperatures_and_idle_rows(dtype, rows, vocab):
+    x = logits(rows, vocab, dtype, seed=4)
+    t = np.ones(rows, np.float32)
+    t[:12] = [0, 0, 1e-3, 100.0, -1, np.nan, np.inf, 1, 1, 1, 1e30, 0]
+    token = np.arange(rows) * 7
+    first = x.float().argmax(1).cpu().numpy()
+    token[1] = first[1]
+    token[7:10] = [-1, vocab, -(2 ** 31)]
+    for top in (0, 4):
+        check(x, run(x, token, t, top), token, t, top)
+    check(x, run(x, None, t, 2), None, t, 2)
+
+
+@pytest.mark.gpu
+def test_against_a_long_tail():
+    # one weight of one beside half a million of 2^-26: their sum counts
+    x = torch.zeros((2, 524288), device=DEV)
+    x[:, 77] = 26 * np.log(2)
+    x[1, ::2] = -1.0
+    x[1, 77] = 26 * np.log(2)
+    check(x, run(x, [77, 3], None, 3), [77, 3], None, 3)
+
+
+@pytest.mark.gpu
+def test_shapes_streams_graphs_and_repeats():
+    build.build()
+    x = logits(64, 30000, torch.float32, seed=6).view(8, 8, 30000)
+    token = torch.randint(-1, 30000, (8, 8), dtype=torch.int32, device=DEV)
+    out = sv.logprobs(x, token, top=3)
+    assert out["top_ids"].shape == (8, 8, 3) and out["logprob"].shape == (8, 8)
+    check(x.view(64, -1), {k: v.flatten(0, 1) for k, v in out.items()},
+          token.flatten().tolist(), None, 3)
+    again = sv.logprobs(x, token, top=3)
+    assert all(torch.equal(out[k], again[k]) for k in out)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = sv.logprobs(x, token, top=3, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    assert all(torch.equal(out[k], got[k]) for k in out)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        held = sv.logprobs(x, token, top=3)
+    x.mul_(0.5)
+    token.fill_(5)
+    g.replay()
+    check(x.view(64, -1), {k: v.flatten(0, 1) for k, v in held.items()},
+          [5] * 64, None, 3)
+
+
+@pytest.mark.gpu
+def test_agrees_with_the_sampler():
+    # the drawn token's log p is the log of the probability it was drawn with
+    build.build()
+    x = logits(20, 50000, torch.bfloat16, seed=8)
+    t = torch.linspace(0.5, 1.5, 20, device=DEV)
+    t[3] = 0
+    u = torch.rand(20, device=DEV)
+    probs = torch.empty((20, 50000), device=DEV)
+    token = sv.sample(x, u, temperature=t, probs=probs)
+    out = sv.logprobs(x, token, temperature=t, top=1)
+    p = probs.gather(1, token.long()[:, None])[:, 0]
+    # a weight of the sampler is a multiple of 2^-43 of the largest
+    assert torch.allclose(out["logprob"].exp(), p, rtol=1e-4, atol=1e-11)
+    assert torch.equal(out["top_ids"][:, 0].long(),
+                       x.float().argmax(1)) and int(token[3]) == int(
+        out["top_ids"][3, 0])
+
+
+# ---------------------------------------------------------------- CPU tests
+
+FAKE = ctypes.c_void_p(0x100000)   # never dereferenced: checks come first
+
+
+def _raw(lib, **kw):
+    d = _native.LogprobDesc(4, 1000, 0, 5, 1000)
+    ptr = dict(logits=FAKE, token=FAKE, temperature=None, logprob=FAKE,
+               entropy=FAKE, top_ids=FAKE, top_logprobs=FAKE)
+    for name, val in kw.items():
+        if name in ptr:
+            ptr[name] = val
+        else:
+            setattr(d, name, val)
+    return lib.spec_logprobs(ctypes.byref(d), *ptr.values(), None)
+
+
+ODD = ctypes.c_void_p(0x100002)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(rows=-1), _native.SPEC_ERR_ARG),
+    (dict(rows=(1 << 24) + 1), _native.SPEC_ERR_ARG),
+    (dict(vocab=0), _native.SPEC_ERR_ARG),
+    (dict(vocab=524289, row_stride=524289), _native.SPEC_ERR_UNSUPPORTED),
+    (dict(dtype=2), _native.SPEC_ERR_ARG),
+    (dict(row_stride=999), _native.SPEC_ERR_ARG),
+    (dict(top=-1), _native.SPEC_ERR_ARG),
+    (dict(top=33), _native.SPEC_ERR_ARG),
+    (dict(top=0), _native.SPEC_ERR_ARG),
+    (dict(top_ids=None), _native.SPEC_ERR_ARG),
+    (dict(logits=None), _native.SPEC_ERR_ARG),
+    (dict(token=None), _native.SPEC_ERR_ARG),
+    (dict(top=0, top_ids=None, top_logprobs=None, logprob=None, entropy=None),
+     _native.SPEC_ERR_ARG),
+    (dict(logits=ODD), _native.SPEC_ERR_ALIGN),
+    (dict(dtype=1, logits=ctypes.c_void_p(0x100001)), _native.SPEC_ERR_ALIGN),
+    (dict(token=ODD), _native.SPEC_ERR_ALIGN),
+    (dict(top_logprobs=ODD), _native.SPEC_ERR_ALIGN),
+])
+def test_refusals(kw, code):
+    build.build()
+    lib = _native.load()
+    assert _raw(lib, **kw) == code
+    assert lib.spec_last_error()
+
+
+def test_no_rows_is_a_noop():
+    build.build()
+    assert _raw(_native.load(), rows=0, logits=None) == _native.SPEC_OK
+
+
+def test_binding_refuses_wrong_tensors():
+    x = torch.zeros((4, 100))
+    tok = torch.zeros(4, dtype=torch.int32)
+
+    def refused(match, x=x, token=tok, **kw):
+        with pytest.raises(sv.SpecError, match=match):
+            sv.logprobs(x, token, **kw)
+    refused("logits are", x=x.half())
+    refused("token must be", token=tok.long())
+    refused("token must be", token=tok[:3])
+    refused("temperature", temperature=torch.ones(3))
+    refused("temperature", temperature=torch.ones(4, dtype=torch.float64))
+    refused("CUDA device")                      # host tensors

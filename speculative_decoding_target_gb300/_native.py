@@ -43,6 +43,7 @@ EXPORTED = (
     "spec_verify_attention_shared", "spec_verify_shared_workspace_size",
     "spec_sample", "spec_norm_rope_append", "spec_chunk_attention",
     "spec_chunk_workspace_size", "spec_logprobs",
+    "spec_logprob_workspace_size",
 )
 SELECT_MODES = {"greedy": 0, "map": 1}
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
@@ -150,7 +151,10 @@ def load(path: str = LIB_PATH):
     lib.spec_chunk_attention.restype = ctypes.c_int
     lib.spec_sample.argtypes = [ctypes.POINTER(SampleDesc)] + [P] * 10
     lib.spec_sample.restype = ctypes.c_int
-    lib.spec_logprobs.argtypes = [ctypes.POINTER(LogprobDesc)] + [P] * 8
+    lib.spec_logprob_workspace_size.argtypes = [ctypes.POINTER(LogprobDesc)]
+    lib.spec_logprob_workspace_size.restype = sz
+    lib.spec_logprobs.argtypes = ([ctypes.POINTER(LogprobDesc)] + [P] * 8
+                                  + [sz, P])
     lib.spec_logprobs.restype = ctypes.c_int
     lib.spec_rope_append.argtypes = [ctypes.POINTER(RopeDesc)] + [P] * 15
     lib.spec_rope_append.restype = ctypes.c_int
@@ -796,8 +800,15 @@ def sample(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None,
     return token
 
 
+def logprob_workspace_size(desc: LogprobDesc) -> int:
+    n = load().spec_logprob_workspace_size(ctypes.byref(desc))
+    if n == 0:
+        raise SpecError(SPEC_ERR_ARG, load().spec_last_error().decode())
+    return int(n)
+
+
 def logprobs(logits, token=None, *, temperature=None, top: int = 0,
-             stream=None) -> dict:
+             workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
     """Log probabilities of the given tokens (int32 [..], or None) under the
     rows of logits (fp32 or bf16 [.., vocab], rows contiguous, evenly spaced),
     with an optional per-row temperature (fp32 [..]).  Returns a dict of
@@ -812,7 +823,7 @@ def logprobs(logits, token=None, *, temperature=None, top: int = 0,
         _expect(token, torch.int32, "token", lead, True)
     if temperature is not None:
         _expect(temperature, torch.float32, "temperature", lead, True)
-    on = _on_current_device((logits, token, temperature), stream)
+    on = _on_current_device((logits, token, temperature, workspace), stream)
     rows = lead.numel()
     stride = _row_stride(logits, rows)
     out = {}
@@ -827,10 +838,15 @@ def logprobs(logits, token=None, *, temperature=None, top: int = 0,
             out["top_logprobs"] = torch.empty((*lead, top), **f32)
     desc = LogprobDesc(rows, vocab, int(logits.dtype == torch.bfloat16), top,
                        stride)
+    if workspace is None:
+        with _made_on(stream):
+            workspace = alloc_workspace(logprob_workspace_size(desc),
+                                        logits.device)
     rc = load().spec_logprobs(
         ctypes.byref(desc), _at(logits), _at(token), _at(temperature),
         _at(out.get("logprob")), _at(out["entropy"]), _at(out.get("top_ids")),
-        _at(out.get("top_logprobs")), on)
+        _at(out.get("top_logprobs")), _at(workspace),
+        workspace.numel() * workspace.element_size(), on)
     if rc:
         _check(rc)
     return out

@@ -8,16 +8,27 @@
 // ascending).  4 or 2 bytes a token against about five instructions: HBM bounds
 // it as long as the sums keep up.
 //
-// A cluster of CTAs takes a row; a thread takes every 512th 16-byte vector of
-// its CTA's part.  In base 2, with t = (x - ref) log2(e) / T:
+// As many CTAs as are resident share the rows.  With many rows each takes whole
+// ones, every grid'th.  Otherwise the rows that are not idle are laid end to end,
+// in slices of about kSlice tokens, and cut into equal runs: a CTA has the end of
+// one row, whole rows and the start of another, and a second kernel joins the
+// parts of rows that were cut.  (A cluster a row, instead: 1,024 bf16 rows of
+// 248,320 are 3.4 rounds of the GPU and took 4, and 8 CTAs a row cost more in
+// cluster launches than the rows; 64 rows 28 us with 8, 20.7 with 4.)
+//
+// A thread takes every 512th 16-byte vector of its CTA's part of a row.  In
+// base 2, with t = (x - ref) log2(e) / T:
 //   s = sum 2^t,  h = sum 2^t t
 // against a reference of the thread's own, its first batch's largest value; a
 // batch that exceeds it by 2^kRebase moves it (the sums stay far inside fp32's
 // range, so nothing has to follow each new maximum).  A batch is summed by
 // itself before it joins the sums: beside a weight of one, single small weights
-// would be lost.  Threads' sums join in fp32 inside a warp and in fp64 beyond.
-// Values below ref - kLow T / log2(e) weigh nothing in fp32 and are raised to
-// that, -inf and NaN among them, so that t stays a number.
+// would be lost.
+// t is one fused step on the logit, x c - fl(ref c); what that product was
+// rounded by (delta) is put right where the threads' sums join.  A batch with
+// values that are not finite makes h NaN or infinite; it, and one whose ref c is
+// too large to be rounded so, is summed from (x - ref) c, where -inf and NaN
+// weigh nothing.
 //
 // Alternatives.  Each thread keeps its largest value and the vector that holds
 // it (the first, of equals).  The `top` best tokens of a CTA lie in the vectors'
@@ -38,15 +49,21 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+constexpr int kCtasPerSm = 2;
 constexpr int kVecs = 4;          // 16-byte vectors of a batch
+constexpr int kSlice = 4096;      // tokens
+// rows per CTA from which on whole rows are dealt
+constexpr int kManyRows = 16;
+// rows that a cluster each takes
+constexpr int kFewRows = 64;
 constexpr int kMaxCluster = 16;
 constexpr float kRebase = 8.f;    // log2
 constexpr float kLow = 160.f;     // log2
+constexpr float kLargeRef = 1048576.f;
 constexpr int kTop = kLogprobMaxTop;
 constexpr int kGroups = 64;       // groups of 8 threads
-// what winners of ranks 0 .. top - 1 may hand in; also a cluster's lists
+// what winners of ranks 0 .. top - 1 may hand in
 constexpr int kCands = kTop * (kTop + 1) / 2;
-static_assert(kCands >= kMaxCluster * kTop, "");
 constexpr float kMaxFinite = 3.402823466e+38f;
 typedef unsigned long long u64;
 
@@ -62,24 +79,18 @@ __device__ __forceinline__ float2 unpack2(u64 v) {
 }
 __device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
   u64 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  asm("fma.rn.ftz.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
 __device__ __forceinline__ u64 add2(u64 a, u64 b) {
   u64 d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  asm("add.rn.ftz.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-
-__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
-  u64 d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
 }
 
 // NaN counts as -inf, +inf as the type's largest value.
@@ -127,73 +138,63 @@ __device__ __forceinline__ float largest(uint4 v, float*) {
                      fmaxf(__uint_as_float(v.z), __uint_as_float(v.w))),
                -INFINITY);
 }
-// A vector's values, those below `low` (and NaN) raised to it.
-__device__ __forceinline__ void widen_from(uint4 v, float low, float (&x)[8],
-                                           __nv_bfloat16* t) {
-  // `low` rounded down
-  const uint32_t l = (__float_as_uint(low) + (low < 0.f ? 0xffffu : 0u)) &
-                     0xffff0000u;
-  const uint32_t l2 = l | l >> 16;
-  v.x = max_bf16x2(v.x, l2);
-  v.y = max_bf16x2(v.y, l2);
-  v.z = max_bf16x2(v.z, l2);
-  v.w = max_bf16x2(v.w, l2);
-  widen(v, x, t);
+// A token as one number: larger value first, then the smaller place (its own, or
+// its vector's first token's).  0 is no token.
+__device__ __forceinline__ u64 key_of(float v, int place) {
+  const uint32_t b = __float_as_uint(v + 0.f);  // -0 as 0
+  const uint32_t o = b & 0x80000000u ? ~b : b | 0x80000000u;
+  return (u64)o << 32 | (0xffffffffu - (uint32_t)place);
 }
-__device__ __forceinline__ void widen_from(uint4 v, float low, float (&x)[4],
-                                           float* t) {
-  widen(v, x, t);
-#pragma unroll
-  for (int k = 0; k < 4; ++k) x[k] = fmaxf(x[k], low);
+__device__ __forceinline__ float value_of(u64 key) {
+  const uint32_t o = (uint32_t)(key >> 32);
+  return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
 }
-
-// Larger value first, then the smaller number.
-__device__ __forceinline__ bool better(float a, int ia, float b, int ib) {
-  return a > b || (a == b && ia < ib);
+__device__ __forceinline__ int place_of(u64 key) {
+  return (int)(0xffffffffu - (uint32_t)key);
 }
 
 struct Shared {
-  float max[kWarps];
-  double s[kWarps], h[kWarps];
-  // a CTA's results, read by the cluster's first
-  float row_max;
-  double row_s, row_h;
-  float top_v[kTop];
-  int top_i[kTop];
-  // selection
-  __align__(16) float group[kGroups];
-  float bound;
-  int listed, cands;
-  float list_v[kThreads];
-  int list_vec[kThreads], list_t[kThreads];
-  int winner[kTop];
-  float cand_v[kCands];
-  int cand_i[kCands];
+  float max[kWarps], s[kWarps], h[kWarps];
+  // selection: keys, in pairs
+  __align__(16) u64 group[kGroups];
+  __align__(16) u64 list[kThreads + 2];
+  __align__(16) u64 cands[kCands + 2];
+  u64 bound;
+  int listed, found;
+  uint16_t list_t[kThreads];
+  uint16_t winner[kTop];
+  u64 top[kTop];
+  // live rows
+  int scan[kWarps], live, first;
 };
 
 // A CTA's part of a row: vectors [begin, end) from the first 16-byte boundary
-// on; the tokens in front of that and behind the last vector, at most 7 each,
-// are the first CTA's, one a thread (the thread's "odd" token).
+// on, slices [q0, q1) of `slices`.  The tokens in front of that and behind the
+// last vector, at most 7 each, go with slice 0, one a thread (the thread's "odd"
+// token).
 template <typename T>
 struct Part {
   const T* x;
   int head;          // tokens in front of the first vector
   int begin, end;
+  int odds;          // odd tokens behind the last vector start here; -1: none here
   int odd;           // this thread's odd token, or -1
-  __device__ Part(const T* x, int vocab, int rank, int csize) : x(x) {
+  int vocab;
+  __device__ Part(const T* x, int vocab, int q0, int q1, int slices)
+      : x(x), vocab(vocab) {
     constexpr int kN = Vec<T>::kN;
     const int off = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
     head = min((kN - off) % kN, vocab);
     const int nv = (vocab - head) / kN;
-    begin = (int)((long long)nv * rank / csize);
-    end = (int)((long long)nv * (rank + 1) / csize);
-    odd = odd_of(threadIdx.x, vocab, rank, nv);
+    begin = (int)((long long)nv * q0 / slices);
+    end = (int)((long long)nv * q1 / slices);
+    odds = q0 ? -1 : head + nv * kN;
+    odd = odd_of(threadIdx.x);
   }
-  __device__ __forceinline__ int odd_of(int t, int vocab, int rank, int nv) const {
-    if (rank) return -1;
+  __device__ __forceinline__ int odd_of(int t) const {
+    if (odds < 0) return -1;
     if (t < head) return t;
-    const int tail = head + nv * Vec<T>::kN + t - 8;
-    return t >= 8 && tail < vocab ? tail : -1;
+    return t >= 8 && odds + t - 8 < vocab ? odds + t - 8 : -1;
   }
   __device__ __forceinline__ const uint4* vec(int v) const {
     return reinterpret_cast<const uint4*>(x + head) + v;
@@ -207,114 +208,194 @@ __device__ __forceinline__ float to_float(__nv_bfloat16 x) {
 
 // A thread's sums against ref, its largest value and where it is.
 struct Sums {
-  float ref, low, s, h, max;
-  int vec;
+  float ref, rc, s, h, max;  // rc = fl(ref c)
+  int vec;                   // (-1: the odd token)
 };
 
+// What ref c was rounded by; 0 where that is no small number any more, and t is
+// taken from the difference of the logits.
+__device__ __forceinline__ float delta_of(float ref, float c) {
+  const float rc = ref * c;
+  return fabsf(rc) <= kLargeRef ? fmaf(ref, c, -rc) : 0.f;
+}
+
 // Moves the reference to `ref`, a finite value.
-template <typename T>
 __device__ __forceinline__ void rebase(Sums& a, float ref, float c) {
   if (a.ref > -INFINITY) {
-    const float d = (a.ref - ref) * c, k = ex2(d);
-    a.h = (a.h + fmaxf(d, -kLow) * a.s) * k;
+    const float d = fmaxf(
+        fmaf(a.ref - ref, c, delta_of(ref, c) - delta_of(a.ref, c)), -kLow);
+    const float k = ex2(d);
+    a.h = (a.h + d * a.s) * k;
     a.s *= k;
   }
   a.ref = ref;
-  // below ref by more than its rounding
-  a.low = fmaxf(ref - fmaxf(kLow / c, fabsf(ref) * 4.8e-7f), -most_of<T>());
+  a.rc = ref * c;
 }
 
-// A batch of vectors v0, v0 + kThreads, .. joins the sums.
-template <typename T>
+// A batch of vectors v0, v0 + kThreads, .. joins the sums; `refill` is called
+// with a number that all of the batch went into.
+template <typename T, typename F>
 __device__ __forceinline__ void join(Sums& a, const uint4 (&raw)[kVecs], int v0,
-                                     float c) {
+                                     float c, F refill) {
   constexpr int kN = Vec<T>::kN;
   float most = -INFINITY;
 #pragma unroll
   for (int u = 0; u < kVecs; ++u) {
     const float m = largest(raw[u], static_cast<T*>(nullptr));
     most = fmaxf(most, m);
-    const float fine = fminf(m, most_of<T>());
-    if (fine > a.max) {
-      a.max = fine;
+    if (m > a.max) {
+      a.max = m;
       a.vec = v0 + u * kThreads;
     }
   }
-  if (most == -INFINITY) return;  // nothing that weighs
-  const bool endless = most == INFINITY;
-  most = fminf(most, most_of<T>());
-  if (!((most - a.ref) * c <= kRebase)) rebase<T>(a, most, c);
-  if (endless || a.ref < -1e38f) {  // no number to raise to, or none below
-    float s = 0.f, h = 0.f;
+  refill(most);
+  if (!((most - a.ref) * c <= kRebase)) {  // (also for an infinite one)
+    if (most == -INFINITY) return;         // nothing so far that weighs
+    if (most == INFINITY) {
+      // no value is larger, and the first of the type's largest counts
+      most = a.max = most_of<T>();
+#pragma unroll
+      for (int u = kVecs - 1; u >= 0; --u)
+        if (largest(raw[u], static_cast<T*>(nullptr)) >= most)
+          a.vec = v0 + u * kThreads;
+    }
+    rebase(a, most, c);
+  }
+  const u64 c2 = pack2(c, c), r2 = pack2(-a.rc, -a.rc);
+  u64 s2 = 0, h2 = 0;  // two zeros each
+#pragma unroll
+  for (int u = 0; u < kVecs; ++u) {
+    float x[kN];
+    widen(raw[u], x, static_cast<T*>(nullptr));
+#pragma unroll
+    for (int k = 0; k < kN; k += 2) {
+      const u64 t = fma2(pack2(x[k], x[k + 1]), c2, r2);
+      const float2 tf = unpack2(t);
+      const u64 e = pack2(ex2(tf.x), ex2(tf.y));
+      s2 = add2(s2, e);
+      h2 = fma2(e, t, h2);
+    }
+  }
+  const float2 sf = unpack2(s2), hf = unpack2(h2);
+  float s = sf.x + sf.y, h = hf.x + hf.y;
+  if (!(fabsf(h) <= kMaxFinite && fabsf(a.rc) <= kLargeRef)) {
+    const float delta = delta_of(a.ref, c);
+    s = h = 0.f;
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) {
       float x[kN];
       widen(raw[u], x, static_cast<T*>(nullptr));
 #pragma unroll
       for (int k = 0; k < kN; ++k) {
-        const float t = fmaxf((clean<T>(x[k]) - a.ref) * c, -kLow), e = ex2(t);
+        const float t = fmaxf(fmaf(clean<T>(x[k]) - a.ref, c, delta), -kLow);
+        const float e = ex2(t);
         s += e;
         h = fmaf(e, t, h);
       }
     }
-    a.s += s;
-    a.h += h;
-    return;
   }
-  const u64 c2 = pack2(c, c), r2 = pack2(-a.ref, -a.ref);
-  u64 s = 0, h = 0;  // two zeros each
-#pragma unroll
-  for (int u = 0; u < kVecs; ++u) {
-    float x[kN];
-    widen_from(raw[u], a.low, x, static_cast<T*>(nullptr));
-#pragma unroll
-    for (int k = 0; k < kN; k += 2) {
-      const u64 t = mul2(add2(pack2(x[k], x[k + 1]), r2), c2);
-      const float2 tf = unpack2(t);
-      const u64 e = pack2(ex2(tf.x), ex2(tf.y));
-      s = add2(s, e);
-      h = fma2(e, t, h);
-    }
-  }
-  const float2 sf = unpack2(s), hf = unpack2(h);
-  a.s += sf.x + sf.y;
-  a.h += hf.x + hf.y;
+  a.s += s;
+  a.h += h;
 }
 
-template <typename T>
-__device__ __forceinline__ Sums stream(const Part<T>& part, float c) {
-  Sums a{-INFINITY, 0.f, 0.f, 0.f, -INFINITY, 0};
-  const uint32_t none = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;  // -inf
-  const uint4 empty = make_uint4(none, none, none, none);
-  int v = part.begin + (int)threadIdx.x;
-  uint4 raw[kVecs];
-  auto load = [&](int at) {
+// A thread's own ring of batches in shared memory: it copies its vectors there
+// and reads them back, so no thread waits for another.
+constexpr int kStages = 3;
+constexpr int kStep = kVecs * kThreads;
+constexpr int kRingBytes = kStages * kStep * 16;
+
+struct Ring {
+  uint32_t base;  // this thread's first place
+  uint32_t at;    // and that of the next batch
+  __device__ __forceinline__ explicit Ring(const void* smem)
+      : base((uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16),
+        at(base) {}
+  __device__ __forceinline__ uint32_t behind(uint32_t place) const {
+    place += kStep * 16;
+    return place == base + kRingBytes ? base : place;
+  }
+  // A batch of vectors from v on, `left` of them in the part.  `after`: what
+  // has to be known before (what was read from the place).
+  __device__ __forceinline__ void load(const uint4* from, int left, uint32_t to,
+                                       float after) {
+    if (left >= kStep) {  // (uniform)
 #pragma unroll
-    for (int u = 0; u < kVecs; ++u) {
-      const int w = at + u * kThreads;
-      raw[u] = empty;
-      if (w < part.end) raw[u] = __ldg(part.vec(w));
+      for (int u = 0; u < kVecs; ++u) copy(from, u, to, after);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kVecs; ++u)
+        if ((int)threadIdx.x + u * kThreads < left) copy(from, u, to, after);
     }
-  };
-  load(v);
-  for (; v < part.end; v += kVecs * kThreads) {
-    uint4 now[kVecs];
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  static __device__ __forceinline__ void copy(const uint4* from, int u,
+                                              uint32_t to, float after) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                     to + u * kThreads * 16),
+                 "l"(from + u * kThreads), "f"(after)
+                 : "memory");
+  }
+  // The first batches of a part.
+  template <typename T>
+  __device__ __forceinline__ void start(const Part<T>& part) {
+    const uint4* from = part.vec(part.begin + (int)threadIdx.x);
+    uint32_t to = at;
 #pragma unroll
-    for (int u = 0; u < kVecs; ++u) now[u] = raw[u];
-    load(v + kVecs * kThreads);
-    join<T>(a, now, v, c);
+    for (int k = 0; k < kStages; ++k, from += kStep, to = behind(to))
+      load(from, part.end - part.begin - k * kStep, to, 0.f);
+  }
+};
+
+// The sums of a part that the ring has started.
+template <typename T>
+__device__ __forceinline__ Sums stream(const Part<T>& part, Ring& ring, float c) {
+  Sums a{-INFINITY, 0.f, 0.f, 0.f, -INFINITY, 0};
+  int v = part.begin + (int)threadIdx.x;
+  int left = part.end - part.begin;
+  const uint4* ahead = part.vec(v + kStages * kStep);
+  uint4 raw[kVecs];
+  auto get = [&]() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(raw[u].x), "=r"(raw[u].y), "=r"(raw[u].z),
+                     "=r"(raw[u].w)
+                   : "r"(ring.at + u * kThreads * 16)
+                   : "memory");
+  };
+#pragma unroll 1
+  for (; left >= kStep; left -= kStep, v += kStep, ahead += kStep) {
+    get();
+    join<T>(a, raw, v, c, [&](float most) {
+      ring.load(ahead, left - kStages * kStep, ring.at, most);
+    });
+    ring.at = ring.behind(ring.at);
+  }
+  if (left > 0) {  // the last batch, -inf behind the last vector
+    get();
+    const uint32_t none = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u)
+      if ((int)threadIdx.x + u * kThreads >= left)
+        raw[u] = make_uint4(none, none, none, none);
+    join<T>(a, raw, v, c, [&](float) {
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    });
+    ring.at = ring.behind(ring.at);
   }
   if (part.odd >= 0) {
     const float x = clean<T>(to_float(part.x[part.odd]));
-    // before every vector, or behind them
-    const int at = part.odd < part.head ? -1 : 1 << 30;
-    if (x > a.max || (x == a.max && at < a.vec && x > -INFINITY)) {
+    // in front of every vector, or behind them
+    if (x > a.max || (x == a.max && part.odd < part.head && x > -INFINITY)) {
       a.max = x;
-      a.vec = at;
+      a.vec = -1;
     }
     if (x > -INFINITY) {
-      if (!((x - a.ref) * c <= kRebase)) rebase<T>(a, x, c);
-      const float t = fmaxf((x - a.ref) * c, -kLow), e = ex2(t);
+      if (!((x - a.ref) * c <= kRebase)) rebase(a, x, c);
+      const float t =
+          fmaxf(fmaf(x - a.ref, c, delta_of(a.ref, c)), -kLow);
+      const float e = ex2(t);
       a.s += e;
       a.h = fmaf(e, t, a.h);
     }
@@ -328,301 +409,606 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-// The CTA's best `top` tokens into sh.top_v / top_i (-inf and -1 behind the
-// last finite one).  Called by the whole CTA; ends with a barrier.
-template <typename T>
-__device__ void select(Shared& sh, const Part<T>& part, const Sums& a, int vocab,
-                       int rank, int top) {
-  constexpr int kN = Vec<T>::kN;
-  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
-  // a bound: the top-th largest of 64 groups' maxima
-  float g = a.max;
-#pragma unroll
-  for (int o = 4; o; o >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
-  if ((lane & 7) == 0) sh.group[tid >> 3] = g;
-  if (tid == 0) sh.listed = sh.cands = 0;
-  if (tid < kTop) {
-    sh.top_v[tid] = -INFINITY;
-    sh.top_i[tid] = -1;
+// How many of the n keys beat `mine` (behind the last stands a 0).
+__device__ __forceinline__ int rank_in(const u64* keys, int n, u64 mine) {
+  int r = 0;
+#pragma unroll 4
+  for (int k = 0; k < n; k += 2) {
+    const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(keys + k);
+    r += (two.x > mine) + (two.y > mine);
   }
-  __syncthreads();
-  if (tid < kGroups) {
-    const float mine = sh.group[tid];
-    int rank_g = 0;
-#pragma unroll 8
-    for (int k = 0; k < kGroups; ++k)
-      rank_g += better(sh.group[k], k, mine, tid);
-    if (rank_g == top - 1) sh.bound = mine;
-  }
-  __syncthreads();
-  // the threads at or above it, in any order
-  const bool in = a.max >= sh.bound && a.max > -INFINITY;
-  const unsigned who = __ballot_sync(0xffffffffu, in);
-  int at = 0;
-  if (lane == 0 && who) at = atomicAdd(&sh.listed, __popc(who));
-  at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1));
-  if (in) {
-    sh.list_v[at] = a.max;
-    sh.list_vec[at] = a.vec;
-    sh.list_t[at] = tid;
-  }
-  __syncthreads();
-  const int n = sh.listed;
-  if (tid < n) {
-    const float v = sh.list_v[tid];
-    const int vec = sh.list_vec[tid];
-    const int key_t = sh.list_t[tid];  // odd tokens: in the threads' order
-    int r = 0;
-    for (int k = 0; k < n; ++k) {
-      const float kv = sh.list_v[k];
-      const int kvec = sh.list_vec[k];
-      r += kv > v || (kv == v && (kvec < vec ||
-                                  (kvec == vec && sh.list_t[k] < key_t)));
-    }
-    if (r < top) sh.winner[r] = key_t;
-    if (r == top - 1) sh.bound = v;
-  }
-  __syncthreads();
-  const int winners = min(n, top);
-  const float bound = n >= top ? sh.bound : -INFINITY;
-  const int nv = (vocab - part.head) / kN;
-  for (int r = w; r < winners; r += kWarps) {
-    const int t = sh.winner[r];
-    constexpr int kHold = kLogprobMaxVocab / kThreads / 32;  // 32 values a lane
-    float x[kHold];
-    const int v0 = part.begin + t + lane * kThreads;
-#pragma unroll
-    for (int q = 0; q < kHold / kN; ++q) {
-      const int v = v0 + q * 32 * kThreads;
-      float y[kN];
-#pragma unroll
-      for (int k = 0; k < kN; ++k) y[k] = -INFINITY;
-      if (v < part.end) widen(__ldg(part.vec(v)), y, static_cast<T*>(nullptr));
-#pragma unroll
-      for (int k = 0; k < kN; ++k) x[q * kN + k] = clean<T>(y[k]);
-    }
-    // the odd token, lane 31's only
-    float odd_x = -INFINITY;
-    const int odd = part.odd_of(t, vocab, rank, nv);
-    if (lane == 31 && odd >= 0) odd_x = clean<T>(to_float(part.x[odd]));
-    for (int left = top - r; left; --left) {
-      float best = odd_x;
-      int id = odd_x > -INFINITY ? odd : 0x7fffffff;
-#pragma unroll
-      for (int k = 0; k < kHold; ++k) {
-        const int i = part.head + (v0 + k / kN * 32 * kThreads) * kN + k % kN;
-        if (x[k] > -INFINITY && better(x[k], i, best, id)) {
-          best = x[k];
-          id = i;
-        }
-      }
-      float wb = best;
-      int wi = id;
-#pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        const float ov = __shfl_xor_sync(0xffffffffu, wb, o);
-        const int oi = __shfl_xor_sync(0xffffffffu, wi, o);
-        if (better(ov, oi, wb, wi)) {
-          wb = ov;
-          wi = oi;
-        }
-      }
-      if (wb == -INFINITY || wb < bound) break;  // uniform
-      if (lane == 0) {
-        const int c = atomicAdd(&sh.cands, 1);
-        sh.cand_v[c] = wb;
-        sh.cand_i[c] = wi;
-      }
-      // taken out
-      if (wi == odd) odd_x = -INFINITY;
-#pragma unroll
-      for (int k = 0; k < kHold; ++k)
-        if (part.head + (v0 + k / kN * 32 * kThreads) * kN + k % kN == wi)
-          x[k] = -INFINITY;
-    }
-  }
-  __syncthreads();
-  const int cands = sh.cands;
-  for (int j = tid; j < cands; j += kThreads) {
-    const float v = sh.cand_v[j];
-    const int i = sh.cand_i[j];
-    int r = 0;
-    for (int k = 0; k < cands; ++k) r += better(sh.cand_v[k], sh.cand_i[k], v, i);
-    if (r < top) {
-      sh.top_v[r] = v;
-      sh.top_i[r] = i;
-    }
-  }
-  __syncthreads();
+  return r;
 }
 
-template <typename V>
-__device__ __forceinline__ V peer_load(const V* p, uint32_t rank) {
-  const uint32_t at = tc::map_to(tc::smem_u32(p), rank);
-  V v;
-  if constexpr (sizeof(V) == 8) {
-    u64 r;
-    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(r) : "r"(at));
-    v = *reinterpret_cast<const V*>(&r);
-  } else {
-    uint32_t r;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(r) : "r"(at));
-    v = *reinterpret_cast<const V*>(&r);
-  }
-  return v;
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 2)
-    logprobs_kernel(const LogprobParams p, int csize) {
-  __shared__ Shared sh;
-  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
-  const int row = blockIdx.x / csize, rank = blockIdx.x - row * csize;
-  const T* x = static_cast<const T*>(p.logits) + row * p.row_stride;
-  const float temp = p.temperature ? p.temperature[row] : 1.f;
-  const int token = p.token ? p.token[row] : 0;
-  const long long out = (long long)row * p.top;
-  if (token < 0 || token >= p.vocab || !(temp >= 0.f && temp <= kMaxFinite)) {
-    if (rank) return;  // an idle row
-    if (tid == 0 && p.logprob) p.logprob[row] = 0.f;
-    if (tid == 0 && p.entropy) p.entropy[row] = 0.f;
-    if (tid < p.top) {
-      p.top_ids[out + tid] = -1;
-      p.top_logprobs[out + tid] = -INFINITY;
-    }
-    return;
-  }
-  const bool one = temp == 0.f;  // all the mass on the first of the largest
-  const int top = one ? max(p.top, 1) : p.top;
-  // 1 / T stays inside fp32's range
-  const float c =
-      one ? 1.f
-          : fminf(fmaxf(__fdiv_rn(1.4426950408889634f, temp), 1e-37f), 1e37f);
-  float given = 0.f;
-  if (tid == 0) given = clean<T>(to_float(x[token]));
-  const Part<T> part(x, p.vocab, rank, csize);
-  const Sums a = stream(part, c);
-  // the CTA's sums
-  const float wm = warp_max(a.max);
-  if (lane == 0) sh.max[w] = wm;
-  __syncthreads();
-  float m = sh.max[lane & (kWarps - 1)];
-  m = warp_max(m);
-  float s = 0.f, h = 0.f;
-  if (a.ref > -INFINITY) {
-    const float d = fmaxf((a.ref - m) * c, -kLow), k = ex2(d);
-    s = a.s * k;
-    h = fmaf(d, s, a.h * k);
-  }
+__device__ __forceinline__ void warp_sum(float& s, float& h) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
     s += __shfl_xor_sync(0xffffffffu, s, o);
     h += __shfl_xor_sync(0xffffffffu, h, o);
   }
+}
+
+// The CTA's best `top` tokens into sh.top (0 behind the last finite one).
+// Called by the whole CTA; ends with a barrier.
+template <typename T>
+__device__ void select(Shared& sh, const Part<T>& part, const Sums& a,
+                       int top) {
+  constexpr int kN = Vec<T>::kN;
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  const int place = a.vec < 0 ? part.odd : part.head + a.vec * kN;
+  const u64 mine = a.max > -INFINITY ? key_of(a.max, place) : 0;
+  // a bound: the top-th largest of 64 groups' maxima
+  u64 g = mine;
+#pragma unroll
+  for (int o = 4; o; o >>= 1) {
+    const u64 other = __shfl_xor_sync(0xffffffffu, g, o);
+    g = other > g ? other : g;
+  }
+  if ((lane & 7) == 0) sh.group[tid >> 3] = g;
+  if (tid == 0) {
+    sh.listed = sh.found = 0;
+    sh.bound = 0;
+  }
+  if (tid < kTop) sh.top[tid] = 0;
+  __syncthreads();
+  if (tid < kGroups) {
+    const u64 group = sh.group[tid];
+    if (group && rank_in(sh.group, kGroups, group) == top - 1) sh.bound = group;
+  }
+  __syncthreads();
+  // the threads at or above it, in any order
+  const bool in = mine && mine >= sh.bound;
+  const unsigned who = __ballot_sync(0xffffffffu, in);
+  if (who) {
+    int at = 0;
+    if (lane == 0) at = atomicAdd(&sh.listed, __popc(who));
+    at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1));
+    if (in) {
+      sh.list[at] = mine;
+      sh.list_t[at] = (uint16_t)tid;
+    }
+  }
+  __syncthreads();
+  const int n = sh.listed;
+  if (tid == 0) sh.list[n] = 0;
+  if (n & 1) __syncthreads();  // uniform
+  if (tid < n) {
+    const u64 key = sh.list[tid];
+    const int r = rank_in(sh.list, n, key);
+    if (r < top) sh.winner[r] = sh.list_t[tid];
+    if (r == top - 1) sh.bound = key;
+  }
+  __syncthreads();
+  const int winners = min(n, top);
+  // the last winner's value: what lies below it is no candidate
+  const float bound = n >= top ? value_of(sh.bound) : -INFINITY;
+  // half a warp each
+  const int r = tid >> 4, sub = tid & 15;
+  if (r < winners) {  // (uniform in a half)
+    const unsigned half = lane & 16 ? 0xffff0000u : 0x0000ffffu;
+    const int t = sh.winner[r];
+    const float low = fmaxf(bound, -kMaxFinite);
+    // this lane's vectors of the thread, every 16th, a bit for each value that
+    // is a candidate
+    constexpr int kStride = 16 * kThreads;
+    const int v0 = part.begin + t + sub * kThreads;
+    static_assert(kLogprobMaxVocab / kThreads / 16 <= 64, "");
+    u64 hit = 0;
+    int bit = 0;
+    for (int v = v0; v < part.end; v += 4 * kStride) {
+      uint4 raw[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t none = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
+        raw[q] = make_uint4(none, none, none, none);
+        if (v + q * kStride < part.end) raw[q] = __ldg(part.vec(v + q * kStride));
+      }
+      uint32_t bits = 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float x[kN];
+        widen(raw[q], x, static_cast<T*>(nullptr));
+#pragma unroll
+        for (int k = 0; k < kN; ++k)
+          if (x[k] >= low) bits |= 1u << (q * kN + k);
+      }
+      hit |= (u64)bits << bit;
+      bit += 4 * kN;
+    }
+    const int odd = part.odd_of(t);
+    const float odd_x =
+        sub == 15 && odd >= 0 ? clean<T>(to_float(part.x[odd])) : -INFINITY;
+    const bool odd_hit = odd_x >= low;
+    int hits = __popcll(hit) + odd_hit;
+#pragma unroll
+    for (int o = 8; o; o >>= 1) hits += __shfl_xor_sync(half, hits, o);
+    // the key of the value at a bit
+    auto key_at = [&](int b) {
+      const int place = part.head + (v0 + b / kN * kStride) * kN + b % kN;
+      return key_of(clean<T>(to_float(part.x[place])), place);
+    };
+    if (hits <= top - r) {
+      if (odd_hit) sh.cands[atomicAdd(&sh.found, 1)] = key_of(odd_x, odd);
+      for (; hit; hit &= hit - 1)
+        sh.cands[atomicAdd(&sh.found, 1)] = key_at(__ffsll(hit) - 1);
+    } else {
+      // many equals, or many large values: the first top - r of them
+      u64 last = ~0ull;
+      for (int n_left = top - r; n_left; --n_left) {
+        u64 best = odd_hit ? key_of(odd_x, odd) : 0;
+        if (best >= last) best = 0;
+        for (u64 h = hit; h; h &= h - 1) {
+          const u64 key = key_at(__ffsll(h) - 1);
+          if (key < last && key > best) best = key;
+        }
+#pragma unroll
+        for (int o = 8; o; o >>= 1) {
+          const u64 other = __shfl_xor_sync(half, best, o);
+          best = other > best ? other : best;
+        }
+        last = best;
+        if (sub == 0) sh.cands[atomicAdd(&sh.found, 1)] = best;
+      }
+    }
+  }
+  __syncthreads();
+  const int found = sh.found;
+  if (tid == 0) sh.cands[found] = 0;
+  if (found & 1) __syncthreads();
+  for (int j = tid; j < found; j += kThreads) {
+    const u64 key = sh.cands[j];
+    const int r = rank_in(sh.cands, found, key);
+    if (r < top) sh.top[r] = key;
+  }
+  __syncthreads();
+}
+
+// Natural logarithm of S >= 1 (below 2^24), within 2^-22 of itself: S = m 2^e with m
+// within a factor sqrt(2) of 1, ln m = 2 artanh((m - 1) / (m + 1)).
+__device__ __forceinline__ float ln_of(float S) {
+  int e = (int)((__float_as_uint(S) - 0x3f3504f3u) >> 23);
+  const float m = __uint_as_float(__float_as_uint(S) - ((uint32_t)e << 23));
+  const float z = __fdiv_rn(m - 1.f, m + 1.f), z2 = z * z;
+  float p = fmaf(z2, 1.f / 11.f, 1.f / 9.f);
+  p = fmaf(p, z2, 1.f / 7.f);
+  p = fmaf(p, z2, 1.f / 5.f);
+  p = fmaf(p, z2, 1.f / 3.f);
+  const float lm = fmaf(2.f * z, p * z2, 2.f * z);
+  return fmaf((float)e, 0.693147180559945f, lm);
+}
+
+// A row's inputs.
+struct Row {
+  float temp, c;
+  int token;
+  bool live, one;  // one: all the mass on the first of the largest
+};
+__device__ __forceinline__ Row row_of(const LogprobParams& p, int row) {
+  Row r;
+  r.token = p.token ? p.token[row] : 0;
+  r.temp = p.temperature ? p.temperature[row] : 1.f;
+  r.live = r.token >= 0 && r.token < p.vocab && r.temp >= 0.f &&
+           r.temp <= kMaxFinite;
+  r.one = r.temp == 0.f;
+  // 1 / T stays inside fp32's range
+  r.c = r.one ? 1.f
+              : fminf(fmaxf(__fdiv_rn(1.4426950408889634f, r.temp), 1e-37f),
+                      1e37f);
+  return r;
+}
+__device__ __forceinline__ int top_of(const LogprobParams& p, const Row& r) {
+  return r.one ? max(p.top, 1) : p.top;
+}
+
+// The outputs of a row with largest logit m, sums s and h and its best tokens
+// in `top`.  Called by one warp.
+template <typename T>
+__device__ __forceinline__ void finish(const LogprobParams& p, int row,
+                                       const Row& r, float m, float s, float h,
+                                       const u64* top) {
+  const int lane = threadIdx.x & 31;
+  const bool none = m == -INFINITY;  // no finite logit
+  const float lns = none ? 0.f : ln_of(s);
+  auto logprob = [&](float v, bool first) {
+    if (r.one) return first ? 0.f : -INFINITY;
+    if (none || v == -INFINITY) return -INFINITY;
+    return __fdiv_rn(v - m, r.temp) - lns;
+  };
+  const u64 first = top_of(p, r) ? top[0] : 0;
+  if (lane == 0) {
+    if (p.logprob) {
+      const T* x = static_cast<const T*>(p.logits) + row * p.row_stride;
+      p.logprob[row] = logprob(clean<T>(to_float(x[r.token])),
+                               first && r.token == place_of(first));
+    }
+    if (p.entropy)
+      p.entropy[row] = r.one || none
+                           ? 0.f
+                           : fmaxf(fmaf(__fdiv_rn(h, s), -0.693147180559945f,
+                                        lns),
+                                   0.f);
+  }
+  if (lane < p.top) {
+    const long long out = (long long)row * p.top + lane;
+    const u64 key = top[lane];
+    p.top_ids[out] = key ? place_of(key) : -1;
+    p.top_logprobs[out] = key ? logprob(value_of(key), lane == 0) : -INFINITY;
+  }
+}
+
+__device__ __forceinline__ void finish_idle(const LogprobParams& p, int row) {
+  const int tid = threadIdx.x;
+  if (tid == 0 && p.logprob) p.logprob[row] = 0.f;
+  if (tid == 0 && p.entropy) p.entropy[row] = 0.f;
+  if (tid < p.top) {
+    p.top_ids[(long long)row * p.top + tid] = -1;
+    p.top_logprobs[(long long)row * p.top + tid] = -INFINITY;
+  }
+}
+
+// A part of a row: its largest logit, sums (in warp 0) and best tokens (sh.top).
+// `then` starts the next part's copies, which run under the selection.  Called by
+// the whole CTA.
+template <typename T, typename F>
+__device__ __forceinline__ void work_on(Shared& sh, Ring& ring,
+                                        const Part<T>& part, float c, int top,
+                                        F then, float& m, float& s, float& h) {
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Sums a = stream(part, ring, c);
+  then();
+  const float wm = warp_max(a.max);
+  if (lane == 0) sh.max[w] = wm;
+  __syncthreads();
+  m = warp_max(sh.max[lane & (kWarps - 1)]);
+  s = h = 0.f;
+  if (a.ref > -INFINITY) {
+    const float d = fmaxf(fmaf(a.ref - m, c, -delta_of(a.ref, c)), -kLow);
+    const float k = ex2(d);
+    s = a.s * k;
+    h = fmaf(d, s, a.h * k);
+  }
+  warp_sum(s, h);
   if (lane == 0) {
     sh.s[w] = s;
     sh.h[w] = h;
   }
   __syncthreads();
-  if (tid == 0) {
-    double ss = 0., hh = 0.;
-    for (int k = 0; k < kWarps; ++k) {
-      ss += sh.s[k];
-      hh += sh.h[k];
-    }
-    sh.row_max = m;
-    sh.row_s = ss;
-    sh.row_h = hh;
+  if (w == 0) {
+    s = lane < kWarps ? sh.s[lane] : 0.f;
+    h = lane < kWarps ? sh.h[lane] : 0.f;
+    warp_sum(s, h);
   }
-  if (top) select(sh, part, a, p.vocab, rank, top);
-  if (csize > 1) {
-    tc::cluster_sync();
-    if (rank == 0) {
-      if (w == 0) {  // sums, a lane for each CTA
-        float pm = -INFINITY;
-        double ps = 0., ph = 0.;
-        if (lane < csize) {
-          pm = peer_load(&sh.row_max, lane);
-          ps = peer_load(&sh.row_s, lane);
-          ph = peer_load(&sh.row_h, lane);
-        }
-        const float all = warp_max(pm);
-        if (pm > -INFINITY) {
-          const float d = fmaxf((pm - all) * c, -kLow), k = ex2(d);
-          ph = (ph + (double)d * ps) * k;
-          ps *= k;
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) {
-          ps += __shfl_xor_sync(0xffffffffu, ps, o);
-          ph += __shfl_xor_sync(0xffffffffu, ph, o);
-        }
-        __syncwarp();
-        if (lane == 0) {
-          sh.max[0] = all;
-          sh.s[0] = ps;
-          sh.h[0] = ph;
-        }
-      }
-      const int n = csize * top;
-      for (int j = tid; j < n; j += kThreads) {
-        const int from = j / top, k = j - from * top;
-        sh.cand_v[j] = peer_load(&sh.top_v[k], from);
-        sh.cand_i[j] = peer_load(&sh.top_i[k], from);
-      }
-    }
-    tc::cluster_sync();  // no CTA leaves while the first reads
-    if (rank) return;
-    const int n = csize * top;
-    for (int j = tid; j < n; j += kThreads) {
-      const float v = sh.cand_v[j];
-      const int i = sh.cand_i[j];
-      int r = 0;
-      for (int k = 0; k < n; ++k)
-        r += better(sh.cand_v[k], sh.cand_i[k], v, i);
-      if (r < top && i >= 0) {
-        sh.top_v[r] = v;
-        sh.top_i[r] = i;
-      }
-      if (r < top && i < 0) {
-        sh.top_v[r] = -INFINITY;
-        sh.top_i[r] = -1;
-      }
-    }
-    __syncthreads();
-    m = sh.max[0];
-  } else {
-    if (tid == 0) {
-      sh.s[0] = sh.row_s;
-      sh.h[0] = sh.row_h;
-    }
-    __syncthreads();
-  }
-  const double ln2 = 0.69314718055994530942;
-  const bool none = m == -INFINITY;  // no finite logit
-  const double sum = sh.s[0];
-  const double log2s = none ? 0. : log2(sum);
-  auto logprob = [&](float v, bool first) {
-    if (one) return first ? 0.f : -INFINITY;
-    if (none || v == -INFINITY) return -INFINITY;
-    return (float)((((double)v - m) * c - log2s) * ln2);
-  };
-  if (tid == 0) {
-    if (p.logprob)
-      p.logprob[row] = logprob(given, token == sh.top_i[0]);
-    if (p.entropy)
-      p.entropy[row] =
-          one || none ? 0.f : fmaxf((float)((log2s - sh.h[0] / sum) * ln2), 0.f);
-  }
-  if (tid < p.top) {
-    const int i = sh.top_i[tid];
-    p.top_ids[out + tid] = i;
-    p.top_logprobs[out + tid] = i < 0 ? -INFINITY : logprob(sh.top_v[tid], tid == 0);
-  }
+  if (top) select(sh, part, a, top);
 }
 
 template <typename T>
-cudaError_t launch(const LogprobParams& p, int csize, cudaStream_t s) {
+__device__ __forceinline__ const T* row_at(const LogprobParams& p, int row) {
+  return static_cast<const T*>(p.logits) + row * p.row_stride;
+}
+
+// Whole rows, every grid'th.
+template <typename T>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+    logprobs_rows_kernel(const LogprobParams p) {
+  extern __shared__ __align__(16) uint8_t ring_smem[];
+  __shared__ Shared sh;
+  tc_grid_launch_dependents();
+  Ring ring(ring_smem);
+  // the next live row, and its copies started
+  int row = blockIdx.x;
+  Row r;
+  auto seek = [&]() {
+    for (; row < p.rows; row += gridDim.x) {
+      r = row_of(p, row);
+      if (r.live) {
+        ring.start(Part<T>(row_at<T>(p, row), p.vocab, 0, 1, 1));
+        return;
+      }
+      finish_idle(p, row);
+    }
+  };
+  seek();
+  while (row < p.rows) {
+    const int now = row;
+    const Row rn = r;
+    float m, s, h;
+    work_on(sh, ring, Part<T>(row_at<T>(p, now), p.vocab, 0, 1, 1), rn.c,
+            top_of(p, rn),
+            [&] {
+              row += gridDim.x;
+              seek();
+            },
+            m, s, h);
+    if (threadIdx.x < 32) finish<T>(p, now, rn, m, s, h, sh.top);
+    __syncthreads();  // before the next row's sums and lists
+  }
+}
+
+// The live rows' slices in equal runs.  part[0]: the CTA's part of a row that an
+// earlier CTA started; part[1]: of one that it starts and a later one ends.
+template <typename T>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+    logprobs_runs_kernel(const LogprobParams p) {
+  extern __shared__ __align__(16) uint8_t ring_smem[];
+  __shared__ Shared sh;
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  // the merge may be scheduled; it waits for this grid
+  tc_grid_launch_dependents();
+  LogprobPart* mine = p.parts + 2 * blockIdx.x;
+  // consecutive rows a thread
+  const int per = (p.rows + kThreads - 1) / kThreads;
+  const int r0 = min(tid * per, p.rows), r1 = min(r0 + per, p.rows);
+  int live = 0;
+  for (int row = r0; row < r1; ++row) live += row_of(p, row).live;
+  int upto = live;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int n = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += n;
+  }
+  if (lane == 31) sh.scan[w] = upto;
+  if (tid < 2) mine[tid].row = -1;
+  __syncthreads();
+  int total = 0;
+#pragma unroll
+  for (int k = 0; k < kWarps; ++k) {
+    if (k < w) upto += sh.scan[k];
+    total += sh.scan[k];
+  }
+  const long long units = (long long)total * p.slices;
+  const long long u0 = units * blockIdx.x / gridDim.x;
+  const long long u1 = units * (blockIdx.x + 1) / gridDim.x;
+  const int n0 = (int)(u0 / p.slices);  // first live row of the run
+  if (u0 < u1 && n0 >= upto - live && n0 < upto) {
+    int row = r0;
+    for (int n = upto - live;; ++row)
+      if (row_of(p, row).live && n++ == n0) break;
+    sh.first = row;
+  }
+  // idle rows
+  for (int row = blockIdx.x; row < p.rows; row += gridDim.x)
+    if (!row_of(p, row).live) finish_idle(p, row);
+  __syncthreads();
+  if (u0 >= u1) return;
+  Ring ring(ring_smem);
+  // the part at slice u, and its copies started (there are live rows up to u1)
+  int row = sh.first - 1, q0, q1;
+  long long u = u0;
+  Row r;
+  auto seek = [&]() {
+    if (u >= u1) return;
+    do {
+      r = row_of(p, ++row);
+    } while (!r.live);
+    const long long at = u / p.slices * p.slices;  // the row's first slice
+    q0 = (int)(u - at);
+    q1 = (int)min(u1 - at, (long long)p.slices);
+    u = at + q1;
+    ring.start(Part<T>(row_at<T>(p, row), p.vocab, q0, q1, p.slices));
+  };
+  seek();
+  for (bool more = true; more;) {
+    const int now = row, n0q = q0, n1q = q1;
+    const Row rn = r;
+    const int top = top_of(p, rn);
+    more = u < u1;
+    float m, s, h;
+    work_on(sh, ring, Part<T>(row_at<T>(p, now), p.vocab, n0q, n1q, p.slices),
+            rn.c, top, seek, m, s, h);
+    const bool ends = n1q == p.slices;
+    if (n0q == 0 && ends) {
+      if (w == 0) finish<T>(p, now, rn, m, s, h, sh.top);
+    } else if (w == 0) {
+      LogprobPart& to = mine[n0q ? 0 : 1];
+      if (lane == 0) {
+        to.row = now;
+        to.m = m;
+        to.s = s;
+        to.h = h;
+      }
+      if (lane < top) to.top[lane] = sh.top[lane];
+    }
+    __syncthreads();  // before the next row's sums and lists
+  }
+}
+
+// Keys that beat or equal `low`, of `n` (key(i), 0 for none), ranked: the best
+// `top` into sh.top.  Called by the whole CTA; ends with a barrier.
+template <typename F>
+__device__ __forceinline__ void join_tops(Shared& sh, int n, int top, u64 low,
+                                          F key) {
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  if (tid == 0) sh.found = 0;
+  if (tid < kTop) sh.top[tid] = 0;
+  __syncthreads();
+#pragma unroll 4
+  for (int i = tid; i < n; i += kThreads) {
+    const u64 k = key(i);
+    if (k && k >= low) {
+      const int at = atomicAdd(&sh.found, 1);
+      if (at < kCands) sh.cands[at] = k;
+    }
+  }
+  __syncthreads();
+  const int found = sh.found;
+  if (found <= kCands) {
+    if (tid == 0) sh.cands[found] = 0;
+    __syncthreads();
+    for (int i = tid; i < found; i += kThreads) {
+      const u64 k = sh.cands[i];
+      const int at = rank_in(sh.cands, found, k);
+      if (at < top) sh.top[at] = k;
+    }
+  } else {
+    // parts with many large values each: one place after the other
+    u64 before = ~0ull;
+    for (int at = 0; at < top; ++at) {
+      u64 most = 0;
+      for (int i = tid; i < n; i += kThreads) {
+        const u64 k = key(i);
+        if (k < before && k > most) most = k;
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        const u64 other = __shfl_xor_sync(0xffffffffu, most, o);
+        most = other > most ? other : most;
+      }
+      __syncthreads();  // list is read
+      if (lane == 0) sh.list[w] = most;
+      __syncthreads();
+      for (int k = 0; k < kWarps; ++k) most = sh.list[k] > most ? sh.list[k] : most;
+      if (tid == 0) sh.top[at] = most;
+      before = most;
+      if (!most) break;  // uniform
+    }
+  }
+  __syncthreads();
+}
+
+// CTA j joins the row that run j starts and does not end with the parts that the
+// runs behind it have of it: a thread for each.
+constexpr int kMaxRuns = kThreads;
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+    logprobs_merge_kernel(const LogprobParams p) {
+  __shared__ Shared sh;
+  __shared__ uint16_t s_part[kMaxRuns];
+  __shared__ int s_parts;
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  if (tid == 0) s_parts = 0;
+  tc_grid_dependency_wait();
+  const int j = blockIdx.x, at = 2 * (j + tid) + (tid == 0);
+  const int row = p.parts[2 * j + 1].row;
+  if (row < 0) return;  // uniform
+  const bool in_grid = j + tid < (int)gridDim.x;
+  int mine = -1;
+  float pm = -INFINITY, s = 0.f, h = 0.f;
+  if (in_grid) {
+    mine = p.parts[at].row;
+    pm = p.parts[at].m;
+    s = p.parts[at].s;
+    h = p.parts[at].h;
+  }
+  const Row r = row_of(p, row);
+  const int top = top_of(p, r);
+  u64 last = in_grid && top ? p.parts[at].top[top - 1] : 0;
+  const bool is = mine == row;
+  if (!is) {
+    pm = -INFINITY;
+    last = 0;
+  }
+  // largest logit, and a bound: no part's last place is above the row's
+  float m = warp_max(pm);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const u64 other = __shfl_xor_sync(0xffffffffu, last, o);
+    last = other > last ? other : last;
+  }
+  if (lane == 0) {
+    sh.max[w] = m;
+    sh.list[w] = last;
+  }
+  __syncthreads();
+  m = warp_max(sh.max[lane & (kWarps - 1)]);
+  for (int k = 0; k < kWarps; ++k) last = sh.list[k] > last ? sh.list[k] : last;
+  if (pm > -INFINITY) {
+    const float d = fmaxf((pm - m) * r.c, -kLow), e = ex2(d);
+    s *= e;
+    h = fmaf(d, s, h * e);
+  } else {
+    s = h = 0.f;
+  }
+  warp_sum(s, h);
+  if (lane == 0) {
+    sh.s[w] = s;
+    sh.h[w] = h;
+  }
+  if (is) s_part[atomicAdd(&s_parts, 1)] = (uint16_t)at;  // in any order
+  __syncthreads();
+  if (top)
+    join_tops(sh, s_parts * top, top, last, [&](int i) {
+      const int k = i / top;
+      return p.parts[s_part[k]].top[i - k * top];
+    });
+  if (w == 0) {
+    s = lane < kWarps ? sh.s[lane] : 0.f;
+    h = lane < kWarps ? sh.h[lane] : 0.f;
+    warp_sum(s, h);
+    finish<T>(p, row, r, m, s, h, sh.top);
+  }
+}
+
+// Few rows: a cluster each, joined through distributed shared memory.
+template <typename V>
+__device__ __forceinline__ void store_first(V* p, V v) {
+  const uint32_t at = tc::map_to(tc::smem_u32(p), 0);
+  if constexpr (sizeof(V) == 8)
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(v) : "memory");
+  else
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
+}
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+    logprobs_cluster_kernel(const LogprobParams p, int csize) {
+  extern __shared__ __align__(16) uint8_t ring_smem[];
+  __shared__ Shared sh;
+  __shared__ float c_max[kMaxCluster], c_s[kMaxCluster], c_h[kMaxCluster];
+  __shared__ u64 c_top[kMaxCluster * kTop];
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  const int row = blockIdx.x / csize, rank = blockIdx.x - row * csize;
+  const Part<T> part(row_at<T>(p, row), p.vocab, rank, rank + 1, csize);
+  Ring ring(ring_smem);
+  const Row r = row_of(p, row);
+  if (!r.live) {  // the whole cluster
+    if (rank == 0) finish_idle(p, row);
+    return;
+  }
+  ring.start(part);
+  cluster_arrive();  // started
+  const int top = top_of(p, r);
+  float m, s, h;
+  work_on(sh, ring, part, r.c, top, [] {}, m, s, h);
+  cluster_wait();  // every CTA has started
+  if (tid == 0) {
+    store_first(&c_max[rank], m);
+    store_first(&c_s[rank], s);
+    store_first(&c_h[rank], h);
+  }
+  if (tid < top) store_first(&c_top[rank * top + tid], sh.top[tid]);
+  cluster_arrive();
+  if (rank) return;
+  cluster_wait();
+  const float pm = lane < csize ? c_max[lane] : -INFINITY;
+  m = warp_max(pm);
+  s = h = 0.f;
+  if (pm > -INFINITY) {
+    const float d = fmaxf((pm - m) * r.c, -kLow), k = ex2(d);
+    s = c_s[lane] * k;
+    h = fmaf(d, s, c_h[lane] * k);
+  }
+  warp_sum(s, h);
+  if (top) {
+    // no CTA's last place is above the row's
+    u64 last = lane < csize ? c_top[lane * top + top - 1] : 0;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      const u64 other = __shfl_xor_sync(0xffffffffu, last, o);
+      last = other > last ? other : last;
+    }
+    join_tops(sh, csize * top, top, last, [&](int i) { return c_top[i]; });
+  }
+  if (w == 0) finish<T>(p, row, r, m, s, h, sh.top);
+}
+
+template <typename T>
+cudaError_t launch(const LogprobParams& p, int runs, int csize, cudaStream_t s) {
   // once per device (an attribute call per launch costs microseconds)
   static std::atomic<uint64_t> ready{0};
   int dev;
@@ -630,35 +1016,68 @@ cudaError_t launch(const LogprobParams& p, int csize, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(ready.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(logprobs_kernel<T>,
-                             cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    const auto smem = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    e = cudaFuncSetAttribute(logprobs_rows_kernel<T>, smem, kRingBytes);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(logprobs_runs_kernel<T>, smem, kRingBytes);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(logprobs_cluster_kernel<T>, smem, kRingBytes);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(logprobs_cluster_kernel<T>,
+                               cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)p.rows * csize);
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = csize;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, logprobs_kernel<T>, p, csize);
+  cudaLaunchAttribute attr[1];
+  if (csize) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)p.rows * csize);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kRingBytes;
+    cfg.stream = s;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = csize;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, logprobs_cluster_kernel<T>, p, csize);
+  }
+  if (!p.slices) {
+    logprobs_rows_kernel<T><<<runs, kThreads, kRingBytes, s>>>(p);
+    return cudaGetLastError();
+  }
+  logprobs_runs_kernel<T><<<runs, kThreads, kRingBytes, s>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const cudaLaunchConfig_t cfg =
+      pdl_config(dim3(runs), dim3(kThreads), 0, s, attr);
+  return cudaLaunchKernelEx(&cfg, logprobs_merge_kernel<T>, p);
 }
 
 }  // namespace
 
-cudaError_t launch_logprobs(const LogprobParams& p, bool bf16, int sms,
+int logprob_runs(int sms) {
+  return sms * kCtasPerSm < kMaxRuns ? sms * kCtasPerSm : kMaxRuns;
+}
+
+cudaError_t launch_logprobs(LogprobParams p, bool bf16, int sms,
                             cudaStream_t s) {
-  int csize = 1;
-  const int batch = kThreads * kVecs * (bf16 ? 8 : 4);  // tokens
-  while (csize < kMaxCluster && (long long)p.rows * csize < 2 * sms &&
-         p.vocab > csize * batch)
-    csize *= 2;
-  return bf16 ? launch<__nv_bfloat16>(p, csize, s) : launch<float>(p, csize, s);
+  int runs = logprob_runs(sms);
+  int csize = 0;
+  p.slices = 0;
+  if (p.rows <= kFewRows) {
+    csize = 1;
+    while (csize < kMaxCluster && 2 * csize * p.rows <= runs &&
+           2 * csize * kSlice <= p.vocab)
+      csize *= 2;
+  } else if (p.rows < kManyRows * runs) {
+    // no run shorter than a slice
+    p.slices = max(1, p.vocab / kSlice);
+    runs = (int)min((long long)runs, (long long)p.rows * p.slices);
+  }
+  return bf16 ? launch<__nv_bfloat16>(p, runs, csize, s)
+              : launch<float>(p, runs, csize, s);
 }
 
 }  // namespace specv

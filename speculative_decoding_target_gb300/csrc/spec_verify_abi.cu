@@ -1144,12 +1144,8 @@ int spec_sample(const spec_sample_desc* desc, const void* logits,
   return SPEC_OK;
 }
 
-int spec_logprobs(const spec_logprob_desc* desc, const void* logits,
-                  const int32_t* token, const float* temperature,
-                  float* logprob, float* entropy, int32_t* top_ids,
-                  float* top_logprobs, void* stream) {
-  g_err[0] = 0;
-  const spec_logprob_desc* d = desc;
+namespace {
+int check_logprobs(const spec_logprob_desc* d) {
   if (!d) return fail(SPEC_ERR_ARG, "desc is NULL");
   if (d->rows < 0 || d->rows > (1 << 24))
     return fail(SPEC_ERR_ARG, "rows %d outside [0, 2^24]", d->rows);
@@ -1165,6 +1161,28 @@ int spec_logprobs(const spec_logprob_desc* desc, const void* logits,
   if (d->top < 0 || d->top > specv::kLogprobMaxTop)
     return fail(SPEC_ERR_ARG, "top %d outside [0, %d]", d->top,
                 specv::kLogprobMaxTop);
+  return SPEC_OK;
+}
+size_t logprob_bytes(int sms) {
+  return 2 * (size_t)specv::logprob_runs(sms) * sizeof(specv::LogprobPart);
+}
+}  // namespace
+
+size_t spec_logprob_workspace_size(const spec_logprob_desc* desc) {
+  int sms;
+  if (check_logprobs(desc) || sm_count(&sms)) return 0;
+  return logprob_bytes(sms);
+}
+
+int spec_logprobs(const spec_logprob_desc* desc, const void* logits,
+                  const int32_t* token, const float* temperature,
+                  float* logprob, float* entropy, int32_t* top_ids,
+                  float* top_logprobs, void* workspace, size_t workspace_bytes,
+                  void* stream) {
+  g_err[0] = 0;
+  const spec_logprob_desc* d = desc;
+  int rc = check_logprobs(d);
+  if (rc) return rc;
   if (d->rows == 0) return SPEC_OK;
   if (!logits) return fail(SPEC_ERR_ARG, "NULL tensor pointer");
   if (logprob && !token) return fail(SPEC_ERR_ARG, "logprob needs token");
@@ -1181,7 +1199,9 @@ int spec_logprobs(const spec_logprob_desc* desc, const void* logits,
   if (!aligned(logits, bf16 ? 2 : 4))
     return fail(SPEC_ERR_ALIGN, "logits are misaligned");
   int sms;
-  int rc = sm_count(&sms);
+  rc = sm_count(&sms);
+  if (rc) return rc;
+  rc = check_workspace(workspace, workspace_bytes, logprob_bytes(sms));
   if (rc) return rc;
   specv::LogprobParams p;
   std::memset(&p, 0, sizeof p);
@@ -1196,6 +1216,7 @@ int spec_logprobs(const spec_logprob_desc* desc, const void* logits,
   p.rows = d->rows;
   p.vocab = d->vocab;
   p.top = d->top;
+  p.parts = static_cast<specv::LogprobPart*>(workspace);
   cudaError_t e =
       specv::launch_logprobs(p, bf16, sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess)

@@ -3,13 +3,15 @@ definition in 64 bits, and the calls that are refused.
 
 Tolerances.  With z = (x - max) / T, E the mean of |z| under p: the factor
 log2(e) / T is off by 2^-24 and its constant by 2^-25, t by two more roundings:
-3.5 2^-24 of z, in a token's own z and in every weight's: 2.1e-7 (|z| + E).  A
+3.5 2^-24 of z in every weight: 2.1e-7 E; a token's own z by two, 2^-23 |z|.  A
 weight is off by ex2's 2^-22.  A sum passes at most 16 + 2 additions in its
 batch, 32 batches, each perhaps with a change of the reference (two roundings
-and an ex2), and 5 more inside the warp: below 40 2^-24 + 32 (2^-23 + 2^-22) <
-1.5e-5 of S.  So log p is off by 1.6e-5 + 2.1e-7 (|z| + E) and its own
-rounding, 2^-24 of it; the entropy, of which both ln S and a mean of z have
-that error, by 1.6e-5 (1 + E) + 2.1e-7 E and 2^-24 of itself."""
+and an ex2), and 5 + 5 + 4 inside the warp, the CTA and the cluster, where the
+reference changes twice more: below 48 2^-24 + 34 (2^-23 + 2^-22) < 1.5e-5 of S.
+ln S is off by 2^-22 of itself, at most 3.2e-6 more with S < 2^19.  So log p is
+off by 1.9e-5 + 2.1e-7 (|z| + E) and its own rounding, 2^-24 of it; the entropy,
+of which both ln S and a mean of z have that error, by 1.9e-5 (1 + E) + 2.1e-7 E
+and 2^-24 of itself."""
 import ctypes
 
 import numpy as np
@@ -71,13 +73,13 @@ def check(x, out, token, t, top):
             fin = np.isfinite(b)
             assert np.array_equal(np.isfinite(a), fin), (r, a, b)
             assert np.all(np.abs(a[fin] - b[fin]) <= tol[fin]), (r, a, b)
-        lp_tol = lambda v: (1.6e-5 + 2.1e-7 * (np.abs(v) + H + E)
+        lp_tol = lambda v: (1.9e-5 + 2.1e-7 * (np.abs(v) + H + E)
                             + 2.0 ** -24 * np.abs(v))
         if token is not None:
             v = np.array([lp])
             near(got["logprob"][r:r + 1], v, lp_tol(v))
         assert abs(got["entropy"][r] - H) <= (
-            1.6e-5 * (1 + E) + 2.1e-7 * E + 2.0 ** -24 * H), (r, H)
+            1.9e-5 * (1 + E) + 2.1e-7 * E + 2.0 ** -24 * H), (r, H)
         if top:
             assert np.array_equal(got["top_ids"][r], ids), (
                 r, got["top_ids"][r], ids)
@@ -267,7 +269,8 @@ FAKE = ctypes.c_void_p(0x100000)   # never dereferenced: checks come first
 def _raw(lib, **kw):
     d = _native.LogprobDesc(4, 1000, 0, 5, 1000)
     ptr = dict(logits=FAKE, token=FAKE, temperature=None, logprob=FAKE,
-               entropy=FAKE, top_ids=FAKE, top_logprobs=FAKE)
+               entropy=FAKE, top_ids=FAKE, top_logprobs=FAKE, ws=None,
+               ws_bytes=0)
     for name, val in kw.items():
         if name in ptr:
             ptr[name] = val

@@ -3,9 +3,12 @@
 // and the plan.
 //
 // The rows of (request b, KV head g) are its new tokens' query heads that read
-// g, token by token: row R is token R / group of the chunk.  They are cut into
-// tiles of kPrefixRows; tile m attends the first t 128-token tiles of the cache
-// that its last row sees.  A piece is a row tile over a run of those.
+// g, token by token: row R is token R / group of the chunk.  They are cut into row
+// tiles of 2 cta_rows, half for each CTA of a pair: as many whole tokens as fit
+// into 128 rows, so that one tensor copy brings a CTA's queries, or 128 rows where
+// whole tokens would leave more than a tenth of them empty.  Row tile m attends
+// the first t 128-token tiles of the cache that its last row sees.  A piece is a
+// row tile over a run of those.
 //
 // Pieces of a whole row tile are sorted by t (in kChunkBuckets steps, longest
 // first; in a step by head, so that pieces that read the same tokens run at the
@@ -29,16 +32,35 @@ struct ChunkHead {
   int pad;
 };
 
+// A row tile of a request and KV head.
+struct __align__(16) ChunkPiece {
+  int b, g, row0, tiles;         // tiles of tokens
+  int rows, first, limit, last;  // the request's rows, block row of row 0, tokens
+                                 // that row 0 sees, last cached token
+};
+// A pair's run of the rest: its first piece, the tile it starts at, its tiles.
+struct __align__(16) ChunkRun {
+  int piece, from, tiles, pad;
+};
+
 struct ChunkParams {
   AttnParams a;       // rows, grid, part_o and part_lse unused
   ChunkHead* head;
-  int4* pieces;       // (request, row tile, KV head, tiles of tokens), in order
-  int* rest_units;    // [pairs + 1]: tiles before each piece of the rest
-  int* ranges;        // [pairs + 1]: each pair's run of the rest's tiles
+  ChunkPiece* pieces; // in order
+  ChunkRun* runs;     // [pairs]
+  int2* rest;         // [pairs]: first and last pair with a run of a rest's piece
   float* pre_o;       // [2 pairs, kPrefixRows, 256]
   float* pre_lse;     // [2 pairs, kPrefixRows]
   int pairs;
+  int cta_rows;       // rows of a CTA: q_tokens * group, or 128
+  int q_tokens;       // tokens of a tensor copy of queries; 0: no such copies
 };
+
+// Tokens whose rows fill a CTA well enough (of 128 rows no more than 12 empty).
+inline int chunk_q_tokens(int group) {
+  const int n = group <= 128 ? 128 / group : 0;
+  return n * group >= 116 ? n : 0;
+}
 
 // A request's rows: of its w new tokens the last `live` are in the cache (all,
 // unless it is longer than its cache); they are block rows first .. w - 1.
@@ -54,22 +76,29 @@ __device__ __forceinline__ ChunkRows chunk_rows(const AttnParams& p, int b) {
   r.rows = r.live * p.group;
   return r;
 }
-__device__ __forceinline__ int chunk_row_tiles(const ChunkRows& r) {
-  return (r.rows + kPrefixRows - 1) / kPrefixRows;
+__device__ __forceinline__ int chunk_row_tiles(const ChunkRows& r, int cta_rows) {
+  return (r.rows + 2 * cta_rows - 1) / (2 * cta_rows);
 }
 // Tokens that row R sees.
 __device__ __forceinline__ int chunk_limit(const ChunkRows& r, int R, int group) {
   return r.len - r.live + R / group + 1;
 }
 // Tiles of tokens of row tile m.
-__device__ __forceinline__ int chunk_tiles(const ChunkRows& r, int m, int group) {
-  const int R = min(m * kPrefixRows + kPrefixRows, r.rows) - 1;
+__device__ __forceinline__ int chunk_tiles(const ChunkRows& r, int m, int group,
+                                           int cta_rows) {
+  const int R = min((m + 1) * 2 * cta_rows, r.rows) - 1;
   return (chunk_limit(r, R, group) + kPrefixTile - 1) / kPrefixTile;
+}
+
+// Row tiles of a request with `rows` rows, at most.
+inline long long chunk_tiles_of(long long rows, int cta_rows) {
+  return (rows + 2 * cta_rows - 1) / (2 * cta_rows);
 }
 
 cudaError_t launch_chunk_plan(const ChunkParams& p, cudaStream_t s);
 cudaError_t launch_chunk_attention(const ChunkParams& p, const CUtensorMap& tm_k,
-                                   const CUtensorMap& tm_v, cudaStream_t s);
+                                   const CUtensorMap& tm_v,
+                                   const CUtensorMap& tm_q, cudaStream_t s);
 cudaError_t launch_chunk_merge(const ChunkParams& p, int sms, cudaStream_t s);
 int chunk_attention_pairs(bool fp8);
 

@@ -7,7 +7,9 @@
 namespace specv {
 namespace {
 
-constexpr int kThreads = 1024;  // at least kMaxBatch, and the pairs
+// At most: a thread for each request and each pair.  Few of both take a small
+// block, whose barriers are cheaper.
+constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 static_assert(kThreads >= kMaxBatch, "");
 // A run of the rest is at least this long, in 128-token tiles, and one that
@@ -29,7 +31,7 @@ __device__ __forceinline__ T block_scan(T v, T* s, T* total) {
   if (lane == 31) s[w] = v;
   __syncthreads();
   if (w == 0) {
-    T x = s[lane];
+    T x = lane < (int)(blockDim.x >> 5) ? s[lane] : T(0);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const T n = __shfl_up_sync(0xffffffffu, x, o);
@@ -38,7 +40,7 @@ __device__ __forceinline__ T block_scan(T v, T* s, T* total) {
     s[lane] = x;
   }
   __syncthreads();
-  *total = s[kWarps - 1];
+  *total = s[(blockDim.x >> 5) - 1];
   return v + (w ? s[w - 1] : T(0));
 }
 
@@ -61,10 +63,11 @@ __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(const ChunkParams 
   __shared__ int s_warp[kWarps][kChunkBuckets];
   __shared__ int s_scan[kWarps];
   __shared__ long long s_scan64[kWarps];
-  __shared__ int s_units[kThreads + 1];
+  __shared__ int s_units[kThreads + 1], s_ranges[kThreads + 1];
   __shared__ int s_longest, s_load;
   const AttnParams& a = p.a;
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  const int nt = blockDim.x, nw = nt >> 5;
   // the attention kernel may set itself up now; it waits for this grid
   tc_grid_launch_dependents();
   if (tid == 0) s_longest = s_load = 0;
@@ -73,7 +76,7 @@ __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(const ChunkParams 
   int tiles = 0;
   if (tid < a.batch) {
     const ChunkRows r = chunk_rows(a, tid);
-    tiles = chunk_row_tiles(r);
+    tiles = chunk_row_tiles(r, p.cta_rows);
     if (tiles) atomicMax(&s_longest, (r.len + kPrefixTile - 1) / kPrefixTile);
   }
   int T;
@@ -85,14 +88,14 @@ __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(const ChunkParams 
   auto tile_at = [&](int i, int* b, int* m) {
     *b = last_at_most(s_tile0, a.batch, i);
     *m = i - s_tile0[*b];
-    return chunk_tiles(chunk_rows(a, *b), *m, a.group);
+    return chunk_tiles(chunk_rows(a, *b), *m, a.group, p.cta_rows);
   };
   // 0 the longest
   auto bucket_of = [&](int t) {
     return kChunkBuckets - 1 -
            (int)((long long)t * kChunkBuckets / (longest + 1));
   };
-  for (int i = tid; i < T; i += kThreads) {
+  for (int i = tid; i < T; i += nt) {
     int b, m;
     atomicAdd(&s_count[bucket_of(tile_at(i, &b, &m))], 1);
   }
@@ -103,8 +106,8 @@ __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(const ChunkParams 
     s_base[tid] = n;
   }
   // places in a bucket, in the tiles' order
-  for (int i0 = 0; i0 < T; i0 += kThreads) {
-    for (int k = tid; k < kWarps * kChunkBuckets; k += kThreads)
+  for (int i0 = 0; i0 < T; i0 += nt) {
+    for (int k = tid; k < nw * kChunkBuckets; k += nt)
       (&s_warp[0][0])[k] = 0;
     __syncthreads();
     const int i = i0 + tid;
@@ -119,7 +122,7 @@ __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(const ChunkParams 
     __syncthreads();
     if (tid < kChunkBuckets) {
       int n = s_run[tid];
-      for (int k = 0; k < kWarps; ++k) {
+      for (int k = 0; k < nw; ++k) {
         const int c = s_warp[k][tid];
         s_warp[k][tid] = n;
         n += c;
@@ -128,10 +131,12 @@ __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(const ChunkParams 
     }
     __syncthreads();
     if (i < T) {
-      int4* to = p.pieces + (long long)s_base[bucket] * a.hkv +
-                 s_warp[w][bucket] + before;
+      ChunkPiece* to = p.pieces + (long long)s_base[bucket] * a.hkv +
+                       s_warp[w][bucket] + before;
+      const ChunkRows r = chunk_rows(a, b);
       for (int g = 0; g < a.hkv; ++g, to += s_count[bucket])
-        *to = make_int4(b, m, g, t);
+        *to = ChunkPiece{b,      g,       m * 2 * p.cta_rows,   t,
+                         r.rows, r.first, r.len - r.live + 1, r.len - 1};
     }
     __syncthreads();
   }
@@ -141,16 +146,14 @@ __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(const ChunkParams 
   if (tid < P) {
 #pragma unroll 4
     for (int r = 0; r < rounds; ++r)
-      dealt += p.pieces[(long long)r * P + (r & 1 ? P - 1 - tid : tid)].w +
+      dealt += p.pieces[(long long)r * P + (r & 1 ? P - 1 - tid : tid)].tiles +
                kPrefixCost;
   }
-  const int4* q = p.pieces + (long long)rounds * P;
+  const ChunkPiece* q = p.pieces + (long long)rounds * P;
   int R;
-  const int units = block_scan(tid < rest ? q[tid].w : 0, s_scan, &R);
+  const int units = block_scan(tid < rest ? q[tid].tiles : 0, s_scan, &R);
   s_units[tid + 1] = units;
   if (tid == 0) s_units[0] = 0;
-  if (tid < rest) p.rest_units[tid + 1] = units;
-  if (tid == 0) p.rest_units[0] = 0;
   long long sum;
   block_scan(dealt, s_scan64, &sum);
   // few tiles go to few pairs
@@ -179,12 +182,21 @@ __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(const ChunkParams 
       else if (s_units[i + 1] - u <= kSnap) u = s_units[i + 1];
     }
     if (tid == P - 1) u = R;
-    p.ranges[tid + 1] = u;
+    s_ranges[tid + 1] = u;
     if (tid == 0) {
-      p.ranges[0] = 0;
+      s_ranges[0] = 0;
       *p.head = ChunkHead{rounds, rest, split, 0};
     }
   }
+  __syncthreads();
+  if (tid < P) {
+    const int from = s_ranges[tid], n = s_ranges[tid + 1] - from;
+    const int i = n ? last_at_most(s_units, rest, from) : 0;
+    p.runs[tid] = ChunkRun{i, from - s_units[i], n, 0};
+  }
+  if (tid < rest)
+    p.rest[tid] = make_int2(last_at_most(s_ranges, P, s_units[tid]),
+                            last_at_most(s_ranges, P, s_units[tid + 1] - 1));
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -210,16 +222,15 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     for (int w = blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
          w < h.rest * kPrefixRows; w += gridDim.x * kMergeWarps) {
       const int i = w / kPrefixRows, r = w % kPrefixRows;
-      const int u0 = p.rest_units[i], u1 = p.rest_units[i + 1];
-      const int c0 = last_at_most(p.ranges, P, u0);
-      if (p.ranges[c0 + 1] >= u1) continue;  // whole
-      const int4 e = p.pieces[(long long)h.rounds * P + i];
-      const ChunkRows cr = chunk_rows(a, e.x);
-      const int R = e.y * kPrefixRows + r;
-      if (R >= cr.rows) continue;
+      const int2 by = p.rest[i];
+      if (by.x == by.y) continue;  // whole
+      const ChunkPiece e = p.pieces[(long long)h.rounds * P + i];
+      const int half = r / 128, in = r - half * 128;
+      const int R = e.row0 + half * p.cta_rows + in;
+      if (in >= p.cta_rows || R >= e.rows) continue;
       float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       float den = 0.f, mx = -INFINITY;
-      for (int c = c0; c < P; c += kBatch) {
+      for (int c = by.x; c <= by.y; c += kBatch) {
         float lv[kBatch];
         float4 x0[kBatch], x1[kBatch];
 #pragma unroll
@@ -227,7 +238,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
           lv[j] = -INFINITY;
           x0[j] = x1[j] = make_float4(0.f, 0.f, 0.f, 0.f);
           const int ch = c + j;
-          if (ch < P && p.ranges[ch] < u1 && p.ranges[ch + 1] > p.ranges[ch]) {
+          if (ch <= by.y && p.runs[ch].tiles) {
             const long long row = (long long)(ch + i) * kPrefixRows + r;
             const float* o = p.pre_o + row * kHeadDim + lane * 8;
             lv[j] = p.pre_lse[row];
@@ -255,7 +266,6 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
           acc[4] += wt * x1[j].x; acc[5] += wt * x1[j].y;
           acc[6] += wt * x1[j].z; acc[7] += wt * x1[j].w;
         }
-        if (c + kBatch < P && p.ranges[c + kBatch] >= u1) break;
       }
       const float inv = den > 0.f ? 1.f / den : 0.f;
       uint4 v;
@@ -264,8 +274,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
       v.z = pack_bf16(acc[4] * inv, acc[5] * inv);
       v.w = pack_bf16(acc[6] * inv, acc[7] * inv);
       const int tok = R / a.group;
-      const long long at = ((long long)e.x * a.q_len + cr.first + tok) * a.hq +
-                           e.z * a.group + (R - tok * a.group);
+      const long long at = ((long long)e.b * a.q_len + e.first + tok) * a.hq +
+                           e.g * a.group + (R - tok * a.group);
       *reinterpret_cast<uint4*>(a.out + at * kHeadDim + lane * 8) = v;
     }
   }
@@ -286,7 +296,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
 }  // namespace
 
 cudaError_t launch_chunk_plan(const ChunkParams& p, cudaStream_t s) {
-  chunk_plan_kernel<<<1, kThreads, 0, s>>>(p);
+  const long long tiles =
+      p.a.batch * chunk_tiles_of((long long)p.a.q_len * p.a.group,
+                                   p.cta_rows);
+  const int small = 128;
+  const bool fits = p.a.batch <= small && p.pairs <= small && tiles <= 4 * small;
+  chunk_plan_kernel<<<1, fits ? small : kThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 

@@ -434,7 +434,7 @@ template <typename T>
 __device__ void select(Shared& sh, const Part<T>& part, const Sums& a,
                        int top) {
   constexpr int kN = Vec<T>::kN;
-  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
   const int place = a.vec < 0 ? part.odd : part.head + a.vec * kN;
   const u64 mine = a.max > -INFINITY ? key_of(a.max, place) : 0;
   // a bound: the top-th largest of 64 groups' maxima

@@ -71,6 +71,18 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst,
       "l"(reinterpret_cast<uint64_t>(map)), "r"(cluster_bar), "r"(x), "r"(y)
       : "memory");
 }
+__device__ __forceinline__ void tma_load_4d_pair(uint32_t dst,
+                                                 const CUtensorMap* map,
+                                                 uint32_t cluster_bar, int x,
+                                                 int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile."
+      "mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(cluster_bar), "r"(x), "r"(y),
+      "r"(z), "r"(w)
+      : "memory");
+}
 __device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a, uint64_t b,
                                          uint32_t idesc, uint32_t accumulate) {
   asm volatile(

@@ -112,6 +112,7 @@ struct Bars {
   uint64_t p_full[2];          // leader: P_j written by both CTAs
   uint64_t pv_done[2];         // both: PV_j complete
   uint64_t q_full;             // leader: Q written by both CTAs
+  uint64_t q_land;             // chunk, FP8, own: bf16 queries landed
   uint64_t raw_full[kRaw];     // FP8, own: staged bytes landed
   uint64_t raw_empty[kRaw];    // FP8, own: staged bytes converted
   // chunk, bf16, own: V that needs zeros landed.  One a slot, as with short
@@ -128,6 +129,8 @@ struct Ctx {
   const AttnParams* a;
   float* pre_o;
   float* pre_lse;
+  const CUtensorMap* tm_q;     // chunk: queries
+  int cta_rows, q_tokens;
 };
 
 __device__ __forceinline__ void give_up(const Ctx& cx) {
@@ -507,18 +510,6 @@ __device__ __forceinline__ void dequant_unit(const Ctx& cx, uint8_t* smem,
   dq.raw.next();
 }
 
-template <bool kCausal>
-__device__ void dequant_piece(const Ctx& cx, const Piece& pc, uint8_t* smem,
-                              Dequant& dq) {
-  // units K0 K1 V0 K2 V1 .. V(n-2) V(n-1): unit 0 and the odd ones but the
-  // last are K
-  const int units = 2 * pc.n_tiles;
-#pragma unroll 1
-  for (int k = 0; k < units; ++k)
-    dequant_unit<kCausal>(cx, smem, dq, is_v_unit(k, units),
-                          kCausal && k == units - 1 ? pc.tail_tokens() : kT);
-}
-
 // ---- warp 1 of the leader, one thread: MMA issue ----------------------------
 // A descriptor's low bits are the address in 16-byte steps, so the operands of
 // a slot's MMAs are its base descriptor plus constants.  (With the descriptors
@@ -582,18 +573,27 @@ __device__ __forceinline__ bool issue_pv(const Ctx& cx, Slots<kFp8>& seq, int gj
   return true;
 }
 
-template <bool kFp8, bool kCausal>
-__device__ void mma_piece(const Ctx& cx, const Piece& pc, int gj0, int n_piece,
-                          Slots<kFp8>& seq, uint32_t tmem, uint8_t* smem_ptr) {
+// `then` is called behind the first QK.
+template <bool kFp8, bool kCausal, typename F>
+__device__ __forceinline__ void mma_piece(const Ctx& cx, const Piece& pc, int gj0,
+                                          int n_piece, Slots<kFp8>& seq,
+                                          uint32_t tmem, uint8_t* smem_ptr,
+                                          F then) {
   const uint32_t smem = tc::smem_u32(smem_ptr);
-  if (!wait_bar<true>(cx, &cx.bars->q_full, (uint32_t)n_piece & 1)) return;
+  if (!wait_bar<true>(cx, &cx.bars->q_full, (uint32_t)n_piece & 1)) {
+    then();
+    return;
+  }
   tc::fence_after();
   const bool tails = kCausal && !kFp8 && pc.tail_tokens() < kT;
 #pragma unroll (kFp8 ? 1 : 2)
   for (int j = -1; j < pc.n_tiles; ++j) {
     if (j + 1 < pc.n_tiles &&
-        !issue_qk<kFp8>(cx, seq, gj0 + j + 1, tmem, smem))
+        !issue_qk<kFp8>(cx, seq, gj0 + j + 1, tmem, smem)) {
+      if (j < 0) then();
       return;
+    }
+    if (j < 0) then();
     if (j >= 0 && !issue_pv<kFp8>(cx, seq, gj0 + j, j == 0,
                                   tails && j + 1 == pc.n_tiles, tmem, smem))
       return;
@@ -621,41 +621,60 @@ __device__ void relay_piece(const Ctx& cx, const Piece& pc, Slots<true>& seq,
   }
 }
 
+template <bool kCausal>
+__device__ void dequant_piece(const Ctx& cx, const Piece& pc, uint8_t* smem,
+                              Dequant& dq) {
+  // units K0 K1 V0 K2 V1 .. V(n-2) V(n-1): unit 0 and the odd ones but the
+  // last are K
+  const int units = 2 * pc.n_tiles;
+#pragma unroll 1
+  for (int k = 0; k < units; ++k) {
+    dequant_unit<kCausal>(cx, smem, dq, is_v_unit(k, units),
+                          kCausal && k == units - 1 ? pc.tail_tokens() : kT);
+  }
+}
+
 // ---- warps 4..7: Q, softmax, epilogue ---------------------------------------
-// A warp writes its 32 rows of Q, one row at a time: lane l moves chunk l (8
-// channels) of the row, eight rows in flight.
+// Place of this CTA's row r in q, or -1.
+template <bool kCausal>
+__device__ __forceinline__ long long q_row(const AttnParams& p, const Piece& pc,
+                                           int r) {
+  const int R = pc.row0 + r;
+  if (R >= pc.rows_total) return -1;
+  if (kCausal) {
+    const int tok = R / p.group;
+    return (((long long)pc.lead * p.q_len + pc.first + tok) * p.hq +
+            pc.g * p.group + (R - tok * p.group)) * kHeadDim;
+  }
+  const int bq = R / p.rows, rb = R - bq * p.rows;
+  const int b = pc.start + bq, i = rb / p.group;
+  if (i >= block_rows(p, b)) return -1;
+  return (((long long)b * p.q_len + i) * p.hq + pc.g * p.group +
+          (rb - i * p.group)) * kHeadDim;
+}
+
+// Through the registers: a warp writes its 32 rows of Q, one row at a time: lane
+// l moves chunk l (8 channels) of the row; bf16 all of them in flight (in the
+// registers that the scores leave free), FP8 eight.
 template <bool kFp8, bool kCausal>
-__device__ void write_q(const Ctx& cx, const Piece& pc, uint8_t* smem) {
+__device__ __forceinline__ void write_q(const Ctx& cx, const Piece& pc,
+                                        uint8_t* smem) {
   const AttnParams& p = *cx.a;
   const int lane = threadIdx.x & 31, w4 = (threadIdx.x >> 5) & 3;
-  // this lane's row: its place in q, or -1
-  const int R = pc.row0 + w4 * 32 + lane;
-  long long src = -1;
-  if (kCausal) {
-    if (R < pc.rows_total) {
-      const int tok = R / p.group;
-      src = (((long long)pc.lead * p.q_len + pc.first + tok) * p.hq +
-             pc.g * p.group + (R - tok * p.group)) * kHeadDim;
-    }
-  } else if (R < pc.rows_total) {
-    const int bq = R / p.rows, r = R - bq * p.rows;
-    const int b = pc.start + bq, i = r / p.group;
-    if (i < block_rows(p, b))
-      src = (((long long)b * p.q_len + i) * p.hq + pc.g * p.group +
-             (r - i * p.group)) * kHeadDim;
-  }
+  const long long src = q_row<kCausal>(p, pc, w4 * 32 + lane);
   const int cb = lane >> 3, c = lane & 7;
+  constexpr int kRows = kFp8 ? 8 : 32;
 #pragma unroll 1
-  for (int r0 = 0; r0 < 32; r0 += 8) {
-    uint4 x[8];
+  for (int r0 = 0; r0 < 32; r0 += kRows) {
+    uint4 x[kRows];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < kRows; ++e) {
       const long long at = __shfl_sync(0xffffffffu, src, r0 + e);
       x[e] = at >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.q + at) + lane)
                      : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < kRows; ++e) {
       const int row = w4 * 32 + r0 + e;
       if (kFp8) {
         uint32_t* v = reinterpret_cast<uint32_t*>(&x[e]);
@@ -673,6 +692,55 @@ __device__ void write_q(const Ctx& cx, const Piece& pc, uint8_t* smem) {
   tc::fence_proxy_async_smem();
   __syncwarp();
   if (lane == 0)
+    tc::arrive_cluster(tc::map_to(tc::smem_u32(&cx.bars->q_full), 0));
+}
+
+// A chunk's whole tokens by tensor copies, one for each column block of 64
+// channels: rows in the order of the tile, in the operand's layout.  (Through the
+// registers, the loads in flight have to fit into the 28 KB of L1 that the rings
+// leave: 7 us for the 64 KB, behind which every piece started.)  Thread 128 of
+// each CTA starts them; bf16, they count on the leader's q_full.
+template <bool kFp8>
+__device__ __forceinline__ void copy_q(const Ctx& cx, const Piece& pc,
+                                       uint8_t* smem) {
+  const AttnParams& p = *cx.a;
+  const uint32_t bytes = 4 * cx.cta_rows * 128;
+  uint32_t bar;
+  if (kFp8) {
+    bar = tc::smem_u32(&cx.bars->q_land);
+    tc::bar_arrive_expect_tx(bar, bytes);
+    bar = tc::map_to(bar, cx.rank);
+  } else {
+    bar = tc::smem_u32(&cx.bars->q_full);
+    if (cx.rank == 0) tc::bar_arrive_expect_tx(bar, 2 * bytes);
+    bar = tc::map_to(bar, 0);
+  }
+  const int tok = pc.lead * p.q_len + pc.first + pc.row0 / p.group;
+#pragma unroll
+  for (int cb = 0; cb < 4; ++cb)
+    tc::tma_load_4d_pair(tc::smem_u32(smem) + cb * (128 * 128), cx.tm_q, bar,
+                         cb * 64, 0, pc.g, tok);
+}
+
+// FP8: the landed bf16 queries to fp16, in place.
+__device__ __forceinline__ void convert_q(const Ctx& cx, uint8_t* smem) {
+  const int tid = threadIdx.x & 127;
+#pragma unroll 4
+  for (int i = tid; i < kQBytes / 16; i += 128) {
+    uint4* at = reinterpret_cast<uint4*>(smem) + i;
+    uint4 x = *at;
+    uint32_t* v = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const __nv_bfloat162 b2 = *reinterpret_cast<const __nv_bfloat162*>(&v[k]);
+      const __half2 h2 = __floats2half2_rn(__low2float(b2), __high2float(b2));
+      v[k] = *reinterpret_cast<const uint32_t*>(&h2);
+    }
+    *at = x;
+  }
+  tc::fence_proxy_async_smem();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0)
     tc::arrive_cluster(tc::map_to(tc::smem_u32(&cx.bars->q_full), 0));
 }
 
@@ -832,6 +900,7 @@ __device__ void write_out(const Ctx& cx, const Piece& pc, uint32_t tmem, float l
   const int lane = threadIdx.x & 31, w4 = (threadIdx.x >> 5) & 3;
   const uint32_t lane_base = tmem + ((uint32_t)(32 * w4) << 16);
   const int R = pc.row0 + w4 * 32 + lane;
+  const bool valid = w4 * 32 + lane < cx.cta_rows && R < pc.rows_total;
   const int tok = R / p.group;
   __nv_bfloat16* dst =
       p.out + (((long long)pc.lead * p.q_len + pc.first + tok) * p.hq +
@@ -841,7 +910,7 @@ __device__ void write_out(const Ctx& cx, const Piece& pc, uint32_t tmem, float l
   for (int cb = 0; cb < 4; ++cb) {
     uint32_t o[64];
     tc::tmem_ld_cols<64>(lane_base + cb * 64, o);
-    if (R < pc.rows_total) {
+    if (valid) {
 #pragma unroll
       for (int k = 0; k < 64; k += 16) {
         uint32_t v[8];
@@ -866,7 +935,7 @@ __device__ void epilogue(const Ctx& cx, const Piece& pc, uint32_t tmem, float m,
   const int lane = threadIdx.x & 31, w4 = (threadIdx.x >> 5) & 3;
   const uint32_t lane_base = tmem + ((uint32_t)(32 * w4) << 16);
   const int r = w4 * 32 + lane;
-  const bool valid = pc.row0 + r < pc.rows_total;
+  const bool valid = r < cx.cta_rows && pc.row0 + r < pc.rows_total;
   const long long row =
       (long long)pc.slot * kPrefixRows + cx.rank * 128 + r;
   float* dst = cx.pre_o + row * kHeadDim;
@@ -931,43 +1000,40 @@ struct ChunkWork {
   const ChunkParams& p;
   uint32_t rank;
   ChunkHead h;
-  int pair, round, unit, end;
+  ChunkRun run;
+  int pair, round;
   __device__ ChunkWork(const ChunkParams& p, uint32_t rank)
-      : p(p), rank(rank), h(*p.head), pair(blockIdx.x >> 1), round(0),
-        unit(p.ranges[pair]), end(p.ranges[pair + 1]) {}
+      : p(p), rank(rank), h(*p.head), run(p.runs[blockIdx.x >> 1]),
+        pair(blockIdx.x >> 1), round(0) {}
   __device__ __forceinline__ bool next(Piece& pc) {
     const int at = round & 1 ? p.pairs - 1 - pair : pair;
-    long long i = (long long)round * p.pairs + at;
-    int from = 0, to = -1, slot = -1;
-    if (round < h.rounds || (!h.split && round == h.rounds && at < h.rest)) {
+    const bool whole =
+        round < h.rounds || (!h.split && round == h.rounds && at < h.rest);
+    if (!whole && !(h.split && run.tiles)) return false;
+    const ChunkPiece e =
+        p.pieces[(long long)(whole ? round : h.rounds) * p.pairs +
+                 (whole ? at : run.piece)];
+    int from = 0, to = e.tiles;
+    pc.slot = -1;
+    if (whole) {
       ++round;
-    } else if (h.split && unit < end) {
-      int lo = 0, hi = h.rest - 1;  // the last piece that starts at or before
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (p.rest_units[mid] <= unit) lo = mid; else hi = mid - 1;
-      }
-      const int u0 = p.rest_units[lo], u1 = p.rest_units[lo + 1];
-      from = unit - u0;
-      to = min(end, u1) - u0;
-      if (from > 0 || end < u1) slot = pair + lo;
-      i = (long long)h.rounds * p.pairs + lo;
-      unit = min(end, u1);
     } else {
-      return false;
+      from = run.from;
+      to = min(to, from + run.tiles);
+      if (to - from < e.tiles) pc.slot = pair + run.piece;
+      ++run.piece;
+      run.tiles -= to - from;
+      run.from = 0;
     }
-    const int4 e = p.pieces[i];
-    const ChunkRows r = chunk_rows(p.a, e.x);
-    pc.lead = pc.start = e.x;
-    pc.rows_total = r.rows;
-    pc.g = e.z;
-    pc.row0 = e.y * kPrefixRows + (int)rank * 128;
+    pc.lead = pc.start = e.b;
+    pc.rows_total = e.rows;
+    pc.g = e.g;
+    pc.row0 = e.row0 + (int)rank * p.cta_rows;
     pc.tok = from * kT;
-    pc.n_tiles = (to < 0 ? e.w : to) - from;
-    pc.slot = slot;
-    pc.last = r.len - 1;
-    pc.first = r.first;
-    pc.limit = r.len - r.live + 1;
+    pc.n_tiles = to - from;
+    pc.last = e.last;
+    pc.first = e.first;
+    pc.limit = e.limit;
     return true;
   }
 };
@@ -979,7 +1045,8 @@ __global__ void __cluster_dims__(2, 1, 1)
             const __grid_constant__
                 std::conditional_t<kCausal, ChunkParams, SharedParams> p,
             const __grid_constant__ CUtensorMap tm_k,
-            const __grid_constant__ CUtensorMap tm_v) {
+            const __grid_constant__ CUtensorMap tm_v,
+            const __grid_constant__ CUtensorMap tm_q) {
   using Work = std::conditional_t<kCausal, ChunkWork, PrefixWork>;
   using C = Cfg<kFp8>;
   extern __shared__ uint8_t smem_raw[];
@@ -992,6 +1059,11 @@ __global__ void __cluster_dims__(2, 1, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = tc::cluster_rank();
 
+  int cta_rows = 128, q_tokens = 0;
+  if constexpr (kCausal) {
+    cta_rows = p.cta_rows;
+    q_tokens = p.q_tokens;
+  }
   if (tid == 0) {
     for (int s = 0; s < C::kSlots; ++s) {
       // bf16: the leader's expect_tx plus both CTAs' bytes; FP8: the four
@@ -1006,7 +1078,10 @@ __global__ void __cluster_dims__(2, 1, 1)
       tc::bar_init(tc::smem_u32(&bars.p_full[s]), 8);
       tc::bar_init(tc::smem_u32(&bars.pv_done[s]), 1);
     }
-    tc::bar_init(tc::smem_u32(&bars.q_full), 8);
+    // Q by tensor copies to both CTAs: the leader's expect_tx; otherwise the
+    // warps that wrote or converted it
+    tc::bar_init(tc::smem_u32(&bars.q_full), !kFp8 && q_tokens ? 1 : 8);
+    tc::bar_init(tc::smem_u32(&bars.q_land), 1);
     for (int s = 0; s < kRaw; ++s) {
       tc::bar_init(tc::smem_u32(&bars.raw_full[s]), 1);
       tc::bar_init(tc::smem_u32(&bars.raw_empty[s]), 8);
@@ -1028,54 +1103,71 @@ __global__ void __cluster_dims__(2, 1, 1)
   tc_grid_launch_dependents();
   const Ctx cx{&bars, &s_abort,
                tc::map_to(tc::smem_u32(&s_abort), rank ^ 1u), rank, &p.a,
-               p.pre_o, p.pre_lse};
+               p.pre_o, p.pre_lse, &tm_q, cta_rows, q_tokens};
 
   // Every role walks the pair's pieces by itself.
   Work work(p, rank);
+  int gj0 = 0;
   if (warp < 4) {
     Producer<kFp8> pr;
     Slots<kFp8> seq;
-    int gj0 = 0, n_piece = 0;
-    Piece pc;
-    for (; work.next(pc); ++n_piece) {
+    int n_piece = 0;
+    Piece pc, nx;
+    bool more = work.next(pc);
+    for (; more; ++n_piece) {
+      bool decoded = false;
       if (warp == 0 || warp == 2) {
         const bool v_side = warp != 0;
         if (pr.live)
           produce<kFp8, kCausal>(cx, pc, pr, smem, v_side ? &tm_v : &tm_k,
                                  v_side);
       } else if (lane == 0) {
-        if (rank == 0 && warp == 1)
-          mma_piece<kFp8, kCausal>(cx, pc, gj0, n_piece, seq, tmem, smem);
+        if (rank == 0 && warp == 1) {
+          // the next piece's numbers are on their way before they are needed
+          mma_piece<kFp8, kCausal>(cx, pc, gj0, n_piece, seq, tmem, smem,
+                                   [&] { more = work.next(nx); });
+          decoded = true;
+        }
         if constexpr (kFp8) {
           if (rank == 1) relay_piece(cx, pc, seq, warp == 3);
         }
       }
       __syncwarp();
       gj0 += pc.n_tiles;
+      if (!decoded) more = work.next(nx);
+      pc = nx;
     }
   } else if (warp < 8) {
     float m = 0.f, l = 0.f;
     Piece prev{};
-    int gj0 = 0;
     uint32_t tails = 0;
+    int n_piece = 0;
     while (true) {
       Piece pc{};
       const bool more = work.next(pc);
+      // These warps have seen the last QK of the piece before: Q may be replaced,
+      // under that piece's last PV.
+      if (more) {
+        if (!kCausal || !q_tokens)
+          write_q<kFp8, kCausal>(cx, pc, smem);
+        else if (tid == 128)
+          copy_q<kFp8>(cx, pc, smem);
+      }
       if (gj0) {
-        // the last piece's MMAs are done: Q may be replaced and O read, the
-        // new Q first, so that its QK runs under the epilogue
+        // the last piece's MMAs are done: O may be read
         wait_bar(cx, &bars.pv_done[(gj0 - 1) & 1],
                  (uint32_t)((gj0 - 1) >> 1) & 1);
         tc::fence_after();
-      }
-      if (more) write_q<kFp8, kCausal>(cx, pc, smem);
-      if (gj0) {
         if (kCausal && prev.slot < 0)
           write_out(cx, prev, tmem, l);
         else
           epilogue(cx, prev, tmem, m, l, C::kShiftLog2);
       }
       if (!more) break;
+      if (kFp8 && kCausal && q_tokens) {
+        wait_bar(cx, &bars.q_land, (uint32_t)n_piece++ & 1);
+        convert_q(cx, smem);
+      }
       softmax_tiles<kFp8, kCausal>(cx, pc, gj0, tmem, smem, tails, m, l);
       prev = pc;
       gj0 += pc.n_tiles;
@@ -1133,12 +1225,14 @@ int pairs_resident() {
 
 template <bool kFp8, bool kCausal, typename P>
 cudaError_t launch(const P& p, const CUtensorMap& tm_k,
-                   const CUtensorMap& tm_v, cudaStream_t s) {
+                   const CUtensorMap& tm_v, const CUtensorMap& tm_q,
+                   cudaStream_t s) {
   using C = Cfg<kFp8>;
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg =
       pdl_config(dim3(2 * p.pairs), dim3(C::kThreads), C::kSmem, s, attr);
-  return cudaLaunchKernelEx(&cfg, prefix_attention_kernel<kFp8, kCausal>, p, tm_k, tm_v);
+  return cudaLaunchKernelEx(&cfg, prefix_attention_kernel<kFp8, kCausal>, p,
+                            tm_k, tm_v, tm_q);
 }
 
 }  // namespace
@@ -1146,15 +1240,16 @@ cudaError_t launch(const P& p, const CUtensorMap& tm_k,
 cudaError_t launch_prefix_attention(const SharedParams& p,
                                     const CUtensorMap& tm_k,
                                     const CUtensorMap& tm_v, cudaStream_t s) {
-  return p.a.k_scales ? launch<true, false>(p, tm_k, tm_v, s)
-                      : launch<false, false>(p, tm_k, tm_v, s);
+  return p.a.k_scales ? launch<true, false>(p, tm_k, tm_v, tm_k, s)
+                      : launch<false, false>(p, tm_k, tm_v, tm_k, s);
 }
 
 cudaError_t launch_chunk_attention(const ChunkParams& p,
                                    const CUtensorMap& tm_k,
-                                   const CUtensorMap& tm_v, cudaStream_t s) {
-  return p.a.k_scales ? launch<true, true>(p, tm_k, tm_v, s)
-                      : launch<false, true>(p, tm_k, tm_v, s);
+                                   const CUtensorMap& tm_v,
+                                   const CUtensorMap& tm_q, cudaStream_t s) {
+  return p.a.k_scales ? launch<true, true>(p, tm_k, tm_v, tm_q, s)
+                      : launch<false, true>(p, tm_k, tm_v, tm_q, s);
 }
 
 int prefix_attention_pairs(bool fp8) {

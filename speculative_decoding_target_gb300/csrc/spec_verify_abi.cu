@@ -125,6 +125,29 @@ int make_pool_map_u8(CUtensorMap* map, const void* base, long long rows,
   return SPEC_OK;
 }
 
+// Queries [tokens, Hkv, group, 256]: boxes of 64 channels of all of a KV head's
+// query heads of n tokens, rows in that order, with the 128-byte swizzle.
+int make_query_map(CUtensorMap* map, const void* q, long long tokens, int hkv,
+                   int group, int n) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc;
+  int rc = tensor_map_encoder(&enc);
+  if (rc) return rc;
+  const cuuint64_t row = specv::kHeadDim * 2;
+  cuuint64_t dims[4] = {(cuuint64_t)specv::kHeadDim, (cuuint64_t)group,
+                        (cuuint64_t)hkv, (cuuint64_t)tokens};
+  cuuint64_t strides[3] = {row, row * group, row * group * hkv};
+  cuuint32_t box[4] = {64, (cuuint32_t)group, 1, (cuuint32_t)n};
+  cuuint32_t elem[4] = {1, 1, 1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                   const_cast<void*>(q), dims, strides, box, elem,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(SPEC_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return SPEC_OK;
+}
+
 int current_device(int* dev) {
   cudaError_t e = cudaGetDevice(dev);
   if (e != cudaSuccess)
@@ -452,8 +475,8 @@ int check_chunk(const spec_attn_desc* d) {
 }
 
 struct ChunkLayout {
-  int pairs;
-  size_t head, pieces, units, ranges, o, lse, bytes;
+  int pairs, q_tokens, cta_rows;
+  size_t head, pieces, runs, rest, o, lse, bytes;
 };
 
 int chunk_layout(const spec_attn_desc* d, ChunkLayout* C) {
@@ -461,8 +484,11 @@ int chunk_layout(const spec_attn_desc* d, ChunkLayout* C) {
   if (rc) return rc;
   const long long rows =
       (long long)d->q_len * (d->num_q_heads / d->num_kv_heads);
+  const int group = d->num_q_heads / d->num_kv_heads;
+  C->q_tokens = specv::chunk_q_tokens(group);
+  C->cta_rows = C->q_tokens ? C->q_tokens * group : 128;
   const size_t tiles = (size_t)d->batch * d->num_kv_heads *
-                       ((rows + specv::kPrefixRows - 1) / specv::kPrefixRows);
+                       specv::chunk_tiles_of(rows, C->cta_rows);
   size_t o = specv::kWsHeader;
   auto take = [&](size_t n) {
     const size_t at = o;
@@ -470,9 +496,9 @@ int chunk_layout(const spec_attn_desc* d, ChunkLayout* C) {
     return at;
   };
   C->head = take(sizeof(specv::ChunkHead));
-  C->pieces = take(tiles * sizeof(int4));
-  C->units = take((C->pairs + 1) * sizeof(int));
-  C->ranges = take((C->pairs + 1) * sizeof(int));
+  C->pieces = take(tiles * sizeof(specv::ChunkPiece));
+  C->runs = take(C->pairs * sizeof(specv::ChunkRun));
+  C->rest = take(C->pairs * sizeof(int2));
   // a partial slot is its pair's number plus its piece's in the rest
   const size_t slots = 2 * (size_t)C->pairs * specv::kPrefixRows;
   C->o = take(slots * specv::kHeadDim * sizeof(float));
@@ -667,16 +693,24 @@ int spec_chunk_attention(const spec_attn_desc* desc, const void* q,
     if (rc) return rc;
   }
   p.head = reinterpret_cast<specv::ChunkHead*>(ws + C.head);
-  p.pieces = reinterpret_cast<int4*>(ws + C.pieces);
-  p.rest_units = reinterpret_cast<int*>(ws + C.units);
-  p.ranges = reinterpret_cast<int*>(ws + C.ranges);
+  p.pieces = reinterpret_cast<specv::ChunkPiece*>(ws + C.pieces);
+  p.runs = reinterpret_cast<specv::ChunkRun*>(ws + C.runs);
+  p.rest = reinterpret_cast<int2*>(ws + C.rest);
   p.pre_o = reinterpret_cast<float*>(ws + C.o);
   p.pre_lse = reinterpret_cast<float*>(ws + C.lse);
   p.pairs = C.pairs;
+  p.cta_rows = C.cta_rows;
+  p.q_tokens = C.q_tokens;
+  CUtensorMap tm_q = tm_k;  // unused without tensor copies of queries
+  if (p.q_tokens) {
+    rc = make_query_map(&tm_q, q, (long long)desc->batch * desc->q_len, p.a.hkv,
+                        p.a.group, p.q_tokens);
+    if (rc) return rc;
+  }
   rc = reset_status(desc, workspace, &p.a, s);
   if (rc) return rc;
   cudaError_t e = specv::launch_chunk_plan(p, s);
-  if (e == cudaSuccess) e = specv::launch_chunk_attention(p, tm_k, tm_v, s);
+  if (e == cudaSuccess) e = specv::launch_chunk_attention(p, tm_k, tm_v, tm_q, s);
   if (e == cudaSuccess) e = specv::launch_chunk_merge(p, sms, s);
   if (e != cudaSuccess)
     return fail(SPEC_ERR_CUDA, "chunk attention launch: %s",

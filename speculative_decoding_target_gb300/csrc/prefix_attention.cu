@@ -229,187 +229,161 @@ __device__ __forceinline__ int checked_page(const AttnParams& p, int page) {
   return page;
 }
 
-__device__ __forceinline__ long long pool_row(const AttnParams& p, int page,
-                                              int g, int t) {
-  return ((long long)(page * p.hkv + g) << p.log2_ps) + (t & (p.page_size - 1));
+// (The pool has fewer than 2^31 rows.)
+__device__ __forceinline__ int pool_row(const AttnParams& p, int page, int g,
+                                        int t) {
+  return ((page * p.hkv + g) << p.log2_ps) + (t & (p.page_size - 1));
 }
 
-// ---- warp 0: loads ----------------------------------------------------------
-// A half of 64 tokens is 64 / box_rows boxes of each column block.  With whole
-// boxes (pages of 64 tokens and more, kOne) lane 0 works alone; otherwise lane
-// b looks up the pages of box b, and lane 0 issues the copies, so that a copy's
-// operands are uniform.  (Two lanes issuing a box each, with 64-bit ring
-// arithmetic, took 900 cycles a slot and set the pace of the kernel.)
+// ---- warps 0 and 2: loads -----------------------------------------------------
+// A half of 64 tokens is kNb boxes of each column block, of 64 / kNb tokens (one
+// with pages of 64 tokens and more).  One thread looks up the pages, a tile
+// ahead, and issues the copies, straight-line: with the page ids in other lanes
+// and shuffled, pages of 16 tokens set the pace of the kernel (2,048 rows behind
+// 32K, bf16: 1,181 us against 956 with pages of 64).
 template <bool kFp8>
 struct Producer {
   Ring<kFp8 ? kRaw : Cfg<kFp8>::kSlots> ring;
   bool live = true;
 };
 
-template <bool kOne>
-__device__ __forceinline__ long long box_row(long long row, int b) {
-  return kOne ? row : __shfl_sync(0xffffffffu, row, b);
-}
-template <bool kOne>
-__device__ __forceinline__ bool all_lanes(bool ok) {
-  return kOne ? ok : __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-}
-
 // bf16: one slot, two halves of two column blocks of 64 channels x 64 tokens:
-// K, the CTA's 64 tokens of all channels (row1 = row0); V, its 128 channels of
-// all tokens.
-template <bool kOne>
+// K, the CTA's 64 tokens of all channels; V, its 128 channels of all tokens.
+// rows: the boxes' pool rows, K's kNb, V's 2 kNb.
+template <int kNb, bool kV>
 __device__ __forceinline__ void load_slot(const Ctx& cx, Producer<false>& pr,
                                           uint32_t smem, uint32_t full0,
-                                          const CUtensorMap* map, bool is_v,
-                                          bool tail, long long row0,
-                                          long long row1, int nb, int rpb) {
+                                          const CUtensorMap* map, bool tail,
+                                          const int (&rows)[kV ? 2 * kNb : kNb]) {
   using C = Cfg<false>;
   const int s = pr.ring.at;
-  const bool leads = kOne || (threadIdx.x & 31) == 0;
-  bool ok = true;
-  if (leads && pr.ring.wrapped)
-    ok = wait_bar(cx, &cx.bars->empty[s], pr.ring.parity ^ 1);
-  ok = all_lanes<kOne>(ok && !*cx.abort);
-  if (!ok) {
+  if ((pr.ring.wrapped &&
+       !wait_bar(cx, &cx.bars->empty[s], pr.ring.parity ^ 1)) ||
+      *cx.abort) {
     pr.live = false;
     return;
   }
   // A tail's bytes count on each CTA's own barrier, for the warps that write
   // its zeros; the issuer learns of them with P.
-  if (leads && tail)
-    tc::bar_arrive_expect_tx(tc::smem_u32(&cx.bars->tail_full[s]),
-                             C::kSlotBytes);
-  if (leads && cx.rank == 0) {
-    if (tail)
-      tc::bar_arrive(tc::smem_u32(&cx.bars->full[s]));
-    else
-      tc::bar_arrive_expect_tx(tc::smem_u32(&cx.bars->full[s]),
-                               2 * C::kSlotBytes);
+  uint32_t full = full0 + s * 8;
+  if (tail) {
+    const uint32_t own = tc::smem_u32(&cx.bars->tail_full[s]);
+    tc::bar_arrive_expect_tx(own, C::kSlotBytes);
+    if (cx.rank == 0) tc::bar_arrive(tc::smem_u32(&cx.bars->full[s]));
+    full = tc::map_to(own, cx.rank);
+  } else if (cx.rank == 0) {
+    tc::bar_arrive_expect_tx(tc::smem_u32(&cx.bars->full[s]),
+                             2 * C::kSlotBytes);
   }
   const uint32_t dst = smem + C::kOffRing + s * C::kSlotBytes;
-  const uint32_t full =
-      tail ? tc::map_to(tc::smem_u32(&cx.bars->tail_full[s]), cx.rank)
-           : full0 + s * 8;
-  const int x0 = is_v ? (int)cx.rank * 128 : 0;
-  const int x1 = is_v ? x0 : 128;
-  for (int b = 0; b < nb; ++b) {
-    const int y0 = (int)box_row<kOne>(row0, b);
-    const int y1 = (int)box_row<kOne>(row1, b);
-    if (leads) {
-      const uint32_t d = dst + b * rpb * 128;
-      tc::tma_load_2d_pair(d, map, full, x0, y0);
-      tc::tma_load_2d_pair(d + kBlockBytes, map, full, x0 + 64, y0);
-      tc::tma_load_2d_pair(d + kHalfBytes, map, full, x1, y1);
-      tc::tma_load_2d_pair(d + kHalfBytes + kBlockBytes, map, full, x1 + 64, y1);
-    }
+  const int x0 = kV ? (int)cx.rank * 128 : 0, x1 = kV ? x0 : 128;
+#pragma unroll
+  for (int b = 0; b < kNb; ++b) {
+    const uint32_t d = dst + b * (kBlockBytes / kNb);
+    const int y0 = rows[b], y1 = rows[kV ? kNb + b : b];
+    tc::tma_load_2d_pair(d, map, full, x0, y0);
+    tc::tma_load_2d_pair(d + kBlockBytes, map, full, x0 + 64, y0);
+    tc::tma_load_2d_pair(d + kHalfBytes, map, full, x1, y1);
+    tc::tma_load_2d_pair(d + kHalfBytes + kBlockBytes, map, full, x1 + 64, y1);
   }
   pr.ring.next();
 }
 
 __device__ __forceinline__ void copy_scales(uint32_t dst, const __half* scales,
-                                            long long row, int rows,
-                                            uint32_t full) {
+                                            int row, int rows, uint32_t full) {
   asm volatile(
       "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes "
       "[%0], [%1], %2, [%3];" ::"r"(dst),
-      "l"(reinterpret_cast<const uint8_t*>(scales) + row * 8), "r"(rows * 8),
-      "r"(full)
+      "l"(reinterpret_cast<const uint8_t*>(scales) + (long long)row * 8),
+      "r"(rows * 8), "r"(full)
       : "memory");
 }
 
 // FP8: one staging buffer of 16 KB and its scales.  K: two blocks of 128 bytes
-// x 64 tokens; V: the CTA's 128 bytes of 128 tokens, the second 64 (row1) in
-// the second block.
-template <bool kOne>
+// x 64 tokens; V: the CTA's 128 bytes of 128 tokens, the second 64 in the second
+// block.
+template <int kNb, bool kV>
 __device__ __forceinline__ void load_raw(const Ctx& cx, Producer<true>& pr,
                                          uint32_t smem, const CUtensorMap* map,
-                                         const __half* scales, bool is_v,
-                                         long long row0, long long row1, int nb,
-                                         int rpb) {
+                                         const __half* scales,
+                                         const int (&rows)[kV ? 2 * kNb : kNb]) {
   using C = Cfg<true>;
+  constexpr int kBox = 64 / kNb;
   const int s = pr.ring.at;
-  const bool leads = kOne || (threadIdx.x & 31) == 0;
-  bool ok = true;
-  if (leads && pr.ring.wrapped)
-    ok = wait_bar(cx, &cx.bars->raw_empty[s], pr.ring.parity ^ 1);
   // Once a CTA gives up, its dequant warps release buffers that have not
   // landed; the flag is set before that, and arming a barrier whose bytes are
   // still under way is a fault.
-  ok = all_lanes<kOne>(ok && !*cx.abort);
-  if (!ok) {
+  if ((pr.ring.wrapped &&
+       !wait_bar(cx, &cx.bars->raw_empty[s], pr.ring.parity ^ 1)) ||
+      *cx.abort) {
     pr.live = false;
     return;
   }
   const uint32_t full = tc::smem_u32(&cx.bars->raw_full[s]);
-  if (leads) tc::bar_arrive_expect_tx(full, 16384 + (is_v ? 1024 : 512));
+  tc::bar_arrive_expect_tx(full, 16384 + (kV ? 1024 : 512));
   const uint32_t dst = smem + C::kOffRaw + s * kRawBytes;
-  for (int b = 0; b < nb; ++b) {
-    const long long y0 = box_row<kOne>(row0, b), y1 = box_row<kOne>(row1, b);
-    if (leads) {
-      const int x = is_v ? (int)cx.rank * 128 : 0;
-      const uint32_t o = b * rpb;
-      tc::tma_load_2d(dst + o * 128, map, full, x, (int)y0);
-      tc::tma_load_2d(dst + kBlockBytes + o * 128, map, full,
-                      is_v ? x : 128, (int)(is_v ? y1 : y0));
-      copy_scales(dst + 16384 + o * 8, scales, y0, rpb, full);
-      if (is_v) copy_scales(dst + 16384 + (64 + o) * 8, scales, y1, rpb, full);
-    }
+  const int x = kV ? (int)cx.rank * 128 : 0;
+#pragma unroll
+  for (int b = 0; b < kNb; ++b) {
+    const uint32_t d = dst + b * (kBox * 128), sc = dst + 16384 + b * (kBox * 8);
+    tc::tma_load_2d(d, map, full, x, rows[b]);
+    tc::tma_load_2d(d + kBlockBytes, map, full, kV ? x : 128,
+                    rows[kV ? kNb + b : b]);
+    copy_scales(sc, scales, rows[b], kBox, full);
+    if (kV) copy_scales(sc + 512, scales, rows[kNb + b], kBox, full);
   }
   pr.ring.next();
 }
 
-// One warp loads the K units of the order K0 K1 V0 K2 V1 .., another the V
-// units (with pages of 16 tokens a unit is 16 copies, more than one warp
-// issues in a tile's time); both step through the whole ring.
-template <bool kFp8, bool kCausal, bool kOne>
+// One thread loads the K units of the order K0 K1 V0 K2 V1 .., another the V
+// units; both step through the whole ring.
+template <bool kFp8, bool kCausal, int kNb, bool kV>
 __device__ __forceinline__ void produce_piece(const Ctx& cx, const Piece& pc,
                                               Producer<kFp8>& pr, uint32_t smem,
-                                              const CUtensorMap* map,
-                                              bool v_side) {
+                                              const CUtensorMap* map) {
   const AttnParams& p = *cx.a;
-  const int lane = threadIdx.x & 31;
-  const int rpb = p.box_rows, nb = kOne ? 1 : 64 / rpb;
+  constexpr int kIds = kV ? 2 * kNb : kNb, kBox = 64 / kNb;
   const uint32_t full0 = tc::map_to(tc::smem_u32(&cx.bars->full[0]), 0);
-  const __half* scales = v_side ? p.v_scales : p.k_scales;
+  const __half* scales = kV ? p.v_scales : p.k_scales;
   // K: this CTA's 64 tokens of a tile; V: all 128, in two halves
-  const int t0 = pc.tok + (kOne ? 0 : (lane & (nb - 1)) * rpb) +
-                 (v_side ? 0 : (int)cx.rank * 64);
-  int page0 = page_id<kCausal>(p, pc, t0);
-  int page1 = v_side ? page_id<kCausal>(p, pc, t0 + 64) : 0;
-  const bool tails = kCausal && !kFp8 && v_side && pc.tail_tokens() < kT;
-  if (v_side) pr.ring.next();  // K0
-  for (int j = 0; j < pc.n_tiles && pr.live; ++j) {
+  int t = pc.tok + (kV ? 0 : (int)cx.rank * 64);
+  int page[kIds];
+#pragma unroll
+  for (int b = 0; b < kIds; ++b) page[b] = page_id<kCausal>(p, pc, t + b * kBox);
+  const bool tails = kCausal && !kFp8 && kV && pc.tail_tokens() < kT;
+  if (kV) pr.ring.next();  // K0
+  for (int j = 0; j < pc.n_tiles && pr.live; ++j, t += kT) {
     // V: K of the next tile lies before V of this one; K: V of the tile
     // before the last
-    if (v_side && j + 1 < pc.n_tiles) pr.ring.next();
-    const int t = t0 + j * kT;
-    const long long r0 = pool_row(p, checked_page(p, page0), pc.g, t);
-    const long long r1 =
-        v_side ? pool_row(p, checked_page(p, page1), pc.g, t + 64) : r0;
+    if (kV && j + 1 < pc.n_tiles) pr.ring.next();
+    int rows[kIds];
+#pragma unroll
+    for (int b = 0; b < kIds; ++b)
+      rows[b] = pool_row(p, checked_page(p, page[b]), pc.g, t + b * kBox);
     if (j + 1 < pc.n_tiles) {
-      page0 = page_id<kCausal>(p, pc, t + kT);
-      if (v_side) page1 = page_id<kCausal>(p, pc, t + kT + 64);
+#pragma unroll
+      for (int b = 0; b < kIds; ++b)
+        page[b] = page_id<kCausal>(p, pc, t + kT + b * kBox);
     }
     if constexpr (kFp8)
-      load_raw<kOne>(cx, pr, smem, map, scales, v_side, r0, r1, nb, rpb);
+      load_raw<kNb, kV>(cx, pr, smem, map, scales, rows);
     else
-      load_slot<kOne>(cx, pr, smem, full0, map, v_side,
-                      tails && j + 1 == pc.n_tiles, r0, r1, nb, rpb);
-    if (!v_side && j > 0) pr.ring.next();  // V of tile j - 1
+      load_slot<kNb, kV>(cx, pr, smem, full0, map, tails && j + 1 == pc.n_tiles,
+                         rows);
+    if (!kV && j > 0) pr.ring.next();  // V of tile j - 1
   }
-  if (!v_side) pr.ring.next();  // V of the last tile
+  if (!kV) pr.ring.next();  // V of the last tile
 }
 
-template <bool kFp8, bool kCausal>
+template <bool kFp8, bool kCausal, bool kV>
 __device__ void produce(const Ctx& cx, const Piece& pc, Producer<kFp8>& pr,
-                        uint8_t* smem, const CUtensorMap* map, bool v_side) {
+                        uint8_t* smem, const CUtensorMap* map) {
   const uint32_t base = tc::smem_u32(smem);
-  if (cx.a->box_rows == 64) {
-    if ((threadIdx.x & 31) == 0)
-      produce_piece<kFp8, kCausal, true>(cx, pc, pr, base, map, v_side);
-  } else {
-    produce_piece<kFp8, kCausal, false>(cx, pc, pr, base, map, v_side);
+  switch (cx.a->box_rows) {
+    case 64: return produce_piece<kFp8, kCausal, 1, kV>(cx, pc, pr, base, map);
+    case 32: return produce_piece<kFp8, kCausal, 2, kV>(cx, pc, pr, base, map);
+    case 16: return produce_piece<kFp8, kCausal, 4, kV>(cx, pc, pr, base, map);
+    default: return produce_piece<kFp8, kCausal, 8, kV>(cx, pc, pr, base, map);
   }
 }
 
@@ -1116,11 +1090,11 @@ __global__ void __cluster_dims__(2, 1, 1)
     bool more = work.next(pc);
     for (; more; ++n_piece) {
       bool decoded = false;
-      if (warp == 0 || warp == 2) {
-        const bool v_side = warp != 0;
-        if (pr.live)
-          produce<kFp8, kCausal>(cx, pc, pr, smem, v_side ? &tm_v : &tm_k,
-                                 v_side);
+      if (lane == 0 && (warp == 0 || warp == 2)) {
+        if (pr.live && warp == 0)
+          produce<kFp8, kCausal, false>(cx, pc, pr, smem, &tm_k);
+        else if (pr.live)
+          produce<kFp8, kCausal, true>(cx, pc, pr, smem, &tm_v);
       } else if (lane == 0) {
         if (rank == 0 && warp == 1) {
           // the next piece's numbers are on their way before they are needed

@@ -83,30 +83,36 @@ __device__ __forceinline__ void tma_load_4d_pair(uint32_t dst,
       "r"(z), "r"(w)
       : "memory");
 }
-__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a, uint64_t b,
-                                         uint32_t idesc, uint32_t accumulate) {
+// The whole warp calls the next three, and the lane with `me` issues: with the
+// warp together, operands stay in uniform registers, where the instructions take
+// them from.
+__device__ __forceinline__ void mma_pair(bool me, uint32_t d_tmem, uint64_t a,
+                                         uint64_t b, uint32_t idesc,
+                                         uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(
           d_tmem),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"((uint32_t)me));
 }
-__device__ __forceinline__ void mma_pair_ta(uint32_t d_tmem, uint32_t a_tmem,
-                                            uint64_t b, uint32_t idesc,
+__device__ __forceinline__ void mma_pair_ta(bool me, uint32_t d_tmem,
+                                            uint32_t a_tmem, uint64_t b,
+                                            uint32_t idesc,
                                             uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(
           d_tmem),
-      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate));
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate), "r"((uint32_t)me));
 }
 // Arrive on the barrier at this offset in both CTAs once every MMA issued so
 // far by this thread is done.
-__device__ __forceinline__ void commit_pair(uint32_t bar) {
+__device__ __forceinline__ void commit_pair(bool me, uint32_t bar) {
   asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster."
-      "multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-      "h"((uint16_t)3)
+      "{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n"
+      " @q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster."
+      "multicast::cluster.b64 [%0], %1;\n}\n" ::"r"(bar),
+      "h"((uint16_t)3), "r"((uint32_t)me)
       : "memory");
 }
 // Both CTAs of the pair call these, one warp each.

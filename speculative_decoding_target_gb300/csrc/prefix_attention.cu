@@ -484,7 +484,7 @@ __device__ __forceinline__ void dequant_unit(const Ctx& cx, uint8_t* smem,
   dq.raw.next();
 }
 
-// ---- warp 1 of the leader, one thread: MMA issue ----------------------------
+// ---- warp 1 of the leader: MMA issue -----------------------------------------
 // A descriptor's low bits are the address in 16-byte steps, so the operands of
 // a slot's MMAs are its base descriptor plus constants.  (With the descriptors
 // built anew, issuing took 120 to 160 cycles an MMA, more than the 64 and 128
@@ -501,8 +501,8 @@ __device__ __forceinline__ bool wait_slot(const Ctx& cx,
 }
 
 template <bool kFp8>
-__device__ __forceinline__ bool issue_qk(const Ctx& cx, Slots<kFp8>& seq, int gj,
-                                         uint32_t tmem, uint32_t smem) {
+__device__ __forceinline__ bool issue_qk(const Ctx& cx, bool me, Slots<kFp8>& seq,
+                                         int gj, uint32_t tmem, uint32_t smem) {
   using C = Cfg<kFp8>;
   const uint32_t d = tmem + kColS + (gj & 1) * kT;
   const uint64_t a = tc::desc_sw128(smem, 16, 1024);
@@ -512,19 +512,19 @@ __device__ __forceinline__ bool issue_qk(const Ctx& cx, Slots<kFp8>& seq, int gj
   tc::fence_after();
 #pragma unroll
   for (int k = 0; k < 16; ++k)  // 16 channels each, 64 a column block
-    tc::mma_pair(d, a + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
+    tc::mma_pair(me, d, a + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
                  b + (((k >> 2) * kBlockBytes + (k & 3) * 32) >> 4),
                  C::kIdescQK, k ? 1u : 0u);
-  tc::commit_pair(tc::smem_u32(&cx.bars->empty[seq.at]));
+  tc::commit_pair(me, tc::smem_u32(&cx.bars->empty[seq.at]));
   seq.next();
-  tc::commit_pair(tc::smem_u32(&cx.bars->s_full[gj & 1]));
+  tc::commit_pair(me, tc::smem_u32(&cx.bars->s_full[gj & 1]));
   return true;
 }
 
 // tail: P comes with zeros in V, written by both CTAs.
 template <bool kFp8>
-__device__ __forceinline__ bool issue_pv(const Ctx& cx, Slots<kFp8>& seq, int gj,
-                                         bool first, bool tail, uint32_t tmem,
+__device__ __forceinline__ bool issue_pv(const Ctx& cx, bool me, Slots<kFp8>& seq,
+                                         int gj, bool first, bool tail, uint32_t tmem,
                                          uint32_t smem) {
   using C = Cfg<kFp8>;
   uint64_t* p_full = &cx.bars->p_full[gj & 1];
@@ -538,12 +538,12 @@ __device__ __forceinline__ bool issue_pv(const Ctx& cx, Slots<kFp8>& seq, int gj
   tc::fence_after();
 #pragma unroll
   for (int k = 0; k < 8; ++k)  // 16 tokens each, 64 a half
-    tc::mma_pair_ta(tmem, pt + k * 8,
+    tc::mma_pair_ta(me, tmem, pt + k * 8,
                     b + (((k >> 2) * kHalfBytes + (k & 3) * 2048) >> 4),
                     C::kIdescPV, first && k == 0 ? 0u : 1u);
-  tc::commit_pair(tc::smem_u32(&cx.bars->empty[seq.at]));
+  tc::commit_pair(me, tc::smem_u32(&cx.bars->empty[seq.at]));
   seq.next();
-  tc::commit_pair(tc::smem_u32(&cx.bars->pv_done[gj & 1]));
+  tc::commit_pair(me, tc::smem_u32(&cx.bars->pv_done[gj & 1]));
   return true;
 }
 
@@ -554,6 +554,7 @@ __device__ __forceinline__ void mma_piece(const Ctx& cx, const Piece& pc, int gj
                                           uint32_t tmem, uint8_t* smem_ptr,
                                           F then) {
   const uint32_t smem = tc::smem_u32(smem_ptr);
+  const bool me = (threadIdx.x & 31) == 0;
   if (!wait_bar<true>(cx, &cx.bars->q_full, (uint32_t)n_piece & 1)) {
     then();
     return;
@@ -563,12 +564,12 @@ __device__ __forceinline__ void mma_piece(const Ctx& cx, const Piece& pc, int gj
 #pragma unroll (kFp8 ? 1 : 2)
   for (int j = -1; j < pc.n_tiles; ++j) {
     if (j + 1 < pc.n_tiles &&
-        !issue_qk<kFp8>(cx, seq, gj0 + j + 1, tmem, smem)) {
+        !issue_qk<kFp8>(cx, me, seq, gj0 + j + 1, tmem, smem)) {
       if (j < 0) then();
       return;
     }
     if (j < 0) then();
-    if (j >= 0 && !issue_pv<kFp8>(cx, seq, gj0 + j, j == 0,
+    if (j >= 0 && !issue_pv<kFp8>(cx, me, seq, gj0 + j, j == 0,
                                   tails && j + 1 == pc.n_tiles, tmem, smem))
       return;
   }
@@ -1089,26 +1090,24 @@ __global__ void __cluster_dims__(2, 1, 1)
     Piece pc, nx;
     bool more = work.next(pc);
     for (; more; ++n_piece) {
-      bool decoded = false;
-      if (lane == 0 && (warp == 0 || warp == 2)) {
-        if (pr.live && warp == 0)
-          produce<kFp8, kCausal, false>(cx, pc, pr, smem, &tm_k);
-        else if (pr.live)
-          produce<kFp8, kCausal, true>(cx, pc, pr, smem, &tm_v);
-      } else if (lane == 0) {
-        if (rank == 0 && warp == 1) {
-          // the next piece's numbers are on their way before they are needed
-          mma_piece<kFp8, kCausal>(cx, pc, gj0, n_piece, seq, tmem, smem,
-                                   [&] { more = work.next(nx); });
-          decoded = true;
+      if (warp == 1 && rank == 0) {
+        // the next piece's numbers are on their way before they are needed
+        mma_piece<kFp8, kCausal>(cx, pc, gj0, n_piece, seq, tmem, smem,
+                                 [&] { more = work.next(nx); });
+      } else {
+        if (lane == 0) {
+          if (warp == 0 && pr.live)
+            produce<kFp8, kCausal, false>(cx, pc, pr, smem, &tm_k);
+          if (warp == 2 && pr.live)
+            produce<kFp8, kCausal, true>(cx, pc, pr, smem, &tm_v);
+          if constexpr (kFp8) {
+            if (rank == 1 && (warp & 1)) relay_piece(cx, pc, seq, warp == 3);
+          }
         }
-        if constexpr (kFp8) {
-          if (rank == 1) relay_piece(cx, pc, seq, warp == 3);
-        }
+        __syncwarp();
+        more = work.next(nx);
       }
-      __syncwarp();
       gj0 += pc.n_tiles;
-      if (!decoded) more = work.next(nx);
       pc = nx;
     }
   } else if (warp < 8) {
@@ -1154,9 +1153,10 @@ __global__ void __cluster_dims__(2, 1, 1)
 
   // teardown: no copy or MMA may still be in flight in either CTA.  Every
   // load was consumed by an MMA, and every MMA completes before drain.
-  if (warp == 1 && rank == 0 && lane == 0) {
-    tc::commit_pair(tc::smem_u32(&bars.drain));
+  if (warp == 1 && rank == 0) {
+    tc::commit_pair(lane == 0, tc::smem_u32(&bars.drain));
     wait_bar(cx, &bars.drain, 0, true);
+    __syncwarp();
   }
   tc::fence_before();
   __syncthreads();

@@ -44,6 +44,14 @@ struct RopeParams {
   float eps, w_offset;
 };
 
+// A frequency as a 64-bit fraction of a turn (rope_append.cu).
+__device__ __forceinline__ uint64_t turn_of(double f) {
+  const double turns = f * 0.15915494309189533577;  // 1 / 2 pi
+  const double frac = turns - floor(turns);
+  // 2^64 frac; a fraction that rounds up to a whole turn is none
+  return frac < 1.0 ? __double2ull_rz(frac * 18446744073709551616.0) : 0ull;
+}
+
 // Quantise-on-write of one cached row by a whole warp: lane l holds channels
 // 8l .. 8l+7 in x and the eight lanes of a 64-channel block share its scale.
 // The scale and the codes are computed in fp32 with correctly rounded
@@ -76,6 +84,10 @@ __device__ __forceinline__ void quantise_row(const float (&x)[8], int lane,
 
 cudaError_t launch_rope_append(const RopeParams& p, bool interleaved, int sms,
                                cudaStream_t s);
+// Norms as well (norm_rope.cu), for the layouts that fit its lanes.
+bool norm_rope_fits(const RopeParams& p, bool interleaved);
+cudaError_t launch_norm_rope(const RopeParams& p, bool interleaved, int sms,
+                             cudaStream_t s);
 cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t s);
 
 }  // namespace specv

@@ -37,13 +37,6 @@ constexpr int kWarps = 8;
 constexpr int kRows = 4;        // rows of a warp whose loads are in flight
 constexpr int kCtasPerSm = 4;
 
-__device__ __forceinline__ uint64_t turn_of(double f) {
-  const double turns = f * 0.15915494309189533577;  // 1 / 2 pi
-  const double frac = turns - floor(turns);
-  // 2^64 frac; a fraction that rounds up to a whole turn is none
-  return frac < 1.0 ? __double2ull_rz(frac * 18446744073709551616.0) : 0ull;
-}
-
 __device__ __forceinline__ void unpack4(uint2 r, float* x) {
   const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&r);
   x[0] = __low2float(h[0]);
@@ -285,12 +278,12 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
 
 cudaError_t launch_rope_append(const RopeParams& p, bool interleaved, int sms,
                                cudaStream_t s) {
+  if (p.k_weight && norm_rope_fits(p, interleaved))
+    return launch_norm_rope(p, interleaved, sms, s);
   const int tokens = p.a.batch * p.a.q_len;
   if (tokens == 0) return cudaSuccess;
   const int grid = min(tokens, sms * kCtasPerSm);
-  if (p.k_weight && interleaved)
-    rope_append_kernel<true, true><<<grid, kWarps * 32, 0, s>>>(p);
-  else if (p.k_weight)
+  if (p.k_weight)
     rope_append_kernel<false, true><<<grid, kWarps * 32, 0, s>>>(p);
   else if (interleaved)
     rope_append_kernel<true, false><<<grid, kWarps * 32, 0, s>>>(p);

@@ -152,11 +152,28 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
   const int n_pairs = q_pairs + 2 * kv_pairs;
   // up to 2^31 - 1 tokens: the step past the last one needs the 32nd bit
   const uint32_t q_len = a.q_len, tokens = a.batch * q_len;
-  int buf = 0;
-  int b = blockIdx.x / q_len;
-  uint32_t i = blockIdx.x - b * q_len;
   const int step_b = gridDim.x / q_len;
   const uint32_t step_i = gridDim.x - step_b * q_len;
+  int buf = 0;
+  // With more pairs than the warps hold, the tokens are walked once for each
+  // round of them: what a pair is, is worked out once a round.
+  for (int round = 0; round < n_pairs; round += kWarps * kPairs) {
+  int kind[kPairs], r[kPairs];
+  bool there[kPairs];
+  uint32_t src_at[kPairs];
+#pragma unroll
+  for (int e = 0; e < kPairs; ++e) {
+    const int pr = round + w + e * kWarps;
+    // 0 queries, 1 keys, 2 values, 3 none
+    kind[e] = pr < q_pairs ? 0 : pr < q_pairs + kv_pairs ? 1 : pr < n_pairs ? 2 : 3;
+    r[e] = 2 * (pr - (kind[e] == 0   ? 0
+                      : kind[e] == 1 ? q_pairs
+                                     : q_pairs + kv_pairs)) + sub;
+    there[e] = kind[e] < 3 && r[e] < (kind[e] == 0 ? p.hq : a.hkv);
+    src_at[e] = r[e] * kHeadDim + (kind[e] == 2 ? 16 * l : ca);
+  }
+  int b = blockIdx.x / q_len;
+  uint32_t i = blockIdx.x - b * q_len;
   for (uint32_t tok = blockIdx.x; tok < tokens; tok += gridDim.x, buf ^= 1) {
     const int width = a.q_lens ? min(max(a.q_lens[b], 0), a.q_len) : a.q_len;
     const long long t = (long long)a.seq_lens[b] - width + i;
@@ -168,13 +185,13 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
       const int at = (int)(t & (a.page_size - 1));
       if (page >= 0 && page < a.num_pages) {
         slot = (long long)page * a.hkv * a.page_size + at;
-        if (tid == 0 && a.cache_loc)
+        if (tid == 0 && round == 0 && a.cache_loc)
           a.cache_loc[tok] = (long long)page * a.page_size + at;
       } else if (a.status && tid == 0) {
         atomicOr(a.status, SPEC_STATUS_BAD_PAGE);
       }
     }
-    if (tid == 0) {
+    if (tid == 0 && round == 0) {
       if (a.positions) a.positions[tok] = live ? (int32_t)t : -1;
       if (a.cache_loc && slot < 0) a.cache_loc[tok] = -1;
     }
@@ -189,28 +206,19 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
       s_cos[buf][tid] = cs * p.factor;
       s_sin[buf][tid] = sn * p.factor;
     }
-    bool ready = false;
     u64 c_a[4], s_a[4], c_b[4], s_b[4];
-    for (int base = w; base < n_pairs; base += kWarps * kPairs) {
-      uint4 xa[kPairs], xb[kPairs];
+    uint4 xa[kPairs], xb[kPairs];
 #pragma unroll
-      for (int e = 0; e < kPairs; ++e) {
-        // pairs of query rows, then of keys, then of values
-        const int pr = base + e * kWarps;
-        xa[e] = xb[e] = make_uint4(0u, 0u, 0u, 0u);
-        if (pr >= n_pairs || !live) continue;
-        const bool is_q = pr < q_pairs, is_v = pr >= q_pairs + kv_pairs;
-        const int r = 2 * (pr - (is_q ? 0 : is_v ? q_pairs + kv_pairs : q_pairs)) + sub;
-        if (r >= (is_q ? p.hq : a.hkv)) continue;
-        const __nv_bfloat16* src =
-            (is_q ? q_src : is_v ? v_src : k_src) + r * kHeadDim;
-        xa[e] = __ldcs(reinterpret_cast<const uint4*>(src + (is_v ? 16 * l : ca)));
-        xb[e] =
-            __ldcs(reinterpret_cast<const uint4*>(src + (is_v ? 16 * l + 8 : cb)));
-      }
-      if (!ready) {  // once per token, after the first loads are on their way
-        __syncthreads();
-        ready = true;
+    for (int e = 0; e < kPairs; ++e) {
+      xa[e] = xb[e] = make_uint4(0u, 0u, 0u, 0u);
+      if (!there[e] || !live) continue;
+      const __nv_bfloat16* src =
+          (kind[e] == 0 ? q_src : kind[e] == 1 ? k_src : v_src) + src_at[e];
+      xa[e] = __ldcs(reinterpret_cast<const uint4*>(src));
+      xb[e] = __ldcs(
+          reinterpret_cast<const uint4*>(src + (kind[e] == 2 ? 8 : cb - ca)));
+    }
+    __syncthreads();  // (the loads are on their way)
         load8(&s_cos[buf][kInterleaved ? 0 : (rot_a ? pa : 0)], c_a);
         load8(&s_sin[buf][kInterleaved ? 0 : (rot_a ? pa : 0)], s_a);
         if (kInterleaved) {
@@ -237,16 +245,11 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
             s_a[k] = 0ull;
           }
         }
-      }
 #pragma unroll
       for (int e = 0; e < kPairs; ++e) {
-        const int pr = base + e * kWarps;
-        if (pr >= n_pairs) continue;
-        const bool is_q = pr < q_pairs, is_v = pr >= q_pairs + kv_pairs;
-        if (!is_q && slot < 0) continue;
-        const int r = 2 * (pr - (is_q ? 0 : is_v ? q_pairs + kv_pairs : q_pairs)) + sub;
-        const bool there = r < (is_q ? p.hq : a.hkv);
-        const long long row = slot + (long long)r * a.page_size;  // in the pool
+        const bool is_q = kind[e] == 0, is_v = kind[e] == 2;
+        if (kind[e] == 3 || (!is_q && slot < 0)) continue;
+        const long long row = slot + (long long)r[e] * a.page_size;  // in the pool
         if (!is_v && live) {
           u64 ya[4], yb[4];
           widen(xa[e], ya);
@@ -299,7 +302,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
               *reinterpret_cast<float4*>(x + k) =
                   *reinterpret_cast<const float4*>(mine + 16 * l + k);
             quantise_half(x, l, static_cast<uint8_t*>(a.k_pages) + row * kHeadDim,
-                          a.k_scales + row * (kHeadDim / 64), there);
+                          a.k_scales + row * (kHeadDim / 64), there[e]);
             continue;
           }
           xa[e] = narrow(ya);
@@ -323,25 +326,24 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
             x[9 + 2 * k] = f.y;
           }
           quantise_half(x, l, static_cast<uint8_t*>(a.v_pages) + row * kHeadDim,
-                        a.v_scales + row * (kHeadDim / 64), there);
+                        a.v_scales + row * (kHeadDim / 64), there[e]);
           continue;
         }
-        if (!there) continue;
+        if (!there[e]) continue;
         __nv_bfloat16* dst =
-            is_q ? q_dst + r * kHeadDim
+            is_q ? q_dst + r[e] * kHeadDim
                  : static_cast<__nv_bfloat16*>(is_v ? a.v_pages : a.k_pages) +
                        row * kHeadDim;
         *reinterpret_cast<uint4*>(dst + (is_v ? 16 * l : ca)) = xa[e];
         *reinterpret_cast<uint4*>(dst + (is_v ? 16 * l + 8 : cb)) = xb[e];
       }
-    }
-    if (!ready) __syncthreads();  // a warp without rows
     b += step_b;
     i += step_i;
     if (i >= q_len) {
       i -= q_len;
       ++b;
     }
+  }
   }
 }
 

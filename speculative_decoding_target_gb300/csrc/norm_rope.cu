@@ -11,7 +11,10 @@
 // in two 16-byte pieces, whose pairs lie in the two pieces (or inside them, when
 // interleaved): four shuffles for the sum of squares, one set of sines for all
 // rows of a token, and packed fp32 arithmetic.  (A warp a row with 8 channels a
-// lane took 64.8 us for 8,192 tokens where this takes NN, the copy rate 39.7.)
+// lane took 64.8 us for 8,192 tokens where this takes 51.8, the copy rate 39.7.
+// What is left is instructions and their latency: issue 55% busy.  Rows copied a
+// token or two ahead through shared memory: 54.6 to 57; two tokens a barrier with
+// 128 registers: 56.)
 //
 // Half layouts whose rotary / 2 is no multiple of 8 channels do not split that
 // way; they take the kernel in rope_append.cu.
@@ -22,9 +25,17 @@
 namespace specv {
 namespace {
 
-constexpr int kWarps = 8;
 constexpr int kPairs = 2;       // pairs of rows of a warp whose loads are in flight
-constexpr int kCtasPerSm = 3;
+// Warps of a CTA and CTAs of an SM.  bf16: three of eight (8,192 tokens 51.8 us;
+// four, with 64 registers, 54.2).  FP8: two of ten, four of which have keys or
+// values alone, which are quantised (five ragged prompts 54.4 us, a batch of
+// blocks 4.8; three of eight 56.0 and 5.2).
+template <bool kFp8>
+struct Shape {
+  static constexpr int kWarps = kFp8 ? 10 : 8;
+  static constexpr int kCtasPerSm = kFp8 ? 2 : 3;
+  static constexpr int kThreads = kWarps * 32;
+};
 typedef unsigned long long u64;
 
 __device__ __forceinline__ u64 pack2(float lo, float hi) {
@@ -115,8 +126,10 @@ __device__ __forceinline__ void quantise_half(const float (&x)[16], int l,
 namespace {
 
 template <bool kInterleaved, bool kFp8>
-__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
+__global__ void __launch_bounds__(Shape<kFp8>::kThreads,
+                                  Shape<kFp8>::kCtasPerSm)
     norm_rope_kernel(const RopeParams p) {
+  constexpr int kWarps = Shape<kFp8>::kWarps;
   // two buffers: a token's table is written while slow warps still read the
   // one before it
   __shared__ __align__(16) float s_cos[2][kHeadDim / 2], s_sin[2][kHeadDim / 2];
@@ -130,8 +143,10 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
   const int sub = lane >> 4, l = lane & 15;  // row of a pair, lane of the row
   const int half = p.rotary >> 1;
   const uint64_t turn = tid < half ? turn_of(p.freq[tid]) : 0ull;
-  s_w[0][tid] = norm_weight(p, p.q_weight, tid);
-  s_w[1][tid] = norm_weight(p, p.k_weight, tid);
+  for (int c = tid; c < kHeadDim; c += kWarps * 32) {
+    s_w[0][c] = norm_weight(p, p.q_weight, c);
+    s_w[1][c] = norm_weight(p, p.k_weight, c);
+  }
   // The lane's two pieces of 8 channels, from ca and from cb on, and the pairs of
   // each (interleaved: pa and pb on; otherwise pa on, in both).  Lanes that do
   // not rotate take the remaining channels.
@@ -149,7 +164,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
     }
   }
   const int q_pairs = (p.hq + 1) >> 1, kv_pairs = (a.hkv + 1) >> 1;
-  const int n_pairs = q_pairs + 2 * kv_pairs;
+  const int n_kv = 2 * kv_pairs, n_pairs = q_pairs + n_kv;
   // up to 2^31 - 1 tokens: the step past the last one needs the 32nd bit
   const uint32_t q_len = a.q_len, tokens = a.batch * q_len;
   const int step_b = gridDim.x / q_len;
@@ -163,7 +178,13 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
   uint32_t src_at[kPairs];
 #pragma unroll
   for (int e = 0; e < kPairs; ++e) {
-    const int pr = round + w + e * kWarps;
+    int pr = round + w + e * kWarps;
+    // FP8: keys and values go to the last warps of the first round, which have no
+    // second pair when the warps hold all in two
+    if (kFp8 && n_kv <= kWarps && n_pairs >= kWarps && pr < n_pairs)
+      pr = pr < kWarps - n_kv ? pr
+           : pr < kWarps      ? pr - kWarps + n_kv + q_pairs
+                              : pr - n_kv;
     // 0 queries, 1 keys, 2 values, 3 none
     kind[e] = pr < q_pairs ? 0 : pr < q_pairs + kv_pairs ? 1 : pr < n_pairs ? 2 : 3;
     r[e] = 2 * (pr - (kind[e] == 0   ? 0
@@ -347,12 +368,12 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
   }
 }
 
-template <bool kInterleaved>
-void launch(const RopeParams& p, int grid, cudaStream_t s) {
-  if (p.a.fp8)
-    norm_rope_kernel<kInterleaved, true><<<grid, kWarps * 32, 0, s>>>(p);
-  else
-    norm_rope_kernel<kInterleaved, false><<<grid, kWarps * 32, 0, s>>>(p);
+template <bool kInterleaved, bool kFp8>
+cudaError_t launch(const RopeParams& p, int tokens, int sms, cudaStream_t s) {
+  using S = Shape<kFp8>;
+  norm_rope_kernel<kInterleaved, kFp8>
+      <<<min(tokens, sms * S::kCtasPerSm), S::kThreads, 0, s>>>(p);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -365,12 +386,11 @@ cudaError_t launch_norm_rope(const RopeParams& p, bool interleaved, int sms,
                              cudaStream_t s) {
   const int tokens = p.a.batch * p.a.q_len;
   if (tokens == 0) return cudaSuccess;
-  const int grid = min(tokens, sms * kCtasPerSm);
-  if (interleaved)
-    launch<true>(p, grid, s);
-  else
-    launch<false>(p, grid, s);
-  return cudaGetLastError();
+  if (p.a.fp8)
+    return interleaved ? launch<true, true>(p, tokens, sms, s)
+                       : launch<false, true>(p, tokens, sms, s);
+  return interleaved ? launch<true, false>(p, tokens, sms, s)
+                     : launch<false, false>(p, tokens, sms, s);
 }
 
 }  // namespace specv

@@ -500,7 +500,8 @@ int spec_logprobs(const spec_logprob_desc* desc, const void* logits,
                   float* top_logprobs, void* workspace, size_t workspace_bytes,
                   void* stream);
 
-/* Workspace bytes for spec_logprobs (0 on a bad desc). */
+/* Workspace bytes for spec_logprobs: 0 where none is needed (spec_last_error() is
+ * then empty, and the workspace may be NULL) and on a bad desc. */
 size_t spec_logprob_workspace_size(const spec_logprob_desc* desc);
 
 /* Walks of the DFlash2 candidate selector (spec_select_desc.mode). */

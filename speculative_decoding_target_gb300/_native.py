@@ -10,6 +10,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -81,10 +82,20 @@ class RopeDesc(ctypes.Structure):
                 ("v_strides", ctypes.c_int64 * 2)]
 
 
+# The same struct as bytes: a ctypes structure with arrays takes four times as
+# long to fill.
+_ROPE_DESC = struct.Struct("@9iIP2if6q")
+assert _ROPE_DESC.size == ctypes.sizeof(RopeDesc)
+
+
 class NormDesc(ctypes.Structure):
     _fields_ = [("weight_dtype", ctypes.c_int32), ("eps", ctypes.c_float),
                 ("weight_offset", ctypes.c_float),
                 ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p)]
+
+
+_NORM_DESC = struct.Struct("@i2f2P")
+assert _NORM_DESC.size == ctypes.sizeof(NormDesc)
 
 
 class SampleDesc(ctypes.Structure):
@@ -156,10 +167,9 @@ def load(path: str = LIB_PATH):
     lib.spec_logprobs.argtypes = ([ctypes.POINTER(LogprobDesc)] + [P] * 8
                                   + [sz, P])
     lib.spec_logprobs.restype = ctypes.c_int
-    lib.spec_rope_append.argtypes = [ctypes.POINTER(RopeDesc)] + [P] * 15
+    lib.spec_rope_append.argtypes = [P] * 16
     lib.spec_rope_append.restype = ctypes.c_int
-    lib.spec_norm_rope_append.argtypes = (
-        [ctypes.POINTER(RopeDesc), ctypes.POINTER(NormDesc)] + [P] * 15)
+    lib.spec_norm_rope_append.argtypes = [P] * 17
     lib.spec_norm_rope_append.restype = ctypes.c_int
     lib.spec_verify_set_wait_limit.argtypes = [ctypes.c_int64]
     lib.spec_verify_set_wait_limit.restype = ctypes.c_int
@@ -243,6 +253,14 @@ def _on_current_device(tensors, stream) -> int:
     if stream.device_index != now:
         raise SpecError(SPEC_ERR_ARG, "the stream is another device's")
     return stream.cuda_stream
+
+
+def _packed(layout: struct.Struct, *values) -> bytes:
+    """A descriptor's bytes; numbers that its fields cannot hold are refused."""
+    try:
+        return layout.pack(*values)
+    except (struct.error, OverflowError) as e:
+        raise SpecError(SPEC_ERR_ARG, f"a value out of range: {e}") from None
 
 
 def _made_on(stream):
@@ -545,23 +563,27 @@ def norm_rope_append(q, k_new, v_new, q_weight, k_weight, freq, k_pages,
 def _rope_append(q, k_new, v_new, norm, freq, k_pages, v_pages, page_table,
                  seq_lens, interleaved, attn_factor, q_out, k_scales, v_scales,
                  positions, cache_loc, checked, workspace, q_lens, stream):
-    B, q_len, hkv, d = k_new.shape
+    shape = k_new.shape
+    B, q_len, hkv, d = shape
     hq = 0 if q is None else q.shape[2]
     _expect(k_new, torch.bfloat16, "k_new")
-    _expect(v_new, torch.bfloat16, "v_new", k_new.shape)
+    _expect(v_new, torch.bfloat16, "v_new", shape)
     _expect(freq, torch.float64, "freq", (freq.numel(),), contiguous=True)
     _expect(page_table, torch.int32, "page_table", contiguous=True)
     if page_table.dim() != 2 or page_table.shape[0] != B:
         raise SpecError(SPEC_ERR_ARG, f"page_table must have {B} rows")
     _expect(seq_lens, torch.int32, "seq_lens", (B,), contiguous=True)
     if q is not None:
-        _expect(q, torch.bfloat16, "q", (B, q_len, hq, d))
+        q_shape = (B, q_len, hq, d)
+        _expect(q, torch.bfloat16, "q", q_shape)
         if q_out is None:
-            with _made_on(stream):
-                q_out = torch.empty((B, q_len, hq, d), dtype=q.dtype,
-                                    device=q.device)
-        _expect(q_out, torch.bfloat16, "q_out", (B, q_len, hq, d),
-                contiguous=True)
+            if stream is None:
+                q_out = q.new_empty(q_shape)
+            else:
+                with _made_on(stream):
+                    q_out = q.new_empty(q_shape)
+        else:
+            _expect(q_out, torch.bfloat16, "q_out", q_shape, contiguous=True)
     q_w = k_w = None
     if norm is not None:
         q_w, k_w, eps, offset = norm
@@ -581,25 +603,27 @@ def _rope_append(q, k_new, v_new, norm, freq, k_pages, v_pages, page_table,
                              k_scales, v_scales, page_table, seq_lens, q_lens,
                              positions, cache_loc, workspace, q_w, k_w),
                             stream)
-    desc = RopeDesc(B, q_len, hq, hkv, d, k_pages.shape[2], k_pages.shape[0],
-                    page_table.shape[1],
-                    SPEC_KV_FP8_E4M3 if fp8 else SPEC_KV_BF16,
-                    SPEC_FLAG_CHECKED if checked else 0,
-                    None if q_lens is None else q_lens.data_ptr(),
-                    2 * freq.shape[0], 1 if interleaved else 0, attn_factor,
-                    _strides(q, "q") if q is not None else (0, 0),
-                    _strides(k_new, "k_new"), _strides(v_new, "v_new"))
-    args = (_at(q), _at(k_new), _at(v_new), _at(freq),
-            _at(q_out) if q is not None else None, _at(k_pages), _at(v_pages),
-            _at(k_scales), _at(v_scales), _at(page_table), _at(seq_lens),
-            _at(positions), _at(cache_loc), _at(workspace), on)
+    pages, _, page, _ = k_pages.shape
+    desc = _packed(
+        _ROPE_DESC,
+        B, q_len, hq, hkv, d, page, pages, page_table.shape[1],
+        SPEC_KV_FP8_E4M3 if fp8 else SPEC_KV_BF16,
+        SPEC_FLAG_CHECKED if checked else 0,
+        0 if q_lens is None else q_lens.data_ptr(), 2 * freq.shape[0],
+        1 if interleaved else 0, attn_factor,
+        *(_strides(q, "q") if q is not None else (0, 0)),
+        *_strides(k_new, "k_new"), *_strides(v_new, "v_new"))
+    args = (_at(q), k_new.data_ptr(), v_new.data_ptr(), freq.data_ptr(),
+            q_out.data_ptr() if q is not None else None, k_pages.data_ptr(),
+            v_pages.data_ptr(), _at(k_scales), _at(v_scales),
+            page_table.data_ptr(), seq_lens.data_ptr(), _at(positions),
+            _at(cache_loc), _at(workspace), on)
     if norm is None:
-        rc = load().spec_rope_append(ctypes.byref(desc), *args)
+        rc = load().spec_rope_append(desc, *args)
     else:
-        nd = NormDesc(int(k_w.dtype == torch.bfloat16), eps, offset, _at(q_w),
-                      _at(k_w))
-        rc = load().spec_norm_rope_append(ctypes.byref(desc),
-                                          ctypes.byref(nd), *args)
+        rc = load().spec_norm_rope_append(desc, _packed(
+            _NORM_DESC, k_w.dtype == torch.bfloat16, eps, offset,
+            0 if q_w is None else q_w.data_ptr(), k_w.data_ptr()), *args)
     if rc:
         _check(rc)
     return q_out
@@ -801,8 +825,9 @@ def sample(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None,
 
 
 def logprob_workspace_size(desc: LogprobDesc) -> int:
+    """0: such a call needs none."""
     n = load().spec_logprob_workspace_size(ctypes.byref(desc))
-    if n == 0:
+    if n == 0 and load().spec_last_error():
         raise SpecError(SPEC_ERR_ARG, load().spec_last_error().decode())
     return int(n)
 
@@ -826,27 +851,27 @@ def logprobs(logits, token=None, *, temperature=None, top: int = 0,
     on = _on_current_device((logits, token, temperature, workspace), stream)
     rows = lead.numel()
     stride = _row_stride(logits, rows)
-    out = {}
-    with _made_on(stream):
-        f32 = dict(dtype=torch.float32, device=logits.device)
-        if token is not None:
-            out["logprob"] = torch.empty(lead, **f32)
-        out["entropy"] = torch.empty(lead, **f32)
-        if top > 0:
-            out["top_ids"] = torch.empty((*lead, top), dtype=torch.int32,
-                                         device=logits.device)
-            out["top_logprobs"] = torch.empty((*lead, top), **f32)
     desc = LogprobDesc(rows, vocab, int(logits.dtype == torch.bfloat16), top,
                        stride)
-    if workspace is None:
-        with _made_on(stream):
-            workspace = alloc_workspace(logprob_workspace_size(desc),
-                                        logits.device)
+    need = logprob_workspace_size(desc) if workspace is None else 0
+    with _made_on(stream):
+        new = lambda shape, dtype: torch.empty(shape, dtype=dtype,
+                                               device=logits.device)
+        out = {}
+        if token is not None:
+            out["logprob"] = new(lead, torch.float32)
+        out["entropy"] = new(lead, torch.float32)
+        if top > 0:
+            out["top_ids"] = new((*lead, top), torch.int32)
+            out["top_logprobs"] = new((*lead, top), torch.float32)
+        if need:
+            workspace = alloc_workspace(need, logits.device)
     rc = load().spec_logprobs(
-        ctypes.byref(desc), _at(logits), _at(token), _at(temperature),
-        _at(out.get("logprob")), _at(out["entropy"]), _at(out.get("top_ids")),
-        _at(out.get("top_logprobs")), _at(workspace),
-        workspace.numel() * workspace.element_size(), on)
+        ctypes.byref(desc), logits.data_ptr(), _at(token), _at(temperature),
+        _at(out.get("logprob")), out["entropy"].data_ptr(),
+        _at(out.get("top_ids")), _at(out.get("top_logprobs")), _at(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(),
+        on)
     if rc:
         _check(rc)
     return out

@@ -1061,6 +1061,10 @@ int logprob_runs(int sms) {
   return sms * kCtasPerSm < kMaxRuns ? sms * kCtasPerSm : kMaxRuns;
 }
 
+bool logprob_in_runs(int rows, int sms) {
+  return rows > kFewRows && rows < kManyRows * logprob_runs(sms);
+}
+
 cudaError_t launch_logprobs(LogprobParams p, bool bf16, int sms,
                             cudaStream_t s) {
   int runs = logprob_runs(sms);
@@ -1071,7 +1075,7 @@ cudaError_t launch_logprobs(LogprobParams p, bool bf16, int sms,
     while (csize < kMaxCluster && 2 * csize * p.rows <= runs &&
            2 * csize * kSlice <= p.vocab)
       csize *= 2;
-  } else if (p.rows < kManyRows * runs) {
+  } else if (logprob_in_runs(p.rows, sms)) {
     // no run shorter than a slice
     p.slices = max(1, p.vocab / kSlice);
     runs = (int)min((long long)runs, (long long)p.rows * p.slices);

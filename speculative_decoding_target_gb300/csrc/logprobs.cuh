@@ -32,6 +32,8 @@ struct LogprobParams {
 
 // CTAs of a call, at most.
 int logprob_runs(int sms);
+// Whether a call of so many rows cuts them into runs, and needs `parts`.
+bool logprob_in_runs(int rows, int sms);
 cudaError_t launch_logprobs(LogprobParams p, bool bf16, int sms, cudaStream_t s);
 
 }  // namespace specv

@@ -1197,15 +1197,19 @@ int check_logprobs(const spec_logprob_desc* d) {
                 specv::kLogprobMaxTop);
   return SPEC_OK;
 }
-size_t logprob_bytes(int sms) {
-  return 2 * (size_t)specv::logprob_runs(sms) * sizeof(specv::LogprobPart);
+// (only calls that cut rows into parts of runs need any)
+size_t logprob_bytes(const spec_logprob_desc* d, int sms) {
+  return specv::logprob_in_runs(d->rows, sms)
+             ? 2 * (size_t)specv::logprob_runs(sms) * sizeof(specv::LogprobPart)
+             : 0;
 }
 }  // namespace
 
 size_t spec_logprob_workspace_size(const spec_logprob_desc* desc) {
+  g_err[0] = 0;
   int sms;
   if (check_logprobs(desc) || sm_count(&sms)) return 0;
-  return logprob_bytes(sms);
+  return logprob_bytes(desc, sms);
 }
 
 int spec_logprobs(const spec_logprob_desc* desc, const void* logits,
@@ -1235,8 +1239,11 @@ int spec_logprobs(const spec_logprob_desc* desc, const void* logits,
   int sms;
   rc = sm_count(&sms);
   if (rc) return rc;
-  rc = check_workspace(workspace, workspace_bytes, logprob_bytes(sms));
-  if (rc) return rc;
+  const size_t need = logprob_bytes(d, sms);
+  if (need) {
+    rc = check_workspace(workspace, workspace_bytes, need);
+    if (rc) return rc;
+  }
   specv::LogprobParams p;
   std::memset(&p, 0, sizeof p);
   p.logits = logits;

@@ -38,9 +38,10 @@ struct __align__(16) ChunkPiece {
   int rows, first, limit, last;  // the request's rows, block row of row 0, tokens
                                  // that row 0 sees, last cached token
 };
-// A pair's run of the rest: its first piece, the tile it starts at, its tiles.
+// A pair's run of the rest: its first piece, the tile it starts at, its tiles, and
+// the partial slot of that first piece if it does not start it.
 struct __align__(16) ChunkRun {
-  int piece, from, tiles, pad;
+  int piece, from, tiles, slot;
 };
 
 struct ChunkParams {
@@ -48,7 +49,8 @@ struct ChunkParams {
   ChunkHead* head;
   ChunkPiece* pieces; // in order
   ChunkRun* runs;     // [pairs]
-  int2* rest;         // [pairs]: first and last pair with a run of a rest's piece
+  int2* rest;         // [pairs]: a rest's piece's first partial slot, and partials
+                      // (1: whole)
   float* pre_o;       // [2 pairs, kPrefixRows, 256]
   float* pre_lse;     // [2 pairs, kPrefixRows]
   int pairs;

@@ -15,6 +15,7 @@ static_assert(kThreads >= kMaxBatch, "");
 // A run of the rest is at least this long, in 128-token tiles, and one that
 // would start or end as close as kSnap to a piece's border starts or ends there
 // (a piece costs as much as kPrefixCost tiles).
+constexpr int kHeld = 4096;
 constexpr int kMinRun = 2;
 constexpr int kSnap = 2;
 
@@ -64,6 +65,8 @@ __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(const ChunkParams 
   __shared__ int s_scan[kWarps];
   __shared__ long long s_scan64[kWarps];
   __shared__ int s_units[kThreads + 1], s_ranges[kThreads + 1];
+  __shared__ int s_before[kThreads];  // runs that are not empty, before each
+  __shared__ int s_tiles[kHeld];      // of the pieces, when they are few
   __shared__ int s_longest, s_load;
   const AttnParams& a = p.a;
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
@@ -85,6 +88,7 @@ __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(const ChunkParams 
   if (tid == 0) s_tile0[0] = 0;
   __syncthreads();
   const int longest = s_longest;
+  const bool held = (long long)T * a.hkv <= kHeld;
   auto tile_at = [&](int i, int* b, int* m) {
     *b = last_at_most(s_tile0, a.batch, i);
     *m = i - s_tile0[*b];
@@ -134,24 +138,29 @@ __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(const ChunkParams 
       ChunkPiece* to = p.pieces + (long long)s_base[bucket] * a.hkv +
                        s_warp[w][bucket] + before;
       const ChunkRows r = chunk_rows(a, b);
-      for (int g = 0; g < a.hkv; ++g, to += s_count[bucket])
+      for (int g = 0; g < a.hkv; ++g, to += s_count[bucket]) {
+        if (held) s_tiles[to - p.pieces] = t;
         *to = ChunkPiece{b,      g,       m * 2 * p.cta_rows,   t,
                          r.rows, r.first, r.len - r.live + 1, r.len - 1};
+      }
     }
     __syncthreads();
   }
   // rounds, and the rest
   const int P = p.pairs, N = T * a.hkv, rounds = N / P, rest = N - rounds * P;
+  auto tiles_of = [&](long long i) {
+    return held ? s_tiles[i] : p.pieces[i].tiles;
+  };
   long long dealt = 0;  // of pair tid
   if (tid < P) {
 #pragma unroll 4
     for (int r = 0; r < rounds; ++r)
-      dealt += p.pieces[(long long)r * P + (r & 1 ? P - 1 - tid : tid)].tiles +
+      dealt += tiles_of((long long)r * P + (r & 1 ? P - 1 - tid : tid)) +
                kPrefixCost;
   }
-  const ChunkPiece* q = p.pieces + (long long)rounds * P;
   int R;
-  const int units = block_scan(tid < rest ? q[tid].tiles : 0, s_scan, &R);
+  const int units = block_scan(
+      tid < rest ? tiles_of((long long)rounds * P + tid) : 0, s_scan, &R);
   s_units[tid + 1] = units;
   if (tid == 0) s_units[0] = 0;
   long long sum;
@@ -189,14 +198,30 @@ __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(const ChunkParams 
     }
   }
   __syncthreads();
-  if (tid < P) {
-    const int from = s_ranges[tid], n = s_ranges[tid + 1] - from;
-    const int i = n ? last_at_most(s_units, rest, from) : 0;
-    p.runs[tid] = ChunkRun{i, from - s_units[i], n, 0};
+  // a cut piece's partials have neighbouring slots, in the order of its runs
+  const int n = tid < P ? s_ranges[tid + 1] - s_ranges[tid] : 0;
+  int sum_n;
+  const int filled = block_scan(n ? 1 : 0, s_scan, &sum_n) - (n ? 1 : 0);
+  if (tid < P) s_before[tid] = filled;
+  __syncthreads();
+  int first = 0, parts = 0;
+  if (tid < rest) {
+    first = s_before[last_at_most(s_ranges, P, s_units[tid])];
+    parts = s_before[last_at_most(s_ranges, P, s_units[tid + 1] - 1)] + 1 - first;
   }
-  if (tid < rest)
-    p.rest[tid] = make_int2(last_at_most(s_ranges, P, s_units[tid]),
-                            last_at_most(s_ranges, P, s_units[tid + 1] - 1));
+  const int slots = parts > 1 ? parts : 0;
+  const int slot = block_scan(slots, s_scan, &sum_n) - slots;
+  __syncthreads();
+  if (tid < rest) {
+    p.rest[tid] = make_int2(slot, parts);
+    s_tiles[tid] = slot - first;  // (a rest is shorter than kHeld)
+  }
+  __syncthreads();
+  if (tid < P) {
+    const int i = n ? last_at_most(s_units, rest, s_ranges[tid]) : 0;
+    p.runs[tid] =
+        ChunkRun{i, s_ranges[tid] - s_units[i], n, n ? s_tiles[i] + filled : 0};
+  }
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -215,31 +240,42 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   const int lane = threadIdx.x & 31;
   // the call that follows may set itself up
   tc_grid_launch_dependents();
+  // Block rows in front of and behind the live ones, which no other kernel of the
+  // call writes (the attention has waited for whatever wrote them before).
+  const long long vecs = (long long)a.hq * (kHeadDim / 8);  // 16 bytes, a token
+  for (int b = 0; b < a.batch; ++b) {
+    const ChunkRows cr = chunk_rows(a, b);
+    if (cr.live == a.q_len) continue;
+    uint4* o = reinterpret_cast<uint4*>(a.out) + (long long)b * a.q_len * vecs;
+    const long long front = cr.first * vecs, from = (cr.first + cr.live) * vecs;
+    const long long n = front + a.q_len * vecs - from;
+    for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < n;
+         i += (long long)gridDim.x * blockDim.x)
+      o[i < front ? i : from + (i - front)] = make_uint4(0, 0, 0, 0);
+  }
   tc_grid_dependency_wait();
   const ChunkHead h = *p.head;
-  const int P = p.pairs;
   if (h.split) {
     for (int w = blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
          w < h.rest * kPrefixRows; w += gridDim.x * kMergeWarps) {
       const int i = w / kPrefixRows, r = w % kPrefixRows;
-      const int2 by = p.rest[i];
-      if (by.x == by.y) continue;  // whole
-      const ChunkPiece e = p.pieces[(long long)h.rounds * P + i];
+      const int2 at = p.rest[i];
+      const ChunkPiece e = p.pieces[(long long)h.rounds * p.pairs + i];
+      if (at.y <= 1) continue;  // whole
       const int half = r / 128, in = r - half * 128;
       const int R = e.row0 + half * p.cta_rows + in;
       if (in >= p.cta_rows || R >= e.rows) continue;
       float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       float den = 0.f, mx = -INFINITY;
-      for (int c = by.x; c <= by.y; c += kBatch) {
+      for (int c = 0; c < at.y; c += kBatch) {
         float lv[kBatch];
         float4 x0[kBatch], x1[kBatch];
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
           lv[j] = -INFINITY;
           x0[j] = x1[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-          const int ch = c + j;
-          if (ch <= by.y && p.runs[ch].tiles) {
-            const long long row = (long long)(ch + i) * kPrefixRows + r;
+          if (c + j < at.y) {
+            const long long row = (long long)(at.x + c + j) * kPrefixRows + r;
             const float* o = p.pre_o + row * kHeadDim + lane * 8;
             lv[j] = p.pre_lse[row];
             x0[j] = *reinterpret_cast<const float4*>(o);
@@ -274,22 +310,10 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
       v.z = pack_bf16(acc[4] * inv, acc[5] * inv);
       v.w = pack_bf16(acc[6] * inv, acc[7] * inv);
       const int tok = R / a.group;
-      const long long at = ((long long)e.b * a.q_len + e.first + tok) * a.hq +
+      const long long to = ((long long)e.b * a.q_len + e.first + tok) * a.hq +
                            e.g * a.group + (R - tok * a.group);
-      *reinterpret_cast<uint4*>(a.out + at * kHeadDim + lane * 8) = v;
+      *reinterpret_cast<uint4*>(a.out + to * kHeadDim + lane * 8) = v;
     }
-  }
-  // block rows in front of and behind the live ones
-  const long long vecs = (long long)a.hq * (kHeadDim / 8);  // 16 bytes, a token
-  for (int b = 0; b < a.batch; ++b) {
-    const ChunkRows cr = chunk_rows(a, b);
-    if (cr.live == a.q_len) continue;
-    uint4* o = reinterpret_cast<uint4*>(a.out) + (long long)b * a.q_len * vecs;
-    const long long front = cr.first * vecs, from = (cr.first + cr.live) * vecs;
-    const long long n = front + a.q_len * vecs - from;
-    for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < n;
-         i += (long long)gridDim.x * blockDim.x)
-      o[i < front ? i : from + (i - front)] = make_uint4(0, 0, 0, 0);
   }
 }
 

@@ -988,6 +988,7 @@ struct ChunkWork {
     const ChunkPiece e =
         p.pieces[(long long)(whole ? round : h.rounds) * p.pairs +
                  (whole ? at : run.piece)];
+    const int slot0 = whole ? 0 : p.rest[run.piece].x;
     int from = 0, to = e.tiles;
     pc.slot = -1;
     if (whole) {
@@ -995,7 +996,9 @@ struct ChunkWork {
     } else {
       from = run.from;
       to = min(to, from + run.tiles);
-      if (to - from < e.tiles) pc.slot = pair + run.piece;
+      // its first run's slot is the piece's first
+      if (from) pc.slot = run.slot;
+      else if (to < e.tiles) pc.slot = slot0;
       ++run.piece;
       run.tiles -= to - from;
       run.from = 0;

@@ -30,12 +30,15 @@
 // too large to be rounded so, is summed from (x - ref) c, where -inf and NaN
 // weigh nothing.
 //
-// Alternatives.  Each thread keeps its largest value and the vector that holds
-// it (the first, of equals).  The `top` best tokens of a CTA lie in the vectors'
-// threads with the `top` best (value, vector); a thread of rank r among them
-// holds at most top - r of them.  So a warp reads each winner's values once more
-// (from L1 or L2), and takes out its best until one falls below the last
-// winner's: one or two each on real rows, and a bounded number on any row.
+// Alternatives.  Each thread keeps its largest value, the vector that holds it
+// (the first, of equals) and the largest value of its other vectors.  The `top`
+// best tokens of a CTA lie in the threads with the `top` best (value, vector); a
+// thread of rank r among them holds at most top - r of them.  Each of these
+// winners reads that one vector again (on its way while they are ranked) and hands
+// in what is not below the last winner's value.  A winner whose other vectors hold
+// such values too, as with many equals, is read by half a warp as a whole, and its
+// best top - r are taken out.  (Reading every winner's values, up to 485 a row:
+// 128 us for 1,024 bf16 rows with top 20, 89 without any.)
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -61,9 +64,9 @@ constexpr float kRebase = 8.f;    // log2
 constexpr float kLow = 160.f;     // log2
 constexpr float kLargeRef = 1048576.f;
 constexpr int kTop = kLogprobMaxTop;
-constexpr int kGroups = 64;       // groups of 8 threads
 // what winners of ranks 0 .. top - 1 may hand in
-constexpr int kCands = kTop * (kTop + 1) / 2;
+// (a vector of 8 even for the last of them)
+constexpr int kCands = kTop * (kTop + 1) / 2 + 28;
 constexpr float kMaxFinite = 3.402823466e+38f;
 typedef unsigned long long u64;
 
@@ -154,15 +157,13 @@ __device__ __forceinline__ int place_of(u64 key) {
 }
 
 struct Shared {
-  float max[kWarps], s[kWarps], h[kWarps];
+  float max[32], s[kWarps], h[kWarps];  // largest of every 16 threads; sums
   // selection: keys, in pairs
-  __align__(16) u64 group[kGroups];
   __align__(16) u64 list[kThreads + 2];
   __align__(16) u64 cands[kCands + 2];
   u64 bound;
-  int listed, found;
-  uint16_t list_t[kThreads];
-  uint16_t winner[kTop];
+  int listed, found, deep;
+  uint16_t deep_t[kTop], deep_r[kTop];
   u64 top[kTop];
   // live rows
   int scan[kWarps], live, first;
@@ -208,8 +209,9 @@ __device__ __forceinline__ float to_float(__nv_bfloat16 x) {
 
 // A thread's sums against ref, its largest value and where it is.
 struct Sums {
-  float ref, rc, s, h, max;  // rc = fl(ref c)
-  int vec;                   // (-1: the odd token)
+  float ref, rc, s, h;   // rc = fl(ref c)
+  float max, next;       // the largest value, and that of all other vectors
+  int vec;               // where the largest is (-1: the odd token)
 };
 
 // What ref c was rounded by; 0 where that is no small number any more, and t is
@@ -238,27 +240,28 @@ template <typename T, typename F>
 __device__ __forceinline__ void join(Sums& a, const uint4 (&raw)[kVecs], int v0,
                                      float c, F refill) {
   constexpr int kN = Vec<T>::kN;
-  float most = -INFINITY;
+  float m[kVecs], most = -INFINITY;
 #pragma unroll
   for (int u = 0; u < kVecs; ++u) {
-    const float m = largest(raw[u], static_cast<T*>(nullptr));
-    most = fmaxf(most, m);
-    if (m > a.max) {
-      a.max = m;
+    m[u] = largest(raw[u], static_cast<T*>(nullptr));
+    most = fmaxf(most, m[u]);
+  }
+  if (most == INFINITY) {  // the type's largest, of which the first counts
+    most = most_of<T>();
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) m[u] = fminf(m[u], most);
+  }
+#pragma unroll
+  for (int u = 0; u < kVecs; ++u) {
+    a.next = fmaxf(a.next, fminf(m[u], a.max));
+    if (m[u] > a.max) {
+      a.max = m[u];
       a.vec = v0 + u * kThreads;
     }
   }
   refill(most);
-  if (!((most - a.ref) * c <= kRebase)) {  // (also for an infinite one)
+  if (!((most - a.ref) * c <= kRebase)) {  // (also without a reference)
     if (most == -INFINITY) return;         // nothing so far that weighs
-    if (most == INFINITY) {
-      // no value is larger, and the first of the type's largest counts
-      most = a.max = most_of<T>();
-#pragma unroll
-      for (int u = kVecs - 1; u >= 0; --u)
-        if (largest(raw[u], static_cast<T*>(nullptr)) >= most)
-          a.vec = v0 + u * kThreads;
-    }
     rebase(a, most, c);
   }
   const u64 c2 = pack2(c, c), r2 = pack2(-a.rc, -a.rc);
@@ -349,7 +352,7 @@ struct Ring {
 // The sums of a part that the ring has started.
 template <typename T>
 __device__ __forceinline__ Sums stream(const Part<T>& part, Ring& ring, float c) {
-  Sums a{-INFINITY, 0.f, 0.f, 0.f, -INFINITY, 0};
+  Sums a{-INFINITY, 0.f, 0.f, 0.f, -INFINITY, -INFINITY, 0};
   int v = part.begin + (int)threadIdx.x;
   int left = part.end - part.begin;
   const uint4* ahead = part.vec(v + kStages * kStep);
@@ -386,6 +389,7 @@ __device__ __forceinline__ Sums stream(const Part<T>& part, Ring& ring, float c)
   }
   if (part.odd >= 0) {
     const float x = clean<T>(to_float(part.x[part.odd]));
+    a.next = fmaxf(a.next, fminf(x, a.max));
     // in front of every vector, or behind them
     if (x > a.max || (x == a.max && part.odd < part.head && x > -INFINITY)) {
       a.max = x;
@@ -435,59 +439,66 @@ __device__ void select(Shared& sh, const Part<T>& part, const Sums& a,
                        int top) {
   constexpr int kN = Vec<T>::kN;
   const int tid = threadIdx.x, lane = tid & 31;
-  const int place = a.vec < 0 ? part.odd : part.head + a.vec * kN;
-  const u64 mine = a.max > -INFINITY ? key_of(a.max, place) : 0;
-  // a bound: the top-th largest of 64 groups' maxima
-  u64 g = mine;
+  // a bound: the top-th largest of 32 groups' maxima
+  const float group = sh.max[lane];
+  int ahead = 0;
 #pragma unroll
-  for (int o = 4; o; o >>= 1) {
-    const u64 other = __shfl_xor_sync(0xffffffffu, g, o);
-    g = other > g ? other : g;
+  for (int k = 0; k < 32; ++k) {
+    const float other = __shfl_sync(0xffffffffu, group, k);
+    ahead += other > group || (other == group && k < lane);
   }
-  if ((lane & 7) == 0) sh.group[tid >> 3] = g;
-  if (tid == 0) {
-    sh.listed = sh.found = 0;
-    sh.bound = 0;
-  }
-  if (tid < kTop) sh.top[tid] = 0;
-  __syncthreads();
-  if (tid < kGroups) {
-    const u64 group = sh.group[tid];
-    if (group && rank_in(sh.group, kGroups, group) == top - 1) sh.bound = group;
-  }
-  __syncthreads();
-  // the threads at or above it, in any order
-  const bool in = mine && mine >= sh.bound;
+  const unsigned last_group = __ballot_sync(0xffffffffu, ahead == top - 1);
+  const float low = __shfl_sync(0xffffffffu, group, __ffs(last_group) - 1);
+  // the threads at or above it, in any order, and their vectors
+  const bool in = a.max >= low && a.max > -INFINITY;
+  uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+  if (in && a.vec >= 0) raw = __ldg(part.vec(a.vec));
+  const u64 mine =
+      in ? key_of(a.max, a.vec < 0 ? part.odd : part.head + a.vec * kN) : 0;
   const unsigned who = __ballot_sync(0xffffffffu, in);
   if (who) {
     int at = 0;
     if (lane == 0) at = atomicAdd(&sh.listed, __popc(who));
     at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1));
-    if (in) {
-      sh.list[at] = mine;
-      sh.list_t[at] = (uint16_t)tid;
-    }
+    if (in) sh.list[at] = mine;
   }
   __syncthreads();
   const int n = sh.listed;
   if (tid == 0) sh.list[n] = 0;
   if (n & 1) __syncthreads();  // uniform
-  if (tid < n) {
-    const u64 key = sh.list[tid];
-    const int r = rank_in(sh.list, n, key);
-    if (r < top) sh.winner[r] = sh.list_t[tid];
-    if (r == top - 1) sh.bound = key;
+  int rank = top;
+  if (in) {
+    rank = rank_in(sh.list, n, mine);
+    if (rank == top - 1) sh.bound = mine;
   }
   __syncthreads();
-  const int winners = min(n, top);
   // the last winner's value: what lies below it is no candidate
-  const float bound = n >= top ? value_of(sh.bound) : -INFINITY;
+  const float bound =
+      n >= top ? fmaxf(value_of(sh.bound), -kMaxFinite) : -kMaxFinite;
+  if (rank < top) {
+    if (a.next >= bound) {
+      const int at = atomicAdd(&sh.deep, 1);
+      sh.deep_t[at] = (uint16_t)tid;
+      sh.deep_r[at] = (uint16_t)rank;
+    } else if (a.vec < 0) {
+      sh.cands[atomicAdd(&sh.found, 1)] = mine;
+    } else {
+      float x[kN];
+      widen(raw, x, static_cast<T*>(nullptr));
+#pragma unroll
+      for (int k = 0; k < kN; ++k)
+        if (x[k] >= bound)
+          sh.cands[atomicAdd(&sh.found, 1)] =
+              key_of(clean<T>(x[k]), part.head + a.vec * kN + k);
+    }
+  }
+  __syncthreads();
+  const int deep = sh.deep;
   // half a warp each
-  const int r = tid >> 4, sub = tid & 15;
-  if (r < winners) {  // (uniform in a half)
+  const int d = tid >> 4, sub = tid & 15;
+  if (d < deep) {  // (uniform in a half)
     const unsigned half = lane & 16 ? 0xffff0000u : 0x0000ffffu;
-    const int t = sh.winner[r];
-    const float low = fmaxf(bound, -kMaxFinite);
+    const int t = sh.deep_t[d], r = sh.deep_r[d];
     // this lane's vectors of the thread, every 16th, a bit for each value that
     // is a candidate
     constexpr int kStride = 16 * kThreads;
@@ -510,7 +521,7 @@ __device__ void select(Shared& sh, const Part<T>& part, const Sums& a,
         widen(raw[q], x, static_cast<T*>(nullptr));
 #pragma unroll
         for (int k = 0; k < kN; ++k)
-          if (x[k] >= low) bits |= 1u << (q * kN + k);
+          if (x[k] >= bound) bits |= 1u << (q * kN + k);
       }
       hit |= (u64)bits << bit;
       bit += 4 * kN;
@@ -518,7 +529,7 @@ __device__ void select(Shared& sh, const Part<T>& part, const Sums& a,
     const int odd = part.odd_of(t);
     const float odd_x =
         sub == 15 && odd >= 0 ? clean<T>(to_float(part.x[odd])) : -INFINITY;
-    const bool odd_hit = odd_x >= low;
+    const bool odd_hit = odd_x >= bound;
     int hits = __popcll(hit) + odd_hit;
 #pragma unroll
     for (int o = 8; o; o >>= 1) hits += __shfl_xor_sync(half, hits, o);
@@ -551,7 +562,7 @@ __device__ void select(Shared& sh, const Part<T>& part, const Sums& a,
       }
     }
   }
-  __syncthreads();
+  if (deep) __syncthreads();  // uniform
   const int found = sh.found;
   if (tid == 0) sh.cands[found] = 0;
   if (found & 1) __syncthreads();
@@ -656,10 +667,15 @@ __device__ __forceinline__ void work_on(Shared& sh, Ring& ring,
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Sums a = stream(part, ring, c);
   then();
-  const float wm = warp_max(a.max);
-  if (lane == 0) sh.max[w] = wm;
+  float gm = a.max;
+#pragma unroll
+  for (int o = 8; o; o >>= 1)
+    gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, o));
+  if ((lane & 15) == 0) sh.max[threadIdx.x >> 4] = gm;
+  if (threadIdx.x == 0) sh.listed = sh.found = sh.deep = 0;
+  if (threadIdx.x < kTop) sh.top[threadIdx.x] = 0;
   __syncthreads();
-  m = warp_max(sh.max[lane & (kWarps - 1)]);
+  m = warp_max(sh.max[lane]);
   s = h = 0.f;
   if (a.ref > -INFINITY) {
     const float d = fmaxf(fmaf(a.ref - m, c, -delta_of(a.ref, c)), -kLow);

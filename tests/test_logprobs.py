@@ -243,6 +243,74 @@ def test_shapes_streams_graphs_and_repeats():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,vocab", [(1, 300000), (4870, 9001)])
+def test_infinities_in_many_vectors(dtype, rows, vocab):
+    # all count alike, so the first are the best; ends of threads differ
+    inf = float("inf")
+    x = logits(rows, vocab, dtype, seed=9)
+    x[0] = inf
+    x[0, 0] = -inf
+    if rows > 1:
+        x[1, 100::3] = inf
+        x[1, 105] = MOST[dtype]
+        token = np.full(rows, 101)
+        token[5:] = -1
+        token[0] = 7
+    else:
+        token = [3]
+    check(x, run(x, token, None, 32), token, None, 32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rows_of_their_own(dtype):
+    # several rows a CTA, idle ones and rows without mass between
+    rows, vocab = 5003, 517
+    x = logits(rows, vocab, dtype, seed=10)
+    x[40] = -float("inf")
+    token = np.arange(rows) % vocab
+    token[::7] = -1
+    t = np.where(np.arange(rows) % 5 == 0, 0.0, 0.7).astype(np.float32)
+    for top in (0, 3):
+        check(x, run(x, token, t, top), token, t, top)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows", [1, 70])
+def test_parts_with_many_large_logits(dtype, rows):
+    # 31 large logits in each of a row's parts, however it is cut, and no 32nd
+    # that a part's last place could rule them out by
+    vocab = 60 * 4096
+    x = logits(rows, vocab, dtype, seed=11, peaks=0)
+    live = rows // 2
+    at = torch.arange(60, device=DEV)[:, None] * 4096 + 64 * torch.arange(
+        31, device=DEV)
+    x[live, at.flatten()] = 100 + torch.randint(
+        0, 64, (at.numel(),), device=DEV).to(dtype) / 2
+    token = np.full(rows, -1)
+    token[live] = 64 * 7
+    check(x, run(x, token, None, 32), token, None, 32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [9, 90])
+def test_two_calls_at_once(rows):
+    x = [logits(rows, 120000, torch.bfloat16, seed=12 + k) for k in range(2)]
+    token = torch.arange(rows, dtype=torch.int32, device=DEV)
+    want = [sv.logprobs(v, token, top=9) for v in x]
+    streams = [torch.cuda.Stream() for _ in x]
+    torch.cuda.synchronize()
+    got = [[sv.logprobs(v, token, top=9, stream=s) for v, s in zip(x, streams)]
+           for _ in range(10)]
+    torch.cuda.synchronize()
+    for pair in got:
+        for a, b in zip(pair, want):
+            assert all(torch.equal(a[k], b[k]) for k in a)
+
+
+@pytest.mark.gpu
 def test_agrees_with_the_sampler():
     # the drawn token's log p is the log of the probability it was drawn with
     build.build()

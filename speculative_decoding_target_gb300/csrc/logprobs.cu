@@ -775,20 +775,22 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   const long long u0 = units * blockIdx.x / gridDim.x;
   const long long u1 = units * (blockIdx.x + 1) / gridDim.x;
   const int n0 = (int)(u0 / p.slices);  // first live row of the run
-  if (u0 < u1 && n0 >= upto - live && n0 < upto) {
+  const bool idle = total < p.rows;
+  if (idle && u0 < u1 && n0 >= upto - live && n0 < upto) {
     int row = r0;
     for (int n = upto - live;; ++row)
       if (row_of(p, row).live && n++ == n0) break;
     sh.first = row;
   }
-  // idle rows
-  for (int row = blockIdx.x; row < p.rows; row += gridDim.x)
-    if (!row_of(p, row).live) finish_idle(p, row);
-  __syncthreads();
+  if (idle) {
+    for (int row = blockIdx.x; row < p.rows; row += gridDim.x)
+      if (!row_of(p, row).live) finish_idle(p, row);
+    __syncthreads();
+  }
   if (u0 >= u1) return;
   Ring ring(ring_smem);
   // the part at slice u, and its copies started (there are live rows up to u1)
-  int row = sh.first - 1, q0, q1;
+  int row = (idle ? sh.first : n0) - 1, q0, q1;
   long long u = u0;
   Row r;
   auto seek = [&]() {
@@ -895,19 +897,19 @@ __global__ void __launch_bounds__(kThreads)
   tc_grid_dependency_wait();
   const int j = blockIdx.x, at = 2 * (j + tid) + (tid == 0);
   const int row = p.parts[2 * j + 1].row;
-  if (row < 0) return;  // uniform
-  const bool in_grid = j + tid < (int)gridDim.x;
   int mine = -1;
   float pm = -INFINITY, s = 0.f, h = 0.f;
-  if (in_grid) {
+  u64 last = 0;
+  if (j + tid < (int)gridDim.x) {
     mine = p.parts[at].row;
     pm = p.parts[at].m;
     s = p.parts[at].s;
     h = p.parts[at].h;
+    if (p.top) last = p.parts[at].top[p.top - 1];
   }
+  if (row < 0) return;  // uniform
   const Row r = row_of(p, row);
   const int top = top_of(p, r);
-  u64 last = in_grid && top ? p.parts[at].top[top - 1] : 0;
   const bool is = mine == row;
   if (!is) {
     pm = -INFINITY;

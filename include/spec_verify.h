@@ -489,20 +489,12 @@ typedef struct {
  *                0); below zero, NaN or infinite marks an idle row
  *   logprob, entropy   optional fp32 [rows]
  *   top_ids int32, top_logprobs fp32 [rows, top], contiguous; NULL with top 0
- *   workspace    >= spec_logprob_workspace_size(desc) bytes, 256-byte aligned;
- *                contents need no initialisation
- * 4-byte aligned (bf16 logits 2).  One or two launches; the result is the same on
- * every run.
+ * 4-byte aligned (bf16 logits 2).  One launch; the result is the same on every run.
  */
 int spec_logprobs(const spec_logprob_desc* desc, const void* logits,
                   const int32_t* token, const float* temperature,
                   float* logprob, float* entropy, int32_t* top_ids,
-                  float* top_logprobs, void* workspace, size_t workspace_bytes,
-                  void* stream);
-
-/* Workspace bytes for spec_logprobs: 0 where none is needed (spec_last_error() is
- * then empty, and the workspace may be NULL) and on a bad desc. */
-size_t spec_logprob_workspace_size(const spec_logprob_desc* desc);
+                  float* top_logprobs, void* stream);
 
 /* Walks of the DFlash2 candidate selector (spec_select_desc.mode). */
 #define SPEC_SELECT_GREEDY 0  /* best successor of the token already chosen */

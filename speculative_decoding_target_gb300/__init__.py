@@ -9,8 +9,7 @@ from ._native import (SpecError, accept_workspace_size, alloc_workspace,
                       chunk_attention, chunk_workspace_size,
                       desc_for, dflash2_select, dflash2_select_into, greedy_accept, greedy_accept_commit,
                       greedy_accept_commit_into, greedy_accept_into,
-                      kv_append, load, logprob_workspace_size,
-                      logprobs, make_desc, norm_rope_append,
+                      kv_append, load, logprobs, make_desc, norm_rope_append,
                       prepare_next_block,
                       prepare_next_block_into, rope_append, sample, set_wait_limit,
                       shared_workspace_size,
@@ -28,7 +27,7 @@ __all__ = [
     "dflash2_select", "dflash2_select_into",
     "greedy_accept", "greedy_accept_commit", "greedy_accept_commit_into",
     "greedy_accept_into", "kv_append", "load",
-    "logprob_workspace_size", "logprobs", "make_desc",
+    "logprobs", "make_desc",
     "norm_rope_append", "prepare_next_block", "prepare_next_block_into", "rope_append",
     "rope_frequencies", "sample", "set_wait_limit", "shared_workspace_size",
     "stochastic_accept",

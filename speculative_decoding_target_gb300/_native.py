@@ -44,7 +44,6 @@ EXPORTED = (
     "spec_verify_attention_shared", "spec_verify_shared_workspace_size",
     "spec_sample", "spec_norm_rope_append", "spec_chunk_attention",
     "spec_chunk_workspace_size", "spec_logprobs",
-    "spec_logprob_workspace_size",
 )
 SELECT_MODES = {"greedy": 0, "map": 1}
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
@@ -162,10 +161,7 @@ def load(path: str = LIB_PATH):
     lib.spec_chunk_attention.restype = ctypes.c_int
     lib.spec_sample.argtypes = [ctypes.POINTER(SampleDesc)] + [P] * 10
     lib.spec_sample.restype = ctypes.c_int
-    lib.spec_logprob_workspace_size.argtypes = [ctypes.POINTER(LogprobDesc)]
-    lib.spec_logprob_workspace_size.restype = sz
-    lib.spec_logprobs.argtypes = ([ctypes.POINTER(LogprobDesc)] + [P] * 8
-                                  + [sz, P])
+    lib.spec_logprobs.argtypes = [ctypes.POINTER(LogprobDesc)] + [P] * 8
     lib.spec_logprobs.restype = ctypes.c_int
     lib.spec_rope_append.argtypes = [P] * 16
     lib.spec_rope_append.restype = ctypes.c_int
@@ -824,16 +820,8 @@ def sample(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None,
     return token
 
 
-def logprob_workspace_size(desc: LogprobDesc) -> int:
-    """0: such a call needs none."""
-    n = load().spec_logprob_workspace_size(ctypes.byref(desc))
-    if n == 0 and load().spec_last_error():
-        raise SpecError(SPEC_ERR_ARG, load().spec_last_error().decode())
-    return int(n)
-
-
 def logprobs(logits, token=None, *, temperature=None, top: int = 0,
-             workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+             stream=None) -> dict:
     """Log probabilities of the given tokens (int32 [..], or None) under the
     rows of logits (fp32 or bf16 [.., vocab], rows contiguous, evenly spaced),
     with an optional per-row temperature (fp32 [..]).  Returns a dict of
@@ -848,12 +836,11 @@ def logprobs(logits, token=None, *, temperature=None, top: int = 0,
         _expect(token, torch.int32, "token", lead, True)
     if temperature is not None:
         _expect(temperature, torch.float32, "temperature", lead, True)
-    on = _on_current_device((logits, token, temperature, workspace), stream)
+    on = _on_current_device((logits, token, temperature), stream)
     rows = lead.numel()
     stride = _row_stride(logits, rows)
     desc = LogprobDesc(rows, vocab, int(logits.dtype == torch.bfloat16), top,
                        stride)
-    need = logprob_workspace_size(desc) if workspace is None else 0
     with _made_on(stream):
         new = lambda shape, dtype: torch.empty(shape, dtype=dtype,
                                                device=logits.device)
@@ -864,14 +851,10 @@ def logprobs(logits, token=None, *, temperature=None, top: int = 0,
         if top > 0:
             out["top_ids"] = new((*lead, top), torch.int32)
             out["top_logprobs"] = new((*lead, top), torch.float32)
-        if need:
-            workspace = alloc_workspace(need, logits.device)
     rc = load().spec_logprobs(
         ctypes.byref(desc), logits.data_ptr(), _at(token), _at(temperature),
         _at(out.get("logprob")), out["entropy"].data_ptr(),
-        _at(out.get("top_ids")), _at(out.get("top_logprobs")), _at(workspace),
-        0 if workspace is None else workspace.numel() * workspace.element_size(),
-        on)
+        _at(out.get("top_ids")), _at(out.get("top_logprobs")), on)
     if rc:
         _check(rc)
     return out

@@ -8,15 +8,21 @@
 // ascending).  4 or 2 bytes a token against about five instructions: HBM bounds
 // it as long as the sums keep up.
 //
-// As many CTAs as are resident share the rows.  With many rows each takes whole
-// ones, every grid'th.  Otherwise the rows that are not idle are laid end to end,
-// in slices of about kSlice tokens, and cut into equal runs: a CTA has the end of
-// one row, whole rows and the start of another, and a second kernel joins the
-// parts of rows that were cut.  (A cluster a row, instead: 1,024 bf16 rows of
-// 248,320 are 3.4 rounds of the GPU and took 4, and 8 CTAs a row cost more in
-// cluster launches than the rows; 64 rows 28 us with 8, 20.7 with 4.)
+// A CTA a row: 256 threads, four CTAs an SM, so that one row's reductions and
+// selection run under the others' loads, and the hardware deals the rows out.
+// (1,024 bf16 rows of 248,320 with top 20: 90.7 us, 5.6 TB/s; 512 threads 90.6, but
+// 6,000 rows of 33,000 then take 186 us instead of 112.  Resident CTAs that start on
+// their next row under the last one's selection: 103 and 223 us.  Equal runs of
+// slices that cut rows, joined by a second kernel: 112 us, and 256 rows 44 instead
+// of 27.  Such runs dealt out by a counter, shorter ones last: 121 to 150 us.)
 //
-// A thread takes every 512th 16-byte vector of its CTA's part of a row.  In
+// While that leaves SMs idle, a cluster a row, of a size that puts up to two CTAs on
+// an SM: 100 rows of 33,000 11.1 us with two CTAs a row, 12.2 with four; 64 fp32
+// rows of 248,320 17.8 with four and 20.1 with eight; 152 rows 31.5 with two and 35.2
+// with four, and 153, with one, 30.7.  (Sizes that are no power of two leave parts of
+// the GPU's groups of SMs empty: 100 rows 26 us with three, 20 with two.)
+//
+// A thread takes every 256th 16-byte vector of its CTA's part of a row.  In
 // base 2, with t = (x - ref) log2(e) / T:
 //   s = sum 2^t,  h = sum 2^t t
 // against a reference of the thread's own, its first batch's largest value; a
@@ -36,9 +42,9 @@
 // thread of rank r among them holds at most top - r of them.  Each of these
 // winners reads that one vector again (on its way while they are ranked) and hands
 // in what is not below the last winner's value.  A winner whose other vectors hold
-// such values too, as with many equals, is read by half a warp as a whole, and its
-// best top - r are taken out.  (Reading every winner's values, up to 485 a row:
-// 128 us for 1,024 bf16 rows with top 20, 89 without any.)
+// such values too, as with many equals, is read by a warp as a whole, and its best
+// top - r are taken out.  (1,024 bf16 rows: top 20 takes 11 us more than none;
+// reading all values of every winner took 38.)
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -50,16 +56,14 @@
 namespace specv {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCtasPerSm = 2;
+constexpr int kGroup = kThreads / 32;  // threads of a group of the bound
+constexpr int kCtasPerSm = 4;
 constexpr int kVecs = 4;          // 16-byte vectors of a batch
-constexpr int kSlice = 4096;      // tokens
-// rows per CTA from which on whole rows are dealt
-constexpr int kManyRows = 16;
-// rows that a cluster each takes
-constexpr int kFewRows = 64;
+constexpr int kSlice = 4096;      // tokens of a CTA of a cluster, at least
 constexpr int kMaxCluster = 16;
+constexpr int kClusterCtas = 2;   // of clusters on an SM, at most
 constexpr float kRebase = 8.f;    // log2
 constexpr float kLow = 160.f;     // log2
 constexpr float kLargeRef = 1048576.f;
@@ -165,8 +169,6 @@ struct Shared {
   int listed, found, deep;
   uint16_t deep_t[kTop], deep_r[kTop];
   u64 top[kTop];
-  // live rows
-  int scan[kWarps], live, first;
 };
 
 // A CTA's part of a row: vectors [begin, end) from the first 16-byte boundary
@@ -181,15 +183,15 @@ struct Part {
   int odds;          // odd tokens behind the last vector start here; -1: none here
   int odd;           // this thread's odd token, or -1
   int vocab;
-  __device__ Part(const T* x, int vocab, int q0, int q1, int slices)
+  __device__ Part(const T* x, int vocab, int rank, int size)
       : x(x), vocab(vocab) {
     constexpr int kN = Vec<T>::kN;
     const int off = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
     head = min((kN - off) % kN, vocab);
     const int nv = (vocab - head) / kN;
-    begin = (int)((long long)nv * q0 / slices);
-    end = (int)((long long)nv * q1 / slices);
-    odds = q0 ? -1 : head + nv * kN;
+    begin = (int)((long long)nv * rank / size);
+    end = (int)((long long)nv * (rank + 1) / size);
+    odds = rank ? -1 : head + nv * kN;
     odd = odd_of(threadIdx.x);
   }
   __device__ __forceinline__ int odd_of(int t) const {
@@ -494,16 +496,14 @@ __device__ void select(Shared& sh, const Part<T>& part, const Sums& a,
   }
   __syncthreads();
   const int deep = sh.deep;
-  // half a warp each
-  const int d = tid >> 4, sub = tid & 15;
-  if (d < deep) {  // (uniform in a half)
-    const unsigned half = lane & 16 ? 0xffff0000u : 0x0000ffffu;
+  // a warp each
+  for (int d = tid >> 5; d < deep; d += kWarps) {
     const int t = sh.deep_t[d], r = sh.deep_r[d];
-    // this lane's vectors of the thread, every 16th, a bit for each value that
+    // this lane's vectors of the thread, every 32nd, a bit for each value that
     // is a candidate
-    constexpr int kStride = 16 * kThreads;
-    const int v0 = part.begin + t + sub * kThreads;
-    static_assert(kLogprobMaxVocab / kThreads / 16 <= 64, "");
+    constexpr int kStride = 32 * kThreads;
+    const int v0 = part.begin + t + lane * kThreads;
+    static_assert(kLogprobMaxVocab / kThreads / 32 <= 64, "");
     u64 hit = 0;
     int bit = 0;
     for (int v = v0; v < part.end; v += 4 * kStride) {
@@ -528,11 +528,11 @@ __device__ void select(Shared& sh, const Part<T>& part, const Sums& a,
     }
     const int odd = part.odd_of(t);
     const float odd_x =
-        sub == 15 && odd >= 0 ? clean<T>(to_float(part.x[odd])) : -INFINITY;
+        lane == 31 && odd >= 0 ? clean<T>(to_float(part.x[odd])) : -INFINITY;
     const bool odd_hit = odd_x >= bound;
     int hits = __popcll(hit) + odd_hit;
 #pragma unroll
-    for (int o = 8; o; o >>= 1) hits += __shfl_xor_sync(half, hits, o);
+    for (int o = 16; o; o >>= 1) hits += __shfl_xor_sync(0xffffffffu, hits, o);
     // the key of the value at a bit
     auto key_at = [&](int b) {
       const int place = part.head + (v0 + b / kN * kStride) * kN + b % kN;
@@ -553,12 +553,12 @@ __device__ void select(Shared& sh, const Part<T>& part, const Sums& a,
           if (key < last && key > best) best = key;
         }
 #pragma unroll
-        for (int o = 8; o; o >>= 1) {
-          const u64 other = __shfl_xor_sync(half, best, o);
+        for (int o = 16; o; o >>= 1) {
+          const u64 other = __shfl_xor_sync(0xffffffffu, best, o);
           best = other > best ? other : best;
         }
         last = best;
-        if (sub == 0) sh.cands[atomicAdd(&sh.found, 1)] = best;
+        if (lane == 0) sh.cands[atomicAdd(&sh.found, 1)] = best;
       }
     }
   }
@@ -658,20 +658,18 @@ __device__ __forceinline__ void finish_idle(const LogprobParams& p, int row) {
 }
 
 // A part of a row: its largest logit, sums (in warp 0) and best tokens (sh.top).
-// `then` starts the next part's copies, which run under the selection.  Called by
-// the whole CTA.
-template <typename T, typename F>
+// Called by the whole CTA.
+template <typename T>
 __device__ __forceinline__ void work_on(Shared& sh, Ring& ring,
                                         const Part<T>& part, float c, int top,
-                                        F then, float& m, float& s, float& h) {
+                                        float& m, float& s, float& h) {
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Sums a = stream(part, ring, c);
-  then();
   float gm = a.max;
 #pragma unroll
-  for (int o = 8; o; o >>= 1)
+  for (int o = kGroup / 2; o; o >>= 1)
     gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, o));
-  if ((lane & 15) == 0) sh.max[threadIdx.x >> 4] = gm;
+  if (threadIdx.x % kGroup == 0) sh.max[threadIdx.x / kGroup] = gm;
   if (threadIdx.x == 0) sh.listed = sh.found = sh.deep = 0;
   if (threadIdx.x < kTop) sh.top[threadIdx.x] = 0;
   __syncthreads();
@@ -702,132 +700,21 @@ __device__ __forceinline__ const T* row_at(const LogprobParams& p, int row) {
   return static_cast<const T*>(p.logits) + row * p.row_stride;
 }
 
-// Whole rows, every grid'th.
+// A row a CTA.
 template <typename T>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     logprobs_rows_kernel(const LogprobParams p) {
   extern __shared__ __align__(16) uint8_t ring_smem[];
   __shared__ Shared sh;
-  tc_grid_launch_dependents();
+  const int row = blockIdx.x;
+  const Row r = row_of(p, row);
+  if (!r.live) return finish_idle(p, row);
   Ring ring(ring_smem);
-  // the next live row, and its copies started
-  int row = blockIdx.x;
-  Row r;
-  auto seek = [&]() {
-    for (; row < p.rows; row += gridDim.x) {
-      r = row_of(p, row);
-      if (r.live) {
-        ring.start(Part<T>(row_at<T>(p, row), p.vocab, 0, 1, 1));
-        return;
-      }
-      finish_idle(p, row);
-    }
-  };
-  seek();
-  while (row < p.rows) {
-    const int now = row;
-    const Row rn = r;
-    float m, s, h;
-    work_on(sh, ring, Part<T>(row_at<T>(p, now), p.vocab, 0, 1, 1), rn.c,
-            top_of(p, rn),
-            [&] {
-              row += gridDim.x;
-              seek();
-            },
-            m, s, h);
-    if (threadIdx.x < 32) finish<T>(p, now, rn, m, s, h, sh.top);
-    __syncthreads();  // before the next row's sums and lists
-  }
-}
-
-// The live rows' slices in equal runs.  part[0]: the CTA's part of a row that an
-// earlier CTA started; part[1]: of one that it starts and a later one ends.
-template <typename T>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
-    logprobs_runs_kernel(const LogprobParams p) {
-  extern __shared__ __align__(16) uint8_t ring_smem[];
-  __shared__ Shared sh;
-  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
-  // the merge may be scheduled; it waits for this grid
-  tc_grid_launch_dependents();
-  LogprobPart* mine = p.parts + 2 * blockIdx.x;
-  // consecutive rows a thread
-  const int per = (p.rows + kThreads - 1) / kThreads;
-  const int r0 = min(tid * per, p.rows), r1 = min(r0 + per, p.rows);
-  int live = 0;
-  for (int row = r0; row < r1; ++row) live += row_of(p, row).live;
-  int upto = live;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int n = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += n;
-  }
-  if (lane == 31) sh.scan[w] = upto;
-  if (tid < 2) mine[tid].row = -1;
-  __syncthreads();
-  int total = 0;
-#pragma unroll
-  for (int k = 0; k < kWarps; ++k) {
-    if (k < w) upto += sh.scan[k];
-    total += sh.scan[k];
-  }
-  const long long units = (long long)total * p.slices;
-  const long long u0 = units * blockIdx.x / gridDim.x;
-  const long long u1 = units * (blockIdx.x + 1) / gridDim.x;
-  const int n0 = (int)(u0 / p.slices);  // first live row of the run
-  const bool idle = total < p.rows;
-  if (idle && u0 < u1 && n0 >= upto - live && n0 < upto) {
-    int row = r0;
-    for (int n = upto - live;; ++row)
-      if (row_of(p, row).live && n++ == n0) break;
-    sh.first = row;
-  }
-  if (idle) {
-    for (int row = blockIdx.x; row < p.rows; row += gridDim.x)
-      if (!row_of(p, row).live) finish_idle(p, row);
-    __syncthreads();
-  }
-  if (u0 >= u1) return;
-  Ring ring(ring_smem);
-  // the part at slice u, and its copies started (there are live rows up to u1)
-  int row = (idle ? sh.first : n0) - 1, q0, q1;
-  long long u = u0;
-  Row r;
-  auto seek = [&]() {
-    if (u >= u1) return;
-    do {
-      r = row_of(p, ++row);
-    } while (!r.live);
-    const long long at = u / p.slices * p.slices;  // the row's first slice
-    q0 = (int)(u - at);
-    q1 = (int)min(u1 - at, (long long)p.slices);
-    u = at + q1;
-    ring.start(Part<T>(row_at<T>(p, row), p.vocab, q0, q1, p.slices));
-  };
-  seek();
-  for (bool more = true; more;) {
-    const int now = row, n0q = q0, n1q = q1;
-    const Row rn = r;
-    const int top = top_of(p, rn);
-    more = u < u1;
-    float m, s, h;
-    work_on(sh, ring, Part<T>(row_at<T>(p, now), p.vocab, n0q, n1q, p.slices),
-            rn.c, top, seek, m, s, h);
-    const bool ends = n1q == p.slices;
-    if (n0q == 0 && ends) {
-      if (w == 0) finish<T>(p, now, rn, m, s, h, sh.top);
-    } else if (w == 0) {
-      LogprobPart& to = mine[n0q ? 0 : 1];
-      if (lane == 0) {
-        to.row = now;
-        to.m = m;
-        to.s = s;
-        to.h = h;
-      }
-      if (lane < top) to.top[lane] = sh.top[lane];
-    }
-    __syncthreads();  // before the next row's sums and lists
-  }
+  const Part<T> part(row_at<T>(p, row), p.vocab, 0, 1);
+  ring.start(part);
+  float m, s, h;
+  work_on(sh, ring, part, r.c, top_of(p, r), m, s, h);
+  if (threadIdx.x < 32) finish<T>(p, row, r, m, s, h, sh.top);
 }
 
 // Keys that beat or equal `low`, of `n` (key(i), 0 for none), ranked: the best
@@ -883,80 +770,7 @@ __device__ __forceinline__ void join_tops(Shared& sh, int n, int top, u64 low,
   __syncthreads();
 }
 
-// CTA j joins the row that run j starts and does not end with the parts that the
-// runs behind it have of it: a thread for each.
-constexpr int kMaxRuns = kThreads;
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
-    logprobs_merge_kernel(const LogprobParams p) {
-  __shared__ Shared sh;
-  __shared__ uint16_t s_part[kMaxRuns];
-  __shared__ int s_parts;
-  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
-  if (tid == 0) s_parts = 0;
-  tc_grid_dependency_wait();
-  const int j = blockIdx.x, at = 2 * (j + tid) + (tid == 0);
-  const int row = p.parts[2 * j + 1].row;
-  int mine = -1;
-  float pm = -INFINITY, s = 0.f, h = 0.f;
-  u64 last = 0;
-  if (j + tid < (int)gridDim.x) {
-    mine = p.parts[at].row;
-    pm = p.parts[at].m;
-    s = p.parts[at].s;
-    h = p.parts[at].h;
-    if (p.top) last = p.parts[at].top[p.top - 1];
-  }
-  if (row < 0) return;  // uniform
-  const Row r = row_of(p, row);
-  const int top = top_of(p, r);
-  const bool is = mine == row;
-  if (!is) {
-    pm = -INFINITY;
-    last = 0;
-  }
-  // largest logit, and a bound: no part's last place is above the row's
-  float m = warp_max(pm);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const u64 other = __shfl_xor_sync(0xffffffffu, last, o);
-    last = other > last ? other : last;
-  }
-  if (lane == 0) {
-    sh.max[w] = m;
-    sh.list[w] = last;
-  }
-  __syncthreads();
-  m = warp_max(sh.max[lane & (kWarps - 1)]);
-  for (int k = 0; k < kWarps; ++k) last = sh.list[k] > last ? sh.list[k] : last;
-  if (pm > -INFINITY) {
-    const float d = fmaxf((pm - m) * r.c, -kLow), e = ex2(d);
-    s *= e;
-    h = fmaf(d, s, h * e);
-  } else {
-    s = h = 0.f;
-  }
-  warp_sum(s, h);
-  if (lane == 0) {
-    sh.s[w] = s;
-    sh.h[w] = h;
-  }
-  if (is) s_part[atomicAdd(&s_parts, 1)] = (uint16_t)at;  // in any order
-  __syncthreads();
-  if (top)
-    join_tops(sh, s_parts * top, top, last, [&](int i) {
-      const int k = i / top;
-      return p.parts[s_part[k]].top[i - k * top];
-    });
-  if (w == 0) {
-    s = lane < kWarps ? sh.s[lane] : 0.f;
-    h = lane < kWarps ? sh.h[lane] : 0.f;
-    warp_sum(s, h);
-    finish<T>(p, row, r, m, s, h, sh.top);
-  }
-}
-
-// Few rows: a cluster each, joined through distributed shared memory.
+// A cluster a row, joined through distributed shared memory.
 template <typename V>
 __device__ __forceinline__ void store_first(V* p, V v) {
   const uint32_t at = tc::map_to(tc::smem_u32(p), 0);
@@ -978,10 +792,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   extern __shared__ __align__(16) uint8_t ring_smem[];
   __shared__ Shared sh;
   __shared__ float c_max[kMaxCluster], c_s[kMaxCluster], c_h[kMaxCluster];
-  __shared__ u64 c_top[kMaxCluster * kTop];
+  u64* c_top = reinterpret_cast<u64*>(ring_smem + kRingBytes);  // [csize, top]
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   const int row = blockIdx.x / csize, rank = blockIdx.x - row * csize;
-  const Part<T> part(row_at<T>(p, row), p.vocab, rank, rank + 1, csize);
+  const Part<T> part(row_at<T>(p, row), p.vocab, rank, csize);
   Ring ring(ring_smem);
   const Row r = row_of(p, row);
   if (!r.live) {  // the whole cluster
@@ -992,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   cluster_arrive();  // started
   const int top = top_of(p, r);
   float m, s, h;
-  work_on(sh, ring, part, r.c, top, [] {}, m, s, h);
+  work_on(sh, ring, part, r.c, top, m, s, h);
   cluster_wait();  // every CTA has started
   if (tid == 0) {
     store_first(&c_max[rank], m);
@@ -1026,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 }
 
 template <typename T>
-cudaError_t launch(const LogprobParams& p, int runs, int csize, cudaStream_t s) {
+cudaError_t launch(const LogprobParams& p, int csize, cudaStream_t s) {
   // once per device (an attribute call per launch costs microseconds)
   static std::atomic<uint64_t> ready{0};
   int dev;
@@ -1037,69 +851,42 @@ cudaError_t launch(const LogprobParams& p, int runs, int csize, cudaStream_t s) 
     const auto smem = cudaFuncAttributeMaxDynamicSharedMemorySize;
     e = cudaFuncSetAttribute(logprobs_rows_kernel<T>, smem, kRingBytes);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(logprobs_runs_kernel<T>, smem, kRingBytes);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(logprobs_cluster_kernel<T>, smem, kRingBytes);
+      e = cudaFuncSetAttribute(logprobs_cluster_kernel<T>, smem,
+                               kRingBytes + kMaxCluster * kTop * (int)sizeof(u64));
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(logprobs_cluster_kernel<T>,
                                cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
-  cudaLaunchAttribute attr[1];
-  if (csize) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.rows * csize);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kRingBytes;
-    cfg.stream = s;
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = csize;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, logprobs_cluster_kernel<T>, p, csize);
-  }
-  if (!p.slices) {
-    logprobs_rows_kernel<T><<<runs, kThreads, kRingBytes, s>>>(p);
+  if (csize == 1) {
+    logprobs_rows_kernel<T><<<p.rows, kThreads, kRingBytes, s>>>(p);
     return cudaGetLastError();
   }
-  logprobs_runs_kernel<T><<<runs, kThreads, kRingBytes, s>>>(p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  const cudaLaunchConfig_t cfg =
-      pdl_config(dim3(runs), dim3(kThreads), 0, s, attr);
-  return cudaLaunchKernelEx(&cfg, logprobs_merge_kernel<T>, p);
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.rows * csize));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kRingBytes + csize * max(p.top, 1) * sizeof(u64);
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = csize;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, logprobs_cluster_kernel<T>, p, csize);
 }
 
 }  // namespace
 
-int logprob_runs(int sms) {
-  return sms * kCtasPerSm < kMaxRuns ? sms * kCtasPerSm : kMaxRuns;
-}
-
-bool logprob_in_runs(int rows, int sms) {
-  return rows > kFewRows && rows < kManyRows * logprob_runs(sms);
-}
-
-cudaError_t launch_logprobs(LogprobParams p, bool bf16, int sms,
+cudaError_t launch_logprobs(const LogprobParams& p, bool bf16, int sms,
                             cudaStream_t s) {
-  int runs = logprob_runs(sms);
-  int csize = 0;
-  p.slices = 0;
-  if (p.rows <= kFewRows) {
-    csize = 1;
-    while (csize < kMaxCluster && 2 * csize * p.rows <= runs &&
-           2 * csize * kSlice <= p.vocab)
-      csize *= 2;
-  } else if (logprob_in_runs(p.rows, sms)) {
-    // no run shorter than a slice
-    p.slices = max(1, p.vocab / kSlice);
-    runs = (int)min((long long)runs, (long long)p.rows * p.slices);
-  }
-  return bf16 ? launch<__nv_bfloat16>(p, runs, csize, s)
-              : launch<float>(p, runs, csize, s);
+  int csize = 1;
+  while (csize < kMaxCluster && 2ll * csize * p.rows <= kClusterCtas * sms &&
+         2 * csize * kSlice <= p.vocab)
+    csize *= 2;
+  return bf16 ? launch<__nv_bfloat16>(p, csize, s) : launch<float>(p, csize, s);
 }
 
 }  // namespace specv

@@ -1197,26 +1197,12 @@ int check_logprobs(const spec_logprob_desc* d) {
                 specv::kLogprobMaxTop);
   return SPEC_OK;
 }
-// (only calls that cut rows into parts of runs need any)
-size_t logprob_bytes(const spec_logprob_desc* d, int sms) {
-  return specv::logprob_in_runs(d->rows, sms)
-             ? 2 * (size_t)specv::logprob_runs(sms) * sizeof(specv::LogprobPart)
-             : 0;
-}
 }  // namespace
-
-size_t spec_logprob_workspace_size(const spec_logprob_desc* desc) {
-  g_err[0] = 0;
-  int sms;
-  if (check_logprobs(desc) || sm_count(&sms)) return 0;
-  return logprob_bytes(desc, sms);
-}
 
 int spec_logprobs(const spec_logprob_desc* desc, const void* logits,
                   const int32_t* token, const float* temperature,
                   float* logprob, float* entropy, int32_t* top_ids,
-                  float* top_logprobs, void* workspace, size_t workspace_bytes,
-                  void* stream) {
+                  float* top_logprobs, void* stream) {
   g_err[0] = 0;
   const spec_logprob_desc* d = desc;
   int rc = check_logprobs(d);
@@ -1239,11 +1225,6 @@ int spec_logprobs(const spec_logprob_desc* desc, const void* logits,
   int sms;
   rc = sm_count(&sms);
   if (rc) return rc;
-  const size_t need = logprob_bytes(d, sms);
-  if (need) {
-    rc = check_workspace(workspace, workspace_bytes, need);
-    if (rc) return rc;
-  }
   specv::LogprobParams p;
   std::memset(&p, 0, sizeof p);
   p.logits = logits;
@@ -1257,7 +1238,6 @@ int spec_logprobs(const spec_logprob_desc* desc, const void* logits,
   p.rows = d->rows;
   p.vocab = d->vocab;
   p.top = d->top;
-  p.parts = static_cast<specv::LogprobPart*>(workspace);
   cudaError_t e =
       specv::launch_logprobs(p, bf16, sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess)

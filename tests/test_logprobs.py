@@ -5,7 +5,7 @@ Tolerances.  With z = (x - max) / T, E the mean of |z| under p: the factor
 log2(e) / T is off by 2^-24 and its constant by 2^-25, t by two more roundings:
 3.5 2^-24 of z in every weight: 2.1e-7 E; a token's own z by two, 2^-23 |z|.  A
 weight is off by ex2's 2^-22.  A sum passes at most 16 + 2 additions in its
-batch, 32 batches, each perhaps with a change of the reference (two roundings
+batch, at most 32 batches in these calls, each perhaps with a change of the reference (two roundings
 and an ex2), and 5 + 5 + 4 inside the warp, the CTA and the cluster, where the
 reference changes twice more: below 48 2^-24 + 34 (2^-23 + 2^-22) < 1.5e-5 of S.
 ln S is off by 2^-22 of itself, at most 3.2e-6 more with S < 2^19.  So log p is
@@ -337,8 +337,7 @@ FAKE = ctypes.c_void_p(0x100000)   # never dereferenced: checks come first
 def _raw(lib, **kw):
     d = _native.LogprobDesc(4, 1000, 0, 5, 1000)
     ptr = dict(logits=FAKE, token=FAKE, temperature=None, logprob=FAKE,
-               entropy=FAKE, top_ids=FAKE, top_logprobs=FAKE, ws=None,
-               ws_bytes=0)
+               entropy=FAKE, top_ids=FAKE, top_logprobs=FAKE)
     for name, val in kw.items():
         if name in ptr:
             ptr[name] = val

@@ -877,6 +877,9 @@ __device__ void write_out(const Ctx& cx, const Piece& pc, uint32_t tmem, float l
   const int R = pc.row0 + w4 * 32 + lane;
   const bool valid = w4 * 32 + lane < cx.cta_rows && R < pc.rows_total;
   const int tok = R / p.group;
+  // out is 16-byte aligned; with stores of 32 bytes 4,096 tokens into an empty cache
+  // take 155 us, with 16 bytes 160
+  const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
   __nv_bfloat16* dst =
       p.out + (((long long)pc.lead * p.q_len + pc.first + tok) * p.hq +
                pc.g * p.group + (R - tok * p.group)) * kHeadDim;
@@ -892,12 +895,17 @@ __device__ void write_out(const Ctx& cx, const Piece& pc, uint32_t tmem, float l
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           v[e] = bf16_pair(o[k + 2 * e], o[k + 2 * e + 1], inv);
-        asm volatile(
-            "st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(
-                dst + cb * 64 + k),
-            "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]),
-            "r"(v[6]), "r"(v[7])
-            : "memory");
+        __nv_bfloat16* to = dst + cb * 64 + k;
+        if (wide) {
+          asm volatile(
+              "st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to),
+              "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]),
+              "r"(v[6]), "r"(v[7])
+              : "memory");
+        } else {
+          reinterpret_cast<uint4*>(to)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+          reinterpret_cast<uint4*>(to)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+        }
       }
     }
   }

@@ -470,7 +470,8 @@ bool chunk_is_block(const spec_attn_desc* d) {
 int check_chunk(const spec_attn_desc* d) {
   int rc = check_desc(d, INT_MAX);
   if (rc) return rc;
-  if ((long long)d->batch * d->q_len * d->num_q_heads >= (1LL << 31))
+  const long long tokens = (long long)d->batch * d->q_len;
+  if (tokens >= (1LL << 31) || tokens * d->num_q_heads >= (1LL << 31))
     return fail(SPEC_ERR_ARG, "batch * q_len * num_q_heads must be < 2^31");
   if (!chunk_is_block(d) && !use_tc(d))
     return fail(SPEC_ERR_UNSUPPORTED, "chunks need page_size >= %d",

@@ -279,6 +279,28 @@ def test_streams_graphs_and_repeats(kv):
     c.check(outs[0])
 
 
+def shifted(t):
+    """The same tensor 16 bytes behind a 512-byte border."""
+    if t is None:
+        return None
+    n = 16 // t.element_size()
+    buf = torch.empty(t.numel() + n, dtype=t.dtype, device=t.device)
+    buf[n:].copy_(t.reshape(-1))
+    return buf[n:].view(t.shape)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_addresses_of_16_bytes(kv):
+    c = Case([70, 300], [500, 64], kv=kv, seed=11)
+    want = c.run()
+    c.q, c.k, c.v = shifted(c.q), shifted(c.k), shifted(c.v)
+    c.ks, c.vs = shifted(c.ks), shifted(c.vs)
+    out = shifted(torch.full_like(c.q, 7))
+    assert out.data_ptr() % 32 == 16
+    assert torch.equal(c.run(out=out), want)
+
+
 @pytest.mark.gpu
 def test_status_of_bad_pages():
     c = Case([60, 40], [500, 100], seed=6)
@@ -341,6 +363,8 @@ def _raw(lib, **kw):
     (dict(batch=1025), _native.SPEC_ERR_ARG),
     (dict(q_len=0), _native.SPEC_ERR_ARG),
     (dict(q_len=1 << 27), _native.SPEC_ERR_ARG),
+    (dict(batch=4, q_len=2 ** 31 - 1, num_q_heads=2 ** 31 - 1,
+          num_kv_heads=1), _native.SPEC_ERR_ARG),   # 2^64 and more
     (dict(num_kv_heads=5), _native.SPEC_ERR_ARG),
     (dict(head_dim=128), _native.SPEC_ERR_UNSUPPORTED),
     (dict(page_size=24), _native.SPEC_ERR_ARG),

@@ -163,6 +163,51 @@ def test_many_tokens_and_other_head_counts():
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("hq,hkv", [(64, 8), (96, 1), (6, 21)])
+def test_more_heads_than_a_round_of_warps(kv, hq, hkv):
+    build.build()
+    freq, m = sv.rope_frequencies(128)
+    w = weights(9, torch.float32, 0.0)
+    c = make_case(kv, 16, [5, 33, 0], [40, 33, 9], 33, hq=hq, hkv=hkv, seed=8)
+    for inter in (False, True):
+        check(c, call(c, w, freq, inter, m), w, freq.numpy(), inter, m)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_addresses_of_16_bytes_and_two_calls_at_once(kv):
+    def shifted(t):
+        if t is None:
+            return None
+        n = 16 // t.element_size()
+        buf = torch.empty(t.numel() + n, dtype=t.dtype, device=t.device)
+        buf[n:].copy_(t.reshape(-1))
+        return buf[n:].view(t.shape)
+    build.build()
+    freq, m = sv.rope_frequencies(64)
+    w = weights(10, torch.bfloat16, 0.0)
+    cases = [make_case(kv, 16, None, [100, 70], 50, seed=20 + k)
+             for k in range(2)]
+    for c in cases:
+        for x in ("q", "k", "v", "kp", "vp", "ks", "vs"):
+            c[x] = shifted(c[x])
+        c["out"] = shifted(torch.zeros_like(c["q"]))
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for c, s in zip(cases, streams):
+            call(c, w, freq, False, m, q_out=c["out"], stream=s,
+                 positions=None, cache_loc=None)
+    torch.cuda.synchronize()
+    for c in cases:
+        n = c["kp"].clone()
+        check(c, call(c, w, freq, False, m, q_out=c["out"]), w, freq.numpy(),
+              False, m)
+        assert torch.equal(n.view(torch.uint8), c["kp"].view(torch.uint8))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
 def test_small_large_and_zero_heads(kv):
     # rows whose size eps decides, rows of 2^40, rows of zeros; a block longer
     # than its cache, a table that ends inside the block

@@ -771,8 +771,14 @@ def _row_stride(logits: torch.Tensor, rows: int) -> int:
     elif rows == 1 and (vocab == 1 or logits.stride(-1) == 1):
         stride = vocab
     else:
-        raise SpecError(SPEC_ERR_ARG, "logits rows must be contiguous and "
-                                      "evenly spaced")
+        try:                    # [.., vocab] of a padded vocabulary
+            flat = logits.view(rows, vocab)
+        except RuntimeError:
+            flat = None
+        if flat is None or (vocab > 1 and flat.stride(1) != 1):
+            raise SpecError(SPEC_ERR_ARG, "logits rows must be contiguous and "
+                                          "evenly spaced")
+        stride = flat.stride(0)
     if rows > 1 and stride < vocab:
         raise SpecError(SPEC_ERR_ARG, "logits rows overlap")
     return stride

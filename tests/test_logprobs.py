@@ -381,6 +381,19 @@ def test_no_rows_is_a_noop():
     assert _raw(_native.load(), rows=0, logits=None) == _native.SPEC_OK
 
 
+def test_row_strides():
+    stride = lambda x: _native._row_stride(x, x.shape[:-1].numel())
+    x = torch.zeros((4, 6, 100))
+    assert stride(x) == stride(x[0]) == 100
+    assert stride(x[..., :90]) == stride(x[0, :, 5:95]) == 100
+    assert stride(x[:, ::2, :90]) == 200 and stride(x[:, 3]) == 600
+    assert stride(x[2:3, 3:4, 7:]) == 93
+    for bad in (x[:, :4, :90], x[..., ::2], x.transpose(1, 2),
+                x[0, :1].expand(3, 100), x[:, :1, :].expand(4, 2, 100)):
+        with pytest.raises(sv.SpecError):
+            stride(bad)
+
+
 def test_binding_refuses_wrong_tensors():
     x = torch.zeros((4, 100))
     tok = torch.zeros(4, dtype=torch.int32)

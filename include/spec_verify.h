@@ -795,7 +795,7 @@ int spec_rope_append(const spec_rope_desc* desc, const void* q,
 /*
  * Norms of query and key heads.
  *   weight_dtype   SPEC_WEIGHTS_*
- *   eps            finite, > 0
+ *   eps            a normal number > 0 (below 2^-126 zeros would have no root)
  *   weight_offset  finite; 0 for weights kept as they multiply, 1 for weights
  *                  kept as their distance from one
  *   q_weight       [256], one for all query heads, 4-byte aligned device

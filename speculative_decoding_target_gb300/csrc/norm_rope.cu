@@ -173,99 +173,99 @@ __global__ void __launch_bounds__(Shape<kFp8>::kThreads,
   // With more pairs than the warps hold, the tokens are walked once for each
   // round of them: what a pair is, is worked out once a round.
   for (int round = 0; round < n_pairs; round += kWarps * kPairs) {
-  int kind[kPairs], r[kPairs];
-  bool there[kPairs];
-  uint32_t src_at[kPairs];
-#pragma unroll
-  for (int e = 0; e < kPairs; ++e) {
-    int pr = round + w + e * kWarps;
-    // FP8: keys and values go to the last warps of the first round, which have no
-    // second pair when the warps hold all in two
-    if (kFp8 && n_kv <= kWarps && n_pairs >= kWarps && pr < n_pairs)
-      pr = pr < kWarps - n_kv ? pr
-           : pr < kWarps      ? pr - kWarps + n_kv + q_pairs
-                              : pr - n_kv;
-    // 0 queries, 1 keys, 2 values, 3 none
-    kind[e] = pr < q_pairs ? 0 : pr < q_pairs + kv_pairs ? 1 : pr < n_pairs ? 2 : 3;
-    r[e] = 2 * (pr - (kind[e] == 0   ? 0
-                      : kind[e] == 1 ? q_pairs
-                                     : q_pairs + kv_pairs)) + sub;
-    there[e] = kind[e] < 3 && r[e] < (kind[e] == 0 ? p.hq : a.hkv);
-    src_at[e] = r[e] * kHeadDim + (kind[e] == 2 ? 16 * l : ca);
-  }
-  int b = blockIdx.x / q_len;
-  uint32_t i = blockIdx.x - b * q_len;
-  for (uint32_t tok = blockIdx.x; tok < tokens; tok += gridDim.x, buf ^= 1) {
-    const int width = a.q_lens ? min(max(a.q_lens[b], 0), a.q_len) : a.q_len;
-    const long long t = (long long)a.seq_lens[b] - width + i;
-    const bool live = (int)i < width && t >= 0;
-    long long slot = -1;  // row of KV head 0 in the pool
-    if (live && t < a.max_tokens) {
-      const int page =
-          a.page_table[(long long)b * a.max_pages + (t >> a.log2_ps)];
-      const int at = (int)(t & (a.page_size - 1));
-      if (page >= 0 && page < a.num_pages) {
-        slot = (long long)page * a.hkv * a.page_size + at;
-        if (tid == 0 && round == 0 && a.cache_loc)
-          a.cache_loc[tok] = (long long)page * a.page_size + at;
-      } else if (a.status && tid == 0) {
-        atomicOr(a.status, SPEC_STATUS_BAD_PAGE);
-      }
-    }
-    if (tid == 0 && round == 0) {
-      if (a.positions) a.positions[tok] = live ? (int32_t)t : -1;
-      if (a.cache_loc && slot < 0) a.cache_loc[tok] = -1;
-    }
-    const __nv_bfloat16* q_src = p.q + b * p.q_req + i * p.q_tok;
-    const __nv_bfloat16* k_src = a.k_new + b * p.k_req + i * p.k_tok;
-    const __nv_bfloat16* v_src = a.v_new + b * p.v_req + i * p.v_tok;
-    __nv_bfloat16* q_dst = p.q_out + (long long)tok * p.hq * kHeadDim;
-    if (live && tid < half) {
-      const uint64_t frac = (uint64_t)t * turn;
-      float sn, cs;
-      sincospif((float)(int32_t)(frac >> 32) * 4.656612873077393e-10f, &sn, &cs);
-      s_cos[buf][tid] = cs * p.factor;
-      s_sin[buf][tid] = sn * p.factor;
-    }
-    u64 c_a[4], s_a[4], c_b[4], s_b[4];
-    uint4 xa[kPairs], xb[kPairs];
+    int kind[kPairs], r[kPairs];
+    bool there[kPairs];
+    uint32_t src_at[kPairs];
 #pragma unroll
     for (int e = 0; e < kPairs; ++e) {
-      xa[e] = xb[e] = make_uint4(0u, 0u, 0u, 0u);
-      if (!there[e] || !live) continue;
-      const __nv_bfloat16* src =
-          (kind[e] == 0 ? q_src : kind[e] == 1 ? k_src : v_src) + src_at[e];
-      xa[e] = __ldcs(reinterpret_cast<const uint4*>(src));
-      xb[e] = __ldcs(
-          reinterpret_cast<const uint4*>(src + (kind[e] == 2 ? 8 : cb - ca)));
+      int pr = round + w + e * kWarps;
+      // FP8: keys and values go to the last warps of the first round, which have no
+      // second pair when the warps hold all in two
+      if (kFp8 && n_kv <= kWarps && n_pairs >= kWarps && pr < n_pairs)
+        pr = pr < kWarps - n_kv ? pr
+             : pr < kWarps      ? pr - kWarps + n_kv + q_pairs
+                                : pr - n_kv;
+      // 0 queries, 1 keys, 2 values, 3 none
+      kind[e] = pr < q_pairs ? 0 : pr < q_pairs + kv_pairs ? 1 : pr < n_pairs ? 2 : 3;
+      r[e] = 2 * (pr - (kind[e] == 0   ? 0
+                        : kind[e] == 1 ? q_pairs
+                                       : q_pairs + kv_pairs)) + sub;
+      there[e] = kind[e] < 3 && r[e] < (kind[e] == 0 ? p.hq : a.hkv);
+      src_at[e] = r[e] * kHeadDim + (kind[e] == 2 ? 16 * l : ca);
     }
-    __syncthreads();  // (the loads are on their way)
-        load8(&s_cos[buf][kInterleaved ? 0 : (rot_a ? pa : 0)], c_a);
-        load8(&s_sin[buf][kInterleaved ? 0 : (rot_a ? pa : 0)], s_a);
-        if (kInterleaved) {
-          // a pair of channels is one packed pair: cosine twice, sine with signs
-          const float4 ka = *reinterpret_cast<const float4*>(&s_cos[buf][pa]);
-          const float4 za = *reinterpret_cast<const float4*>(&s_sin[buf][pa]);
-          const float4 kb = *reinterpret_cast<const float4*>(&s_cos[buf][pb]);
-          const float4 zb = *reinterpret_cast<const float4*>(&s_sin[buf][pb]);
-          const float ca4[4] = {ka.x, ka.y, ka.z, ka.w};
-          const float sa4[4] = {za.x, za.y, za.z, za.w};
-          const float cb4[4] = {kb.x, kb.y, kb.z, kb.w};
-          const float sb4[4] = {zb.x, zb.y, zb.z, zb.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            c_a[k] = rot_a ? pack2(ca4[k], ca4[k]) : pack2(1.f, 1.f);
-            s_a[k] = rot_a ? pack2(-sa4[k], sa4[k]) : 0ull;
-            c_b[k] = rot_b ? pack2(cb4[k], cb4[k]) : pack2(1.f, 1.f);
-            s_b[k] = rot_b ? pack2(-sb4[k], sb4[k]) : 0ull;
-          }
-        } else if (!rot_a) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            c_a[k] = pack2(1.f, 1.f);
-            s_a[k] = 0ull;
-          }
+    int b = blockIdx.x / q_len;
+    uint32_t i = blockIdx.x - b * q_len;
+    for (uint32_t tok = blockIdx.x; tok < tokens; tok += gridDim.x, buf ^= 1) {
+      const int width = a.q_lens ? min(max(a.q_lens[b], 0), a.q_len) : a.q_len;
+      const long long t = (long long)a.seq_lens[b] - width + i;
+      const bool live = (int)i < width && t >= 0;
+      long long slot = -1;  // row of KV head 0 in the pool
+      if (live && t < a.max_tokens) {
+        const int page =
+            a.page_table[(long long)b * a.max_pages + (t >> a.log2_ps)];
+        const int at = (int)(t & (a.page_size - 1));
+        if (page >= 0 && page < a.num_pages) {
+          slot = (long long)page * a.hkv * a.page_size + at;
+          if (tid == 0 && round == 0 && a.cache_loc)
+            a.cache_loc[tok] = (long long)page * a.page_size + at;
+        } else if (a.status && tid == 0) {
+          atomicOr(a.status, SPEC_STATUS_BAD_PAGE);
         }
+      }
+      if (tid == 0 && round == 0) {
+        if (a.positions) a.positions[tok] = live ? (int32_t)t : -1;
+        if (a.cache_loc && slot < 0) a.cache_loc[tok] = -1;
+      }
+      const __nv_bfloat16* q_src = p.q + b * p.q_req + i * p.q_tok;
+      const __nv_bfloat16* k_src = a.k_new + b * p.k_req + i * p.k_tok;
+      const __nv_bfloat16* v_src = a.v_new + b * p.v_req + i * p.v_tok;
+      __nv_bfloat16* q_dst = p.q_out + (long long)tok * p.hq * kHeadDim;
+      if (live && tid < half) {
+        const uint64_t frac = (uint64_t)t * turn;
+        float sn, cs;
+        sincospif((float)(int32_t)(frac >> 32) * 4.656612873077393e-10f, &sn, &cs);
+        s_cos[buf][tid] = cs * p.factor;
+        s_sin[buf][tid] = sn * p.factor;
+      }
+      u64 c_a[4], s_a[4], c_b[4], s_b[4];
+      uint4 xa[kPairs], xb[kPairs];
+#pragma unroll
+      for (int e = 0; e < kPairs; ++e) {
+        xa[e] = xb[e] = make_uint4(0u, 0u, 0u, 0u);
+        if (!there[e] || !live) continue;
+        const __nv_bfloat16* src =
+            (kind[e] == 0 ? q_src : kind[e] == 1 ? k_src : v_src) + src_at[e];
+        xa[e] = __ldcs(reinterpret_cast<const uint4*>(src));
+        xb[e] = __ldcs(
+            reinterpret_cast<const uint4*>(src + (kind[e] == 2 ? 8 : cb - ca)));
+      }
+      __syncthreads();  // (the loads are on their way)
+      load8(&s_cos[buf][kInterleaved ? 0 : (rot_a ? pa : 0)], c_a);
+      load8(&s_sin[buf][kInterleaved ? 0 : (rot_a ? pa : 0)], s_a);
+      if (kInterleaved) {
+        // a pair of channels is one packed pair: cosine twice, sine with signs
+        const float4 ka = *reinterpret_cast<const float4*>(&s_cos[buf][pa]);
+        const float4 za = *reinterpret_cast<const float4*>(&s_sin[buf][pa]);
+        const float4 kb = *reinterpret_cast<const float4*>(&s_cos[buf][pb]);
+        const float4 zb = *reinterpret_cast<const float4*>(&s_sin[buf][pb]);
+        const float ca4[4] = {ka.x, ka.y, ka.z, ka.w};
+        const float sa4[4] = {za.x, za.y, za.z, za.w};
+        const float cb4[4] = {kb.x, kb.y, kb.z, kb.w};
+        const float sb4[4] = {zb.x, zb.y, zb.z, zb.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          c_a[k] = rot_a ? pack2(ca4[k], ca4[k]) : pack2(1.f, 1.f);
+          s_a[k] = rot_a ? pack2(-sa4[k], sa4[k]) : 0ull;
+          c_b[k] = rot_b ? pack2(cb4[k], cb4[k]) : pack2(1.f, 1.f);
+          s_b[k] = rot_b ? pack2(-sb4[k], sb4[k]) : 0ull;
+        }
+      } else if (!rot_a) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          c_a[k] = pack2(1.f, 1.f);
+          s_a[k] = 0ull;
+        }
+      }
 #pragma unroll
       for (int e = 0; e < kPairs; ++e) {
         const bool is_q = kind[e] == 0, is_v = kind[e] == 2;
@@ -358,13 +358,13 @@ __global__ void __launch_bounds__(Shape<kFp8>::kThreads,
         *reinterpret_cast<uint4*>(dst + (is_v ? 16 * l : ca)) = xa[e];
         *reinterpret_cast<uint4*>(dst + (is_v ? 16 * l + 8 : cb)) = xb[e];
       }
-    b += step_b;
-    i += step_i;
-    if (i >= q_len) {
-      i -= q_len;
-      ++b;
+      b += step_b;
+      i += step_i;
+      if (i >= q_len) {
+        i -= q_len;
+        ++b;
+      }
     }
-  }
   }
 }
 

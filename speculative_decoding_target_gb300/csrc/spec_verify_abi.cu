@@ -857,8 +857,9 @@ int rope_append(const spec_rope_desc* d, const spec_norm_desc* norm,
     if (norm->weight_dtype != SPEC_WEIGHTS_FP32 &&
         norm->weight_dtype != SPEC_WEIGHTS_BF16)
       return fail(SPEC_ERR_ARG, "weight_dtype %d", norm->weight_dtype);
-    if (!(norm->eps > 0.f && norm->eps < 3.0e38f))
-      return fail(SPEC_ERR_ARG, "eps must be finite and > 0");
+    // (the root's argument is flushed to zero below the normal numbers)
+    if (!(norm->eps >= 1.17549435e-38f && norm->eps < 3.0e38f))
+      return fail(SPEC_ERR_ARG, "eps must be a normal number > 0");
     if (!(norm->weight_offset > -3.0e38f && norm->weight_offset < 3.0e38f))
       return fail(SPEC_ERR_ARG, "weight_offset must be finite");
   }

@@ -291,6 +291,7 @@ def _raw(lib, norm=True, **kw):
     (dict(norm=False), _native.SPEC_ERR_ARG),
     (dict(weight_dtype=2), _native.SPEC_ERR_ARG),
     (dict(eps=0.0), _native.SPEC_ERR_ARG),
+    (dict(eps=1e-40), _native.SPEC_ERR_ARG),
     (dict(eps=float("nan")), _native.SPEC_ERR_ARG),
     (dict(eps=float("inf")), _native.SPEC_ERR_ARG),
     (dict(weight_offset=float("inf")), _native.SPEC_ERR_ARG),

@@ -678,6 +678,9 @@ __device__ __forceinline__ void write_q(const Ctx& cx, const Piece& pc,
 template <bool kFp8>
 __device__ __forceinline__ void copy_q(const Ctx& cx, const Piece& pc,
                                        uint8_t* smem) {
+  // Without a give-up the last piece's queries have landed; with one they may be
+  // under way still, and the barrier is not armed over them.
+  if (*cx.abort) return;
   const AttnParams& p = *cx.a;
   const uint32_t bytes = 4 * cx.cta_rows * 128;
   uint32_t bar;

@@ -315,6 +315,26 @@ def test_status_of_bad_pages():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("page,hq,hkv", [(16, 24, 4), (64, 48, 1)])
+def test_waits_that_run_out_are_reported(kv, page, hq, hkv):
+    # several pieces a pair; queries by tensor copies and by threads
+    c = Case([2500, 70], [1000, 5000], page=page, kv=kv, hq=hq, hkv=hkv,
+             seed=12)
+    ws = sv.alloc_workspace(256 << 20, DEV)
+    sv.set_wait_limit(200)      # SM clock cycles: the first waits run out
+    try:
+        c.run(checked=True, workspace=ws)
+        torch.cuda.synchronize()
+    finally:
+        sv.set_wait_limit(0)
+    assert sv.verify_status(ws) & _native.SPEC_STATUS_TIMEOUT
+    out = c.run(checked=True, workspace=ws)
+    assert sv.verify_status(ws) == 0
+    c.check(out, rows=8)
+
+
+@pytest.mark.gpu
 def test_pool_of_more_than_2_31_elements():
     page, pages = 64, 140000
     c = Case([40], [1000], page=page, hq=6, hkv=1, seed=9)

@@ -749,6 +749,25 @@ __device__ __forceinline__ void zero_tail(const Ctx& cx, const Piece& pc,
   tc::fence_proxy_async_smem();
 }
 
+// Two fused steps, and two additions, in one instruction.
+__device__ __forceinline__ float2 fma_pair(float x0, float x1, float a, float b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, m, n;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 m, {%4, %4};\n\tmov.b64 n, {%5, %5};\n\t"
+      "fma.rn.ftz.f32x2 x, x, m, n;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x0), "f"(x1), "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void add_pair(float& s0, float& s1, float x0,
+                                         float x1) {
+  asm("{\n\t.reg .b64 s, x;\n\t"
+      "mov.b64 s, {%0, %1};\n\tmov.b64 x, {%2, %3};\n\t"
+      "add.rn.ftz.f32x2 s, s, x;\n\tmov.b64 {%0, %1}, s;\n\t}"
+      : "+f"(s0), "+f"(s1)
+      : "f"(x0), "f"(x1));
+}
+
 // Scores from column n on count for nothing.
 template <int N>
 __device__ __forceinline__ void hide(uint32_t* s, int n) {
@@ -832,10 +851,9 @@ __device__ void softmax_tiles(const Ctx& cx, const Piece& pc, int gj0,
       }
 #pragma unroll
       for (int k = 0; k < kC; k += 2) {
-        const float x0 = exp2f(fmaf(s[k], sl2, -mu));
-        const float x1 = exp2f(fmaf(s[k + 1], sl2, -mu));
-        sum4[k & 3] += x0;
-        sum4[(k & 3) + 1] += x1;
+        const float2 t = fma_pair(s[k], s[k + 1], sl2, -mu);
+        const float x0 = exp2f(t.x), x1 = exp2f(t.y);
+        add_pair(sum4[k & 3], sum4[(k & 3) + 1], x0, x1);
         if (kFp8) {
           const __half2 hh = __floats2half2_rn(x0, x1);
           raw[k >> 1] = *reinterpret_cast<const uint32_t*>(&hh);

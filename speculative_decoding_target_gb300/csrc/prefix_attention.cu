@@ -57,6 +57,11 @@
 // 65,536, 103 Gflop: 121 us, 0.45 of that rate; the conversion of E4M3 to fp16
 // through shared memory bounds it (issue slots 54% busy, the tensor pipe 52%).
 //
+// Causal (chunk_attention.cuh), bf16: 4,096 tokens into an empty cache, 206 Gflop,
+// 146 us, 132 of them here; 2,048 tokens behind 32,768, 1.70 Pflop, 941 us at full
+// clocks, 0.94 of the measured bf16 rate, 1,036 under the power limit.  FP8, six
+// ragged requests, 319 Gflop: 316 us.
+//
 // Every wait is bounded as in verify_attention_tc.cu.
 #include <cuda_fp8.h>
 
@@ -898,8 +903,8 @@ __device__ void write_out(const Ctx& cx, const Piece& pc, uint32_t tmem, float l
   const int R = pc.row0 + w4 * 32 + lane;
   const bool valid = w4 * 32 + lane < cx.cta_rows && R < pc.rows_total;
   const int tok = R / p.group;
-  // out is 16-byte aligned; with stores of 32 bytes 4,096 tokens into an empty cache
-  // take 155 us, with 16 bytes 160
+  // out is 16-byte aligned; stores of 32 bytes, where they fit, take 5 us from 4,096
+  // tokens into an empty cache (160 us with 16 bytes)
   const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
   __nv_bfloat16* dst =
       p.out + (((long long)pc.lead * p.q_len + pc.first + tok) * p.hq +

@@ -108,6 +108,10 @@ class LogprobDesc(ctypes.Structure):
                 ("row_stride", ctypes.c_int64)]
 
 
+_LOGPROB_DESC = struct.Struct("@4iq")
+assert _LOGPROB_DESC.size == ctypes.sizeof(LogprobDesc)
+
+
 class SelectDesc(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("positions", ctypes.c_int32),
                 ("vocab", ctypes.c_int32), ("top", ctypes.c_int32),
@@ -161,7 +165,7 @@ def load(path: str = LIB_PATH):
     lib.spec_chunk_attention.restype = ctypes.c_int
     lib.spec_sample.argtypes = [ctypes.POINTER(SampleDesc)] + [P] * 10
     lib.spec_sample.restype = ctypes.c_int
-    lib.spec_logprobs.argtypes = [ctypes.POINTER(LogprobDesc)] + [P] * 8
+    lib.spec_logprobs.argtypes = [P] * 9
     lib.spec_logprobs.restype = ctypes.c_int
     lib.spec_rope_append.argtypes = [P] * 16
     lib.spec_rope_append.restype = ctypes.c_int
@@ -265,6 +269,14 @@ def _made_on(stream):
     dropped, before the call has run."""
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(
         stream)
+
+
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """torch.empty on the call's stream (see _made_on)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _expect_pools(k_pages, v_pages, k_scales, v_scales, hkv: int,
@@ -573,11 +585,7 @@ def _rope_append(q, k_new, v_new, norm, freq, k_pages, v_pages, page_table,
         q_shape = (B, q_len, hq, d)
         _expect(q, torch.bfloat16, "q", q_shape)
         if q_out is None:
-            if stream is None:
-                q_out = q.new_empty(q_shape)
-            else:
-                with _made_on(stream):
-                    q_out = q.new_empty(q_shape)
+            q_out = _empty(q_shape, torch.bfloat16, q.device, stream)
         else:
             _expect(q_out, torch.bfloat16, "q_out", q_shape, contiguous=True)
     q_w = k_w = None
@@ -845,24 +853,25 @@ def logprobs(logits, token=None, *, temperature=None, top: int = 0,
     on = _on_current_device((logits, token, temperature), stream)
     rows = lead.numel()
     stride = _row_stride(logits, rows)
-    desc = LogprobDesc(rows, vocab, int(logits.dtype == torch.bfloat16), top,
-                       stride)
-    with _made_on(stream):
-        new = lambda shape, dtype: torch.empty(shape, dtype=dtype,
-                                               device=logits.device)
-        out = {}
-        if token is not None:
-            out["logprob"] = new(lead, torch.float32)
-        out["entropy"] = new(lead, torch.float32)
-        if top > 0:
-            out["top_ids"] = new((*lead, top), torch.int32)
-            out["top_logprobs"] = new((*lead, top), torch.float32)
+    desc = _packed(_LOGPROB_DESC, rows, vocab, logits.dtype == torch.bfloat16,
+                   top, stride)
+    dev, f32 = logits.device, torch.float32
+    logprob = top_ids = top_logprobs = None
+    if token is not None:
+        logprob = _empty(lead, f32, dev, stream)
+    entropy = _empty(lead, f32, dev, stream)
+    if top > 0:
+        top_ids = _empty((*lead, top), torch.int32, dev, stream)
+        top_logprobs = _empty((*lead, top), f32, dev, stream)
     rc = load().spec_logprobs(
-        ctypes.byref(desc), logits.data_ptr(), _at(token), _at(temperature),
-        _at(out.get("logprob")), out["entropy"].data_ptr(),
-        _at(out.get("top_ids")), _at(out.get("top_logprobs")), on)
+        desc, logits.data_ptr(), _at(token), _at(temperature), _at(logprob),
+        entropy.data_ptr(), _at(top_ids), _at(top_logprobs), on)
     if rc:
         _check(rc)
+    out = {} if token is None else {"logprob": logprob}
+    out["entropy"] = entropy
+    if top > 0:
+        out["top_ids"], out["top_logprobs"] = top_ids, top_logprobs
     return out
 
 

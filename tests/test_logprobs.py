@@ -5,9 +5,10 @@ Tolerances.  With z = (x - max) / T, E the mean of |z| under p: the factor
 log2(e) / T is off by 2^-24 and its constant by 2^-25, t by two more roundings:
 3.5 2^-24 of z in every weight: 2.1e-7 E; a token's own z by two, 2^-23 |z|.  A
 weight is off by ex2's 2^-22.  A sum passes at most 16 + 2 additions in its
-batch, at most 32 batches in these calls, each perhaps with a change of the reference (two roundings
-and an ex2), and 5 + 5 + 4 inside the warp, the CTA and the cluster, where the
-reference changes twice more: below 48 2^-24 + 34 (2^-23 + 2^-22) < 1.5e-5 of S.
+batch, 128 batches and 5 + 5 + 4 inside the warp, the CTA and the cluster, 160
+2^-24.  A change of the reference (two roundings and an ex2, 2^-23 + 2^-22) makes
+what it touches 2^-8 of itself or less, so all of them count for 1.01 such errors;
+the joins change it twice more: 1.1e-5, below 1.5e-5 of S.
 ln S is off by 2^-22 of itself, at most 3.2e-6 more with S < 2^19.  So log p is
 off by 1.9e-5 + 2.1e-7 (|z| + E) and its own rounding, 2^-24 of it; the entropy,
 of which both ln S and a mean of z have that error, by 1.9e-5 (1 + E) + 2.1e-7 E
@@ -292,6 +293,19 @@ def test_parts_with_many_large_logits(dtype, rows):
     token = np.full(rows, -1)
     token[live] = 64 * 7
     check(x, run(x, token, None, 32), token, None, 32)
+
+
+@pytest.mark.gpu
+def test_long_rows_whole():
+    # half a million fp32 tokens a CTA, values that rise through the row
+    x = torch.zeros((310, 524288), device=DEV)
+    x[5] = logits(1, 524288, torch.float32, seed=14)[0]
+    x[5] += torch.linspace(0, 60, 524288, device=DEV)
+    x[9, 77] = 26 * np.log(2)
+    x[200] = torch.linspace(40, 0, 524288, device=DEV)
+    token = np.full(310, -1)
+    token[[5, 9, 200]] = [524287, 77, 100000]
+    check(x, run(x, token, None, 3), token, None, 3)
 
 
 @pytest.mark.gpu

@@ -805,9 +805,11 @@ __device__ void softmax_tiles(const Ctx& cx, const Piece& pc, int gj0,
     const uint32_t sbuf = lane_base + kColS + (gj & 1) * kT;
     wait_bar(cx, &cx.bars->s_full[gj & 1], (uint32_t)(gj >> 1) & 1);
     tc::fence_after();
-    // bf16: the tile's scores in registers; FP8: 32 columns at a time, read
-    // twice, in rolled loops
-    constexpr int kC = kFp8 ? 32 : kT;
+    // 32 columns at a time, read twice, in rolled loops, which fit the instruction
+    // cache: ragged shared groups 82.3 us, 86.8 with the tile's scores in registers.
+    // Causal bf16 holds them all: its short pieces, whose first tile nothing hides,
+    // are faster so (4,096 tokens into an empty cache 144.7 us, 148.8 with 32).
+    constexpr int kC = kFp8 || !kCausal ? 32 : kT;
     uint32_t raw[kC];
     const float* s = reinterpret_cast<const float*>(raw);
     float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -850,7 +852,7 @@ __device__ void softmax_tiles(const Ctx& cx, const Piece& pc, int gj0,
     float sum4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
     for (int c = 0; c < kT; c += kC) {
-      if (kFp8) {
+      if (kC < kT) {
         tc::tmem_ld_cols<kC>(sbuf + c, raw);
         if (masked) hide<kC>(raw, seen - jt * kT - c);
       }

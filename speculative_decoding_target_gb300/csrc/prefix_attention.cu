@@ -50,12 +50,12 @@
 // leaves with the division by the sum, and the log-sum-exp's 11.
 //
 // Measured (24 query heads, 4 KV heads): bf16, 32 requests x 8 rows over 32,768
-// shared tokens, 206 Gflop: 117-121 us, 1.71 to 1.76 Pflop/s, 0.89 to 0.91 of
-// the measured bf16 rate; the tensor pipe is busy 81% of the time, DRAM reads
-// 137.5 MB of the prefix's 134.2.  What is left is the first and last tile of
-// each piece and the issuer's waits on the softmax.  FP8, 64 single tokens over
-// 65,536, 103 Gflop: 117 us, 0.46 of that rate; the conversion of E4M3 to fp16
-// through shared memory bounds it (issue slots 51% busy, the tensor pipe 53%).
+// shared tokens, 206 Gflop: 121 us, 1.71 Pflop/s, 0.89 of the measured bf16 rate;
+// the tensor pipe is busy 81% of the time, DRAM reads 137.5 MB of the prefix's
+// 134.2.  What is left is the first and last tile of each piece and the issuer's
+// waits on the softmax.  FP8, 64 single tokens over 65,536, 103 Gflop: 117 us, 0.46
+// of that rate; the conversion of E4M3 to fp16 through shared memory bounds it
+// (issue slots 51% busy, the tensor pipe 53%).
 //
 // Causal (chunk_attention.cuh), bf16: 4,096 tokens into an empty cache, 206 Gflop,
 // 146 us, 136 of them here; 2,048 tokens behind 32,768, 1.70 Pflop, 941 us at full

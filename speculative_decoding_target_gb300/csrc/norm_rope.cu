@@ -93,6 +93,17 @@ __device__ __forceinline__ float norm_weight(const RopeParams& p, const void* w,
                            : static_cast<const float*>(w)[c]);
 }
 
+// Correctly rounded quotients by a finite scale s, with r the
+// correctly rounded reciprocal (Markstein 1990: q within one step of x / s, the
+// remainder x - q s exact in one fused step, q + r (x - q s) is the rounded
+// quotient).  Quotients so small that the remainder is not exact are zeros in E4M3
+// whatever their last digit; the sign is x's, of zeros too.
+__device__ __forceinline__ float2 quotients(u64 x, u64 r, u64 minus_s) {
+  const u64 q = mul2(x, r);
+  const u64 v = fma2(fma2(q, minus_s, x), r, q);
+  return unpack2(v | (x & 0x8000000080000000ull));
+}
+
 // Quantise-on-write of a row by half a warp: lane l holds channels 16l .. 16l+15
 // and four lanes share a 64-channel block; the rule of quantise_row.
 __device__ __forceinline__ void quantise_half(const float (&x)[16], int l,
@@ -106,11 +117,14 @@ __device__ __forceinline__ void quantise_half(const float (&x)[16], int l,
   __half scale = __float2half_rn(__fdiv_rn(amax, 448.f));
   if (__half2float(scale) == 0.f) scale = __float2half_rn(1.f);
   const float sf = __half2float(scale);
+  // by an infinite scale, of values too large for any: zeros, or NaN of infinities
+  const bool finite = sf <= 65504.f;
+  const float rf = finite ? __frcp_rn(sf) : 0.f, ms = finite ? -sf : 0.f;
+  const u64 r = pack2(rf, rf), minus_s = pack2(ms, ms);
   uint32_t packed[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float2 qv =
-        make_float2(__fdiv_rn(x[2 * e], sf), __fdiv_rn(x[2 * e + 1], sf));
+    const float2 qv = quotients(pack2(x[2 * e], x[2 * e + 1]), r, minus_s);
     const uint32_t pair =
         __nv_cvt_float2_to_fp8x2(qv, __NV_SATFINITE, __NV_E4M3) & 0xFFFFu;
     packed[e >> 1] |= pair << (16 * (e & 1));

@@ -174,6 +174,43 @@ def test_more_heads_than_a_round_of_warps(kv, hq, hkv):
 
 
 @pytest.mark.gpu
+def test_quantised_values_are_rope_append_s():
+    # byte for byte: all sizes, borders between codes, zeros of both signs, NaN,
+    # infinities, rows whose scale is infinite, one or a subnormal
+    build.build()
+    freq, m = sv.rope_frequencies(64)
+    w = weights(11, torch.bfloat16, 0.0)
+    c = make_case("fp8", 16, None, [700, 700], 700, seed=30)
+    g = torch.Generator(device=DEV).manual_seed(31)
+    v = torch.randn(c["v"].shape, generator=g, device=DEV)
+    at = torch.arange(700, device=DEV)[:, None, None]
+    v = torch.where(at < 300, v * 2.0 ** (at - 150) / 4, v)
+    steps = torch.randint(-448 * 16, 448 * 16, v.shape, generator=g,
+                          device=DEV) / 16.0     # on and between codes
+    v = torch.where((at >= 300) & (at < 450), steps, v)
+    v[:, 450:500] *= 2.0 ** torch.randint(
+        -40, 1, v[:, 450:500].shape, generator=g, device=DEV)
+    v[:, 500:520, :, ::3] = 0.0
+    v[:, 510:530, :, ::5] = -0.0
+    v[:, 540, :, 7] = float("nan")
+    v[:, 541, :, 9] = float("inf")
+    v[:, 542, :, 70] = -float("inf")
+    v[:, 543] = 0.0
+    v[:, 544:546] = 1e30
+    v[:, 546] = -1e-39
+    c["v"].copy_(v)
+    want = [torch.full_like(c[x], 0) for x in ("kp", "vp", "ks", "vs")]
+    got = [t.clone() for t in want]
+    sv.rope_append(None, c["k"], c["v"], freq.to(DEV), want[0], want[1],
+                   c["table"], c["seq"], k_scales=want[2], v_scales=want[3])
+    c["kp"], c["vp"], c["ks"], c["vs"] = got
+    for inter in (False, True):
+        call(c, w, freq, inter, m)
+        assert torch.equal(got[3].view(torch.int16), want[3].view(torch.int16))
+        assert torch.equal(got[1], want[1])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
 def test_addresses_of_16_bytes_and_two_calls_at_once(kv):
     def shifted(t):

@@ -28,8 +28,8 @@ namespace {
 constexpr int kPairs = 2;       // pairs of rows of a warp whose loads are in flight
 // Warps of a CTA and CTAs of an SM.  bf16: three of eight (8,192 tokens 51.8 us;
 // four, with 64 registers, 54.2).  FP8: two of ten, four of which have keys or
-// values alone, which are quantised (five ragged prompts 54.4 us, a batch of
-// blocks 4.8; three of eight 56.0 and 5.2).
+// values alone, which are quantised (five ragged prompts 52.9 us, a batch of
+// blocks 4.4; three of eight 56.6 and 5.0, four of six 67.6 and 5.6).
 template <bool kFp8>
 struct Shape {
   static constexpr int kWarps = kFp8 ? 10 : 8;
@@ -96,7 +96,7 @@ __device__ __forceinline__ float norm_weight(const RopeParams& p, const void* w,
 // Correctly rounded quotients by a finite scale s, with r the
 // correctly rounded reciprocal (Markstein 1990: q within one step of x / s, the
 // remainder x - q s exact in one fused step, q + r (x - q s) is the rounded
-// quotient).  Quotients so small that the remainder is not exact are zeros in E4M3
+// quotient; 54.3 us with divisions where this takes 52.9).  Quotients so small that the remainder is not exact are zeros in E4M3
 // whatever their last digit; the sign is x's, of zeros too.
 __device__ __forceinline__ float2 quotients(u64 x, u64 r, u64 minus_s) {
   const u64 q = mul2(x, r);

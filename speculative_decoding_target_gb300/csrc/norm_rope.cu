@@ -93,11 +93,12 @@ __device__ __forceinline__ float norm_weight(const RopeParams& p, const void* w,
                            : static_cast<const float*>(w)[c]);
 }
 
-// Correctly rounded quotients by a finite scale s, with r the
-// correctly rounded reciprocal (Markstein 1990: q within one step of x / s, the
-// remainder x - q s exact in one fused step, q + r (x - q s) is the rounded
-// quotient; 54.3 us with divisions where this takes 52.9).  Quotients so small that the remainder is not exact are zeros in E4M3
-// whatever their last digit; the sign is x's, of zeros too.
+// Correctly rounded quotients by a finite scale s, with r the correctly rounded
+// reciprocal (Markstein 1990: q within one step of x / s, the remainder x - q s
+// exact in one fused step, q + r (x - q s) is the rounded quotient).  Quotients so
+// small that the remainder is not exact are zeros in E4M3 whatever their last
+// digit; the sign is x's, of zeros too.  (Ragged prompts 54.3 us with divisions,
+// 52.9 so.)
 __device__ __forceinline__ float2 quotients(u64 x, u64 r, u64 minus_s) {
   const u64 q = mul2(x, r);
   const u64 v = fma2(fma2(q, minus_s, x), r, q);

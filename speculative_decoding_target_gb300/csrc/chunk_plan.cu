@@ -15,6 +15,7 @@ static_assert(kThreads >= kMaxBatch, "");
 // A run of the rest is at least this long, in 128-token tiles, and one that
 // would start or end as close as kSnap to a piece's border starts or ends there
 // (a piece costs as much as kPrefixCost tiles).
+static_assert(kChunkBuckets == 64, "two a lane");
 constexpr int kHeld = 4096;
 constexpr int kMinRun = 2;
 constexpr int kSnap = 2;
@@ -104,10 +105,16 @@ __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(const ChunkParams 
     atomicAdd(&s_count[bucket_of(tile_at(i, &b, &m))], 1);
   }
   __syncthreads();
-  if (tid < kChunkBuckets) {
-    int n = 0;
-    for (int k = 0; k < tid; ++k) n += s_count[k];
-    s_base[tid] = n;
+  if (w == 0) {  // two buckets a lane
+    const int c0 = s_count[2 * lane], c1 = s_count[2 * lane + 1];
+    int n = c0 + c1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, n, o);
+      if (lane >= o) n += up;
+    }
+    s_base[2 * lane] = n - c0 - c1;
+    s_base[2 * lane + 1] = n - c1;
   }
   // places in a bucket, in the tiles' order
   for (int i0 = 0; i0 < T; i0 += nt) {

@@ -47,6 +47,7 @@ EXPORTED = (
 )
 SELECT_MODES = {"greedy": 0, "map": 1}
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
+LOGPROB_MAX_TOP = 32
 
 
 class SpecError(RuntimeError):
@@ -850,6 +851,8 @@ def logprobs(logits, token=None, *, temperature=None, top: int = 0,
         _expect(token, torch.int32, "token", lead, True)
     if temperature is not None:
         _expect(temperature, torch.float32, "temperature", lead, True)
+    if not 0 <= top <= LOGPROB_MAX_TOP:     # before anything of that size is made
+        raise SpecError(SPEC_ERR_ARG, f"top {top} outside [0, {LOGPROB_MAX_TOP}]")
     on = _on_current_device((logits, token, temperature), stream)
     rows = lead.numel()
     stride = _row_stride(logits, rows)

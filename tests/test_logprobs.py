@@ -418,6 +418,9 @@ def test_binding_refuses_wrong_tensors():
     refused("logits are", x=x.half())
     refused("token must be", token=tok.long())
     refused("token must be", token=tok[:3])
+    refused("top", top=33)
+    refused("top", top=10 ** 12)
+    refused("top", top=-1)
     refused("temperature", temperature=torch.ones(3))
     refused("temperature", temperature=torch.ones(4, dtype=torch.float64))
     refused("CUDA device")                      # host tensors

@@ -1,6 +1,8 @@
 // C ABI of the verify library: host-side validation, workspace layout and
 // kernel launches.  Every error is detected here, before anything is
 // enqueued, except a failed launch (SPEC_ERR_CUDA).
+#include <algorithm>
+#include <cfloat>
 #include <climits>
 #include <cstdarg>
 #include <cstdio>
@@ -346,7 +348,9 @@ int attention_params(const spec_attn_desc* desc, const Layout& L, const void* q,
                  : use_tc(desc) ? specv::kTcPieceCost
                                 : specv::kMmaPieceCost;
   p.box_rows = specv::verify_split_tc_box_rows(desc->page_size);
-  p.scale_log2 = scale * 1.4426950408889634f;
+  // a normal number: the kernels flush smaller ones, and a hidden score, -inf,
+  // times zero is NaN
+  p.scale_log2 = std::max(scale * 1.4426950408889634f, FLT_MIN);
   p.wait_cycles = specv::kDrainWaitCycles;
   if (desc->flags & SPEC_FLAG_CHECKED) {
     const long long w = g_checked_wait_cycles.load(std::memory_order_relaxed);

@@ -359,6 +359,16 @@ def test_many_requests():
     c.check(c.run())
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("widths", [[5, 1], [40, 17], [300, 2]])
+def test_scales_below_the_normal_numbers(kv, widths):
+    # every score is as good as zero: equal weights over what a row sees
+    c = Case(widths, [200, 0], kv=kv, seed=21)
+    for c.scale in (1e-38, 1e-40, 1e-45):
+        c.check(c.run())
+
+
 # ---------------------------------------------------------------- CPU tests
 
 FAKE = ctypes.c_void_p(0x100000)   # never dereferenced: checks come first

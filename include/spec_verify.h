@@ -476,7 +476,8 @@ typedef struct {
  *                 among equals; top_logprobs their log p
  *
  *   logits       [rows, vocab]; NaN counts as -inf, +inf as the type's largest
- *                finite value.  A token at -inf has log p -inf and is no
+ *                finite value; subnormals keep their order (spec_sample takes
+ *                them as zero).  A token at -inf has log p -inf and is no
  *                alternative: ids behind the last finite logit are -1 and their
  *                log p -inf.  A row without a finite logit: logprob -inf,
  *                entropy 0.

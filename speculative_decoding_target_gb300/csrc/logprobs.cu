@@ -100,6 +100,34 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// What orders the logits keeps subnormal ones apart, which fmaxf, fminf and the
+// comparison operators flush here.
+__device__ __forceinline__ float max_of(float a, float b) {
+  float d;
+  asm("max.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float min_of(float a, float b) {
+  float d;
+  asm("min.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ bool above(float a, float b) {
+  int d;
+  asm("{\n\t.reg .pred p;\n\tsetp.gt.f32 p, %1, %2;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(d)
+      : "f"(a), "f"(b));
+  return d;
+}
+// (false for NaN)
+__device__ __forceinline__ bool at_least(float a, float b) {
+  int d;
+  asm("{\n\t.reg .pred p;\n\tsetp.ge.f32 p, %1, %2;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(d)
+      : "f"(a), "f"(b));
+  return d;
+}
+
 // NaN counts as -inf, +inf as the type's largest value.
 template <typename T>
 __device__ __forceinline__ constexpr float most_of() {
@@ -107,7 +135,7 @@ __device__ __forceinline__ constexpr float most_of() {
 }
 template <typename T>
 __device__ __forceinline__ float clean(float x) {
-  return fminf(fmaxf(x, -INFINITY), most_of<T>());
+  return min_of(max_of(x, -INFINITY), most_of<T>());
 }
 
 template <typename T>
@@ -137,18 +165,20 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ float largest(uint4 v, __nv_bfloat16*) {
   const uint32_t m =
       max_bf16x2(max_bf16x2(v.x, v.y), max_bf16x2(v.z, v.w));
-  return fmaxf(fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u)),
-               -INFINITY);
+  return max_of(
+      max_of(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u)),
+      -INFINITY);
 }
 __device__ __forceinline__ float largest(uint4 v, float*) {
-  return fmaxf(fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)),
-                     fmaxf(__uint_as_float(v.z), __uint_as_float(v.w))),
-               -INFINITY);
+  return max_of(max_of(max_of(__uint_as_float(v.x), __uint_as_float(v.y)),
+                       max_of(__uint_as_float(v.z), __uint_as_float(v.w))),
+                -INFINITY);
 }
 // A token as one number: larger value first, then the smaller place (its own, or
 // its vector's first token's).  0 is no token.
 __device__ __forceinline__ u64 key_of(float v, int place) {
-  const uint32_t b = __float_as_uint(v + 0.f);  // -0 as 0
+  uint32_t b = __float_as_uint(v);
+  if (b == 0x80000000u) b = 0;  // -0 as 0
   const uint32_t o = b & 0x80000000u ? ~b : b | 0x80000000u;
   return (u64)o << 32 | (0xffffffffu - (uint32_t)place);
 }
@@ -246,17 +276,17 @@ __device__ __forceinline__ void join(Sums& a, const uint4 (&raw)[kVecs], int v0,
 #pragma unroll
   for (int u = 0; u < kVecs; ++u) {
     m[u] = largest(raw[u], static_cast<T*>(nullptr));
-    most = fmaxf(most, m[u]);
+    most = max_of(most, m[u]);
   }
   if (most == INFINITY) {  // the type's largest, of which the first counts
     most = most_of<T>();
 #pragma unroll
-    for (int u = 0; u < kVecs; ++u) m[u] = fminf(m[u], most);
+    for (int u = 0; u < kVecs; ++u) m[u] = min_of(m[u], most);
   }
 #pragma unroll
   for (int u = 0; u < kVecs; ++u) {
-    a.next = fmaxf(a.next, fminf(m[u], a.max));
-    if (m[u] > a.max) {
+    a.next = max_of(a.next, min_of(m[u], a.max));
+    if (above(m[u], a.max)) {
       a.max = m[u];
       a.vec = v0 + u * kThreads;
     }
@@ -392,9 +422,10 @@ __device__ __forceinline__ Sums stream(const Part<T>& part, Ring& ring, float c)
   }
   if (part.odd >= 0) {
     const float x = clean<T>(to_float(part.x[part.odd]));
-    a.next = fmaxf(a.next, fminf(x, a.max));
+    a.next = max_of(a.next, min_of(x, a.max));
     // in front of every vector, or behind them
-    if (x > a.max || (x == a.max && part.odd < part.head && x > -INFINITY)) {
+    if (above(x, a.max) ||
+        (at_least(x, a.max) && part.odd < part.head && x > -INFINITY)) {
       a.max = x;
       a.vec = -1;
     }
@@ -412,7 +443,7 @@ __device__ __forceinline__ Sums stream(const Part<T>& part, Ring& ring, float c)
 
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  for (int o = 16; o; o >>= 1) v = max_of(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
 
@@ -448,12 +479,12 @@ __device__ void select(Shared& sh, const Part<T>& part, const Sums& a,
 #pragma unroll
   for (int k = 0; k < 32; ++k) {
     const float other = __shfl_sync(0xffffffffu, group, k);
-    ahead += other > group || (other == group && k < lane);
+    ahead += above(other, group) || (k < lane && at_least(other, group));
   }
   const unsigned last_group = __ballot_sync(0xffffffffu, ahead == top - 1);
   const float low = __shfl_sync(0xffffffffu, group, __ffs(last_group) - 1);
   // the threads at or above it, in any order, and their vectors
-  const bool in = a.max >= low && a.max > -INFINITY;
+  const bool in = at_least(a.max, low) && a.max > -INFINITY;
   uint4 raw = make_uint4(0u, 0u, 0u, 0u);
   if (in && a.vec >= 0) raw = __ldg(part.vec(a.vec));
   const u64 mine =
@@ -477,9 +508,9 @@ __device__ void select(Shared& sh, const Part<T>& part, const Sums& a,
   __syncthreads();
   // the last winner's value: what lies below it is no candidate
   const float bound =
-      n >= top ? fmaxf(value_of(sh.bound), -kMaxFinite) : -kMaxFinite;
+      n >= top ? max_of(value_of(sh.bound), -kMaxFinite) : -kMaxFinite;
   if (rank < top) {
-    if (a.next >= bound) {
+    if (at_least(a.next, bound)) {
       const int at = atomicAdd(&sh.deep, 1);
       sh.deep_t[at] = (uint16_t)tid;
       sh.deep_r[at] = (uint16_t)rank;
@@ -490,7 +521,7 @@ __device__ void select(Shared& sh, const Part<T>& part, const Sums& a,
       widen(raw, x, static_cast<T*>(nullptr));
 #pragma unroll
       for (int k = 0; k < kN; ++k)
-        if (x[k] >= bound)
+        if (at_least(x[k], bound))
           sh.cands[atomicAdd(&sh.found, 1)] =
               key_of(clean<T>(x[k]), part.head + a.vec * kN + k);
     }
@@ -522,7 +553,7 @@ __device__ void select(Shared& sh, const Part<T>& part, const Sums& a,
         widen(raw[q], x, static_cast<T*>(nullptr));
 #pragma unroll
         for (int k = 0; k < kN; ++k)
-          if (x[k] >= bound) bits |= 1u << (q * kN + k);
+          if (at_least(x[k], bound)) bits |= 1u << (q * kN + k);
       }
       hit |= (u64)bits << bit;
       bit += 4 * kN;
@@ -530,7 +561,7 @@ __device__ void select(Shared& sh, const Part<T>& part, const Sums& a,
     const int odd = part.odd_of(t);
     const float odd_x =
         lane == 31 && odd >= 0 ? clean<T>(to_float(part.x[odd])) : -INFINITY;
-    const bool odd_hit = odd_x >= bound;
+    const bool odd_hit = at_least(odd_x, bound);
     int hits = __popcll(hit) + odd_hit;
 #pragma unroll
     for (int o = 16; o; o >>= 1) hits += __shfl_xor_sync(0xffffffffu, hits, o);
@@ -669,7 +700,7 @@ __device__ __forceinline__ void work_on(Shared& sh, Ring& ring,
   float gm = a.max;
 #pragma unroll
   for (int o = kGroup / 2; o; o >>= 1)
-    gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, o));
+    gm = max_of(gm, __shfl_xor_sync(0xffffffffu, gm, o));
   if (threadIdx.x % kGroup == 0) sh.max[threadIdx.x / kGroup] = gm;
   if (threadIdx.x == 0) sh.listed = sh.found = sh.deep = 0;
   if (threadIdx.x < kTop) sh.top[threadIdx.x] = 0;

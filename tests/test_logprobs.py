@@ -343,6 +343,54 @@ def test_agrees_with_the_sampler():
         out["top_ids"][3, 0])
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,vocab", [(4, 70), (3, 60000), (400, 9001)])
+def test_subnormal_logits_keep_their_order(dtype, rows, vocab):
+    # the best logits are subnormals and zeros of both signs, single ones and
+    # a thread's worth of neighbours
+    x = logits(rows, vocab, dtype, seed=15, peaks=0) - 40
+    whole = torch.int32 if dtype == torch.float32 else torch.int16
+    g = torch.Generator(device=DEV).manual_seed(16)
+    at = torch.stack([torch.randperm(vocab, generator=g, device=DEV)[:44]
+                      for _ in range(rows)])
+    at[:, 8:20] = vocab // 2 + torch.arange(12, device=DEV)
+    most = 0x7fffff if dtype == torch.float32 else 0x7f
+    small = torch.randint(1, most + 1, (rows, 44), generator=g, device=DEV)
+    small[:, :4] = 0
+    small = small.to(whole).view(dtype)
+    small[:, 1::3] = -small[:, 1::3]
+    x.scatter_(1, at, small)
+    token = at[:, 9].tolist()
+    t = np.where(np.arange(rows) % 2, 0.0, 1.0).astype(np.float32)
+    check(x, run(x, token, t, 32), token, t, 32)
+    check(x, run(x, token, t, 1), token, t, 1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,vocab", [(4, 70), (3, 60000), (400, 9001)])
+def test_subnormal_logits_keep_their_order(dtype, rows, vocab):
+    # the best logits are subnormals and zeros of both signs, single ones and
+    # a thread's worth of neighbours
+    x = logits(rows, vocab, dtype, seed=15, peaks=0) - 40
+    whole = torch.int32 if dtype == torch.float32 else torch.int16
+    g = torch.Generator(device=DEV).manual_seed(16)
+    at = torch.stack([torch.randperm(vocab, generator=g, device=DEV)[:44]
+                      for _ in range(rows)])
+    at[:, 8:20] = vocab // 2 + torch.arange(12, device=DEV)
+    most = 0x7fffff if dtype == torch.float32 else 0x7f
+    small = torch.randint(1, most + 1, (rows, 44), generator=g, device=DEV)
+    small[:, :4] = 0
+    small = small.to(whole).view(dtype)
+    small[:, 1::3] = -small[:, 1::3]
+    x.scatter_(1, at, small)
+    token = at[:, 9].tolist()
+    t = np.where(np.arange(rows) % 2, 0.0, 1.0).astype(np.float32)
+    check(x, run(x, token, t, 32), token, t, 32)
+    check(x, run(x, token, t, 1), token, t, 1)
+
+
 # ---------------------------------------------------------------- CPU tests
 
 FAKE = ctypes.c_void_p(0x100000)   # never dereferenced: checks come first

@@ -651,7 +651,8 @@ __device__ __forceinline__ void finish(const LogprobParams& p, int row,
                                        const u64* top) {
   const int lane = threadIdx.x & 31;
   const bool none = m == -INFINITY;  // no finite logit
-  const float lns = none ? 0.f : ln_of(s);
+  // S >= 1, though its roundings may fall short of that: no log p above zero
+  const float lns = none ? 0.f : fmaxf(ln_of(s), 0.f);
   auto logprob = [&](float v, bool first) {
     if (r.one) return first ? 0.f : -INFINITY;
     if (none || v == -INFINITY) return -INFINITY;

@@ -391,6 +391,26 @@ def test_subnormal_logits_keep_their_order(dtype, rows, vocab):
     check(x, run(x, token, t, 1), token, t, 1)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,vocab", [(3000, 40), (150, 30000)])
+def test_no_log_probability_above_zero(dtype, rows, vocab):
+    # all the mass on one token: log p is 0 within its error, and not above
+    g = torch.Generator(device=DEV).manual_seed(17)
+    x = torch.full((rows, vocab), -float("inf"), device=DEV)
+    token = torch.randint(0, vocab, (rows,), generator=g, device=DEV)
+    x[torch.arange(rows), token] = torch.randn(
+        rows, generator=g, device=DEV) * 10.0 ** torch.randint(
+            -2, 6, (rows,), generator=g, device=DEV)
+    x[::2] = torch.where(x[::2] == -float("inf"),
+                         x[::2].amax(1, keepdim=True) - 30, x[::2])
+    x = x.to(dtype)
+    t = (0.2 + 2 * torch.rand(rows, generator=g, device=DEV)).cpu().numpy()
+    out = run(x, token, t, 2)
+    check(x, out, token.tolist(), t, 2)
+    assert (out["logprob"] <= 0).all() and (out["top_logprobs"] <= 0).all()
+
+
 # ---------------------------------------------------------------- CPU tests
 
 FAKE = ctypes.c_void_p(0x100000)   # never dereferenced: checks come first

@@ -107,17 +107,22 @@ __device__ __forceinline__ float max_of(float a, float b) {
   asm("max.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
   return d;
 }
+__device__ __forceinline__ float max_of(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 __device__ __forceinline__ float min_of(float a, float b) {
   float d;
   asm("min.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
   return d;
 }
-__device__ __forceinline__ bool above(float a, float b) {
-  int d;
-  asm("{\n\t.reg .pred p;\n\tsetp.gt.f32 p, %1, %2;\n\tselp.b32 %0, 1, 0, p;\n\t}"
-      : "=r"(d)
-      : "f"(a), "f"(b));
-  return d;
+// The larger of the two, and its place if that is m.
+__device__ __forceinline__ void rise(float& max, int& at, float m, int place) {
+  asm("{\n\t.reg .pred p;\n\tsetp.gt.f32 p, %2, %0;\n\t"
+      "selp.b32 %1, %3, %1, p;\n\tmax.f32 %0, %0, %2;\n\t}"
+      : "+f"(max), "+r"(at)
+      : "f"(m), "r"(place));
 }
 // (false for NaN)
 __device__ __forceinline__ bool at_least(float a, float b) {
@@ -165,22 +170,24 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ float largest(uint4 v, __nv_bfloat16*) {
   const uint32_t m =
       max_bf16x2(max_bf16x2(v.x, v.y), max_bf16x2(v.z, v.w));
-  return max_of(
-      max_of(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u)),
-      -INFINITY);
+  return max_of(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u),
+                -INFINITY);
 }
 __device__ __forceinline__ float largest(uint4 v, float*) {
-  return max_of(max_of(max_of(__uint_as_float(v.x), __uint_as_float(v.y)),
-                       max_of(__uint_as_float(v.z), __uint_as_float(v.w))),
-                -INFINITY);
+  return max_of(max_of(__uint_as_float(v.x), __uint_as_float(v.y),
+                       __uint_as_float(v.z)),
+                __uint_as_float(v.w), -INFINITY);
+}
+// A value as a whole number of the same order.
+__device__ __forceinline__ uint32_t order_of(float v) {
+  uint32_t b = __float_as_uint(v);
+  if (b == 0x80000000u) b = 0;  // -0 as 0
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 // A token as one number: larger value first, then the smaller place (its own, or
 // its vector's first token's).  0 is no token.
 __device__ __forceinline__ u64 key_of(float v, int place) {
-  uint32_t b = __float_as_uint(v);
-  if (b == 0x80000000u) b = 0;  // -0 as 0
-  const uint32_t o = b & 0x80000000u ? ~b : b | 0x80000000u;
-  return (u64)o << 32 | (0xffffffffu - (uint32_t)place);
+  return (u64)order_of(v) << 32 | (0xffffffffu - (uint32_t)place);
 }
 __device__ __forceinline__ float value_of(u64 key) {
   const uint32_t o = (uint32_t)(key >> 32);
@@ -286,10 +293,7 @@ __device__ __forceinline__ void join(Sums& a, const uint4 (&raw)[kVecs], int v0,
 #pragma unroll
   for (int u = 0; u < kVecs; ++u) {
     a.next = max_of(a.next, min_of(m[u], a.max));
-    if (above(m[u], a.max)) {
-      a.max = m[u];
-      a.vec = v0 + u * kThreads;
-    }
+    rise(a.max, a.vec, m[u], v0 + u * kThreads);
   }
   refill(most);
   if (!((most - a.ref) * c <= kRebase)) {  // (also without a reference)
@@ -424,7 +428,7 @@ __device__ __forceinline__ Sums stream(const Part<T>& part, Ring& ring, float c)
     const float x = clean<T>(to_float(part.x[part.odd]));
     a.next = max_of(a.next, min_of(x, a.max));
     // in front of every vector, or behind them
-    if (above(x, a.max) ||
+    if (!at_least(a.max, x) ||
         (at_least(x, a.max) && part.odd < part.head && x > -INFINITY)) {
       a.max = x;
       a.vec = -1;
@@ -474,17 +478,17 @@ __device__ void select(Shared& sh, const Part<T>& part, const Sums& a,
   constexpr int kN = Vec<T>::kN;
   const int tid = threadIdx.x, lane = tid & 31;
   // a bound: the top-th largest of 32 groups' maxima
-  const float group = sh.max[lane];
+  const uint32_t group = order_of(sh.max[lane]);
   int ahead = 0;
 #pragma unroll
   for (int k = 0; k < 32; ++k) {
-    const float other = __shfl_sync(0xffffffffu, group, k);
-    ahead += above(other, group) || (k < lane && at_least(other, group));
+    const uint32_t other = __shfl_sync(0xffffffffu, group, k);
+    ahead += other > group || (other == group && k < lane);
   }
   const unsigned last_group = __ballot_sync(0xffffffffu, ahead == top - 1);
-  const float low = __shfl_sync(0xffffffffu, group, __ffs(last_group) - 1);
+  const uint32_t low = __shfl_sync(0xffffffffu, group, __ffs(last_group) - 1);
   // the threads at or above it, in any order, and their vectors
-  const bool in = at_least(a.max, low) && a.max > -INFINITY;
+  const bool in = order_of(a.max) >= low && a.max > -INFINITY;
   uint4 raw = make_uint4(0u, 0u, 0u, 0u);
   if (in && a.vec >= 0) raw = __ldg(part.vec(a.vec));
   const u64 mine =

@@ -487,7 +487,8 @@ typedef struct {
  *                -inf.  NULL: no row is idle for it; logprob must be NULL
  *   temperature  optional fp32 [rows] (NULL: 1).  0 puts all the mass on the
  *                first of the largest logits (log p 0, all others -inf, entropy
- *                0); below zero, NaN or infinite marks an idle row
+ *                0); others count as no less than 2^-100 and no more than
+ *                2^100; below zero, NaN or infinite marks an idle row
  *   logprob, entropy   optional fp32 [rows]
  *   top_ids int32, top_logprobs fp32 [rows, top], contiguous; NULL with top 0
  * 4-byte aligned (bf16 logits 2).  One launch; the result is the same on every run.

@@ -72,6 +72,7 @@ constexpr int kTop = kLogprobMaxTop;
 // (a vector of 8 even for the last of them)
 constexpr int kCands = kTop * (kTop + 1) / 2 + 28;
 constexpr float kMaxFinite = 3.402823466e+38f;
+constexpr float kTempMin = 7.8886091e-31f, kTempMax = 1.2676506e+30f;  // 2^-100, 2^100
 typedef unsigned long long u64;
 
 __device__ __forceinline__ u64 pack2(float lo, float hi) {
@@ -634,13 +635,14 @@ __device__ __forceinline__ Row row_of(const LogprobParams& p, int row) {
   Row r;
   r.token = p.token ? p.token[row] : 0;
   r.temp = p.temperature ? p.temperature[row] : 1.f;
-  r.live = r.token >= 0 && r.token < p.vocab && r.temp >= 0.f &&
-           r.temp <= kMaxFinite;
-  r.one = r.temp == 0.f;
-  // 1 / T stays inside fp32's range
-  r.c = r.one ? 1.f
-              : fminf(fmaxf(__fdiv_rn(1.4426950408889634f, r.temp), 1e-37f),
-                      1e37f);
+  // by the bits: comparisons take subnormal numbers of either sign as zero
+  const uint32_t bits = __float_as_uint(r.temp);
+  r.one = bits << 1 == 0;
+  r.live = r.token >= 0 && r.token < p.vocab && (bits < 0x7f800000u || r.one);
+  // With temperatures inside these bounds 1 / T lies in fp32's range, and
+  // logits of T's size are not among the numbers that are flushed.
+  r.temp = fminf(fmaxf(r.temp, kTempMin), kTempMax);
+  r.c = r.one ? 1.f : __fdiv_rn(1.4426950408889634f, r.temp);
   return r;
 }
 __device__ __forceinline__ int top_of(const LogprobParams& p, const Row& r) {

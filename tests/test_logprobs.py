@@ -411,6 +411,24 @@ def test_no_log_probability_above_zero(dtype, rows, vocab):
     assert (out["logprob"] <= 0).all() and (out["top_logprobs"] <= 0).all()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,vocab", [(9, 20000), (320, 3001)])
+def test_temperatures_at_the_ends_of_their_range(rows, vocab):
+    # logits as small or as large as the temperature, which counts as 2^-100
+    # below that and as 2^100 above; subnormal ones are not zero
+    x = logits(rows, vocab, torch.float32, seed=18)
+    t = np.full(rows, 1.0)
+    t[:9] = [1e-38, 1e-30, 1e-40, 1e-45, 3e38, 1e37, 1e30, 1e-31, -1e-45]
+    scale = np.where((t == 1) | (t < 0), t, np.clip(t, 2.0 ** -100,
+                                                    2.0 ** 100))
+    x = x * torch.as_tensor(scale, dtype=torch.float32, device=DEV)[:, None]
+    x[2, 5:9] = x[2].max()                  # equals share the mass
+    x[3] = 0
+    token = np.arange(rows) * 3 + 5
+    out = run(x, token, t.astype(np.float32), 5)
+    check(x, out, token, scale.astype(np.float32), 5)
+
+
 # ---------------------------------------------------------------- CPU tests
 
 FAKE = ctypes.c_void_p(0x100000)   # never dereferenced: checks come first

@@ -199,7 +199,7 @@ __device__ __forceinline__ int place_of(u64 key) {
 }
 
 struct Shared {
-  float max[32], s[kWarps], h[kWarps];  // largest of every 16 threads; sums
+  float max[32], s[kWarps], h[kWarps];  // largest of every kGroup threads; sums
   // selection: keys, in pairs
   __align__(16) u64 list[kThreads + 2];
   __align__(16) u64 cands[kCands + 2];
@@ -756,55 +756,27 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   if (threadIdx.x < 32) finish<T>(p, row, r, m, s, h, sh.top);
 }
 
-// Keys that beat or equal `low`, of `n` (key(i), 0 for none), ranked: the best
-// `top` into sh.top.  Called by the whole CTA; ends with a barrier.
-template <typename F>
-__device__ __forceinline__ void join_tops(Shared& sh, int n, int top, u64 low,
-                                          F key) {
-  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+// The best `top` of `n` keys that beat or equal `low` (0 is none) into sh.top.
+// Called by the whole CTA; ends with a barrier.
+__device__ __forceinline__ void join_tops(Shared& sh, const u64* keys, int n,
+                                          int top, u64 low) {
+  static_assert(kMaxCluster * kTop <= kCands, "all of them may be as good");
+  const int tid = threadIdx.x;
   if (tid == 0) sh.found = 0;
   if (tid < kTop) sh.top[tid] = 0;
   __syncthreads();
-#pragma unroll 4
   for (int i = tid; i < n; i += kThreads) {
-    const u64 k = key(i);
-    if (k && k >= low) {
-      const int at = atomicAdd(&sh.found, 1);
-      if (at < kCands) sh.cands[at] = k;
-    }
+    const u64 k = keys[i];
+    if (k && k >= low) sh.cands[atomicAdd(&sh.found, 1)] = k;
   }
   __syncthreads();
   const int found = sh.found;
-  if (found <= kCands) {
-    if (tid == 0) sh.cands[found] = 0;
-    __syncthreads();
-    for (int i = tid; i < found; i += kThreads) {
-      const u64 k = sh.cands[i];
-      const int at = rank_in(sh.cands, found, k);
-      if (at < top) sh.top[at] = k;
-    }
-  } else {
-    // parts with many large values each: one place after the other
-    u64 before = ~0ull;
-    for (int at = 0; at < top; ++at) {
-      u64 most = 0;
-      for (int i = tid; i < n; i += kThreads) {
-        const u64 k = key(i);
-        if (k < before && k > most) most = k;
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        const u64 other = __shfl_xor_sync(0xffffffffu, most, o);
-        most = other > most ? other : most;
-      }
-      __syncthreads();  // list is read
-      if (lane == 0) sh.list[w] = most;
-      __syncthreads();
-      for (int k = 0; k < kWarps; ++k) most = sh.list[k] > most ? sh.list[k] : most;
-      if (tid == 0) sh.top[at] = most;
-      before = most;
-      if (!most) break;  // uniform
-    }
+  if (tid == 0) sh.cands[found] = 0;
+  __syncthreads();
+  for (int i = tid; i < found; i += kThreads) {
+    const u64 k = sh.cands[i];
+    const int at = rank_in(sh.cands, found, k);
+    if (at < top) sh.top[at] = k;
   }
   __syncthreads();
 }
@@ -873,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       const u64 other = __shfl_xor_sync(0xffffffffu, last, o);
       last = other > last ? other : last;
     }
-    join_tops(sh, csize * top, top, last, [&](int i) { return c_top[i]; });
+    join_tops(sh, c_top, csize * top, top, last);
   }
   if (w == 0) finish<T>(p, row, r, m, s, h, sh.top);
 }

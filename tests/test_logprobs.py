@@ -429,6 +429,31 @@ def test_temperatures_at_the_ends_of_their_range(rows, vocab):
     check(x, out, token, scale.astype(np.float32), 5)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows", [1, 3, 12, 30, 70, 153])
+def test_parts_one_short_of_their_places(dtype, rows):
+    # In each part that a row is cut into, top - 1 large logits and no other
+    # that comes near: no part's last place is a bound for the join, which
+    # then gets as many candidates as it can.
+    top, vocab = 32, 248320
+    size = 1                        # CTAs a row, by the rule of the launch
+    while size < 16 and 2 * size * rows <= 2 * 152 and 2 * size * 4096 <= vocab:
+        size *= 2
+    x = logits(rows, vocab, dtype, seed=19, peaks=0)
+    live = rows - 1
+    part = vocab // size
+    g = torch.Generator(device=DEV).manual_seed(20)
+    for r in range(size):           # (off the parts' borders)
+        at = r * part + 64 + torch.randperm(
+            part - 128, generator=g, device=DEV)[:top - 1]
+        x[live, at] = 100 + torch.randint(
+            0, 64, (top - 1,), generator=g, device=DEV).to(dtype) / 2
+    token = np.full(rows, -1)
+    token[live] = 64
+    check(x, run(x, token, None, top), token, None, top)
+
+
 # ---------------------------------------------------------------- CPU tests
 
 FAKE = ctypes.c_void_p(0x100000)   # never dereferenced: checks come first

@@ -369,6 +369,57 @@ def test_scales_below_the_normal_numbers(kv, widths):
         c.check(c.run())
 
 
+def check_rows(c, out, b, i):
+    """The rows of block rows i of request b against the definition."""
+    G, n = c.hq // c.hkv, c.seqs[b]
+    i = torch.tensor(sorted(i), device=DEV)
+    q = c.q[b, i].double().view(-1, c.hkv, G, D)
+    got = out[b, i].double().view(-1, c.hkv, G, D)
+    hidden = (torch.arange(n, device=DEV)
+              > (n - c.widths[b] + i)[:, None])[:, None]
+    k, v = (c.dense(p, s, b, n) for p, s in ((c.k, c.ks), (c.v, c.vs)))
+    for h in range(c.hkv):
+        z = torch.einsum("rgd,td->rgt", q[:, h], k[h]) * c.scale
+        X = (torch.einsum("rgd,td->rgt", q[:, h].abs(), k[h].abs())
+             .masked_fill(hidden, 0).amax(-1) * c.scale)
+        p = torch.softmax(z.masked_fill(hidden, -np.inf), -1)
+        want, A = p @ v[h], p @ v[h].abs()
+        e = 2.0 ** -13 + 2.0 ** -18 * X + (
+            2.0 ** -8 if c.kv == "bf16" else 2.0 ** -10 + 2.0 ** -10 * X)
+        tol = e[..., None] * A + 2.0 ** -8 * want.abs()
+        assert torch.all((got[:, h] - want).abs() <= tol), (b, h)
+
+
+def rows_beside_borders(c, b, most=40):
+    """Block rows on both sides of the borders of the CTAs' rows (every other
+    one a row tile's) and of the 128-token tiles of the cache."""
+    G, w, n = c.hq // c.hkv, c.widths[b], c.seqs[b]
+    whole = 128 // G * G if G <= 128 else 0
+    rows = whole if whole >= 116 else 128
+    cta = [((R - 1) // G, R // G) for R in range(rows, w * G, rows)]
+    tile = [(t - (n - w) - 1, t - (n - w))
+            for t in range(-(-(n - w + 1) // 128) * 128, n, 128)]
+    pick = {0, w - 1}
+    for borders in (cta, tile):
+        for pair in borders[::-(-len(borders) // most) or 1]:
+            pick |= set(pair)
+    assert all(0 <= x < w for x in pick)
+    return pick
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("hq,hkv,widths,prefixes", [
+    (24, 4, [1500], [0]), (24, 4, [700, 650], [20000, 3]),
+    (24, 4, [300], [5000]), (4, 4, [1100], [77]), (38, 2, [400], [900]),
+    (26, 2, [400], [900]), (150, 1, [90, 70], [0, 1000])])
+def test_rows_beside_borders(kv, hq, hkv, widths, prefixes):
+    c = Case(widths, prefixes, hq=hq, hkv=hkv, kv=kv, seed=22)
+    out = c.run()
+    for b in range(c.B):
+        check_rows(c, out, b, rows_beside_borders(c, b))
+
+
 # ---------------------------------------------------------------- CPU tests
 
 FAKE = ctypes.c_void_p(0x100000)   # never dereferenced: checks come first

@@ -420,6 +420,52 @@ def test_rows_beside_borders(kv, hq, hkv, widths, prefixes):
         check_rows(c, out, b, rows_beside_borders(c, b))
 
 
+# new tokens, cached ones, heads; 4,248, 4,416 and 4,108 pieces of 1,062, 138 and
+# 1,027 row tiles.  Dealt to 76 pairs, four long pieces of the last are left
+# behind 54 rounds, and those are cut.
+LARGE = [([30000, 14500, 1], [0, 300, 2000], 24, 4),
+         ([20000, 15000], [0, 0], 32, 32),
+         ([168] * 256 + [126], [8000] * 257, 24, 4)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("widths,prefixes,hq,hkv", LARGE)
+def test_plans_of_many_pieces(kv, widths, prefixes, hq, hkv):
+    # more pieces than the plan holds in shared memory, more row tiles than it
+    # has threads: sampled rows, the first and the last of requests
+    c = Case(widths, prefixes, page=64, kv=kv, hq=hq, hkv=hkv, seed=23)
+    out = c.run()
+    assert torch.isfinite(out.float()).all()
+    r = np.random.default_rng(24)
+    for b in sorted({0, 1, c.B - 1, *r.integers(0, c.B, 6).tolist()}):
+        w = c.widths[b]
+        check_rows(c, out, b, {0, w - 1, w // 2, *r.integers(0, w, 12)})
+    assert torch.equal(c.run(), out)
+    # every token of every row counts once: equal weights, and V that is a
+    # number of the token's tile
+    c.q.zero_()
+    c.v.zero_()
+    one = 0x38 if kv == "fp8" else 1.0                        # E4M3 one
+    for b, n in enumerate(c.seqs):
+        t = torch.arange(n, device=DEV)
+        c.v[c.table[b, t // 64].long(), :, t % 64, t // 128 % 256] = one
+    if kv == "fp8":
+        c.vs.fill_(1.0)
+    out = c.run()
+    for b, n in enumerate(c.seqs):
+        w = c.widths[b]
+        limit = n - w + torch.arange(w, device=DEV) + 1
+        tiles = torch.arange(-(-n // 128), device=DEV)
+        want = torch.zeros(w, 256, device=DEV, dtype=torch.float64)
+        want.index_add_(1, tiles % 256, (limit[:, None] - tiles * 128)
+                        .clamp(0, 128).double())
+        want = (want / limit[:, None])[:, None]
+        # equal weights are exact; fp32 sums and divisions, a bf16 output
+        assert torch.all((out[b, :w].double() - want).abs()
+                         <= want * (2.0 ** -8 + 2.0 ** -13))
+
+
 # ---------------------------------------------------------------- CPU tests
 
 FAKE = ctypes.c_void_p(0x100000)   # never dereferenced: checks come first

@@ -12,11 +12,11 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 static_assert(kThreads >= kMaxBatch, "");
+static_assert(kChunkBuckets == 64, "two a lane");
+constexpr int kHeld = 4096;  // pieces whose tile counts shared memory holds
 // A run of the rest is at least this long, in 128-token tiles, and one that
 // would start or end as close as kSnap to a piece's border starts or ends there
 // (a piece costs as much as kPrefixCost tiles).
-static_assert(kChunkBuckets == 64, "two a lane");
-constexpr int kHeld = 4096;
 constexpr int kMinRun = 2;
 constexpr int kSnap = 2;
 

@@ -508,7 +508,9 @@ int chunk_layout(const spec_attn_desc* d, ChunkLayout* C) {
   C->pieces = take(tiles * sizeof(specv::ChunkPiece));
   C->runs = take(C->pairs * sizeof(specv::ChunkRun));
   C->rest = take(C->pairs * sizeof(int2));
-  // a partial slot is its pair's number plus its piece's in the rest
+  // Partials: one for each run that is not empty (pairs at most), and one more for
+  // each border of a cut piece inside a run (a piece of the rest, of which there
+  // are fewer than pairs).
   const size_t slots = 2 * (size_t)C->pairs * specv::kPrefixRows;
   C->o = take(slots * specv::kHeadDim * sizeof(float));
   C->lse = take(slots * sizeof(float));

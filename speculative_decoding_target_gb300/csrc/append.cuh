@@ -44,6 +44,16 @@ struct RopeParams {
   float eps, w_offset;
 };
 
+// A channel's factor behind its head's norm.
+__device__ __forceinline__ float norm_weight(const RopeParams& p, const void* w,
+                                             int c) {
+  if (!w) return 0.f;  // no queries
+  return p.w_offset + (p.w_bf16
+                           ? __bfloat162float(
+                                 static_cast<const __nv_bfloat16*>(w)[c])
+                           : static_cast<const float*>(w)[c]);
+}
+
 // A frequency as a 64-bit fraction of a turn (rope_append.cu).
 __device__ __forceinline__ uint64_t turn_of(double f) {
   const double turns = f * 0.15915494309189533577;  // 1 / 2 pi

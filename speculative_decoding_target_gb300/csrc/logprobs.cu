@@ -51,6 +51,7 @@
 
 #include "common.cuh"
 #include "logprobs.cuh"
+#include "packed.cuh"
 #include "pair_ptx.cuh"
 
 namespace specv {
@@ -73,28 +74,7 @@ constexpr int kTop = kLogprobMaxTop;
 constexpr int kCands = kTop * (kTop + 1) / 2 + 28;
 constexpr float kMaxFinite = 3.402823466e+38f;
 constexpr float kTempMin = 7.8886091e-31f, kTempMax = 1.2676506e+30f;  // 2^-100, 2^100
-typedef unsigned long long u64;
 
-__device__ __forceinline__ u64 pack2(float lo, float hi) {
-  u64 v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
-  return v;
-}
-__device__ __forceinline__ float2 unpack2(u64 v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
-  u64 d;
-  asm("fma.rn.ftz.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ u64 add2(u64 a, u64 b) {
-  u64 d;
-  asm("add.rn.ftz.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

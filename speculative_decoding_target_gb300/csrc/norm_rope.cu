@@ -20,6 +20,7 @@
 // way; they take the kernel in rope_append.cu.
 #include "append.cuh"
 #include "common.cuh"
+#include "packed.cuh"
 #include "spec_verify.h"
 
 namespace specv {
@@ -36,28 +37,6 @@ struct Shape {
   static constexpr int kCtasPerSm = kFp8 ? 2 : 3;
   static constexpr int kThreads = kWarps * 32;
 };
-typedef unsigned long long u64;
-
-__device__ __forceinline__ u64 pack2(float lo, float hi) {
-  u64 v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
-  return v;
-}
-__device__ __forceinline__ float2 unpack2(u64 v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
-  u64 d;
-  asm("fma.rn.ftz.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
-  u64 d;
-  asm("mul.rn.ftz.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 
 // Eight bf16 channels as four packed pairs of neighbours.
 __device__ __forceinline__ void widen(uint4 v, u64 (&x)[4]) {
@@ -82,15 +61,6 @@ __device__ __forceinline__ void load8(const float* p, u64 (&x)[4]) {
   x[1] = lo.y;
   x[2] = hi.x;
   x[3] = hi.y;
-}
-
-__device__ __forceinline__ float norm_weight(const RopeParams& p, const void* w,
-                                             int c) {
-  if (!w) return 0.f;  // no queries
-  return p.w_offset + (p.w_bf16
-                           ? __bfloat162float(
-                                 static_cast<const __nv_bfloat16*>(w)[c])
-                           : static_cast<const float*>(w)[c]);
 }
 
 // Correctly rounded quotients by a finite scale s, with r the correctly rounded
@@ -135,10 +105,6 @@ __device__ __forceinline__ void quantise_half(const float (&x)[16], int l,
       make_uint4(packed[0], packed[1], packed[2], packed[3]);
   if ((l & 3) == 0) sdst[l >> 2] = scale;
 }
-
-}  // namespace
-
-namespace {
 
 template <bool kInterleaved, bool kFp8>
 __global__ void __launch_bounds__(Shape<kFp8>::kThreads,

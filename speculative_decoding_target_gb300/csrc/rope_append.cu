@@ -52,15 +52,6 @@ __device__ __forceinline__ uint2 pack4(const float* x) {
                     *reinterpret_cast<const uint32_t*>(&hi));
 }
 
-__device__ __forceinline__ float norm_weight(const RopeParams& p, const void* w,
-                                             int c) {
-  if (!w) return 0.f;  // no queries
-  return p.w_offset + (p.w_bf16
-                           ? __bfloat162float(
-                                 static_cast<const __nv_bfloat16*>(w)[c])
-                           : static_cast<const float*>(w)[c]);
-}
-
 template <bool kInterleaved, bool kNorm>
 __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
     rope_append_kernel(const RopeParams p) {

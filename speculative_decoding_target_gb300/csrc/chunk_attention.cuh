@@ -6,7 +6,7 @@
 // g, token by token: row R is token R / group of the chunk.  They are cut into row
 // tiles of 2 cta_rows, half for each CTA of a pair: as many whole tokens as fit
 // into 128 rows, so that one tensor copy brings a CTA's queries, or 128 rows where
-// whole tokens would leave more than a tenth of them empty.  Row tile m attends
+// whole tokens would leave more than three of them empty.  Row tile m attends
 // the first t 128-token tiles of the cache that its last row sees.  A piece is a
 // row tile over a run of those.
 //
@@ -58,14 +58,18 @@ struct ChunkParams {
   int q_tokens;       // tokens of a tensor copy of queries; 0: no such copies
 };
 
-// Tokens whose rows fill a CTA well enough (of 128 rows no more than 12 empty).
-// With groups of 6, 126 rows: 4,096 tokens into an empty cache 156 us, against 179
-// with 128 rows that threads copy; 2,048 tokens over 32,768, of which the copies
-// are a small part, 1,010 us against 985 (both sides before the softmax's packed
-// arithmetic, which takes 10 us from the first).
+// Tokens whose rows fill a CTA well enough (of 128 rows no more than 3 empty).
+// Whole tokens against 128 rows that threads copy, 22 to 50 query heads, us:
+//   rows a CTA          300 tokens   4,096 tokens   700 behind   2,048 behind
+//                       into empty   into empty     12,000       32,768
+//   126 (groups of 6)   19 / 20.5    145 / 153      149 / 150    1,010 / 996
+//   125 (25)            22.5 / 25    312 / 347      277 / 273    2,074 / 2,008
+//   121 (11)            21.5 / 23    164 / 156      146 / 144    912 / 833
+//   120 (20)            22.5 / 24.5  288 / 281      242 / 216    1,752 / 1,631
+// Short calls gain 1.5 us either way; long ones lose the empty rows' share.
 inline int chunk_q_tokens(int group) {
   const int n = group <= 128 ? 128 / group : 0;
-  return n * group >= 116 ? n : 0;
+  return n * group >= 125 ? n : 0;
 }
 
 // A request's rows: of its w new tokens the last `live` are in the cache (all,

@@ -392,15 +392,15 @@ def check_rows(c, out, b, i):
 
 def rows_beside_borders(c, b, most=40):
     """Block rows on both sides of the borders of the CTAs' rows (every other
-    one a row tile's) and of the 128-token tiles of the cache."""
+    one a row tile's), of 128 or of whole tokens, and of the 128-token tiles
+    of the cache."""
     G, w, n = c.hq // c.hkv, c.widths[b], c.seqs[b]
-    whole = 128 // G * G if G <= 128 else 0
-    rows = whole if whole >= 116 else 128
-    cta = [((R - 1) // G, R // G) for R in range(rows, w * G, rows)]
+    cta = [[((R - 1) // G, R // G) for R in range(rows, w * G, rows)]
+           for rows in {128, 128 // G * G or 128}]
     tile = [(t - (n - w) - 1, t - (n - w))
             for t in range(-(-(n - w + 1) // 128) * 128, n, 128)]
     pick = {0, w - 1}
-    for borders in (cta, tile):
+    for borders in (*cta, tile):
         for pair in borders[::-(-len(borders) // most) or 1]:
             pick |= set(pair)
     assert all(0 <= x < w for x in pick)

@@ -212,10 +212,14 @@ size_t spec_verify_shared_workspace_size(const spec_attn_desc* desc,
  * spec_verify_attention for any q_len >= 1 (batch * q_len * Hq < 2^31): row i <
  * q_b of request b is token seq_lens[b] - q_b + i and attends causally to the
  * first seq_lens[b] - q_b + i + 1 cached tokens; rows i >= q_b, and rows whose
- * window is empty, output zeros.  q_len * Hq / Hkv is not bounded.  The weights
- * are rounded once to the type of the values (fp16 for FP8 KV).  What lies in
+ * window is empty, output zeros.  q_len * Hq / Hkv is not bounded.  What lies in
  * the pool behind a request's tokens may hold any bits; cached values that some
- * row of the chunk sees have to be finite.
+ * row of the chunk sees have to be finite, and with FP8 KV the dequantised keys
+ * and values and the queries have to lie within fp16's range (|x| <= 65504).
+ *
+ * Precision: the weights are rounded once, to bf16 (2^-8 of each at most), or to
+ * fp16 for FP8 KV.  With q_len <= 16 and q_len * Hq / Hkv <= 128 the call is
+ * spec_verify_attention itself, which keeps bf16 KV's weights in two bf16 terms.
  *
  *   page_size  >= 8 (below: SPEC_ERR_UNSUPPORTED unless the chunk fits
  *              spec_verify_attention's block)

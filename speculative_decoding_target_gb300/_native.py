@@ -447,7 +447,9 @@ def chunk_attention(q, k_pages, v_pages, page_table, seq_lens, *,
     """Attention of a chunk of new tokens (a prompt or a piece of one, already
     appended) over the paged cache, causal within the chunk: q bf16
     [B, q_len, Hq, 256] for any q_len, q_lens optional int32 [B] tokens per
-    request of a chunk padded to q_len.  Returns out bf16 [B, q_len, Hq, 256]."""
+    request of a chunk padded to q_len.  Returns out bf16 [B, q_len, Hq, 256].
+    The weights are rounded to bf16 (fp16 for FP8 KV), but a chunk of at most
+    16 tokens and 128 rows per KV head is a block of verify_attention."""
     B, q_len, hq, d = q.shape
     _expect(q, torch.bfloat16, "q", contiguous=True)
     fp8 = _expect_pools(k_pages, v_pages, k_scales, v_scales,

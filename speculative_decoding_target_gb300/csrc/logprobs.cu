@@ -11,10 +11,10 @@
 // A CTA a row: 256 threads, four CTAs an SM, so that one row's reductions and
 // selection run under the others' loads, and the hardware deals the rows out.
 // (1,024 bf16 rows of 248,320 with top 20: 90.7 us, 5.6 TB/s; 512 threads 90.6, but
-// 6,000 rows of 33,000 then take 186 us instead of 112.  Resident CTAs that start on
+// 6,000 rows of 33,000 with top 5 then take 186 us instead of 110.  Resident CTAs that start on
 // their next row under the last one's selection: 103 and 223 us.  Equal runs of
 // slices that cut rows, joined by a second kernel: 112 us, and 256 rows 44 instead
-// of 27.  Such runs dealt out by a counter, shorter ones last: 121 to 150 us.)
+// of 32.  Such runs dealt out by a counter, shorter ones last: 121 to 150 us.)
 //
 // While that leaves SMs idle, a cluster a row, of a size that puts up to two CTAs on
 // an SM: 100 rows of 33,000 11.1 us with two CTAs a row, 12.2 with four; 64 fp32
@@ -34,7 +34,8 @@
 // rounded by (delta) is put right where the threads' sums join.  A batch with
 // values that are not finite makes h NaN or infinite; it, and one whose ref c is
 // too large to be rounded so, is summed from (x - ref) c, where -inf and NaN
-// weigh nothing.
+// weigh nothing.  (Rows with banned tokens, 1,024 bf16 rows of 248,320, top 20: one
+// in a thousand 113 us, half of them 132, all in one half of the row 109.)
 //
 // Alternatives.  Each thread keeps its largest value, the vector that holds it
 // (the first, of equals) and the largest value of its other vectors.  The `top`
@@ -43,7 +44,8 @@
 // winners reads that one vector again (on its way while they are ranked) and hands
 // in what is not below the last winner's value.  A winner whose other vectors hold
 // such values too, as with many equals, is read by a warp as a whole, and its best
-// top - r are taken out.  (1,024 bf16 rows: top 20 takes 11 us more than none;
+// top - r are taken out.  Values are compared without flushing subnormal ones, or
+// as whole numbers of the same order.  (1,024 bf16 rows: top 20 takes 11 us more than none;
 // reading all values of every winner took 38.)
 #include <cuda_bf16.h>
 

@@ -12,9 +12,10 @@
 // interleaved): four shuffles for the sum of squares, one set of sines for all
 // rows of a token, and packed fp32 arithmetic.  (A warp a row with 8 channels a
 // lane took 64.8 us for 8,192 tokens where this takes 51.8, the copy rate 39.7.
-// What is left is instructions and their latency: issue 55% busy.  Rows copied a
-// token or two ahead through shared memory: 54.6 to 57; two tokens at a time with
-// 128 registers: 56; one barrier for the angles of two tokens 52.2, of four 53.3.)
+// What is left is the chain of a token, at one barrier each: issue 55% busy.  Rows
+// copied a token or two ahead through shared memory: 54.6 to 57; two tokens at a
+// time with 128 registers: 56; one barrier for the angles of two tokens 52.2, of
+// four 53.3.)
 //
 // Half layouts whose rotary / 2 is no multiple of 8 channels do not split that
 // way; they take the kernel in rope_append.cu.

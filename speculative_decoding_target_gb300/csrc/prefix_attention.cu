@@ -60,7 +60,8 @@
 // Causal (chunk_attention.cuh), bf16: 4,096 tokens into an empty cache, 206 Gflop,
 // 146 us, 136 of them here; 2,048 tokens behind 32,768, 1.70 Pflop, 941 us at full
 // clocks, 0.94 of the measured bf16 rate, 1,036 under the power limit.  FP8, six
-// ragged requests, 319 Gflop: 316 us.
+// ragged requests on 16-token pages, 274 Gflop: 291 us; 2,048 tokens behind 32,768
+// 1,250.
 //
 // Every wait is bounded as in verify_attention_tc.cu.
 #include <cuda_fp8.h>
